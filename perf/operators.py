@@ -273,7 +273,7 @@ def _own(s):
         s["lens"].copy_(s["lens0"])
         mm.mm_cache_reserve(c, s["need"], s["missing"])
         mm.mm_cache_append(c, 0, s["k_new"], s["v_new"], s["k_new"].stride(0), s["q_start"], s["tokens"], s["max_q"])
-        mm.mm_cache_compact(c, s["q_start"], s["keep"], s["kept"], s["max_q"])
+        mm.mm_cache_compact(c, s["q_start"], s["keep"], s["kept"], s["tokens"], s["max_q"])
         return {x: s[x] for x in ("k", "v", "table", "lens", "refs", "missing")}
     q, out = s["q"], s["out"]
     ws = s.get("workspace")
