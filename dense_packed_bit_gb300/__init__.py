@@ -23,6 +23,9 @@ __all__ = [
     "mm_gemv_packed2_strided_batched", "mm_gemv_packed2_strided_batched_ex", "mm_gemm_f32_bias_act_splitk",
     "mm_gemm_f32_split_plan", "mm_gemm_f32_splitk_ex", "mm_gemm_f32_splitk_workspace_ex", "mm_gemm_f32_split_plan_ex",
     "mm_probe_bounded_wait", "mm_attention_fwd", "mm_attention_bwd",
+    "mm_cache", "mm_cache_reserve", "mm_cache_append", "mm_cache_compact", "mm_cache_fork", "mm_cache_free",
+    "mm_cache_copy_pages", "mm_cache_attention_workspace", "mm_cache_attention", "mm_cache_attention_tree",
+    "mm_sample", "MM_F16", "MM_BF16", "MM_F32",
     "MM_OK", "MM_ERR_INVALID_ARG", "MM_ERR_UNSUPPORTED", "MM_ERR_CUDA", "MM_ERR_TIMEOUT",
     "MM_GEMM_AUTO", "MM_GEMM_FFMA", "MM_GEMM_TF32X3",
     "MM_DEQ_AUTO", "MM_DEQ_SELECT", "MM_DEQ_AFFINE", "MM_DEQ_MMA", "MM_DEQ_FP8", "MM_DEQ_TC", "MM_DEQ_MXF4",
@@ -33,6 +36,7 @@ MM_GEMM_AUTO, MM_GEMM_FFMA, MM_GEMM_TF32X3 = 0, 1, 2
 MM_DEQ_AUTO, MM_DEQ_SELECT, MM_DEQ_AFFINE, MM_DEQ_MMA, MM_DEQ_FP8, MM_DEQ_TC, MM_DEQ_MXF4 = 0, 1, 2, 3, 4, 5, 6
 MM_SPLITK_NOALLOC_MAX_FLOATS = 4194304  # floats of the static split-K scratch (16 MiB), as in mm.h
 MM_ACT_NONE, MM_ACT_GELU_TANH = 0, 1
+MM_F16, MM_BF16, MM_F32 = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -61,6 +65,18 @@ class Gemv4Opts(ctypes.Structure):
     _fields_ = [("blocks", ctypes.c_int), ("pdl", ctypes.c_int), ("weights_static", ctypes.c_int),
                 ("independent", ctypes.c_int), ("staging", ctypes.c_int), ("reserved", ctypes.c_int * 3)]
 
+
+class Cache(ctypes.Structure):
+    """mm_cache of mm.h; mm_cache() makes one from tensors."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("layers", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("reserved", ctypes.c_int * 5)]
+
+
+_PC, _PI64, _F = ctypes.POINTER(Cache), ctypes.POINTER(ctypes.c_int64), ctypes.c_float
 
 SIGNATURES = {
     "mm_version": ([], ctypes.c_int),
@@ -95,6 +111,18 @@ SIGNATURES = {
     "mm_gemv_packed2_strided_batched_ex": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P,
                                             ctypes.POINTER(GemvOpts)], ctypes.c_int),
     "mm_probe_bounded_wait": ([_I, ctypes.c_uint64, _P, _P], ctypes.c_int),
+    "mm_cache_reserve": ([_PC, _P, _P, _P], ctypes.c_int),
+    "mm_cache_append": ([_PC, _I64, _P, _P, _I64, _P, _I64, _I64, _P], ctypes.c_int),
+    "mm_cache_compact": ([_PC, _P, _P, _P, _I64, _I64, _P], ctypes.c_int),
+    "mm_cache_fork": ([_PC, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "mm_cache_free": ([_PC, _P, _I64, _I64, _I64, _P], ctypes.c_int),
+    "mm_cache_copy_pages": ([_PC, _P, _P, _I64, _P], ctypes.c_int),
+    "mm_cache_attention_workspace": ([_PC, _I64, _I64, _I64, _PI64], ctypes.c_int),
+    "mm_cache_attention": ([_PC, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _F, _P, _I64, _P, _I64, _P],
+                           ctypes.c_int),
+    "mm_cache_attention_tree": ([_PC, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _F, _P, _I64, _P,
+                                 _I64, _P], ctypes.c_int),
+    "mm_sample": ([_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "mm_attention_fwd": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P], ctypes.c_int),
     "mm_attention_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P],
                          ctypes.c_int),
@@ -327,3 +355,96 @@ def mm_attention_bwd(Q, K, V, O, dO, L, dQ, dK, dV, heads, T, D, causal, scale, 
     _check(load_library().mm_attention_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(dO), _ptr(L), _ptr(dQ),
                                            _ptr(dK), _ptr(dV), heads, T, D, int(causal), float(scale),
                                            _stream(stream)))
+
+
+def _dtype(t) -> int:
+    name = str(t.dtype)
+    try:
+        return {"torch.float16": MM_F16, "torch.bfloat16": MM_BF16, "torch.float32": MM_F32}[name]
+    except KeyError:
+        raise ValueError(f"no kernel takes {name}") from None
+
+
+def _int32(t, what, shape):
+    if str(t.dtype) != "torch.int32" or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def mm_cache(k, v, table, lens, refs=None) -> Cache:
+    """The description of a paged cache: k, v [layers][pages][kv_heads][page_size][head_dim] (any strides
+    with contiguous rows, the same for both), table [seqs][max_pages], lens [seqs] and refs [pages] int32.
+    It holds the tensors, so it is made once and kept as long as they are used."""
+    if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(4) != 1:
+        raise ValueError("k and v must be alike, [layers][pages][kv_heads][page_size][head_dim] with contiguous rows")
+    seqs, max_pages = table.shape
+    _int32(table, "table", (seqs, max_pages))
+    _int32(lens, "lens", (seqs,))
+    if refs is not None:
+        _int32(refs, "refs", (k.shape[1],))
+    c = Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(refs), *k.shape, seqs, max_pages,
+              *k.stride()[:4], _dtype(k))
+    c.tensors = (k, v, table, lens, refs)
+    return c
+
+
+def mm_cache_reserve(cache, need, missing, stream=None):
+    """Pages for lens[s] + need[s] tokens of every sequence; missing[0]: pages lacking (nothing is changed then)."""
+    _check(load_library().mm_cache_reserve(cache, _ptr(need), _ptr(missing), _stream(stream)))
+
+
+def mm_cache_append(cache, layer, K, V, kv_token_stride, q_start, tokens, max_new, stream=None):
+    """New tokens' keys and values [tokens][kv_heads][head_dim] into the slots behind lens."""
+    _check(load_library().mm_cache_append(cache, layer, _ptr(K), _ptr(V), kv_token_stride, _ptr(q_start), tokens,
+                                          max_new, _stream(stream)))
+
+
+def mm_cache_compact(cache, q_start, keep, kept, tokens, max_new, stream=None):
+    """Keeps kept[s] of each sequence's new tokens (keep: which, ascending; None: the first ones), moved
+    together; lens grows by kept, pages without a token are released."""
+    _check(load_library().mm_cache_compact(cache, _ptr(q_start), _ptr(keep), _ptr(kept), tokens, max_new,
+                                           _stream(stream)))
+
+
+def mm_cache_fork(cache, parents, children, n, missing, stream=None):
+    """children[i] becomes a copy of parents[i]: full pages shared, the last partial page copied."""
+    _check(load_library().mm_cache_fork(cache, _ptr(parents), _ptr(children), n, _ptr(missing), _stream(stream)))
+
+
+def mm_cache_free(cache, list, n, window=0, sinks=0, stream=None):
+    """Releases the pages of sequences list[:n]: all of them, or with a window those no later query sees."""
+    _check(load_library().mm_cache_free(cache, _ptr(list), n, window, sinks, _stream(stream)))
+
+
+def mm_cache_copy_pages(cache, src, dst, n, stream=None):
+    """Page src[i] into page dst[i], i < n, in all layers."""
+    _check(load_library().mm_cache_copy_pages(cache, _ptr(src), _ptr(dst), n, _stream(stream)))
+
+
+def mm_cache_attention_workspace(cache, heads, tokens, max_q) -> int:
+    """Bytes of workspace mm_cache_attention and _tree need for these sizes (zeroed once before its first use)."""
+    out = ctypes.c_int64(0)
+    _check(load_library().mm_cache_attention_workspace(cache, heads, tokens, max_q, ctypes.byref(out)))
+    return out.value
+
+
+def mm_cache_attention(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, window, sinks, scale, O, o_stride,
+                       workspace, workspace_bytes, stream=None):
+    """O = attention of new tokens Q [tokens][heads][head_dim] over the cache, with a window and sinks."""
+    _check(load_library().mm_cache_attention(cache, layer, _ptr(Q), q_stride, heads, _ptr(q_start), tokens, max_q,
+                                             window, sinks, scale, _ptr(O), o_stride, _ptr(workspace), workspace_bytes,
+                                             _stream(stream)))
+
+
+def mm_cache_attention_tree(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, mask, mask_words, window, sinks,
+                            scale, O, o_stride, workspace, workspace_bytes, stream=None):
+    """mm_cache_attention for a tree of drafted tokens: mask [tokens][mask_words], bit t: sees drafted token t."""
+    _check(load_library().mm_cache_attention_tree(cache, layer, _ptr(Q), q_stride, heads, _ptr(q_start), tokens, max_q,
+                                                  _ptr(mask), mask_words, window, sinks, scale, _ptr(O), o_stride,
+                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mm_sample(logits, rows, vocab, stride, temperature, top_k, top_p, min_p, u, tokens, logprobs=None, stream=None):
+    """tokens[r]: the next token of row r by temperature, top-k, top-p and min-p from the uniform number u[r]
+    (each parameter a [rows] tensor or None: off); logprobs[r]: log of its probability among those kept."""
+    _check(load_library().mm_sample(_ptr(logits), _dtype(logits), rows, vocab, stride, _ptr(temperature), _ptr(top_k),
+                                    _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(tokens), _ptr(logprobs), _stream(stream)))

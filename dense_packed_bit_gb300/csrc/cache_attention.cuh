@@ -1,0 +1,196 @@
+// cache_attention.cuh -- what the kernels of attention over a paged cache share: which keys a row
+// sees, the blocks of keys that a set of rows needs, the split's workspace and its join.
+#pragma once
+
+#include "cache_view.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+namespace mm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The keys a row sees: those before `end` (its own position and what precedes it, or with a tree
+// the tokens before the drafts) that are below `sinks` or at `low` and later, and the drafted tokens
+// whose bit is set.
+struct RowView {
+    int64_t low, end;
+    const uint32_t *bits;  // null: none
+};
+
+__device__ __forceinline__ bool sees(const RowView &r, int64_t j, int64_t sinks, int64_t len, int count) {
+    if (j < r.end) return j >= r.low || j < sinks;
+    if (!r.bits) return false;
+    const int64_t t = j - len;
+    return t < count && (__ldg(r.bits + (t >> 5)) >> (t & 31) & 1u);
+}
+
+// Bits of the row's mask below `count`
+__device__ __forceinline__ int mask_depth(const uint32_t *bits, int count) {
+    int n = 0;
+    for (int w = 0; w * 32 < count; ++w) {
+        uint32_t b = __ldg(bits + w);
+        if (count - w * 32 < 32) b &= (1u << (count - w * 32)) - 1u;
+        n += __popc(b);
+    }
+    return n;
+}
+
+// new token i of a sequence with `len` tokens before it
+__device__ __forceinline__ RowView row_view(const CacheAttnArgs &a, int64_t len, int first, int count, int i) {
+    RowView r;
+    int64_t p = len + i;
+    if (a.mask) {
+        r.bits = a.mask + (int64_t)(first + i) * a.mask_words;
+        p = len + mask_depth(r.bits, count) - 1;
+        r.end = len;
+    } else {
+        r.bits = nullptr;
+        r.end = p + 1;
+    }
+    r.low = a.window > 0 ? p - a.window + 1 : 0;
+    return r;
+}
+
+// One sequence of the call, checked: its rows of Q, its cached tokens.
+struct SeqView {
+    int first, count;
+    int64_t len;
+};
+__device__ __forceinline__ SeqView seq_view(const CacheAttnArgs &a, int seq, unsigned int *err) {
+    SeqView s;
+    const RowRange r = rows_of(a.q_start, seq, a.tokens, a.max_q, err);
+    s.first = r.first, s.count = r.count;
+    s.len = __ldg(a.c.lens + seq);
+    if (s.len < 0 || s.len + s.count > row_capacity(a.c)) {
+        *err = kDevErrRange;
+        s.count = 0;
+        s.len = 0;
+    }
+    // a mask narrower than the tree leaves the drafts past it unseen
+    if (a.mask && s.count > a.mask_words * 32) *err = kDevErrRange, s.count = 0;
+    return s;
+}
+
+// Blocks of B keys that rows with their lowest window start at `low` need, of `end` keys: the blocks of
+// the sinks, then those from low on.  block(i) is the i-th one's number.
+struct KeyBlocks {
+    int64_t sink_blocks, first, count;
+    __device__ __forceinline__ int64_t block(int64_t i) const {
+        return i < sink_blocks ? i : first + (i - sink_blocks);
+    }
+};
+template <int B>
+__device__ __forceinline__ KeyBlocks key_blocks(int64_t low, int64_t sinks, int64_t end) {
+    KeyBlocks k;
+    if (low < 0) low = 0;
+    if (low > end) low = end;
+    k.first = low / B;
+    k.sink_blocks = min((min(sinks, end) + B - 1) / B, k.first);
+    k.count = k.sink_blocks + (end + B - 1) / B - k.first;
+    return k;
+}
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+    __device__ static uint32_t pack(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __device__ static float one(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+    static constexpr uint32_t kExp = 0x7c00u;  // all ones: infinity or NaN
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    __device__ static uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __device__ static float one(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+    static constexpr uint32_t kExp = 0x7f80u;
+};
+
+// either 16-bit half of v infinite or NaN
+template <typename T>
+__device__ __forceinline__ bool any_special(uint32_t v) {
+    return (v & Pair<T>::kExp) == Pair<T>::kExp || ((v >> 16) & Pair<T>::kExp) == Pair<T>::kExp;
+}
+// v with such halves replaced by 0
+template <typename T>
+__device__ __forceinline__ uint32_t without_special(uint32_t v) {
+    if ((v & Pair<T>::kExp) == Pair<T>::kExp) v &= 0xffff0000u;
+    if (((v >> 16) & Pair<T>::kExp) == Pair<T>::kExp) v &= 0x0000ffffu;
+    return v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One row by the definition, key by key, a warp to it: O[4 lane + x] in o (unnormalised over l > 0).
+// For what the tiles cannot do (infinities and NaN among values that only some rows see).
+template <typename T>
+__device__ void attend_row(const CacheAttnArgs &a, int seq, const SeqView &sv, int i, int qhead, unsigned int *err) {
+    const CacheView &c = a.c;
+    const int lane = threadIdx.x & 31, kv_head = qhead / a.group;
+    const RowView r = row_view(a, sv.len, sv.first, sv.count, i);
+    const bool mine = 4 * lane < c.head_dim;
+    const auto get4 = [&](const char *p, float (&f)[4]) {
+        uint2 u = make_uint2(0, 0);
+        if (mine) u = *reinterpret_cast<const uint2 *>(p + 8 * lane);
+        f[0] = Pair<T>::one((uint16_t)u.x), f[1] = Pair<T>::one((uint16_t)(u.x >> 16));
+        f[2] = Pair<T>::one((uint16_t)u.y), f[3] = Pair<T>::one((uint16_t)(u.y >> 16));
+    };
+    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+    get4(static_cast<const char *>(a.Q) + ((int64_t)(sv.first + i) * a.q_stride + (int64_t)qhead * c.head_dim) * 2, q);
+    const float scale2 = a.scale * kLog2e;
+    const int64_t end = sv.len + sv.count;
+    const KeyBlocks kb = key_blocks<16>(a.mask ? min(r.low, sv.len) : r.low, a.sinks, end);
+    for (int64_t b = 0; b < kb.count; ++b) {
+        const int64_t key0 = kb.block(b) * 16;
+        const int page = page_of(c, seq, key0 >> c.page_shift);
+        if (page < 0) {
+            *err = kDevErrRange;
+            continue;
+        }
+        for (int64_t j = key0; j < min(key0 + 16, end); ++j) {
+            if (!sees(r, j, a.sinks, sv.len, sv.count)) continue;
+            const int64_t at =
+                (page * c.page_stride + kv_head * c.head_stride + (j & (c.page_size - 1)) * c.token_stride) * 2;
+            float k[4], v[4];
+            get4(c.k + at, k);
+            get4(c.v + at, v);
+            float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+#pragma unroll
+            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+            s *= scale2;
+            const float now = fmaxf(m, s), f = m == now ? 1.f : ex2(m - now), p = s == -INFINITY ? 0.f : ex2(s - now);
+            m = now;
+            l = l * f + p;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x] = o[x] * f + p * v[x];
+        }
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (mine) {
+        uint2 u = make_uint2(Pair<T>::pack(o[0] * inv, o[1] * inv), Pair<T>::pack(o[2] * inv, o[3] * inv));
+        if (m == -INFINITY && l == 0.f) u = make_uint2(0, 0);
+        *reinterpret_cast<uint2 *>(static_cast<char *>(a.O) +
+                                   ((int64_t)(sv.first + i) * a.o_stride + (int64_t)qhead * c.head_dim) * 2 + 8 * lane) = u;
+    }
+}
+
+cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int splits, cudaStream_t s);
+// splits of each unit's keys over CTAs, of the rows kernel
+int cache_attention_rows_splits(const CacheView &c, int sms);
+int64_t cache_attention_rows_workspace(const CacheView &c, int splits);
+unsigned int cache_attention_rows_take_device_error(cudaError_t *err);
+constexpr int kRowsMax = 16;  // rows (new tokens x heads of a kv head) of one sequence in the rows kernel
+
+}  // namespace mm

@@ -880,6 +880,15 @@ mm_status mm_check_device_error(mm_stream_t stream) {
     const unsigned int pr = mm::wait_probe_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
     if (pr != 0) return fail(MM_ERR_TIMEOUT, "the failure-detection probe's bounded wait ran out (code %u)", pr);
+    const unsigned int cp = mm::cache_pages_take_device_error(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
+    if (cp != 0)
+        return fail(MM_ERR_INVALID_ARG, "cache pages: a page, sequence, length or reference count in device memory is out of range");
+    const unsigned int ca = mm::cache_attention_take_device_error(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
+    if (ca == mm::kCacheErrRange)
+        return fail(MM_ERR_INVALID_ARG, "cache attention: a page, length or row range in device memory is out of range");
+    if (ca != 0) return fail(MM_ERR_TIMEOUT, "a bounded device wait ran out in the cache attention (code %u)", ca);
     return ok();
 }
 
@@ -945,6 +954,288 @@ mm_status mm_attention_bwd(const float *Q, const float *K, const float *V, const
     const cudaError_t e = mm::launch_attention_bwd(Q, K, V, O, dO, L, dQ, dK, dV, heads, T, causal, scale,
                                                    reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "attention backward launch");
+    return ok();
+}
+
+namespace {
+
+bool is_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The cache's description, and `out`: the same for the kernels, layer `layer` applied (-1: all).
+mm_status check_cache(const mm_cache *c, int64_t layer, bool needs_refs, mm::CacheView *out) {
+    if (!c) return fail(MM_ERR_INVALID_ARG, "cache is NULL");
+    if (!c->k || !c->v || !c->table || !c->lens || (needs_refs && !c->refs))
+        return fail(MM_ERR_INVALID_ARG, "NULL pointer in the cache");
+    if (!is_aligned(c->k, 16) || !is_aligned(c->v, 16) || !is_aligned(c->table, 4) || !is_aligned(c->lens, 4) ||
+        !is_aligned(c->refs, 4))
+        return fail(MM_ERR_INVALID_ARG, "misaligned pointer in the cache (k, v: 16 bytes)");
+    if (c->dtype != MM_F16 && c->dtype != MM_BF16) return fail(MM_ERR_INVALID_ARG, "cache dtype must be MM_F16 or MM_BF16");
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(MM_ERR_INVALID_ARG, "page_size must be 16, 32, 64 or 128 (got %lld)", (long long)c->page_size);
+    if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8)
+        return fail(MM_ERR_INVALID_ARG, "head_dim must be a multiple of 8 up to 128 (got %lld)", (long long)c->head_dim);
+    if (c->layers < 1 || c->pages < 1 || c->kv_heads < 1 || c->seqs < 1 || c->max_pages < 1)
+        return fail(MM_ERR_INVALID_ARG, "cache sizes must be >= 1");
+    if (c->layers > 32767 || c->pages > 0x7fffffff || c->kv_heads > 65535 || c->seqs > 65535 || c->max_pages > (1 << 24))
+        return fail(MM_ERR_INVALID_ARG, "cache sizes too large (layers 32767, pages 2^31 - 1, kv_heads and seqs 65535, max_pages 2^24)");
+    const int64_t strides[4] = {c->layer_stride, c->page_stride, c->head_stride, c->token_stride};
+    const int64_t counts[4] = {c->layers, c->pages, c->kv_heads, c->page_size};
+    for (int i = 0; i < 4; ++i) {
+        if (strides[i] < 0 || strides[i] % 8 || strides[i] > ((int64_t)1 << 39))
+            return fail(MM_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements, 0 .. 2^39");
+        if (counts[i] > 1 && strides[i] < c->head_dim)
+            return fail(MM_ERR_INVALID_ARG, "a cache stride is below head_dim: rows overlap");
+    }
+    for (int r : c->reserved)
+        if (r != 0) return fail(MM_ERR_INVALID_ARG, "reserved fields of the cache must be 0");
+    if (layer < -1 || layer >= c->layers)
+        return fail(MM_ERR_INVALID_ARG, "layer %lld is not one of %lld", (long long)layer, (long long)c->layers);
+    const int64_t at = layer > 0 ? layer * c->layer_stride * 2 : 0;
+    out->k = static_cast<char *>(c->k) + at;
+    out->v = static_cast<char *>(c->v) + at;
+    out->table = c->table, out->lens = c->lens, out->refs = c->refs;
+    out->layers = c->layers, out->pages = c->pages, out->max_pages = c->max_pages;
+    out->layer_stride = c->layer_stride, out->page_stride = c->page_stride;
+    out->head_stride = c->head_stride, out->token_stride = c->token_stride;
+    out->seqs = (int)c->seqs, out->kv_heads = (int)c->kv_heads, out->head_dim = (int)c->head_dim;
+    out->page_size = (int)c->page_size;
+    out->page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+    out->dtype = c->dtype;
+    return MM_OK;
+}
+
+mm_status check_ints(const void *p, const char *what) {
+    if (!p || !is_aligned(p, 4)) return fail(MM_ERR_INVALID_ARG, "%s is NULL or misaligned", what);
+    return MM_OK;
+}
+
+// rows of the new tokens
+mm_status check_rows(const int32_t *q_start, int64_t tokens, int64_t max_new) {
+    const mm_status s = check_ints(q_start, "q_start");
+    if (s != MM_OK) return s;
+    if (tokens < 1 || tokens > 0x7fffffff || max_new < 1 || max_new > tokens)
+        return fail(MM_ERR_INVALID_ARG, "tokens must be 1 .. 2^31 - 1 and the bound of one sequence's 1 .. tokens");
+    return MM_OK;
+}
+
+int sm_count() {
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+uint64_t page_bytes_span(const mm_cache *c) {
+    return (uint64_t)((c->layers - 1) * c->layer_stride + (c->pages - 1) * c->page_stride +
+                      (c->kv_heads - 1) * c->head_stride + (c->page_size - 1) * c->token_stride + c->head_dim) * 2;
+}
+
+mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, int64_t q_stride, int64_t heads,
+                          const int32_t *q_start, int64_t tokens, int64_t max_q, const uint32_t *mask,
+                          int64_t mask_words, int64_t window, int64_t sinks, float scale, void *O, int64_t o_stride,
+                          void *workspace, int64_t workspace_bytes, mm_stream_t stream) {
+    mm::CacheAttnArgs a;
+    if (layer < 0) return fail(MM_ERR_INVALID_ARG, "layer must be >= 0");
+    mm_status s = check_cache(cache, layer, false, &a.c);
+    if (s == MM_OK) s = check_rows(q_start, tokens, max_q);
+    if (s != MM_OK) return s;
+    if (!Q || !O || !is_aligned(Q, 16) || !is_aligned(O, 16))
+        return fail(MM_ERR_INVALID_ARG, "Q or O is NULL or not 16-byte aligned");
+    if (heads < 1 || heads > 65535 || heads % cache->kv_heads)
+        return fail(MM_ERR_INVALID_ARG, "heads (%lld) must be a multiple of kv_heads (%lld), at most 65535", (long long)heads,
+                    (long long)cache->kv_heads);
+    const int64_t width = heads * cache->head_dim;
+    if ((tokens > 1 && (q_stride < width || o_stride < width)) || q_stride < 0 || o_stride < 0 || q_stride % 8 || o_stride % 8 ||
+        q_stride > ((int64_t)1 << 31) || o_stride > ((int64_t)1 << 31))
+        return fail(MM_ERR_INVALID_ARG, "q_stride and o_stride must be multiples of 8, at least heads * head_dim");
+    if (window < 0 || sinks < 0) return fail(MM_ERR_INVALID_ARG, "window and sinks must be >= 0");
+    if (!std::isfinite(scale)) return fail(MM_ERR_INVALID_ARG, "scale is not finite");
+    const uint64_t ob = span(tokens, width, o_stride, 2), qb = span(tokens, width, q_stride, 2), cb = page_bytes_span(cache);
+    if (overlap(O, ob, Q, qb) || overlap(O, ob, cache->k, cb) || overlap(O, ob, cache->v, cb) ||
+        overlap(O, ob, q_start, (uint64_t)(cache->seqs + 1) * 4) || overlap(O, ob, cache->table, (uint64_t)(cache->seqs * cache->max_pages) * 4) ||
+        overlap(O, ob, cache->lens, (uint64_t)cache->seqs * 4) ||
+        (mask && overlap(O, ob, mask, (uint64_t)(tokens * mask_words) * 4)))
+        return fail(MM_ERR_INVALID_ARG, "O overlaps an input");
+    a.Q = Q, a.O = O, a.q_start = q_start, a.mask = mask;
+    a.q_stride = q_stride, a.o_stride = o_stride, a.tokens = tokens, a.max_q = max_q;
+    a.window = window > ((int64_t)1 << 40) ? 0 : window;
+    a.sinks = a.window ? sinks : 0;
+    a.mask_words = mask_words;
+    a.heads = (int)heads, a.group = (int)(heads / cache->kv_heads);
+    a.scale = scale, a.ws = workspace;
+    s = check_device();
+    if (s != MM_OK) return s;
+    const int sms = sm_count();
+    const int64_t need = mm::cache_attention_workspace(a.c, a.heads, tokens, max_q, sms);
+    if (need > 0 && (!workspace || !is_aligned(workspace, 16) || workspace_bytes < need))
+        return fail(MM_ERR_INVALID_ARG, "the workspace is NULL, not 16-byte aligned or below %lld bytes", (long long)need);
+    if (need > 0 && (overlap(O, ob, workspace, (uint64_t)need) || overlap(Q, qb, workspace, (uint64_t)need)))
+        return fail(MM_ERR_INVALID_ARG, "the workspace overlaps Q or O");
+    const cudaError_t e = mm::launch_cache_attention(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+    return ok();
+}
+
+}  // namespace
+
+mm_status mm_cache_reserve(const mm_cache *cache, const int32_t *need, int32_t *missing, mm_stream_t stream) {
+    mm::CacheView c;
+    mm_status s = check_cache(cache, -1, true, &c);
+    if (s == MM_OK) s = check_ints(need, "need");
+    if (s == MM_OK) s = check_ints(missing, "missing");
+    if (s == MM_OK) s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e = mm::launch_cache_reserve(c, need, missing, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache reserve launch");
+    return ok();
+}
+
+mm_status mm_cache_append(const mm_cache *cache, int64_t layer, const void *K, const void *V, int64_t kv_token_stride,
+                          const int32_t *q_start, int64_t tokens, int64_t max_new, mm_stream_t stream) {
+    mm::CacheView c;
+    if (layer < 0) return fail(MM_ERR_INVALID_ARG, "layer must be >= 0");
+    mm_status s = check_cache(cache, layer, false, &c);
+    if (s == MM_OK) s = check_rows(q_start, tokens, max_new);
+    if (s != MM_OK) return s;
+    if (!K || !V || !is_aligned(K, 16) || !is_aligned(V, 16))
+        return fail(MM_ERR_INVALID_ARG, "K or V is NULL or not 16-byte aligned");
+    const int64_t width = cache->kv_heads * cache->head_dim;
+    if ((tokens > 1 && kv_token_stride < width) || kv_token_stride < 0 || kv_token_stride % 8 || kv_token_stride > ((int64_t)1 << 31))
+        return fail(MM_ERR_INVALID_ARG, "kv_token_stride must be a multiple of 8, at least kv_heads * head_dim");
+    const uint64_t nb = span(tokens, width, kv_token_stride, 2), cb = page_bytes_span(cache);
+    if (overlap(K, nb, cache->k, cb) || overlap(K, nb, cache->v, cb) || overlap(V, nb, cache->k, cb) || overlap(V, nb, cache->v, cb))
+        return fail(MM_ERR_INVALID_ARG, "K or V overlaps the cache");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e = mm::launch_cache_append(c, K, V, kv_token_stride, q_start, tokens, max_new,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+    return ok();
+}
+
+mm_status mm_cache_compact(const mm_cache *cache, const int32_t *q_start, const int32_t *keep, const int32_t *kept,
+                           int64_t tokens, int64_t max_new, mm_stream_t stream) {
+    mm::CacheView c;
+    mm_status s = check_cache(cache, -1, true, &c);
+    if (s == MM_OK) s = check_rows(q_start, tokens, max_new);
+    if (s == MM_OK && keep) s = check_ints(keep, "keep");
+    if (s == MM_OK && kept) s = check_ints(kept, "kept");
+    if (s != MM_OK) return s;
+    if (keep && !kept) return fail(MM_ERR_INVALID_ARG, "keep needs kept");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e =
+        mm::launch_cache_compact(c, q_start, keep, kept, tokens, max_new, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache compact launch");
+    return ok();
+}
+
+mm_status mm_cache_fork(const mm_cache *cache, const int32_t *parents, const int32_t *children, int64_t n,
+                        int32_t *missing, mm_stream_t stream) {
+    mm::CacheView c;
+    mm_status s = check_cache(cache, -1, true, &c);
+    if (s == MM_OK) s = check_ints(parents, "parents");
+    if (s == MM_OK) s = check_ints(children, "children");
+    if (s == MM_OK) s = check_ints(missing, "missing");
+    if (s != MM_OK) return s;
+    if (n < 1 || n > 65535) return fail(MM_ERR_INVALID_ARG, "n must be 1 .. 65535");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e = mm::launch_cache_fork(c, parents, children, n, missing, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache fork launch");
+    return ok();
+}
+
+mm_status mm_cache_free(const mm_cache *cache, const int32_t *list, int64_t n, int64_t window, int64_t sinks,
+                        mm_stream_t stream) {
+    mm::CacheView c;
+    mm_status s = check_cache(cache, -1, true, &c);
+    if (s == MM_OK) s = check_ints(list, "list");
+    if (s != MM_OK) return s;
+    if (n < 1 || n > 65535) return fail(MM_ERR_INVALID_ARG, "n must be 1 .. 65535");
+    if (window < 0 || sinks < 0) return fail(MM_ERR_INVALID_ARG, "window and sinks must be >= 0");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e = mm::launch_cache_free(c, list, n, window, sinks, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache free launch");
+    return ok();
+}
+
+mm_status mm_cache_copy_pages(const mm_cache *cache, const int32_t *src, const int32_t *dst, int64_t n,
+                              mm_stream_t stream) {
+    mm::CacheView c;
+    mm_status s = check_cache(cache, -1, false, &c);
+    if (s == MM_OK) s = check_ints(src, "src");
+    if (s == MM_OK) s = check_ints(dst, "dst");
+    if (s != MM_OK) return s;
+    if (n < 1 || n > 65535) return fail(MM_ERR_INVALID_ARG, "n must be 1 .. 65535");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const cudaError_t e = mm::launch_cache_copy_pages(c, src, dst, n, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache page copy launch");
+    return ok();
+}
+
+mm_status mm_cache_attention_workspace(const mm_cache *cache, int64_t heads, int64_t tokens, int64_t max_q,
+                                       int64_t *bytes) {
+    mm::CacheView c;
+    if (!bytes) return fail(MM_ERR_INVALID_ARG, "bytes is NULL");
+    const mm_status s = check_cache(cache, -1, false, &c);
+    if (s != MM_OK) return s;
+    if (heads < 1 || heads > 65535 || heads % cache->kv_heads || tokens < 1 || tokens > 0x7fffffff || max_q < 1 || max_q > tokens)
+        return fail(MM_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, 1 <= max_q <= tokens");
+    *bytes = mm::cache_attention_workspace(c, (int)heads, tokens, max_q, sm_count());
+    return ok();
+}
+
+mm_status mm_cache_attention(const mm_cache *cache, int64_t layer, const void *Q, int64_t q_stride, int64_t heads,
+                             const int32_t *q_start, int64_t tokens, int64_t max_q, int64_t window, int64_t sinks,
+                             float scale, void *O, int64_t o_stride, void *workspace, int64_t workspace_bytes,
+                             mm_stream_t stream) {
+    return cache_attention(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, nullptr, 0, window, sinks, scale, O,
+                           o_stride, workspace, workspace_bytes, stream);
+}
+
+mm_status mm_cache_attention_tree(const mm_cache *cache, int64_t layer, const void *Q, int64_t q_stride, int64_t heads,
+                                  const int32_t *q_start, int64_t tokens, int64_t max_q, const uint32_t *mask,
+                                  int64_t mask_words, int64_t window, int64_t sinks, float scale, void *O,
+                                  int64_t o_stride, void *workspace, int64_t workspace_bytes, mm_stream_t stream) {
+    const mm_status s = check_ints(mask, "mask");
+    if (s != MM_OK) return s;
+    if (mask_words < 1 || mask_words > (1 << 20) || max_q > mask_words * 32)
+        return fail(MM_ERR_INVALID_ARG, "mask_words must hold a bit for each of max_q drafted tokens");
+    return cache_attention(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, mask, mask_words, window, sinks, scale,
+                           O, o_stride, workspace, workspace_bytes, stream);
+}
+
+mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *tokens,
+                    float *logprobs, mm_stream_t stream) {
+    if (dtype != MM_F16 && dtype != MM_BF16 && dtype != MM_F32) return fail(MM_ERR_INVALID_ARG, "dtype must be MM_F16, MM_BF16 or MM_F32");
+    const int64_t size = dtype == MM_F32 ? 4 : 2;
+    if (!logits || !is_aligned(logits, (uintptr_t)size)) return fail(MM_ERR_INVALID_ARG, "logits is NULL or misaligned");
+    if (rows < 1 || rows > 0x7fffffff || vocab < 1 || vocab > (1 << 24))
+        return fail(MM_ERR_INVALID_ARG, "rows must be 1 .. 2^31 - 1 and vocab 1 .. 2^24 (got %lld, %lld)", (long long)rows,
+                    (long long)vocab);
+    if ((rows > 1 && stride < vocab) || stride < 0 || stride > ((int64_t)1 << 31)) return fail(MM_ERR_INVALID_ARG, "stride is below vocab");
+    if (!u || !tokens) return fail(MM_ERR_INVALID_ARG, "u or tokens is NULL");
+    if (!is_aligned(temperature, 4) || !is_aligned(top_k, 4) || !is_aligned(top_p, 4) || !is_aligned(min_p, 4) ||
+        !is_aligned(u, 4) || !is_aligned(tokens, 4) || !is_aligned(logprobs, 4))
+        return fail(MM_ERR_INVALID_ARG, "misaligned pointer");
+    const uint64_t lb = span(rows, vocab, stride, size), rb = (uint64_t)rows * 4;
+    void *const outs[2] = {tokens, logprobs};
+    const void *const ins[5] = {temperature, top_k, top_p, min_p, u};
+    for (void *o : outs) {
+        if (!o) continue;
+        if (overlap(o, rb, logits, lb)) return fail(MM_ERR_INVALID_ARG, "an output overlaps the logits");
+        for (const void *i : ins)
+            if (i && overlap(o, rb, i, rb)) return fail(MM_ERR_INVALID_ARG, "an output overlaps an input");
+    }
+    if (logprobs && overlap(tokens, rb, logprobs, rb)) return fail(MM_ERR_INVALID_ARG, "the outputs overlap");
+    const mm_status s = check_device();
+    if (s != MM_OK) return s;
+    const mm::SampleArgs a{logits, dtype, rows, vocab, stride, temperature, top_k, top_p, min_p, u, tokens, logprobs};
+    const cudaError_t e = mm::launch_sample(a, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "sample launch");
     return ok();
 }
 

@@ -256,4 +256,59 @@ unsigned int gemm_tf32x3_ws_take_device_error(cudaError_t *err);
 cudaError_t launch_wait_probe(int arrive, unsigned long long limit_ns, unsigned long long *out, cudaStream_t s);
 unsigned int wait_probe_take_device_error(cudaError_t *err);
 
+// ------------------------------------------------------------------ serving from a paged cache
+
+// Code of the device error word for a page, sequence or length out of range.
+constexpr unsigned int kCacheErrRange = 16;
+
+// mm_cache with the layer applied where one is chosen (k, v then point at it).
+struct CacheView {
+    char *k, *v;
+    int32_t *table, *lens, *refs;
+    int64_t layers, pages, max_pages;
+    int64_t layer_stride, page_stride, head_stride, token_stride;  // elements
+    int seqs, kv_heads, head_dim, page_size, page_shift, dtype;
+};
+
+cudaError_t launch_cache_reserve(const CacheView &c, const int32_t *need, int32_t *missing, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheView &c, const void *K, const void *V, int64_t token_stride,
+                                const int32_t *q_start, int64_t tokens, int64_t max_new, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheView &c, const int32_t *q_start, const int32_t *keep, const int32_t *kept,
+                                 int64_t tokens, int64_t max_new, cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheView &c, const int32_t *parents, const int32_t *children, int64_t n,
+                              int32_t *missing, cudaStream_t s);
+cudaError_t launch_cache_free(const CacheView &c, const int32_t *list, int64_t n, int64_t window, int64_t sinks,
+                              cudaStream_t s);
+cudaError_t launch_cache_copy_pages(const CacheView &c, const int32_t *src, const int32_t *dst, int64_t n,
+                                    cudaStream_t s);
+unsigned int cache_pages_take_device_error(cudaError_t *err);
+
+struct CacheAttnArgs {
+    CacheView c;
+    const void *Q;
+    void *O;
+    const int32_t *q_start;
+    const uint32_t *mask;  // null: causal
+    int64_t q_stride, o_stride, tokens, max_q, window, sinks, mask_words;
+    int heads, group;
+    float scale;
+    void *ws;
+};
+// Bytes of workspace a call may use on a GPU with `sms` SMs; the launch chooses the same split.
+int64_t cache_attention_workspace(const CacheView &c, int heads, int64_t tokens, int64_t max_q, int sms);
+cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t s);
+unsigned int cache_attention_take_device_error(cudaError_t *err);
+
+struct SampleArgs {
+    const void *logits;
+    int dtype;
+    int64_t rows, vocab, stride;
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p, *u;
+    int32_t *tokens;
+    float *logprobs;
+};
+cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s);
+
 }  // namespace mm

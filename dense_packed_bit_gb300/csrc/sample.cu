@@ -1,0 +1,552 @@
+// sample.cu -- the next token of each row of logits by temperature, top-k, top-p and min-p, from a
+// given uniform number per row.
+//
+// Mathematics.  A token's weight is a whole number, w_i = rint(2^30 exp((x_i - m) r)), so every sum
+// of weights is exact in 64 bits and no result depends on the order of summation or on how a row is
+// split over threads.  In the order (w descending, index ascending) each filter keeps a prefix; the
+// token is the first in index order at which the running sum of the kept weights exceeds floor(u S).
+//
+// Bound: one pass over the logits.  With top-k on, that pass is all: the k-th largest of the maxima
+// of disjoint groups of 8 logits is a lower bound of the k-th largest logit (k groups hold a logit at
+// least as large), so a bound t from the row's first part lets the pass put the few logits >= t into a
+// shared-memory list, and everything else happens there.  What the list must hold is all tokens whose
+// weight reaches that of the k-th (equal weights can have different logits: t is lowered by 1/16 of a
+// temperature and the list is used only if the weight of the lowered bound is smaller).  Tokens more than
+// 22 temperatures below a logit weigh 0 and are left out.  The list is cut to the k-th largest by a
+// histogram of the weights, then every token's rank and the weight before it are counted against all
+// others (k^2 comparisons, no sort).
+//
+// Rows that the list cannot serve (top-k off or above kMaxListK, a list that overflows) select by a
+// radix descent on the weights: 512 bins by exponent and 4 leading bits, then linear bins inside the
+// chosen one, each level one pass over the row (from L2).
+#include "mm_common.cuh"
+#include "mm_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+#include <math.h>
+
+namespace mm {
+
+namespace {
+
+constexpr int CAP = 4096;       // list entries
+constexpr int CUT = 1024;       // entries left after the histogram's cut
+constexpr int kMaxListK = 512;  // top-k served by the list
+constexpr int BINS = 512;
+constexpr float kOne = 1073741824.0f;  // 2^30
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void get(uint4 v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+    }
+    __device__ static float one(float x) { return x; }
+};
+template <>
+struct Vec<__half> {
+    static constexpr int N = 8;
+    __device__ static void get(uint4 v, float (&x)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+    __device__ static float one(__half x) { return __half2float(x); }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void get(uint4 v, float (&x)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    __device__ static float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+};
+
+struct Shared {
+    float x[CAP];
+    int idx[CAP];
+    unsigned long long mass[BINS];
+    unsigned long long key[CUT];  // w << 32 | ~index: larger is earlier in the order
+    int count[BINS];
+    unsigned long long part[32];
+    unsigned long long total;
+    float fpart[32];
+    int n, cut, picked, bin;
+    unsigned long long acc_mass;
+    int acc_count;
+};
+
+// whole numbers from floats ordered as the floats are (no NaN)
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ uint32_t weight(float x, float m, float rate) {
+    if (!(x > -INFINITY)) return 0;  // NaN and -infinity
+    const float z = x == m ? 0.f : (x - m) * rate;
+    return (uint32_t)__float2ll_rn(expf(z) * kOne);
+}
+
+template <int NT>
+__device__ __forceinline__ float block_max(float v, Shared &sh) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.fpart[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = sh.fpart[(threadIdx.x & 31) % (NT / 32)];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+template <int NT>
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, Shared &sh) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    unsigned long long s = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) s += sh.part[i];
+    return s;
+}
+
+struct Row {
+    float rate;
+    int k;           // 0: off
+    float top_p, u;
+    uint32_t floor_w;  // min-p
+};
+
+__device__ __forceinline__ unsigned long long top_p_target(float p, unsigned long long mass) {
+    if (!(p < 1.f)) return mass;
+    const double t = ceil((double)p * (double)mass);
+    return t < 1.0 ? 1ull : (unsigned long long)t;
+}
+__device__ __forceinline__ unsigned long long wanted(float u, unsigned long long total) {
+    const double t = floor((double)u * (double)total);
+    const unsigned long long w = t > 0.0 ? (unsigned long long)t : 0ull;
+    return w < total ? w : total - 1;
+}
+
+__device__ __forceinline__ void put(const SampleArgs &a, int64_t row, int token, uint32_t w, unsigned long long total) {
+    a.tokens[row] = token;
+    // log(w / S) = -log1p((S - w) / w): exact near probability 1
+    if (a.logprobs) a.logprobs[row] = token < 0 ? -INFINITY : -log1pf((float)(total - w) / (float)w);
+}
+
+__device__ __forceinline__ int bin_of(uint32_t w) { return (int)(__float_as_uint(__uint2float_rz(w)) >> 19) - (127 << 4); }
+__device__ __forceinline__ uint32_t bin_low(int b) {
+    return (uint32_t)ceilf(__uint_as_float((uint32_t)(b + (127 << 4)) << 19));
+}
+
+// The first bin from the top at which the running count (or mass) reaches the target; what lies
+// above it is added to acc.  All of warp 0; 16 bins a lane.
+__device__ __forceinline__ void find_bin(Shared &sh, bool by_mass, unsigned long long target) {
+    const int lane = threadIdx.x;
+    const int top = BINS - 1 - 16 * lane;  // this lane's bins: top, top - 1, ..., top - 15
+    unsigned long long mine_m = 0;
+    int mine_c = 0;
+    for (int i = 0; i < 16; ++i) mine_m += sh.mass[top - i], mine_c += sh.count[top - i];
+    unsigned long long m = mine_m;
+    int c = mine_c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long um = __shfl_up_sync(0xffffffffu, m, o);
+        const int uc = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) m += um, c += uc;
+    }
+    const unsigned long long have_m = sh.acc_mass;
+    const int have_c = sh.acc_count;
+    const bool reached = by_mass ? have_m + m >= target : (unsigned long long)(have_c + c) >= target;
+    const unsigned at = __ballot_sync(0xffffffffu, reached);
+    __syncwarp();
+    if (at == 0) {
+        if (lane == 0) sh.bin = -1;
+    } else if (lane == __ffs(at) - 1) {
+        unsigned long long am = have_m + m - mine_m;
+        int ac = have_c + c - mine_c, b = top;
+        for (; b > top - 15; --b) {
+            if (by_mass ? am + sh.mass[b] >= target : (unsigned long long)(ac + sh.count[b]) >= target) break;
+            am += sh.mass[b], ac += sh.count[b];
+        }
+        sh.bin = b, sh.acc_mass = am, sh.acc_count = ac;
+    }
+    __syncwarp();
+}
+
+// The cut of the row's order at `target` tokens (or so much mass): weights above *cut_w and the
+// first *taken of those equal to it.  Returns the mass in front of the cut; *cut_w = 0 where the whole
+// row does not reach the target.
+template <typename T, int NT>
+__device__ unsigned long long find_cut(const T *x, int64_t n, float m, const Row &r, Shared &sh, bool by_mass,
+                                       unsigned long long target, uint32_t *cut_w, unsigned long long *taken) {
+    uint32_t lo = 1, hi = 1u << 30;
+    int shift = -1;  // the first level: bins by the leading bits
+    if (threadIdx.x == 0) sh.acc_mass = 0, sh.acc_count = 0;
+    while (true) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < BINS; b += NT) sh.mass[b] = 0, sh.count[b] = 0;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < n; i += NT) {
+            const uint32_t w = weight(Vec<T>::one(x[i]), m, r.rate);
+            if (w < lo || w > hi) continue;
+            const int b = shift < 0 ? bin_of(w) : (int)((w - lo) >> shift);
+            atomicAdd(&sh.mass[b], (unsigned long long)w);
+            atomicAdd(&sh.count[b], 1);
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) find_bin(sh, by_mass, target);
+        __syncthreads();
+        const int b = sh.bin;
+        if (b < 0) {  // only at the first level: the row has less
+            *cut_w = 0, *taken = 0;
+            unsigned long long all = 0;
+            for (int q = threadIdx.x; q < BINS; q += NT) all += sh.mass[q];
+            return block_sum<NT>(all, sh);
+        }
+        if (shift < 0) {
+            lo = bin_low(b), hi = bin_low(b + 1) - 1;
+        } else {
+            lo += (uint32_t)b << shift;
+            hi = min(hi, lo + (1u << shift) - 1);
+        }
+        if (lo >= hi) {
+            *cut_w = lo;
+            *taken = by_mass ? (target - sh.acc_mass + lo - 1) / lo : target - (unsigned long long)sh.acc_count;
+            const unsigned long long mass = sh.acc_mass + *taken * lo;
+            __syncthreads();
+            return mass;
+        }
+        const int bits = 32 - __clz(hi - lo);
+        shift = bits > 9 ? bits - 9 : 0;
+    }
+}
+
+// Any row: the cuts by radix descent, then the token by a scan in index order.  A warp walks one
+// contiguous part of the row.
+template <typename T, int NT>
+__device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_t n, float m, const Row &r, Shared &sh) {
+    uint32_t cut = 0;
+    unsigned long long taken = 0, mass = 0;
+    if (r.k > 0 || r.top_p < 1.f) {
+        mass = find_cut<T, NT>(x, n, m, r, sh, false, r.k > 0 ? (unsigned long long)r.k : ~0ull, &cut, &taken);
+        if (r.top_p < 1.f && mass > 0)
+            find_cut<T, NT>(x, n, m, r, sh, true, top_p_target(r.top_p, mass), &cut, &taken);
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t share = ((n + NT / 32 - 1) / (NT / 32) + 31) / 32 * 32;
+    const int64_t from = min(n, warp * share), to = min(n, from + share);
+    // tokens equal to the cut, in front of each warp's part
+    unsigned long long ties = 0;
+    if (cut)
+        for (int64_t i = from + lane; i < to; i += 32) ties += weight(Vec<T>::one(x[i]), m, r.rate) == cut;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ties += __shfl_xor_sync(0xffffffffu, ties, o);
+    __syncthreads();
+    if (lane == 0) sh.part[warp] = ties;
+    __syncthreads();
+    unsigned long long tie0 = 0;
+    for (int i = 0; i < warp; ++i) tie0 += sh.part[i];
+    __syncthreads();
+    // the kept weight of token i of this warp's step (tie is advanced by the whole warp)
+    const auto kept = [&](int64_t i, unsigned long long &tie) -> uint32_t {
+        const uint32_t w = i < to ? weight(Vec<T>::one(x[i]), m, r.rate) : 0u;
+        const unsigned eq = __ballot_sync(0xffffffffu, cut != 0 && w == cut);
+        const bool in = w > cut || (cut != 0 && w == cut && tie + __popc(eq & ((1u << lane) - 1)) < taken);
+        tie += __popc(eq);
+        return in && w >= r.floor_w ? w : 0u;
+    };
+    unsigned long long mine = 0, tie = tie0;
+    for (int64_t i = from; i < to; i += 32) mine += kept(i + lane, tie);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh.part[warp] = mine;
+    __syncthreads();
+    unsigned long long before = 0, total = 0;
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < warp) before += sh.part[i];
+        total += sh.part[i];
+    }
+    if (total == 0) {
+        if (threadIdx.x == 0) put(a, row, -1, 1, 1);
+        return;
+    }
+    const unsigned long long want = wanted(r.u, total);
+    if (want < before || want >= before + mine) return;
+    tie = tie0;
+    for (int64_t i = from; i < to; i += 32) {
+        const uint32_t w = kept(i + lane, tie);
+        unsigned long long s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += up;
+        }
+        const bool here = w != 0 && before + s > want && before + s - w <= want;
+        if (here) put(a, row, (int)(i + lane), w, total);
+        if (__any_sync(0xffffffffu, here)) return;
+        before += __shfl_sync(0xffffffffu, s, 31);
+    }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs a) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(raw);
+    constexpr int N = Vec<T>::N, G = 8 / N;  // vectors per group of 8
+    const int64_t row = blockIdx.x, n = a.vocab;
+    const T *x = static_cast<const T *>(a.logits) + row * a.stride;
+    Row r;
+    const float temp = a.temperature ? a.temperature[row] : 1.f;
+    r.rate = 1.f / fmaxf(temp, 0.f);  // infinity for the greedy choice
+    r.k = a.top_k ? max(a.top_k[row], 0) : 0;
+    if (!(temp > 0.f)) r.k = 1;
+    r.top_p = a.top_p ? a.top_p[row] : 1.f;
+    r.u = a.u[row];
+    const float fw = ceilf((a.min_p ? a.min_p[row] : 0.f) * kOne);
+    r.floor_w = fw > 0.f ? (fw < 4e9f ? (uint32_t)fw : 0xffffffffu) : 0u;
+
+    // 16-byte vectors from the first aligned element on; the few in front and behind are scalars
+    const int64_t head = min(n, (int64_t)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+    const uint4 *body = reinterpret_cast<const uint4 *>(x + head);
+    const int64_t vecs = (n - head) / N, tail = head + vecs * N;
+    const int edge = (int)(head + n - tail);  // < 2 N
+    const auto edge_index = [&](int i) { return i < head ? (int64_t)i : tail + i - head; };
+
+    const bool listed = r.k > 0 && r.k <= kMaxListK;
+    float low = INFINITY;  // logits >= low go to the list
+    if (threadIdx.x == 0) sh.n = 0, sh.cut = 0, sh.picked = 0;
+    float t0 = -INFINITY;
+    bool all_heavy = false;  // what is below `low` weighs 0
+    if (listed) {
+        // the first part: four groups of 8 per thread
+        uint32_t g[4];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float gm = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const int64_t v = (int64_t)(q * G + j) * NT + threadIdx.x;
+                if (v < vecs) {
+                    float f[N];
+                    Vec<T>::get(__ldg(body + v), f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) gm = fmaxf(gm, f[e]);
+                }
+            }
+            g[q] = order_key(gm + 0.f);
+            mx = fmaxf(mx, gm);
+        }
+        mx = block_max<NT>(mx, sh);
+        // a key that between k and a little more of the maxima reach
+        uint32_t lo = order_key(-INFINITY), hi = order_key(mx + 0.f) + 1;
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            int c = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) c += g[q] >= mid;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if ((threadIdx.x & 31) == 0) sh.count[threadIdx.x >> 5] = c;
+            __syncthreads();
+            c = 0;
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) c += sh.count[i];
+            __syncthreads();
+            if (c >= r.k) {
+                lo = mid;
+                if (c <= r.k + r.k / 8 + 2) break;
+            } else {
+                hi = mid;
+            }
+        }
+        t0 = from_key(lo);
+        // a sixteenth of a temperature lower, but not where every weight is 0 whatever the rest holds
+        const float down = t0 - 0.0625f / r.rate;
+        low = down < t0 ? down : from_key(max(lo, order_key(-FLT_MAX)) - 1);
+        const float none = mx - 22.f / r.rate;
+        all_heavy = none >= low;
+        low = fmaxf(fmaxf(low, none), -FLT_MAX);
+    }
+    __syncthreads();
+
+    // the pass over the row
+    float m = -INFINITY;
+    const auto offer = [&](float f, int64_t i) {
+        if (f >= low) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < CAP) sh.x[at] = f, sh.idx[at] = (int)i;
+        }
+    };
+    constexpr int U = 4;
+    for (int64_t v0 = threadIdx.x; v0 < vecs; v0 += U * NT) {
+        uint4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (v0 + j * NT < vecs) v[j] = ld_stream_v4(body + v0 + j * NT);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (v0 + j * NT >= vecs) continue;
+            float f[N], vm = -INFINITY;
+            Vec<T>::get(v[j], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) vm = fmaxf(vm, f[e]);
+            m = fmaxf(m, vm);
+            if (vm >= low) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) offer(f[e], head + (v0 + j * NT) * N + e);
+            }
+        }
+    }
+    if (threadIdx.x < edge) {
+        const int64_t i = edge_index(threadIdx.x);
+        const float f = Vec<T>::one(x[i]);
+        m = fmaxf(m, f);
+        offer(f, i);
+    }
+    m = block_max<NT>(m, sh);
+    if (m == -INFINITY) {  // nothing is left of the row
+        if (threadIdx.x == 0) put(a, row, -1, 1, 1);
+        return;
+    }
+    const int have = sh.n;
+    bool ok = listed && have <= CAP;
+    if (ok && !all_heavy) {  // does the list hold every token that weighs as much as the k-th?
+        const uint32_t wk = weight(t0, m, r.rate), wl = weight(low, m, r.rate);
+        ok = wl == 0 || wl < wk - (wk >> 20);
+    }
+    if (!ok) {
+        general_row<T, NT>(a, row, x, n, m, r, sh);
+        return;
+    }
+
+    // the k heaviest of the list, by bins of their weights
+    for (int b = threadIdx.x; b < BINS; b += NT) sh.count[b] = 0, sh.mass[b] = 0;
+    if (threadIdx.x == 0) sh.acc_mass = 0, sh.acc_count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < have; i += NT) {
+        const uint32_t w = weight(sh.x[i], m, r.rate);
+        sh.x[i] = __uint_as_float(w);
+        if (w) atomicAdd(&sh.count[bin_of(w)], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) find_bin(sh, false, (unsigned long long)r.k);
+    __syncthreads();
+    const uint32_t least = sh.bin < 0 ? 1u : bin_low(sh.bin);
+    for (int i = threadIdx.x; i < have; i += NT) {
+        const uint32_t w = __float_as_uint(sh.x[i]);
+        if (w >= least) {
+            const int at = atomicAdd(&sh.cut, 1);
+            if (at < CUT) sh.key[at] = (unsigned long long)w << 32 | (uint32_t)~sh.idx[i];
+        }
+    }
+    __syncthreads();
+    const int c = sh.cut;
+    if (c > CUT) {  // very many equal weights
+        general_row<T, NT>(a, row, x, n, m, r, sh);
+        return;
+    }
+    // rank and weight in front of each, four lanes per token
+    const int sub = threadIdx.x & 3;
+    unsigned long long mass = 0;
+    constexpr int ROUNDS = CUT * 4 / NT;
+    unsigned long long before[ROUNDS];
+    int rank[ROUNDS];
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) {
+        const int e = q * (NT / 4) + (threadIdx.x >> 2);
+        before[q] = 0, rank[q] = 0;
+        if (q * (NT / 4) < c) {  // the same for the whole block
+            const unsigned long long key = e < c ? sh.key[e] : ~0ull;
+            for (int f = sub; f < c; f += 4) {
+                const unsigned long long o = sh.key[f];
+                if (o > key) before[q] += o >> 32, ++rank[q];
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                before[q] += __shfl_xor_sync(0xffffffffu, before[q], o);
+                rank[q] += __shfl_xor_sync(0xffffffffu, rank[q], o);
+            }
+            if (e < c && sub == 0 && rank[q] < r.k) mass += key >> 32;
+        }
+    }
+    mass = block_sum<NT>(mass, sh);
+    const unsigned long long target = top_p_target(r.top_p, mass);
+    unsigned long long total = 0;
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) {
+        const int e = q * (NT / 4) + (threadIdx.x >> 2);
+        if (e < c && sub == 0) {
+            const unsigned long long key = sh.key[e];
+            const bool in = rank[q] < r.k && (rank[q] == 0 || before[q] < target) && (uint32_t)(key >> 32) >= r.floor_w;
+            if (in) {
+                total += key >> 32;
+                const int at = atomicAdd(&sh.picked, 1);
+                sh.x[at] = __uint_as_float((uint32_t)(key >> 32));
+                sh.idx[at] = (int)~(uint32_t)key;
+            }
+        }
+    }
+    total = block_sum<NT>(total, sh);
+    if (total == 0) {
+        if (threadIdx.x == 0) put(a, row, -1, 1, 1);
+        return;
+    }
+    const unsigned long long want = wanted(r.u, total);
+    const int kept = sh.picked;
+    for (int e0 = 0; e0 < kept; e0 += NT / 4) {
+        const int e = e0 + (threadIdx.x >> 2);
+        unsigned long long s = 0;
+        const int me = e < kept ? sh.idx[e] : 0;
+        for (int f = sub; f < kept; f += 4)
+            if (sh.idx[f] < me) s += __float_as_uint(sh.x[f]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (e < kept && sub == 0) {
+            const uint32_t w = __float_as_uint(sh.x[e]);
+            if (s <= want && want < s + w) put(a, row, me, w, total);
+        }
+    }
+}
+
+template <typename T, int NT>
+cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
+    static const cudaError_t once =
+        cudaFuncSetAttribute(sample_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (once != cudaSuccess) return once;
+    sample_kernel<T, NT><<<(unsigned)a.rows, NT, sizeof(Shared), s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const SampleArgs &a, int sms, cudaStream_t s) {
+    // up to one row per SM: all its warps on the row; more rows: two to an SM, one streaming while the
+    // other chooses
+    return a.rows <= sms ? launch<T, 1024>(a, s) : launch<T, 512>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s) {
+    if (a.dtype == 0) return launch_t<__half>(a, sms, s);
+    if (a.dtype == 1) return launch_t<__nv_bfloat16>(a, sms, s);
+    return launch_t<float>(a, sms, s);
+}
+
+}  // namespace mm

@@ -558,6 +558,146 @@ mm_status mm_gemv_packed4_ex(const uint8_t *codes, const uint16_t *scales, const
                              int64_t rows, int64_t cols, const float codebook[16], mm_stream_t stream,
                              const mm_gemv4_opts *opts);
 
+/* ------------------------------------------------------------------ serving from a paged cache
+ *
+ * What a decode step needs between its packed products: a cache of keys and values held in
+ * pages, attention over it, and the choice of the next token.
+ */
+
+/* Element types of the operators below (the GEMMs and GEMVs above have theirs fixed). */
+typedef enum { MM_F16 = 0, MM_BF16 = 1, MM_F32 = 2 } mm_dtype;
+
+/*
+ * A paged cache of keys and values, all pointers device memory owned by the caller.
+ * k, v: [layers][pages][kv_heads][page_size] rows of head_dim elements (contiguous), the
+ *   four outer strides in elements, the same for k and v: any order of heads and tokens,
+ *   and a k and v interleaved in one allocation, are strides.
+ * table: [seqs][max_pages] page numbers; token t of sequence s lies in page
+ *   table[s][t / page_size], row t % page_size.  -1: no page.
+ * lens: [seqs] tokens each sequence holds for good.  New (or drafted) tokens follow them
+ *   at lens[s] + i until mm_cache_compact makes them part of the sequence.
+ * refs: [pages] sequences that hold each page, 0 = free; NULL where only append and
+ *   attention are called.  A page is allocated by the calls below lowest number first.
+ * page_size: 16, 32, 64 or 128; head_dim: a multiple of 8 up to 128; dtype: MM_F16 or
+ *   MM_BF16; k, v 16-byte aligned and every stride a multiple of 8 elements.
+ * The struct is host memory, read during each call.
+ */
+typedef struct {
+    void *k, *v;
+    int32_t *table;
+    int32_t *lens;
+    int32_t *refs;
+    int64_t layers, pages, kv_heads, page_size, head_dim, seqs, max_pages;
+    int64_t layer_stride, page_stride, head_stride, token_stride;
+    int dtype;
+    int reserved[5];  /* 0 */
+} mm_cache;
+
+/*
+ * Page management.  All calls are asynchronous on `stream` and read and write table, lens
+ * and refs on the device only; calls that change them are ordered by the stream (two at once
+ * on two streams race).  Page, sequence and length values are checked on the device before
+ * each use: an entry out of range is skipped and mm_check_device_error then returns
+ * MM_ERR_INVALID_ARG.
+ *
+ * mm_cache_reserve: gives every sequence the pages of lens[s] + need[s] tokens, in the order
+ *   of the sequences, keeping the pages it has.  Where the free pages do not suffice nothing
+ *   is changed and *missing is how many are lacking (else 0).  A sequence whose tokens do not
+ *   fit max_pages gets max_pages and is reported as out of range.
+ * mm_cache_append: K, V [tokens][kv_heads][head_dim], tokens kv_token_stride elements apart:
+ *   row q_start[s] + i goes to token lens[s] + i of layer `layer`.  q_start: [seqs + 1],
+ *   ascending from 0 to tokens; max_new: an upper bound of q_start[s + 1] - q_start[s].
+ * mm_cache_compact: keeps kept[s] of the new tokens of each sequence in all layers: new token
+ *   keep[q_start[s] + i] (ascending, below q_start[s + 1] - q_start[s]) moves to lens[s] + i,
+ *   lens[s] grows by kept[s], and pages that hold no token any more are released.
+ *   keep: [tokens]; NULL: the first kept[s] stay where they are; kept NULL: all of them.
+ *   The pages of new tokens must not be shared (fork copies the last page, so they are not).
+ * mm_cache_fork: sequence children[i] becomes a copy of parents[i], i < n: the full pages are
+ *   shared, the tokens of a last partial page copied to a page of its own, in all layers.
+ *   Children hold no pages before (mm_cache_free) and are not parents.  *missing as above.
+ * mm_cache_free: releases pages of sequences list[i], i < n.  window = 0: all of them, and
+ *   lens becomes 0.  window > 0: those whose tokens no later query sees under a sliding
+ *   window and `sinks` first tokens (tokens t with sinks <= t <= lens - window).
+ * mm_cache_copy_pages: page src[i] is copied to page dst[i], i < n, in all layers; no page
+ *   is both a source and a destination.
+ * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes < 1, a bad page size,
+ * head_dim, stride or dtype, refs NULL where it is needed.
+ */
+mm_status mm_cache_reserve(const mm_cache *cache, const int32_t *need, int32_t *missing, mm_stream_t stream);
+mm_status mm_cache_append(const mm_cache *cache, int64_t layer, const void *K, const void *V,
+                          int64_t kv_token_stride, const int32_t *q_start, int64_t tokens, int64_t max_new,
+                          mm_stream_t stream);
+mm_status mm_cache_compact(const mm_cache *cache, const int32_t *q_start, const int32_t *keep, const int32_t *kept,
+                           int64_t tokens, int64_t max_new, mm_stream_t stream);
+mm_status mm_cache_fork(const mm_cache *cache, const int32_t *parents, const int32_t *children, int64_t n,
+                        int32_t *missing, mm_stream_t stream);
+mm_status mm_cache_free(const mm_cache *cache, const int32_t *list, int64_t n, int64_t window, int64_t sinks,
+                        mm_stream_t stream);
+mm_status mm_cache_copy_pages(const mm_cache *cache, const int32_t *src, const int32_t *dst, int64_t n,
+                              mm_stream_t stream);
+
+/*
+ * Attention of new tokens over the cache: per sequence s, new token i (row q_start[s] + i
+ * of Q) and head h, over the keys j it sees,
+ *     O = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
+ * with kv head h / (heads / kv_heads).  The new tokens' own keys and values are in the cache
+ * already (mm_cache_append).
+ *
+ * mm_cache_attention: token i sits at position p = lens[s] + i and sees j <= p with
+ *   j > p - window or j < sinks (window = 0: no window).
+ * mm_cache_attention_tree: the new tokens are a tree of drafts: token i sees drafted token t
+ *   (key lens[s] + t) where bit t % 32 of mask[(q_start[s] + i) * mask_words + t / 32] is
+ *   set, and of the keys before lens[s] those that the window and sinks leave to position
+ *   p = lens[s] + (bits set) - 1, its depth.  Bits at or past the sequence's count of new
+ *   tokens are ignored.
+ * A row that sees no key gives 0.  Keys and values that a row does not see have no influence
+ * on it, whatever they hold (NaN and infinities in released or never written rows included).
+ *
+ * Q, O: [tokens][heads][head_dim] of the cache's dtype, tokens q_stride / o_stride elements
+ * apart (multiples of 8; 16-byte aligned).  fp32 scores, softmax statistics and accumulation;
+ * the probabilities are rounded to the cache's dtype for the second product, O once at the
+ * end.  max_q: an upper bound of the new tokens of one sequence.
+ * workspace: mm_cache_attention_workspace bytes for these sizes (at least; 0 is possible),
+ * 16-byte aligned, zeroed once before its first use; every call leaves it ready for the
+ * next one in stream order.  Two calls at once need two workspaces.
+ * Errors: MM_ERR_INVALID_ARG as above, for heads not a multiple of kv_heads, a non-finite
+ * scale, O overlapping an input or a workspace that is too small.
+ */
+mm_status mm_cache_attention_workspace(const mm_cache *cache, int64_t heads, int64_t tokens, int64_t max_q,
+                                       int64_t *bytes);
+mm_status mm_cache_attention(const mm_cache *cache, int64_t layer, const void *Q, int64_t q_stride, int64_t heads,
+                             const int32_t *q_start, int64_t tokens, int64_t max_q, int64_t window, int64_t sinks,
+                             float scale, void *O, int64_t o_stride, void *workspace, int64_t workspace_bytes,
+                             mm_stream_t stream);
+mm_status mm_cache_attention_tree(const mm_cache *cache, int64_t layer, const void *Q, int64_t q_stride,
+                                  int64_t heads, const int32_t *q_start, int64_t tokens, int64_t max_q,
+                                  const uint32_t *mask, int64_t mask_words, int64_t window, int64_t sinks,
+                                  float scale, void *O, int64_t o_stride, void *workspace,
+                                  int64_t workspace_bytes, mm_stream_t stream);
+
+/*
+ * The next token of each row of logits, from a given uniform number per row.
+ * logits: [rows][vocab] of `dtype` (MM_F16, MM_BF16, MM_F32), rows `stride` elements apart.
+ * Per row, with x the logits in fp32 (NaN counts as -infinity), m their maximum and
+ * r = 1 / temperature, the weight of token i is the whole number
+ *     w_i = rint(2^30 exp((x_i - m) r)),    2^30 where x_i = m, 0 where x_i = -infinity,
+ * and tokens are ordered by w (larger first), equal ones by index (lower first).  Of that
+ * order these filters keep a prefix each: the first top_k tokens; of those, the fewest whose
+ * sum reaches top_p times theirs (at least one); of those, w_i >= min_p 2^30.  With S the sum
+ * of what is kept, the token is the first in index order at which the running sum of the kept
+ * weights exceeds floor(u S).  All sums are of whole numbers, so the choice does not depend on
+ * the order of summation.
+ * temperature, top_k, top_p, min_p: [rows] each, NULL: 1, off, off, off.  temperature <= 0
+ * picks the first largest logit; top_k <= 0, top_p >= 1, min_p <= 0 are off.  u: [rows], in
+ * [0, 1).  tokens: [rows].  logprobs: NULL or [rows], log(w_token / S).  A row without a
+ * logit above -infinity gives token -1 and logprob -infinity.  vocab at most 2^24.
+ * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes out of range, a bad dtype,
+ * stride < vocab, or an output overlapping the logits.
+ */
+mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                    const float *u, int32_t *tokens, float *logprobs, mm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
