@@ -191,6 +191,10 @@ cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int splits, cuda
 int cache_attention_rows_splits(const CacheView &c, int sms);
 int64_t cache_attention_rows_workspace(const CacheView &c, int splits);
 unsigned int cache_attention_rows_take_device_error(cudaError_t *err);
+cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int splits, cudaStream_t s);
+int cache_attention_tiles_splits(const CacheView &c, int group, int64_t max_q, int sms);
+int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int splits);
+unsigned int cache_attention_tiles_take_device_error(cudaError_t *err);
 constexpr int kRowsMax = 16;  // rows (new tokens x heads of a kv head) of one sequence in the rows kernel
 
 }  // namespace mm

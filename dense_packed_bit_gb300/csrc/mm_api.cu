@@ -981,8 +981,8 @@ mm_status check_cache(const mm_cache *c, int64_t layer, bool needs_refs, mm::Cac
     const int64_t strides[4] = {c->layer_stride, c->page_stride, c->head_stride, c->token_stride};
     const int64_t counts[4] = {c->layers, c->pages, c->kv_heads, c->page_size};
     for (int i = 0; i < 4; ++i) {
-        if (strides[i] < 0 || strides[i] % 8 || strides[i] > ((int64_t)1 << 39))
-            return fail(MM_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements, 0 .. 2^39");
+        if (strides[i] < 0 || strides[i] % 8 || strides[i] > ((int64_t)1 << 38))
+            return fail(MM_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements, 0 .. 2^38");
         if (counts[i] > 1 && strides[i] < c->head_dim)
             return fail(MM_ERR_INVALID_ARG, "a cache stride is below head_dim: rows overlap");
     }
@@ -1043,6 +1043,7 @@ mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, i
     if (heads < 1 || heads > 65535 || heads % cache->kv_heads)
         return fail(MM_ERR_INVALID_ARG, "heads (%lld) must be a multiple of kv_heads (%lld), at most 65535", (long long)heads,
                     (long long)cache->kv_heads);
+    if (max_q * (heads / cache->kv_heads) > ((int64_t)1 << 30)) return fail(MM_ERR_INVALID_ARG, "max_q * heads / kv_heads is above 2^30");
     const int64_t width = heads * cache->head_dim;
     if ((tokens > 1 && (q_stride < width || o_stride < width)) || q_stride < 0 || o_stride < 0 || q_stride % 8 || o_stride % 8 ||
         q_stride > ((int64_t)1 << 31) || o_stride > ((int64_t)1 << 31))

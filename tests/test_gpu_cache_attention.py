@@ -177,8 +177,8 @@ def test_tree_rows_that_see_nothing(n, heads):
     v[0, page, 0, 4] = float("nan")
     again = run_attention(c, 0, q, [n, n], 0, 0, 0.125, mask=mask)
     assert bool(torch.isnan(again[4]).all())
-    keep = [i for i in range(2 * n) if i != 4]
-    assert bool(((again[keep] - out[keep]).abs().float() <= 0.02 * (0.05 + out[keep].abs().float())).all())
+    again[4] = out[4]  # every other row is as the definition has it
+    check_attention(c, dk, dv, 0, q, [n, n], [0, 50], 0, 0, 0.125, dtype, bits=bits, out=again)
 
 
 @pytest.mark.parametrize("lens,new", [([900, 33], [1, 1]), ([700, 0], [100, 80])])
