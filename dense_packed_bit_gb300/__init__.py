@@ -41,6 +41,7 @@ MM_F16, MM_BF16, MM_F32 = 0, 1, 2
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
+_torch = None
 
 # symbol -> (argtypes, restype); mirrors include/mm.h
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -142,6 +143,8 @@ def library_path() -> str:
 def load_library():
     """Load libmm.so (built by dense_packed_bit_gb300.build); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -167,8 +170,13 @@ def _ptr(t) -> int | None:
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        if _torch.cuda.is_initialized():  # the current stream's handle without an object around it
+            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        return _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "cache_view.cuh"
+#include "tmap.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -12,18 +13,20 @@ namespace mm {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Positions are 32-bit: a sequence holds at most 2^30 tokens.
+//
 // The keys a row sees: those before `end` (its own position and what precedes it, or with a tree
 // the tokens before the drafts) that are below `sinks` or at `low` and later, and the drafted tokens
 // whose bit is set.
 struct RowView {
-    int64_t low, end;
+    int low, end;
     const uint32_t *bits;  // null: none
 };
 
-__device__ __forceinline__ bool sees(const RowView &r, int64_t j, int64_t sinks, int64_t len, int count) {
+__device__ __forceinline__ bool sees(const RowView &r, int j, int sinks, int len, int count) {
     if (j < r.end) return j >= r.low || j < sinks;
     if (!r.bits) return false;
-    const int64_t t = j - len;
+    const int t = j - len;
     return t < count && (__ldg(r.bits + (t >> 5)) >> (t & 31) & 1u);
 }
 
@@ -39,9 +42,9 @@ __device__ __forceinline__ int mask_depth(const uint32_t *bits, int count) {
 }
 
 // new token i of a sequence with `len` tokens before it
-__device__ __forceinline__ RowView row_view(const CacheAttnArgs &a, int64_t len, int first, int count, int i) {
+__device__ __forceinline__ RowView row_view(const CacheAttnArgs &a, int len, int first, int count, int i) {
     RowView r;
-    int64_t p = len + i;
+    int p = len + i;
     if (a.mask) {
         r.bits = a.mask + (int64_t)(first + i) * a.mask_words;
         p = len + mask_depth(r.bits, count) - 1;
@@ -56,15 +59,14 @@ __device__ __forceinline__ RowView row_view(const CacheAttnArgs &a, int64_t len,
 
 // One sequence of the call, checked: its rows of Q, its cached tokens.
 struct SeqView {
-    int first, count;
-    int64_t len;
+    int first, count, len;
 };
 __device__ __forceinline__ SeqView seq_view(const CacheAttnArgs &a, int seq, unsigned int *err) {
     SeqView s;
     const RowRange r = rows_of(a.q_start, seq, a.tokens, a.max_q, err);
     s.first = r.first, s.count = r.count;
     s.len = __ldg(a.c.lens + seq);
-    if (s.len < 0 || s.len + s.count > row_capacity(a.c)) {
+    if (s.len < 0 || (int64_t)s.len + s.count > row_capacity(a.c)) {
         *err = kDevErrRange;
         s.count = 0;
         s.len = 0;
@@ -77,13 +79,13 @@ __device__ __forceinline__ SeqView seq_view(const CacheAttnArgs &a, int seq, uns
 // Blocks of B keys that rows with their lowest window start at `low` need, of `end` keys: the blocks of
 // the sinks, then those from low on.  block(i) is the i-th one's number.
 struct KeyBlocks {
-    int64_t sink_blocks, first, count;
-    __device__ __forceinline__ int64_t block(int64_t i) const {
+    int sink_blocks, first, count;
+    __device__ __forceinline__ int block(int i) const {
         return i < sink_blocks ? i : first + (i - sink_blocks);
     }
 };
 template <int B>
-__device__ __forceinline__ KeyBlocks key_blocks(int64_t low, int64_t sinks, int64_t end) {
+__device__ __forceinline__ KeyBlocks key_blocks(int low, int sinks, int end) {
     KeyBlocks k;
     if (low < 0) low = 0;
     if (low > end) low = end;
@@ -150,19 +152,19 @@ __device__ void attend_row(const CacheAttnArgs &a, int seq, const SeqView &sv, i
     float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
     get4(static_cast<const char *>(a.Q) + ((int64_t)(sv.first + i) * a.q_stride + (int64_t)qhead * c.head_dim) * 2, q);
     const float scale2 = a.scale * kLog2e;
-    const int64_t end = sv.len + sv.count;
+    const int end = sv.len + sv.count;
     const KeyBlocks kb = key_blocks<16>(a.mask ? min(r.low, sv.len) : r.low, a.sinks, end);
-    for (int64_t b = 0; b < kb.count; ++b) {
-        const int64_t key0 = kb.block(b) * 16;
+    for (int b = 0; b < kb.count; ++b) {
+        const int key0 = kb.block(b) * 16;
         const int page = page_of(c, seq, key0 >> c.page_shift);
         if (page < 0) {
             *err = kDevErrRange;
             continue;
         }
-        for (int64_t j = key0; j < min(key0 + 16, end); ++j) {
+        for (int j = key0; j < min(key0 + 16, end); ++j) {
             if (!sees(r, j, a.sinks, sv.len, sv.count)) continue;
             const int64_t at =
-                (page * c.page_stride + kv_head * c.head_stride + (j & (c.page_size - 1)) * c.token_stride) * 2;
+                ((int64_t)page * c.page_stride + kv_head * c.head_stride + (j & (c.page_size - 1)) * c.token_stride) * 2;
             float k[4], v[4];
             get4(c.k + at, k);
             get4(c.v + at, v);
@@ -186,15 +188,31 @@ __device__ void attend_row(const CacheAttnArgs &a, int seq, const SeqView &sv, i
     }
 }
 
-cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int splits, cudaStream_t s);
-// splits of each unit's keys over CTAs, of the rows kernel
-int cache_attention_rows_splits(const CacheView &c, int sms);
-int64_t cache_attention_rows_workspace(const CacheView &c, int splits);
+// CTAs of the rows kernel (the blocks of all units are cut evenly over them)
+int cache_attention_rows_ctas(const CacheView &c, int sms);
+int64_t cache_attention_rows_workspace(const CacheView &c, int ctas);
+cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s);
 unsigned int cache_attention_rows_take_device_error(cudaError_t *err);
 cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int splits, cudaStream_t s);
 int cache_attention_tiles_splits(const CacheView &c, int group, int64_t max_q, int sms);
 int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int splits);
 unsigned int cache_attention_tiles_take_device_error(cudaError_t *err);
 constexpr int kRowsMax = 16;  // rows (new tokens x heads of a kv head) of one sequence in the rows kernel
+
+// The pages of k or v: boxes of `box` tokens of one head, 64 columns, 128-byte swizzle; what is past
+// head_dim, and pages past the last, read as zeros.
+inline cudaError_t cache_tmap(CUtensorMap *map, const CacheView &c, const void *base, int box) {
+    cudaError_t err;
+    auto enc = tmap_encoder(&err);
+    if (err != cudaSuccess) return err;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.pages};
+    const auto bytes = [](int64_t stride, int64_t count) { return (cuuint64_t)(count > 1 ? stride * 2 : 16); };
+    const cuuint64_t strides[3] = {bytes(c.token_stride, c.page_size), bytes(c.head_stride, c.kv_heads), bytes(c.page_stride, c.pages)};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, c.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<void *>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 }  // namespace mm

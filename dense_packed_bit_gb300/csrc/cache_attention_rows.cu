@@ -7,22 +7,24 @@
 // fp16), so most blocks cost no rescaling; the final O / l does not depend on the reference.
 //
 // Bound: reading K and V once (4 D bytes a key and kv head; 16 rows x 4 D operations for them are a
-// twentieth of what the tensor cores could do meanwhile).  So the layout is made for loads in flight:
-// a CTA of four warps owns a range of one kv head's keys; every warp streams its own 16-key blocks
-// (whole rows, 16-byte cp.async) through a ring of three stages of its own, with no barrier between
-// warps until the end; two CTAs are resident per SM, 128 KB in flight.  The 16 x D rows of Q stay in
-// registers as the A operand of mma.sync.m16n8k16 (K rows read by ldmatrix are B as they lie, V rows by
-// ldmatrix.trans); the probabilities go from accumulator registers to A registers without shared
-// memory.  A block lies in one page (pages hold a multiple of 16 tokens).
+// twentieth of what the tensor cores could do meanwhile).  So the layout is made for loads in flight and
+// few instructions per key: blocks of 64 keys pass through a ring of TMA boxes (one per page and 64 columns,
+// 128-byte swizzle) that one warp fills; four warps take 16 keys of each block, with no barrier between them
+// but the ring's; two CTAs per SM with 192 KB of rings between them.  The 16 x D rows of Q stay in registers as the A operand of
+// mma.sync.m16n8k16 (K rows read by ldmatrix are B as they lie, V rows by ldmatrix.trans); the probabilities
+// go from accumulator registers to A registers without shared memory.
 //
-// The keys of a unit (sequence, kv head) are split over CTAs when there are few units; the last CTA
-// of a unit to finish adds the partial O in the order of the splits (a ticket per unit, reset by the
-// last), so the result does not depend on which one is last.
+// Split.  Two CTAs per SM.  With at least two of them to a unit (sequence, kv head), every unit is cut into
+// the same number of parts, one to a CTA.  With more to do, the blocks of all units are laid end to end and cut
+// evenly over the CTAs, so that ragged lengths cost no more than their sum; where all units are short the CTAs
+// take whole ones.  Every CTA finds its part from the lengths itself.  A unit that several CTAs share is joined by
+// the last of them to finish, in the order of its parts (a ticket per unit, reset by the last), so the result
+// does not depend on which one is last.
 //
-// What a row does not see: its score is replaced, not added to.  Keys no row sees are not read (zero
-// filled).  Where a block is cut differently for different rows, infinities and NaN in V are taken
-// out of the product (0 x NaN) and added to the rows that do see them.
+// What a row does not see: its score is replaced, not added to.  In blocks that the mask cuts,
+// infinities and NaN in V are taken out of the product (0 x NaN) and added to the rows that do see them.
 #include "cache_attention.cuh"
+#include "tcgen05.cuh"
 
 namespace mm {
 
@@ -30,25 +32,21 @@ namespace {
 
 __device__ unsigned int g_rows_err;
 
-constexpr int WARPS = 4, NT = WARPS * 32, B = 16, STAGES = 3;
-constexpr int MIN_BLOCKS = 8;  // blocks of a split, at least
+constexpr int WARPS = 4, NT = (WARPS + 1) * 32;  // four warps compute, the fifth loads
+constexpr int SUB = 16, B = WARPS * SUB;         // keys of a warp's part of a block, of a block
+constexpr int MIN_BLOCKS = 3;    // blocks of a part, at least
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA
+constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU
+constexpr int HALF = B * 128;          // bytes of a block's 64 columns
 
 struct RowsArgs {
     CacheAttnArgs a;
-    int splits;
+    int box;           // keys of one TMA box
     int32_t *tickets;  // [seqs][kv_heads]
-    float2 *ml;        // [seqs][kv_heads][splits][16]
-    float *part;       // [seqs][kv_heads][splits][16][head_dim]
+    float2 *ml;        // [CTAs][2][16]
+    float *part;       // [CTAs][2][16][head_dim]
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool read) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -65,383 +63,520 @@ template <typename T>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
 __device__ __forceinline__ void mma16<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// What the rows of one sequence need between them: the blocks, and where the mask cuts between rows
+struct SeqKeys {
+    SeqView v;
+    int end, whole, low, high;
+    KeyBlocks kb;  // count 0: no rows
+};
+__device__ __forceinline__ SeqKeys seq_keys(const CacheAttnArgs &a, int seq) {
+    SeqKeys k;
+    k.v = seq_view(a, seq, &g_rows_err);
+    const int len = k.v.len, count = k.v.count;
+    k.end = len + count;
+    k.whole = a.mask ? len : len + 1;
+    // a drafted token's depth is between 0 and count; a causal row i is at len + i
+    k.low = a.window ? (a.mask ? len - a.window : len - a.window + 1) : 0;
+    k.high = a.window ? len + count - a.window : 0;
+    k.kb = key_blocks<B>(k.low, a.sinks, k.end);
+    if (count == 0 || count * a.group > kRowsMax) k.kb.count = 0;  // the latter: max_q said otherwise
+    return k;
+}
+
+// Over the block's NT values: sums of a and b, inclusive in the reference, totals returned; the largest a
+struct Two {
+    int64_t a, b;
+    int most;
+};
+__device__ __forceinline__ Two scan(Two &v, Two *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v.most = __reduce_max_sync(0xffffffffu, (int)v.a);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v.a, o), y = __shfl_up_sync(0xffffffffu, v.b, o);
+        if (lane >= o) v.a += x, v.b += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = v;
+    __syncthreads();
+    Two all = {0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) v.a += sh[w].a, v.b += sh[w].b;
+        all.a += sh[w].a, all.b += sh[w].b, all.most = max(all.most, sh[w].most);
+    }
+    return all;
+}
+
 // KS: 16-element steps of the head dimension held (head_dim <= 16 KS, the rest zero)
 template <typename T, int KS>
-__global__ void __launch_bounds__(NT, 2) rows_kernel(const RowsArgs p) {
-    constexpr int ROW = KS * 32;              // bytes of a key's row in shared memory
-    constexpr int TILE = B * ROW;             // K or V of one block
-    constexpr int RING = STAGES * 2 * TILE;   // one warp's
-    extern __shared__ __align__(128) uint8_t sm[];
+__global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                     const __grid_constant__ CUtensorMap vmap, const RowsArgs p) {
+    constexpr int HALVES = KS / 4, STAGES = 6 / HALVES;  // 3 stages of 32 KB, or 6 of 16 KB
+    constexpr int TILE = HALVES * HALF;                  // K or V of one block
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ float2 sm_ml[WARPS][16];
-    __shared__ int sm_last;
+    __shared__ float sm_p[WARPS][16][SUB];  // probabilities of a block whose V holds an infinity or NaN
+    __shared__ Two sm_scan[NT / 32];
+    __shared__ int64_t sm_start;
+    __shared__ SeqKeys sm_k;
+    __shared__ int sm_seq, sm_last;
+    uint8_t *sm = smem_aligned<1024>(raw);
     const CacheAttnArgs &a = p.a;
     const CacheView &c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
-    const int seq = unit / c.kv_heads, head = unit - seq * c.kv_heads;
-    const SeqView sv = seq_view(a, seq, &g_rows_err);
-    const int rows = sv.count * a.group;
-    if (rows == 0 || rows > 16) return;  // rows > 16: max_q said otherwise, recorded by seq_view
-
-    // this thread's rows: lane / 4 and 8 later
-    RowView rv[2];
-    uint32_t tree[2];
-    int64_t low = 0;
-    const int64_t end = sv.len + sv.count;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = (lane >> 2) + 8 * h;
-        rv[h] = row_view(a, sv.len, sv.first, sv.count, min(r, rows - 1) / a.group);
-        tree[h] = rv[h].bits ? __ldg(rv[h].bits) & (sv.count < 32 ? (1u << sv.count) - 1u : ~0u) : 0u;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], WARPS);
+        fence_mbar_init();
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
     }
-    // the lowest window start of all rows, and the highest: keys from there on are cut by no window
-    low = min(rv[0].low, rv[1].low);
-    int64_t high = max(rv[0].low, rv[1].low);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
-        high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
-    }
-    if (a.mask) low = min(low, sv.len);  // the window does not cut drafted tokens
-    const KeyBlocks kb = key_blocks<B>(low, a.sinks, end);
-    int64_t per = (kb.count + p.splits - 1) / p.splits;
-    if (per < MIN_BLOCKS) per = MIN_BLOCKS;
-    const int used = (int)((kb.count + per - 1) / per);  // splits of this unit, >= 1
-    if (split >= used) return;
-    const int64_t b0 = split * per, b1 = min(kb.count, b0 + per);
+    pdl_launch_dependents();
+    pdl_wait();
 
-    const int64_t whole = a.mask ? sv.len : sv.len + 1;  // keys before it are cut by no row's end
-    const float scale2 = a.scale * kLog2e;
-    uint32_t q[KS][4];
+    // This CTA's part [at, stop) of the call, in one of two measures laid end to end over the units that have
+    // blocks.  A unit measures `parts` (its blocks cut into as many, or whole: parts = 1), or, where parts is 0,
+    // cost + n for its n blocks (the blocks last); the cost is up to UNIT_COST, but no more than half of what a CTA gets.
+    SeqKeys k;
+    const auto blocks = [&](int s) {
+        if (s >= c.seqs) return Two{0, 0, 0};
+        k = seq_keys(a, s);
+        return Two{k.kb.count, k.kb.count > 0, 0};
+    };
+    Two mine, sum, total = {0, 0, 0};
+    for (int s0 = 0; s0 < c.seqs; s0 += NT) {
+        mine = sum = blocks(s0 + threadIdx.x);
+        const Two t = scan(sum, sm_scan);
+        total.a += t.a, total.b += t.b, total.most = max(total.most, t.most);
+    }
+    const int64_t units = total.b * c.kv_heads;
+    if (units == 0) return;
+    int parts = 0;
+    if (2 * units <= gridDim.x)
+        parts = min((int)(gridDim.x / (uint32_t)units), (total.most + MIN_BLOCKS - 1) / MIN_BLOCKS);
+    else if (total.most <= WHOLE_BLOCKS)
+        parts = 1;
+    const int cost = parts ? 0 : (int)min(total.a * c.kv_heads / gridDim.x / 2, (int64_t)UNIT_COST);
+    const auto weight = [&](const Two &t) { return parts ? t.b * parts : t.a + cost * t.b; };
+    const int64_t all = weight(total) * c.kv_heads;
+    const int64_t ctas = min((int64_t)gridDim.x, parts ? all : (all + MIN_BLOCKS - 1) / MIN_BLOCKS);
+    if (blockIdx.x >= ctas) return;
+    const auto part = [&](int64_t cta) {  // cta * all / ctas
+        const int64_t x = cta * all;
+        return x >> 32 ? x / ctas : (int64_t)((uint32_t)x / (uint32_t)ctas);
+    };
+    int64_t at = part(blockIdx.x);
+    const int64_t stop = part(blockIdx.x + 1);
     {
-        const char *Q = static_cast<const char *>(a.Q);
-        const uint32_t *src[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = min((lane >> 2) + 8 * h, rows - 1), i = r / a.group;
-            src[h] = reinterpret_cast<const uint32_t *>(
-                Q + ((int64_t)(sv.first + i) * a.q_stride + (int64_t)(head * a.group + r - i * a.group) * c.head_dim) * 2);
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int d = k * 16 + (x >> 1) * 8 + 2 * (lane & 3);
-                q[k][x] = d < c.head_dim ? __ldg(src[x & 1] + d / 2) : 0u;
-            }
-    }
-
-    uint8_t *ring = sm + warp * RING;
-    const uint32_t ring_s = smem_u32(ring);
-    const int vecs = c.head_dim / 8;
-    if (vecs < 2 * KS)  // columns past head_dim stay zero
-        for (int e = lane; e < RING / 16; e += 32) *reinterpret_cast<uint4 *>(ring + e * 16) = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-
-    const char *kbase = c.k + head * c.head_stride * 2, *vbase = c.v + head * c.head_stride * 2;
-    // block i of this warp: b0 + warp + i WARPS
-    const auto page_at = [&](int64_t b) {
-        if (b >= b1) return -1;
-        return page_of(c, seq, (kb.block(b) * B) >> c.page_shift);
-    };
-    const auto load = [&](int64_t b, int page, int stage) {
-        if (b < b1) {
-            const int64_t key0 = kb.block(b) * B;
-            const uint32_t dst = ring_s + stage * 2 * TILE;
-            const int64_t base = page < 0 ? 0 : (page * c.page_stride + (key0 & (c.page_size - 1)) * c.token_stride) * 2;
-            if (page < 0) g_rows_err = kDevErrRange;
-#pragma unroll
-            for (int i = 0; i < B * 2 * KS / 32; ++i) {
-                const int e = i * 32 + lane, r = e / (2 * KS), x = e % (2 * KS);
-                const int64_t j = key0 + r;
-                const bool read = page >= 0 && j < end && (j >= low || j < a.sinks);
-                if (x < vecs) {
-                    const int64_t off = read ? base + (r * c.token_stride + x * 8) * 2 : 0;
-                    const uint32_t at = dst + r * ROW + ((x ^ (r & 7)) << 4);
-                    cp16(at, kbase + off, read);
-                    cp16(at + TILE, vbase + off, read);
+        int64_t before = 0;
+        for (int s0 = 0; s0 < c.seqs; s0 += NT) {
+            if (c.seqs > NT) {  // else the sums are still in registers
+                mine = sum = blocks(s0 + threadIdx.x);
+                const int64_t here = weight(scan(sum, sm_scan));
+                if (at >= (before + here) * c.kv_heads) {  // the same for all threads
+                    before += here;
+                    continue;
                 }
             }
+            const int64_t w = weight(mine), first = (before + weight(sum) - w) * c.kv_heads;
+            if (w > 0 && at >= first && at < first + w * c.kv_heads) sm_seq = s0 + threadIdx.x, sm_start = first, sm_k = k;
+            break;
         }
-        cp_commit();
-    };
-
-    float o[2 * KS][4];
-#pragma unroll
-    for (int n = 0; n < 2 * KS; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    int64_t b = b0 + warp;
-    int page = page_at(b);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        const int next = page_at(b + (s + 1) * WARPS);
-        load(b + s * WARPS, page, s);
-        page = next;
+        __syncthreads();
     }
-    int stage = 0;
-    for (; b < b1; b += WARPS) {
-        const int next = page_at(b + STAGES * WARPS);
-        {
-            const int to = stage + STAGES - 1;
-            load(b + (STAGES - 1) * WARPS, page, to >= STAGES ? to - STAGES : to);
-        }
-        page = next;
-        cp_wait<STAGES - 1>();
-        __syncwarp();
-        const uint32_t kt = ring_s + stage * 2 * TILE, vt = kt + TILE;
-        const int64_t key0 = kb.block(b) * B;
+    int seq = sm_seq;
+    int64_t seq_first = sm_start;  // where the sequence begins
+    k = sm_k;
 
-        float s[2][4] = {};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            uint32_t f[4];
-            const int r = (lane & 7) + ((lane >> 4) << 3), x = 2 * k + ((lane >> 3) & 1);
-            ldsm4(f, kt + r * ROW + ((x ^ (r & 7)) << 4));
-            mma16<T>(s[0], q[k], f[0], f[1]);
-            mma16<T>(s[1], q[k], f[2], f[3]);
+    const uint32_t ring_s = smem_u32(sm);
+    const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);  // > 0: a masked score stays -infinity
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;       // of Q, for a negative scale
+    const int D = c.head_dim, pairs = D / 2;
+    uint32_t it = 0;  // blocks that have passed through the ring
+    bool ok = true;
+
+    while (at < stop) {
+        const int n = k.kb.count;
+        const int64_t size = parts ? parts : n + cost;  // of a unit of this sequence
+        const int head = (int)(((at - seq_first) | size) >> 32 ? (at - seq_first) / size
+                                                                : (uint32_t)(at - seq_first) / (uint32_t)size);
+        const int64_t u0 = seq_first + head * size, u1 = u0 + size;
+        // its blocks here [b0, b1), and the parts the unit is joined of: in CTA g0 and the next
+        int b0, b1, used;
+        int64_t g0;
+        if (parts) {
+            const int per = max((n + parts - 1) / parts, min(n, MIN_BLOCKS));
+            b0 = (int)(at - u0) * per, b1 = min(n, b0 + per);
+            used = (n + per - 1) / per;
+            g0 = u0;  // with more than one part, each CTA has one
+        } else {
+            b0 = max((int)(at - u0) - cost, 0), b1 = (int)(min(stop, u1) - u0) - cost;
+            g0 = ((u0 + cost + 1) * ctas - 1) / all;
+            used = (int)((u1 * ctas - 1) / all - g0) + 1;
         }
-        // whether some row does not see some key of this block
-        const bool cut = key0 + B > whole || (key0 < high && key0 + B > a.sinks);
-        bool seen[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                seen[n][x] = true;
-                if (cut) {
-                    const int64_t j = key0 + n * 8 + 2 * (lane & 3) + (x & 1);
-                    const RowView &r = rv[x >> 1];
-                    if (j < r.end) {
-                        seen[n][x] = j >= r.low || j < a.sinks;
-                    } else {
-                        const int64_t t = j - sv.len;
-                        seen[n][x] = t < 32 && (tree[x >> 1] >> t & 1u);
-                    }
+        if (b1 <= b0) break;  // nothing of the unit but its cost, or a part that a short unit does not have
+        const SeqView sv = k.v;
+        const int rows = sv.count * a.group;
+        constexpr int OS = KS * 16 + 4;  // the warps' O side by side, fp32, rows padded by 4 words
+        float *so = reinterpret_cast<float *>(sm);
+
+        if (warp == WARPS) {
+            // a lane to each box: page lane / (2 HALVES) of the block, K or V, 64 columns
+            const int boxes = B / p.box * 2 * HALVES, x = lane % (2 * HALVES), row = lane / (2 * HALVES) * p.box;
+            const CUtensorMap *map = x < HALVES ? &kmap : &vmap;
+            uint8_t *dst = sm + x * HALF + row * 128;
+            const auto page_at = [&](int b) {
+                const int key = k.kb.block(b) * B + row;
+                if (b >= b1 || lane >= boxes || key >= k.end) return -1;
+                const int page = page_of(c, seq, key >> c.page_shift);
+                if (page < 0) g_rows_err = kDevErrRange;
+                return page;
+            };
+            int page = page_at(b0), page2 = page_at(b0 + 1);
+            for (int b = b0; b < b1; ++b, ++it) {
+                const int page3 = page_at(b + 2);
+                const uint32_t st = it % STAGES;
+                if (it >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (it / STAGES - 1) & 1))) {
+                    atomicExch(&g_rows_err, kDevErrWaitEmpty);
+                    ok = false;
+                    break;
                 }
-                s[n][x] = seen[n][x] ? s[n][x] * scale2 : -INFINITY;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * TILE);
+                __syncwarp();
+                if (lane < boxes)  // no page: out of the tensor, reads as zeros
+                    tma_load_4d(dst + st * 2 * TILE, map, &full[st], x % HALVES * 64, (k.kb.block(b) * B + row) & (c.page_size - 1),
+                                head, page < 0 ? (int)min(c.pages, (int64_t)0x7fffffff) : page);
+                page = page2, page2 = page3;
             }
-        float mx[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        }
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+            if (!ok)  // nothing of this CTA's may be in flight when it ends
+                for (uint32_t y = it > STAGES ? it - STAGES : 0; y < it; ++y) mbar_wait(&full[y % STAGES], (y / STAGES) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (__syncthreads_or(!ok)) return;
+        } else {
+            // this thread's rows: lane / 4 and 8 later
+            RowView rv[2];
+            uint32_t tree[2], q[KS][4];
+            const uint32_t *src[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float now = fmaxf(m[h], mx[h]);
-                const float f = now == -INFINITY ? 1.f : ex2(m[h] - now);
-                m[h] = now;
-                l[h] *= f;
-#pragma unroll
-                for (int n = 0; n < 2 * KS; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+                const int r = min((lane >> 2) + 8 * h, rows - 1), i = r / a.group;
+                rv[h] = row_view(a, sv.len, sv.first, sv.count, i);
+                tree[h] = rv[h].bits ? __ldg(rv[h].bits) & ((1u << sv.count) - 1u) : 0u;  // count <= 16
+                src[h] = reinterpret_cast<const uint32_t *>(
+                    static_cast<const char *>(a.Q) +
+                    ((int64_t)(sv.first + i) * a.q_stride + (int64_t)(head * a.group + r - i * a.group) * D) * 2);
             }
-        }
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+            for (int e = 0; e < KS; ++e)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                s[n][x] = seen[n][x] ? ex2(s[n][x] - m[x >> 1]) : 0.f;
-                l[x >> 1] += s[n][x];
-            }
-        uint32_t pr[4];
-        pr[0] = Pair<T>::pack(s[0][0], s[0][1]);
-        pr[1] = Pair<T>::pack(s[0][2], s[0][3]);
-        pr[2] = Pair<T>::pack(s[1][0], s[1][1]);
-        pr[3] = Pair<T>::pack(s[1][2], s[1][3]);
-        bool special = false;
-#pragma unroll
-        for (int n = 0; n < KS; ++n) {
-            uint32_t f[4];
-            const int r = (lane & 7) + (((lane >> 3) & 1) << 3), x = 2 * n + (lane >> 4);
-            ldsm4t(f, vt + r * ROW + ((x ^ (r & 7)) << 4));
-            if (cut) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    special |= any_special<T>(f[i]);
-                    f[i] = without_special<T>(f[i]);
+                for (int x = 0; x < 4; ++x) {
+                    const int d = e * 16 + (x >> 1) * 8 + 2 * (lane & 3);
+                    q[e][x] = d < D ? __ldg(src[x & 1] + d / 2) ^ flip : 0u;
                 }
-            }
-            mma16<T>(o[2 * n], pr, f[0], f[1]);
-            mma16<T>(o[2 * n + 1], pr, f[2], f[3]);
-        }
-        if (cut && __any_sync(0xffffffffu, special)) {  // rare: added where they are seen, key by key
+            const auto in = [&](int h, int j) {
+                const int t = j - sv.len;
+                return j < rv[h].end ? j >= rv[h].low || j < a.sinks : t < 32 && (tree[h] >> t & 1u);
+            };
+            float o[2 * KS][4];
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int64_t j = key0 + i;
+            for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bool in = j < rv[h].end ? j >= rv[h].low || j < a.sinks
-                                                  : j - sv.len < 32 && (tree[h] >> (j - sv.len) & 1u);
-                    // the probability of key i lies with the lane of its column
-                    const int owner = (lane & ~3) | ((i & 7) >> 1);
-                    const float pv = __shfl_sync(0xffffffffu, s[i >> 3][2 * h + (i & 1)], owner);
-                    if (!in) continue;
+                for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            // ldmatrix: this lane's row of K and V, its chunk 2 e + (0 or 1) swizzled by the row's low bits
+            const int kr = (lane & 7) + ((lane >> 4) << 3), vr = (lane & 7) + (((lane >> 3) & 1) << 3), x6 = lane & 6;
+            const int kb0 = (((lane >> 3) ^ lane) & 1) << 4, vb0 = (((lane >> 4) ^ lane) & 1) << 4;
+
+            for (int b = b0; b < b1; ++b, ++it) {
+                const uint32_t st = it % STAGES;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (it / STAGES) & 1))) {
+                    atomicExch(&g_rows_err, kDevErrWaitFull);
+                    ok = false;  // the loader waits for what is in flight
+                    break;
+                }
+                const uint32_t kt = ring_s + st * 2 * TILE + warp * SUB * 128, vt = kt + TILE;
+                const int key0 = k.kb.block(b) * B + warp * SUB;
+                if (key0 >= k.end || (key0 + SUB <= k.low && key0 >= a.sinks)) {  // no row sees any of these
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[st]);
+                    continue;
+                }
+
+                // four ldmatrix at a time, so that their latency is paid once
+                float s[2][4] = {};
 #pragma unroll
-                    for (int n = 0; n < 2 * KS; ++n) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                            ring + stage * 2 * TILE + TILE + i * ROW + ((n ^ (i & 7)) << 4) + 4 * (lane & 3));
-                        if (any_special<T>(w)) {
-                            const uint16_t lo = (uint16_t)w, hi = (uint16_t)(w >> 16);
-                            if ((lo & Pair<T>::kExp) == Pair<T>::kExp) o[n][2 * h] += pv * Pair<T>::one(lo);
-                            if ((hi & Pair<T>::kExp) == Pair<T>::kExp) o[n][2 * h + 1] += pv * Pair<T>::one(hi);
-                        }
+                for (int h = 0; h < HALVES; ++h) {
+                    uint32_t f[4][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ldsm4(f[e], kt + h * HALF + kr * 128 + kb0 + ((2 * e ^ x6) << 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        mma16<T>(s[0], q[4 * h + e], f[e][0], f[e][1]);
+                        mma16<T>(s[1], q[4 * h + e], f[e][2], f[e][3]);
                     }
                 }
+                uint32_t fv[4][4];  // V's first half, on its way during the softmax
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ldsm4t(fv[e], vt + vr * 128 + vb0 + ((2 * e ^ x6) << 4));
+                // whether some row does not see some of these keys
+                const bool cut = key0 + SUB > k.whole || (key0 < k.high && key0 + SUB > a.sinks);
+                if (cut) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!in(x >> 1, key0 + n * 8 + 2 * (lane & 3) + (x & 1))) s[n][x] = -INFINITY;
+                }
+                float mx[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])) * scale2;
+                if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                        const float now = fmaxf(m[h], mx[h]);
+                        const float f = now == -INFINITY ? 1.f : ex2(m[h] - now);
+                        m[h] = now;
+                        l[h] *= f;
+#pragma unroll
+                        for (int n = 0; n < 2 * KS; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+                    }
+                }
+                // a row that has seen nothing yet has scores of -infinity here: 2^-infinity = 0
+                const float base[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[n][x] = ex2(fmaf(s[n][x], scale2, base[x >> 1]));
+                        l[x >> 1] += s[n][x];
+                    }
+                uint32_t pr[4];
+                pr[0] = Pair<T>::pack(s[0][0], s[0][1]);
+                pr[1] = Pair<T>::pack(s[0][2], s[0][3]);
+                pr[2] = Pair<T>::pack(s[1][0], s[1][1]);
+                pr[3] = Pair<T>::pack(s[1][2], s[1][3]);
+                bool special = false;
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    if (h > 0)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ldsm4t(fv[e], vt + h * HALF + vr * 128 + vb0 + ((2 * e ^ x6) << 4));
+                    if (cut) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                special |= any_special<T>(fv[e][i]);
+                                fv[e][i] = without_special<T>(fv[e][i]);
+                            }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        mma16<T>(o[8 * h + 2 * e], pr, fv[e][0], fv[e][1]);
+                        mma16<T>(o[8 * h + 2 * e + 1], pr, fv[e][2], fv[e][3]);
+                    }
+                }
+                if (cut && __any_sync(0xffffffffu, special)) {  // rare: added where they are seen, key by key
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            sm_p[warp][(lane >> 2) + 8 * (x >> 1)][n * 8 + 2 * (lane & 3) + (x & 1)] = s[n][x];
+                    __syncwarp();
+                    for (int i = 0; i < SUB; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!in(h, key0 + i)) continue;
+                            const float pv = sm_p[warp][(lane >> 2) + 8 * h][i];
+#pragma unroll
+                            for (int n = 0; n < 2 * KS; ++n) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                                    sm + st * 2 * TILE + TILE + (n >> 3) * HALF + (warp * SUB + i) * 128 + (((n & 7) ^ (i & 7)) << 4) + 4 * (lane & 3));
+                                const uint16_t lo = (uint16_t)w, hi = (uint16_t)(w >> 16);
+                                if ((lo & Pair<T>::kExp) == Pair<T>::kExp) o[n][2 * h] += pv * Pair<T>::one(lo);
+                                if ((hi & Pair<T>::kExp) == Pair<T>::kExp) o[n][2 * h + 1] += pv * Pair<T>::one(hi);
+                            }
+                        }
+                }
+                __syncwarp();  // the warp is through with this stage
+                if (lane == 0) mbar_arrive(&empty[st]);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                if ((lane & 3) == 0) sm_ml[warp][(lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
+            }
+            if (__syncthreads_or(!ok)) return;
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2) + 8 * h) * OS + n * 8 + 2 * (lane & 3)) =
+                        make_float2(o[n][2 * h], o[n][2 * h + 1]);
         }
-        __syncwarp();  // this stage is free
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-    cp_wait<0>();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if ((lane & 3) == 0) sm_ml[warp][(lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
-    }
-    // the warps' O side by side in shared memory, fp32, rows padded by 4 words
-    constexpr int OS = KS * 16 + 4;
-    float *so = reinterpret_cast<float *>(sm);
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < 2 * KS; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2 *>(so + (warp * 16 + (lane >> 2) + 8 * h) * OS + n * 8 + 2 * (lane & 3)) =
-                make_float2(o[n][2 * h], o[n][2 * h + 1]);
-    __syncthreads();
+        __syncthreads();
 
-    const int D = c.head_dim, pairs = D / 2;
-    const int64_t slot = ((int64_t)unit * p.splits + split) * 16;
-    const auto out_at = [&](int r, int d) {
-        const int i = r / a.group;
-        return reinterpret_cast<uint32_t *>(
-            static_cast<char *>(a.O) +
-            ((int64_t)(sv.first + i) * a.o_stride + (int64_t)(head * a.group + r - i * a.group) * D + d) * 2);
-    };
-    for (int e = threadIdx.x; e < rows * pairs; e += NT) {
-        const int r = e / pairs, d = 2 * (e - r * pairs);
-        float mt = -INFINITY, lt = 0.f;
-        float2 v = make_float2(0.f, 0.f);
+        const bool alone = b0 == 0 && b1 == n;
+        // a part's slot: 0 for the CTA's first unit, 1 for one that it begins later and does not finish
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + (b0 == 0 && part(blockIdx.x) < u0)) * 16;
+        const auto out_at = [&](int r, int d) {
+            const int i = r / a.group;
+            return reinterpret_cast<uint32_t *>(
+                static_cast<char *>(a.O) +
+                ((int64_t)(sv.first + i) * a.o_stride + (int64_t)(head * a.group + r - i * a.group) * D + d) * 2);
+        };
+        for (int e = threadIdx.x; e < rows * pairs; e += NT) {
+            const int r = e / pairs, d = 2 * (e - r * pairs);
+            float mt = -INFINITY, lt = 0.f;
+            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) mt = fmaxf(mt, sm_ml[w][r].x);
-        if (mt > -INFINITY) {
+            for (int w = 0; w < WARPS; ++w) mt = fmaxf(mt, sm_ml[w][r].x);
+            if (mt > -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float2 ml = sm_ml[w][r];
-                if (ml.x == -INFINITY) continue;
-                const float f = ex2(ml.x - mt);
-                const float2 x = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * OS + d);
-                lt += f * ml.y;
-                v.x += f * x.x, v.y += f * x.y;
+                for (int w = 0; w < WARPS; ++w) {
+                    const float2 ml = sm_ml[w][r];
+                    if (ml.x == -INFINITY) continue;
+                    const float f = ex2(ml.x - mt);
+                    const float2 x = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * OS + d);
+                    lt += f * ml.y;
+                    v.x += f * x.x, v.y += f * x.y;
+                }
+            }
+            if (alone) {
+                const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
+                *out_at(r, d) = Pair<T>::pack(v.x * inv, v.y * inv);
+            } else {
+                *reinterpret_cast<float2 *>(p.part + (slot + r) * D + d) = v;
+                if (d == 0) p.ml[slot + r] = make_float2(mt, lt);
             }
         }
-        if (used == 1) {
-            const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
-            *out_at(r, d) = Pair<T>::pack(v.x * inv, v.y * inv);
-        } else {
-            *reinterpret_cast<float2 *>(p.part + (slot + r) * D + d) = v;
-            if (d == 0) p.ml[slot + r] = make_float2(mt, lt);
-        }
-    }
-    if (used == 1) return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const int t = atomicAdd(p.tickets + unit, 1);
-        sm_last = t == used - 1;
-        if (sm_last) p.tickets[unit] = 0;  // ready for the next call
-    }
-    __syncthreads();
-    if (!sm_last) return;
-    __threadfence();
-    const int64_t slot0 = (int64_t)unit * p.splits * 16;
-    for (int e = threadIdx.x; e < rows * pairs; e += NT) {
-        const int r = e / pairs, d = 2 * (e - r * pairs);
-        float mt = -INFINITY, lt = 0.f;
-        float2 v = make_float2(0.f, 0.f);
-        for (int s = 0; s < used; ++s) mt = fmaxf(mt, __ldcg(&p.ml[slot0 + s * 16 + r]).x);
-        if (mt > -INFINITY) {
-#pragma unroll 4
-            for (int s = 0; s < used; ++s) {
-                const float2 ml = __ldcg(&p.ml[slot0 + s * 16 + r]);
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(p.part + (slot0 + s * 16 + r) * D + d));
-                const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
-                lt += f * ml.y;
-                v.x += f * x.x, v.y += f * x.y;
+        if (!alone) {
+            const int unit = seq * c.kv_heads + head;
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                sm_last = atomicAdd(p.tickets + unit, 1) == used - 1;
+                if (sm_last) p.tickets[unit] = 0;  // ready for the next call
+            }
+            __syncthreads();
+            if (sm_last) {
+                __threadfence();
+                const int64_t slot0 = (g0 * 2 + (part(g0) < u0)) * 16;
+                const int quads = D / 4;
+                for (int e = threadIdx.x; e < rows * quads; e += NT) {
+                    const int r = e / quads, d = 4 * (e - r * quads);
+                    float mt = -INFINITY, lt = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int y = 0; y < used; y += 4) {  // four parts' loads at a time
+                        float2 ml[4];
+                        float4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int64_t sl = (y + i == 0 ? slot0 : (g0 + min(y + i, used - 1)) * 32) + r;
+                            ml[i] = __ldcg(&p.ml[sl]);
+                            x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * D + d));
+                            if (y + i >= used) ml[i].x = -INFINITY;
+                        }
+                        float now = mt;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) now = fmaxf(now, ml[i].x);
+                        if (now == -INFINITY) continue;
+                        const float f = ex2(mt - now);
+                        mt = now;
+                        lt *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float w = ex2(ml[i].x - now);
+                            if (ml[i].x == -INFINITY) continue;
+                            lt += w * ml[i].y;
+                            v.x += w * x[i].x, v.y += w * x[i].y, v.z += w * x[i].z, v.w += w * x[i].w;
+                        }
+                    }
+                    const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
+                    *reinterpret_cast<uint2 *>(out_at(r, d)) =
+                        make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
+                }
             }
         }
-        const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
-        *out_at(r, d) = Pair<T>::pack(v.x * inv, v.y * inv);
+        at = parts ? at + 1 : min(stop, u1);
+        if (at >= stop) break;
+        if (at == seq_first + size * c.kv_heads) {  // on to the next sequence that has rows
+            seq_first = at;
+            do k = seq_keys(a, ++seq);
+            while (k.kb.count == 0);
+        }
+        fence_proxy_async_smem();  // the ring was written by threads; TMA writes it next
+        __syncthreads();
     }
 }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 template <typename T, int KS>
-cudaError_t launch(const RowsArgs &p, cudaStream_t s) {
-    constexpr int SMEM = WARPS * STAGES * 2 * B * KS * 32;
-    static_assert(SMEM >= WARPS * 16 * (KS * 16 + 4) * 4, "the warps' O fit in the rings");
+cudaError_t launch(const RowsArgs &p, int ctas, cudaStream_t s) {
+    constexpr int SMEM = 6 * 2 * HALF + 1024;  // the ring, and alignment
+    static_assert(SMEM - 1024 >= WARPS * 16 * (KS * 16 + 4) * 4, "the warps' O fit in the rings");
     static const cudaError_t once =
         cudaFuncSetAttribute(rows_kernel<T, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (once != cudaSuccess) return once;
-    rows_kernel<T, KS><<<(unsigned)((int64_t)p.splits * p.a.c.seqs * p.a.c.kv_heads), NT, SMEM, s>>>(p);
-    return cudaGetLastError();
+    CUtensorMap k, v;
+    cudaError_t e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
+    if (e == cudaSuccess) e = cache_tmap(&v, p.a.c, p.a.c.v, p.box);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rows_kernel<T, KS>, dim3((unsigned)ctas), NT, SMEM, s, k, v, p);
 }
 
 template <typename T>
-cudaError_t launch_t(const RowsArgs &p, cudaStream_t s) {
-    return p.a.c.head_dim <= 64 ? launch<T, 4>(p, s) : launch<T, 8>(p, s);
+cudaError_t launch_t(const RowsArgs &p, int ctas, cudaStream_t s) {
+    return p.a.c.head_dim <= 64 ? launch<T, 4>(p, ctas, s) : launch<T, 8>(p, ctas, s);
 }
 
 }  // namespace
 
-int cache_attention_rows_splits(const CacheView &c, int sms) {
-    const int64_t units = (int64_t)c.seqs * c.kv_heads, blocks = (c.max_pages << c.page_shift) / B;
-    // four CTAs for each resident one, so that ragged lengths even out, but no less than MIN_BLOCKS each
-    int64_t s = (8 * (int64_t)sms + units - 1) / units;
-    const int64_t most = (blocks + MIN_BLOCKS - 1) / MIN_BLOCKS;
-    if (s > most) s = most;
-    if (s > 64) s = 64;
-    return (int)(s < 1 ? 1 : s);
+int cache_attention_rows_ctas(const CacheView &c, int sms) {
+    const int64_t most = (int64_t)c.seqs * c.kv_heads * (((c.max_pages << c.page_shift) + B - 1) / B);  // blocks
+    const int64_t ctas = (most + MIN_BLOCKS - 1) / MIN_BLOCKS;
+    return (int)(ctas < 2 * (int64_t)sms ? ctas : 2 * (int64_t)sms);
 }
 
-int64_t cache_attention_rows_workspace(const CacheView &c, int splits) {
-    if (splits <= 1) return 0;
-    const int64_t units = (int64_t)c.seqs * c.kv_heads;
-    return round256(units * 4) + round256(units * splits * 16 * 8) + units * splits * 16 * c.head_dim * 4;
+int64_t cache_attention_rows_workspace(const CacheView &c, int ctas) {
+    return round256((int64_t)c.seqs * c.kv_heads * 4) + (int64_t)ctas * 32 * (8 + (int64_t)c.head_dim * 4);
 }
 
-cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int splits, cudaStream_t s) {
-    RowsArgs p{a, splits, nullptr, nullptr, nullptr};
-    if (splits > 1) {
-        const int64_t units = (int64_t)a.c.seqs * a.c.kv_heads;
-        char *w = static_cast<char *>(a.ws);
-        p.tickets = reinterpret_cast<int32_t *>(w);
-        w += round256(units * 4);
-        p.ml = reinterpret_cast<float2 *>(w);
-        w += round256(units * splits * 16 * 8);
-        p.part = reinterpret_cast<float *>(w);
-    }
-    return a.c.dtype == 0 ? launch_t<__half>(p, s) : launch_t<__nv_bfloat16>(p, s);
+cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
+    char *w = static_cast<char *>(a.ws);
+    RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, nullptr, nullptr, nullptr};
+    p.tickets = reinterpret_cast<int32_t *>(w);
+    w += round256((int64_t)a.c.seqs * a.c.kv_heads * 4);
+    p.part = reinterpret_cast<float *>(w);
+    p.ml = reinterpret_cast<float2 *>(w + (int64_t)ctas * 32 * a.c.head_dim * 4);
+    return a.c.dtype == 0 ? launch_t<__half>(p, ctas, s) : launch_t<__nv_bfloat16>(p, ctas, s);
 }
 
 unsigned int cache_attention_rows_take_device_error(cudaError_t *err) {

@@ -27,7 +27,6 @@
 // the partial results in the order of the splits.
 #include "cache_attention.cuh"
 #include "tcgen05.cuh"
-#include "tmap.h"
 
 namespace mm {
 
@@ -129,15 +128,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_
 }
 
 // bits of [0, 32) below n
-__device__ __forceinline__ uint32_t below(int64_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << (int)n) - 1u; }
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 // which of keys j0 .. j0 + 31 the row sees
-__device__ __forceinline__ uint32_t seen_bits(const RowView &r, int64_t j0, int64_t sinks, int64_t len, int count) {
+__device__ __forceinline__ uint32_t seen_bits(const RowView &r, int j0, int sinks, int len, int count) {
     uint32_t s = below(r.end - j0) & (~below(r.low - j0) | below(sinks - j0));
     if (r.bits) {
-        const int64_t t0 = j0 - len;
+        const int t0 = j0 - len;
         if (t0 > -32 && t0 < count) {
-            const int w = (int)(t0 >> 5), words = (count + 31) >> 5;
+            const int w = t0 >> 5, words = (count + 31) >> 5;
             const uint32_t lo = w >= 0 ? __ldg(r.bits + w) : 0u, hi = w + 1 < words ? __ldg(r.bits + w + 1) : 0u;
             s |= __funnelshift_r(lo, hi, (unsigned)(t0 & 31)) & below(count - t0);
         }
@@ -168,6 +167,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     const int head = unit % c.kv_heads, seq = unit / c.kv_heads % c.seqs;
     const int tile = p.tiles - 1 - unit / c.kv_heads / c.seqs;  // the later rows, with more keys, first
 
+    pdl_launch_dependents();
+    pdl_wait();
     const SeqView sv = seq_view(a, seq, &g_tiles_err);
     const int row0 = tile * ROWS;
     const int nrows = min(sv.count * a.group - row0, ROWS);
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     const bool single = nrows <= 128;
     const int i_first = row0 / a.group, i_last = (row0 + nrows - 1) / a.group;
     // keys the rows need between them, and where the mask cuts between rows: see KeyBlocks and cut()
-    int64_t end, whole, low = 0, high = 0;
+    int end, whole, low = 0, high = 0;
     if (a.mask) {  // a row's depth is between 0 and count drafted tokens
         end = sv.len + sv.count, whole = sv.len;
         if (a.window) low = sv.len - a.window, high = sv.len + sv.count - a.window;
@@ -183,16 +184,15 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
         end = sv.len + i_last + 1, whole = sv.len + i_first + 1;
         if (a.window) low = sv.len + i_first - a.window + 1, high = sv.len + i_last - a.window + 1;
     }
-    const int64_t sinks = a.sinks;
+    const int sinks = a.sinks;
     const KeyBlocks kb = key_blocks<B>(low, sinks, end);
-    int64_t per = (kb.count + p.splits - 1) / p.splits;
-    if (per < MIN_BLOCKS) per = MIN_BLOCKS;
-    const int used = (int)((kb.count + per - 1) / per);
+    const int per = max((kb.count + p.splits - 1) / p.splits, MIN_BLOCKS);
+    const int used = (kb.count + per - 1) / per;
     if (split >= used) return;
-    const int64_t b0 = split * per;
-    const int n = (int)(min(kb.count, b0 + per) - b0);
+    const int b0 = split * per;
+    const int n = min(kb.count, b0 + per) - b0;
     const auto key_of = [&](int i) { return kb.block(b0 + i) * B; };
-    const auto cut = [&](int64_t key0) { return key0 + B > whole || (key0 < high && key0 + B > sinks); };
+    const auto cut = [&](int key0) { return key0 + B > whole || (key0 < high && key0 + B > sinks); };
     // loads in the order of their use: K 0, then K i + 1 and V i
     const auto slot_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
     const auto slot_v = [&](int i) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             tc_fence_after_sync();
             float v[128];
             tmem_ld128(ts, v);
-            const int64_t key0 = key_of(blk);
+            const int key0 = key_of(blk);
             if (cut(key0)) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             for (; x < 2 * n; ++x) {
                 const bool is_v = x == 2 * n - 1 || (x > 0 && !(x & 1));
                 const int blk = x == 0 ? 0 : x == 2 * n - 1 ? n - 1 : x & 1 ? (x + 1) / 2 : x / 2 - 1;
-                const int64_t key = key_of(blk) + lane / HALVES * p.box;
+                const int key = key_of(blk) + lane / HALVES * p.box;
                 int page = -1;
                 if (lane < ops && key < end) {
                     page = page_of(c, seq, key >> c.page_shift);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 __syncwarp();
                 if (lane < ops)  // a page out of range is out of the tensor: zeros
                     tma_load_4d(sm + P::RING + st * P::TILE + (lane % HALVES) * HALF + lane / HALVES * p.box * 128,
-                                is_v ? &vmap : &kmap, full + st, (lane % HALVES) * 64, (int)(key & (c.page_size - 1)), head,
+                                is_v ? &vmap : &kmap, full + st, (lane % HALVES) * 64, key & (c.page_size - 1), head,
                                 page < 0 ? (int)min(c.pages, (int64_t)0x7fffffff) : page);
             }
             // nothing of this CTA's may be in flight when it ends
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             const int ft = tid - 320;
             uint32_t looked = 0;
             for (int i = 0; i < n; ++i) {
-                const int64_t key0 = key_of(i);
+                const int key0 = key_of(i);
                 if (!cut(key0)) continue;
                 const int x = slot_v(i), st = x % ST;
                 if (!__all_sync(0xffffffffu, wait(fix, looked++ & 1, kDevErrWaitFull) &&
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 bool special = false;
 #pragma unroll 4
                 for (int e = ft; e < P::TILE / 16; e += 64) {
-                    const int64_t j = key0 + ((e & 1023) >> 3);
+                    const int j = key0 + ((e & 1023) >> 3);
                     uint4 *at = reinterpret_cast<uint4 *>(v + e * 16);
                     if (j >= end || (j >= sinks && j < low)) {
                         *at = make_uint4(0, 0, 0, 0);
@@ -566,32 +566,17 @@ int64_t unit_count(const CacheView &c, int group, int64_t max_q, int *tiles) {
     return (int64_t)*tiles * c.seqs * c.kv_heads;
 }
 
-cudaError_t make_map(CUtensorMap *map, const CacheView &c, const void *base, int box) {
-    cudaError_t err;
-    auto enc = tmap_encoder(&err);
-    if (err != cudaSuccess) return err;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.pages};
-    const auto bytes = [&](int64_t stride, int64_t count) { return (cuuint64_t)(count > 1 ? stride * 2 : 16); };
-    const cuuint64_t strides[3] = {bytes(c.token_stride, c.page_size), bytes(c.head_stride, c.kv_heads), bytes(c.page_stride, c.pages)};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, one[4] = {1, 1, 1, 1};
-    const CUresult r = enc(map, c.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                           const_cast<void *>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <typename T, int HALVES>
 cudaError_t launch(const TilesArgs &p, cudaStream_t s) {
     static const cudaError_t once = cudaFuncSetAttribute(
         tiles_kernel<T, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<HALVES>::BYTES);
     if (once != cudaSuccess) return once;
     CUtensorMap k, v;
-    cudaError_t e = make_map(&k, p.a.c, p.a.c.k, p.box);
-    if (e == cudaSuccess) e = make_map(&v, p.a.c, p.a.c.v, p.box);
+    cudaError_t e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
+    if (e == cudaSuccess) e = cache_tmap(&v, p.a.c, p.a.c.v, p.box);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.tiles * p.a.c.seqs * p.a.c.kv_heads;
-    tiles_kernel<T, HALVES><<<(unsigned)(units * p.splits), NT, Plan<HALVES>::BYTES, s>>>(k, v, p);
-    return cudaGetLastError();
+    return launch_pdl(tiles_kernel<T, HALVES>, dim3((unsigned)(units * p.splits)), NT, Plan<HALVES>::BYTES, s, k, v, p);
 }
 
 }  // namespace

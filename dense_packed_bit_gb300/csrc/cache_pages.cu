@@ -167,6 +167,8 @@ __device__ __forceinline__ void reserve_range(const CacheView &c, const int32_t 
 // counts as wanted and the ranks stay; the marks are turned into pages at the end.
 __global__ void __launch_bounds__(NT, 1) reserve_kernel(const CacheView c, const int32_t *need, int32_t *missing) {
     __shared__ AllocShared sh;
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // f(seq, entry, rank of the entry among the sequence's wanted ones)
     const auto each_wanted = [&](int64_t s, const auto &f) {
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(NT, 1) fork_alloc_kernel(const CacheView c, co
                                                            const int32_t *children, int64_t n, int32_t *missing) {
     __shared__ AllocShared sh;
     pdl_launch_dependents();
+    pdl_wait();
     const auto count = [&](int64_t i0) {
         const int64_t i = i0 + threadIdx.x;
         int p, ch, want = 0;
@@ -289,6 +292,7 @@ __device__ __forceinline__ void copy_page(const CacheView &c, char *base, int64_
 // full pages and fill the child's row of the table
 __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const int32_t *parents,
                                                        const int32_t *children, const int32_t *missing) {
+    pdl_launch_dependents();
     pdl_wait();
     int p, ch;
     int64_t len;
@@ -324,6 +328,8 @@ __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const 
 }
 
 __global__ void __launch_bounds__(CT) copy_pages_kernel(const CacheView c, const int32_t *src, const int32_t *dst) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int s = src[blockIdx.z], d = dst[blockIdx.z];
     if (s < 0 || s >= c.pages || d < 0 || d >= c.pages) {
         range_error();
@@ -345,6 +351,8 @@ __device__ __forceinline__ void release(const CacheView &c, int32_t *entry) {
 
 __global__ void __launch_bounds__(CT) free_kernel(const CacheView c, const int32_t *list, int64_t window,
                                                   int64_t sinks) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int s = list[blockIdx.x];
     if (s < 0 || s >= c.seqs) {
         range_error();
@@ -363,6 +371,8 @@ __global__ void __launch_bounds__(CT) free_kernel(const CacheView c, const int32
 __global__ void __launch_bounds__(CT) append_kernel(const CacheView c, const char *K, const char *V,
                                                     int64_t token_stride, const int32_t *q_start, int64_t tokens,
                                                     int64_t max_new) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int s = blockIdx.y;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
     const int64_t len = c.lens[s];
@@ -406,6 +416,7 @@ __global__ void __launch_bounds__(CT) compact_move_kernel(const CacheView c, con
                                                           const int32_t *keep, const int32_t *kept, int64_t tokens,
                                                           int64_t max_new) {
     pdl_launch_dependents();
+    pdl_wait();
     const int s = blockIdx.y;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
     const int n = kept_of(kept, s, r.count);
@@ -452,6 +463,7 @@ __global__ void __launch_bounds__(CT) compact_move_kernel(const CacheView c, con
 
 __global__ void __launch_bounds__(CT) compact_table_kernel(const CacheView c, const int32_t *q_start,
                                                            const int32_t *kept, int64_t tokens, int64_t max_new) {
+    pdl_launch_dependents();
     pdl_wait();
     const int s = blockIdx.x;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
@@ -467,21 +479,6 @@ __global__ void __launch_bounds__(CT) compact_table_kernel(const CacheView c, co
         release(c, c.table + (int64_t)s * c.max_pages + j);
 }
 
-// the next kernel of a call, resident while the one before it ends
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = grid;
-    lc.blockDim = dim3((unsigned)threads);
-    lc.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, kern, P(args)...);
-}
-
 // CTAs that share one layer's page: about 32 KB each
 unsigned copy_parts(const CacheView &c) {
     const int64_t bytes = (int64_t)c.kv_heads * c.page_size * c.head_dim * 2;
@@ -491,52 +488,45 @@ unsigned copy_parts(const CacheView &c) {
 }  // namespace
 
 cudaError_t launch_cache_reserve(const CacheView &c, const int32_t *need, int32_t *missing, cudaStream_t s) {
-    reserve_kernel<<<1, NT, 0, s>>>(c, need, missing);
-    return cudaGetLastError();
+    return launch_pdl(reserve_kernel, dim3(1), NT, 0, s, c, need, missing);
 }
 
 cudaError_t launch_cache_append(const CacheView &c, const void *K, const void *V, int64_t token_stride,
                                 const int32_t *q_start, int64_t tokens, int64_t max_new, cudaStream_t s) {
     const int64_t vecs = max_new * c.kv_heads * (c.head_dim / 8) * 2;
     const int64_t blocks = (vecs + CT - 1) / CT;
-    append_kernel<<<dim3((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)c.seqs), CT, 0, s>>>(
-        c, static_cast<const char *>(K), static_cast<const char *>(V), token_stride, q_start, tokens, max_new);
-    return cudaGetLastError();
+    return launch_pdl(append_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)c.seqs), CT, 0, s, c,
+                      static_cast<const char *>(K), static_cast<const char *>(V), token_stride, q_start, tokens, max_new);
 }
 
 cudaError_t launch_cache_compact(const CacheView &c, const int32_t *q_start, const int32_t *keep, const int32_t *kept,
                                  int64_t tokens, int64_t max_new, cudaStream_t s) {
     const dim3 seqs((unsigned)c.seqs);
-    if (!keep) {
-        compact_table_kernel<<<seqs, CT, 0, s>>>(c, q_start, kept, tokens, max_new);
-        return cudaGetLastError();
+    if (keep) {
+        const cudaError_t e =
+            launch_pdl(compact_move_kernel, dim3((unsigned)(2 * c.kv_heads * c.layers), (unsigned)c.seqs), CT, 0, s, c,
+                       q_start, keep, kept, tokens, max_new);
+        if (e != cudaSuccess) return e;
     }
-    compact_move_kernel<<<dim3((unsigned)(2 * c.kv_heads * c.layers), (unsigned)c.seqs), CT, 0, s>>>(c, q_start, keep, kept,
-                                                                                              tokens, max_new);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_after(compact_table_kernel, seqs, CT, s, c, q_start, kept, tokens, max_new);
+    return launch_pdl(compact_table_kernel, seqs, CT, 0, s, c, q_start, kept, tokens, max_new);
 }
 
 cudaError_t launch_cache_fork(const CacheView &c, const int32_t *parents, const int32_t *children, int64_t n,
                               int32_t *missing, cudaStream_t s) {
-    fork_alloc_kernel<<<1, NT, 0, s>>>(c, parents, children, n, missing);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(fork_alloc_kernel, dim3(1), NT, 0, s, c, parents, children, n, missing);
     if (e != cudaSuccess) return e;
-    return launch_after(fork_copy_kernel, dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, s, c, parents,
-                        children, missing);
+    return launch_pdl(fork_copy_kernel, dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, 0, s, c, parents,
+                      children, missing);
 }
 
 cudaError_t launch_cache_free(const CacheView &c, const int32_t *list, int64_t n, int64_t window, int64_t sinks,
                               cudaStream_t s) {
-    free_kernel<<<(unsigned)n, CT, 0, s>>>(c, list, window, sinks);
-    return cudaGetLastError();
+    return launch_pdl(free_kernel, dim3((unsigned)n), CT, 0, s, c, list, window, sinks);
 }
 
 cudaError_t launch_cache_copy_pages(const CacheView &c, const int32_t *src, const int32_t *dst, int64_t n,
                                     cudaStream_t s) {
-    copy_pages_kernel<<<dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, 0, s>>>(c, src, dst);
-    return cudaGetLastError();
+    return launch_pdl(copy_pages_kernel, dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, 0, s, c, src, dst);
 }
 
 unsigned int cache_pages_take_device_error(cudaError_t *err) {

@@ -36,4 +36,21 @@ __device__ __forceinline__ RowRange rows_of(const int32_t *q_start, int seq, int
     return {(int)a, (int)(b - a)};
 }
 
+// Launches a kernel whose first step is pdl_wait(): it may become resident while the kernel before it in
+// the stream ends (that one's results are visible after the wait), which hides the launch itself.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3((unsigned)threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kern, args...);
+}
+
 }  // namespace mm

@@ -986,6 +986,8 @@ mm_status check_cache(const mm_cache *c, int64_t layer, bool needs_refs, mm::Cac
         if (counts[i] > 1 && strides[i] < c->head_dim)
             return fail(MM_ERR_INVALID_ARG, "a cache stride is below head_dim: rows overlap");
     }
+    if (c->max_pages * c->page_size > ((int64_t)1 << 30))
+        return fail(MM_ERR_INVALID_ARG, "a sequence holds at most 2^30 tokens (max_pages * page_size)");
     for (int r : c->reserved)
         if (r != 0) return fail(MM_ERR_INVALID_ARG, "reserved fields of the cache must be 0");
     if (layer < -1 || layer >= c->layers)
@@ -1058,8 +1060,10 @@ mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, i
         return fail(MM_ERR_INVALID_ARG, "O overlaps an input");
     a.Q = Q, a.O = O, a.q_start = q_start, a.mask = mask;
     a.q_stride = q_stride, a.o_stride = o_stride, a.tokens = tokens, a.max_q = max_q;
-    a.window = window > ((int64_t)1 << 40) ? 0 : window;
-    a.sinks = a.window ? sinks : 0;
+    // a window or sinks as long as any sequence can be cut nothing
+    const int64_t capacity = cache->max_pages * cache->page_size;
+    a.window = window >= capacity || sinks >= capacity ? 0 : (int)window;
+    a.sinks = a.window ? (int)sinks : 0;
     a.mask_words = mask_words;
     a.heads = (int)heads, a.group = (int)(heads / cache->kv_heads);
     a.scale = scale, a.ws = workspace;

@@ -289,8 +289,8 @@ struct CacheAttnArgs {
     void *O;
     const int32_t *q_start;
     const uint32_t *mask;  // null: causal
-    int64_t q_stride, o_stride, tokens, max_q, window, sinks, mask_words;
-    int heads, group;
+    int64_t q_stride, o_stride, tokens, max_q, mask_words;
+    int heads, group, window, sinks;  // window 0: none
     float scale;
     void *ws;
 };

@@ -19,8 +19,7 @@
 // Rows that the list cannot serve (top-k off or above kMaxListK, a list that overflows) select by a
 // radix descent on the weights: 512 bins by exponent and 4 leading bits, then linear bins inside the
 // chosen one, each level one pass over the row (from L2).
-#include "mm_common.cuh"
-#include "mm_internal.h"
+#include "cache_view.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -310,6 +309,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     extern __shared__ __align__(16) uint8_t raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     constexpr int N = Vec<T>::N, G = 8 / N;  // vectors per group of 8
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t row = blockIdx.x, n = a.vocab;
     const T *x = static_cast<const T *>(a.logits) + row * a.stride;
     Row r;
@@ -530,8 +531,7 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
     static const cudaError_t once =
         cudaFuncSetAttribute(sample_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (once != cudaSuccess) return once;
-    sample_kernel<T, NT><<<(unsigned)a.rows, NT, sizeof(Shared), s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(sample_kernel<T, NT>, dim3((unsigned)a.rows), NT, sizeof(Shared), s, a);
 }
 
 template <typename T>

@@ -575,7 +575,8 @@ typedef enum { MM_F16 = 0, MM_BF16 = 1, MM_F32 = 2 } mm_dtype;
  * table: [seqs][max_pages] page numbers; token t of sequence s lies in page
  *   table[s][t / page_size], row t % page_size.  -1: no page.
  * lens: [seqs] tokens each sequence holds for good.  New (or drafted) tokens follow them
- *   at lens[s] + i until mm_cache_compact makes them part of the sequence.
+ *   at lens[s] + i until mm_cache_compact makes them part of the sequence.  max_pages *
+ *   page_size is at most 2^30.
  * refs: [pages] sequences that hold each page, 0 = free; NULL where only append and
  *   attention are called.  A page is allocated by the calls below lowest number first.
  * page_size: 16, 32, 64 or 128; head_dim: a multiple of 8 up to 128; dtype: MM_F16 or
