@@ -10,12 +10,12 @@ int64_t cache_attention_workspace(const CacheView &c, int heads, int64_t tokens,
     (void)tokens;
     const int group = heads / c.kv_heads;
     if (max_q * group <= kRowsMax) return cache_attention_rows_workspace(c, cache_attention_rows_ctas(c, sms));
-    return cache_attention_tiles_workspace(c, group, max_q, cache_attention_tiles_splits(c, group, max_q, sms));
+    return cache_attention_tiles_workspace(c, group, max_q, cache_attention_tiles_ctas(c, group, max_q, sms));
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t s) {
     if (a.max_q * a.group <= kRowsMax) return launch_cache_attention_rows(a, cache_attention_rows_ctas(a.c, sms), s);
-    return launch_cache_attention_tiles(a, cache_attention_tiles_splits(a.c, a.group, a.max_q, sms), s);
+    return launch_cache_attention_tiles(a, cache_attention_tiles_ctas(a.c, a.group, a.max_q, sms), s);
 }
 
 unsigned int cache_attention_take_device_error(cudaError_t *err) {

@@ -193,9 +193,10 @@ int cache_attention_rows_ctas(const CacheView &c, int sms);
 int64_t cache_attention_rows_workspace(const CacheView &c, int ctas);
 cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s);
 unsigned int cache_attention_rows_take_device_error(cudaError_t *err);
-cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int splits, cudaStream_t s);
-int cache_attention_tiles_splits(const CacheView &c, int group, int64_t max_q, int sms);
-int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int splits);
+// CTAs of the tiles kernel, one per SM at most
+int cache_attention_tiles_ctas(const CacheView &c, int group, int64_t max_q, int sms);
+int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int ctas);
+cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaStream_t s);
 unsigned int cache_attention_tiles_take_device_error(cudaError_t *err);
 constexpr int kRowsMax = 16;  // rows (new tokens x heads of a kv head) of one sequence in the rows kernel
 

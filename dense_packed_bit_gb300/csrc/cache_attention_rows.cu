@@ -36,6 +36,7 @@ constexpr int WARPS = 4, NT = (WARPS + 1) * 32;  // four warps compute, the fift
 constexpr int SUB = 16, B = WARPS * SUB;         // keys of a warp's part of a block, of a block
 constexpr int MIN_BLOCKS = 3;    // blocks of a part, at least
 constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA
+constexpr int JOIN = 8;          // parts joined at a time
 constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU
 constexpr int HALF = B * 128;          // bytes of a block's 64 columns
 
@@ -104,7 +105,8 @@ __device__ __forceinline__ SeqKeys seq_keys(const CacheAttnArgs &a, int seq) {
     return k;
 }
 
-// Over the block's NT values: sums of a and b, inclusive in the reference, totals returned; the largest a
+// Over the block's NT values: sums of a and of b (0 or 1), inclusive in the reference, totals returned; the
+// largest a
 struct Two {
     int64_t a, b;
     int most;
@@ -112,11 +114,14 @@ struct Two {
 __device__ __forceinline__ Two scan(Two &v, Two *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     v.most = __reduce_max_sync(0xffffffffu, (int)v.a);
+    int n = (int)v.a;  // a sequence has at most 2^24 blocks: a warp's sum fits 32 bits
+    v.b = __popc(__ballot_sync(0xffffffffu, v.b != 0) & (0xffffffffu >> (31 - lane)));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, v.a, o), y = __shfl_up_sync(0xffffffffu, v.b, o);
-        if (lane >= o) v.a += x, v.b += y;
+        const int x = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += x;
     }
+    v.a = n;
     __syncthreads();
     if (lane == 31) sh[warp] = v;
     __syncthreads();
@@ -478,26 +483,26 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
         }
         if (!alone) {
             const int unit = seq * c.kv_heads + head;
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                __threadfence();  // the block's partial results before its ticket, the others' after it
                 sm_last = atomicAdd(p.tickets + unit, 1) == used - 1;
                 if (sm_last) p.tickets[unit] = 0;  // ready for the next call
+                __threadfence();
             }
             __syncthreads();
             if (sm_last) {
-                __threadfence();
                 const int64_t slot0 = (g0 * 2 + (part(g0) < u0)) * 16;
                 const int quads = D / 4;
                 for (int e = threadIdx.x; e < rows * quads; e += NT) {
                     const int r = e / quads, d = 4 * (e - r * quads);
                     float mt = -INFINITY, lt = 0.f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int y = 0; y < used; y += 4) {  // four parts' loads at a time
-                        float2 ml[4];
-                        float4 x[4];
+                    for (int y = 0; y < used; y += JOIN) {  // so many parts' loads at a time
+                        float2 ml[JOIN];
+                        float4 x[JOIN];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < JOIN; ++i) {
                             const int64_t sl = (y + i == 0 ? slot0 : (g0 + min(y + i, used - 1)) * 32) + r;
                             ml[i] = __ldcg(&p.ml[sl]);
                             x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * D + d));
@@ -505,13 +510,13 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
                         }
                         float now = mt;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) now = fmaxf(now, ml[i].x);
+                        for (int i = 0; i < JOIN; ++i) now = fmaxf(now, ml[i].x);
                         if (now == -INFINITY) continue;
                         const float f = ex2(mt - now);
                         mt = now;
                         lt *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < JOIN; ++i) {
                             const float w = ex2(ml[i].x - now);
                             if (ml[i].x == -INFINITY) continue;
                             lt += w * ml[i].y;
