@@ -135,6 +135,152 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Division by a number that is known at the launch: n / d = (n m) >> (31 + s) for 0 <= n < 2^31, with 2^s >= d
+// and m = ceil(2^(31 + s) / d) <= 2^32 - 1 (d = 1: m 0).
+struct FastDiv {
+    uint32_t m, s;
+    int d;
+    __device__ __forceinline__ int div(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> s) : n; }
+};
+inline FastDiv fast_div(int d) {
+    if (d <= 1) return {0, 0, 1};
+    uint32_t s = 0;
+    while ((1ll << s) < d) ++s;
+    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s - 1, d};
+}
+
+// ---------------------------------------------------------------- which CTA does what
+//
+// An item is what a kernel's units are grouped by (a sequence, or 256 rows of one); each item that has n > 0
+// blocks of keys has kv_heads units of n blocks.  The units are laid end to end in one of two measures and cut
+// at multiples of `chunk`:
+//   parts > 0: a unit measures `parts`, and its blocks are cut into as many parts (or whole: 1);
+//   parts = 0: a unit measures cost + n, its blocks last; the cost stands for what beginning and ending a unit
+//   takes, so that CTAs with many short units get fewer blocks.
+// With at least two CTAs to a unit every unit is cut into equal parts, one to a CTA; with more to do the second
+// measure, or whole units where all are short.
+struct Share {
+    int at, stop;     // this CTA's part
+    int item, first;  // the item that `at` lies in, and where it begins
+    int parts, cost, chunk;
+};
+
+struct ShareRules {
+    int min_blocks, whole_blocks, unit_cost;
+    int force_whole;  // the sums could pass 31 bits: whole units only
+};
+
+struct ShareScratch {
+    int a[32], b[32], most[32];
+    int item, first;
+};
+
+// One unit of a CTA, or one part of it
+struct UnitPart {
+    int head, u0, u1;    // its place in the measure
+    int b0, b1;          // its blocks here (b1 <= b0: none)
+    int used, g0;        // the parts it is joined of: in CTA g0 and those that follow
+    bool second;         // this part goes to the CTA's second slot (it begins a unit here that it does not finish)
+    bool first_second;   // the same for the unit's first part
+};
+
+// at: a place in the item that begins at `first` and has n blocks
+__device__ __forceinline__ UnitPart unit_part(const Share &s, int at, int first, int n, int min_blocks) {
+    UnitPart u;
+    const int size = s.parts ? s.parts : n + s.cost;
+    u.head = (int)((uint32_t)(at - first) / (uint32_t)size);
+    u.u0 = first + u.head * size, u.u1 = u.u0 + size;
+    if (s.parts) {
+        const int per = s.parts == 1 ? n : max((int)((uint32_t)(n + s.parts - 1) / (uint32_t)s.parts), min(n, min_blocks));
+        u.b0 = (at - u.u0) * per, u.b1 = min(n, u.b0 + per);
+        u.used = s.parts == 1 ? 1 : (int)((uint32_t)(n + per - 1) / (uint32_t)per);
+        u.g0 = u.u0;  // with more than one part, each CTA has one
+        u.second = u.first_second = false;
+    } else {
+        u.b0 = max(at - u.u0 - s.cost, 0), u.b1 = min(s.stop, u.u1) - u.u0 - s.cost;
+        u.g0 = (int)((uint32_t)(u.u0 + s.cost) / (uint32_t)s.chunk);
+        u.used = (int)((uint32_t)(u.u1 - 1) / (uint32_t)s.chunk) - u.g0 + 1;
+        u.second = u.b0 == 0 && (int)blockIdx.x * s.chunk < u.u0;
+        u.first_second = u.g0 * s.chunk < u.u0;
+    }
+    return u;
+}
+
+// Sums over the block's NT values: inclusive ones in a and b (b is 0 or 1), totals in ta, tb, the largest a in most
+template <int NT>
+__device__ __forceinline__ void share_scan(int &a, int &b, ShareScratch &sh, int &ta, int &tb, int &most) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int m = __reduce_max_sync(0xffffffffu, a);
+    b = __popc(__ballot_sync(0xffffffffu, b != 0) & (0xffffffffu >> (31 - lane)));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, a, o);
+        if (lane >= o) a += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh.a[warp] = a, sh.b[warp] = b, sh.most[warp] = m;
+    __syncthreads();
+    // the warps' sums, one to a lane
+    int wa = lane < NT / 32 ? sh.a[lane] : 0, wb = lane < NT / 32 ? sh.b[lane] : 0;
+    most = __reduce_max_sync(0xffffffffu, lane < NT / 32 ? sh.most[lane] : 0);
+    ta = __reduce_add_sync(0xffffffffu, wa), tb = __reduce_add_sync(0xffffffffu, wb);
+    a += __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
+    b += __reduce_add_sync(0xffffffffu, lane < warp ? wb : 0);
+}
+
+// blocks(i): the blocks of item i (0 past the last).  Every thread of the block calls it and gets the same
+// Share; false: nothing to do here.
+template <int NT, typename Blocks>
+__device__ __forceinline__ bool share_of(int items, int kv_heads, const ShareRules &rules, const Blocks &blocks,
+                                         ShareScratch &sh, Share &s) {
+    int total = 0, count = 0, most = 0, mine = 0, a = 0, b = 0;
+    for (int i0 = 0; i0 < items; i0 += NT) {
+        mine = a = blocks(i0 + threadIdx.x);
+        b = mine > 0;
+        int ta, tb, m;
+        share_scan<NT>(a, b, sh, ta, tb, m);
+        total += ta, count += tb, most = max(most, m);
+    }
+    const int units = count * kv_heads, grid = (int)gridDim.x;
+    if (units == 0) return false;
+    s.parts = s.cost = 0;
+    if (rules.force_whole)
+        s.parts = 1;
+    else if (2 * (int64_t)units <= grid)
+        s.parts = min((int)((uint32_t)grid / (uint32_t)units), (most + rules.min_blocks - 1) / rules.min_blocks);
+    else if (most <= rules.whole_blocks)
+        s.parts = 1;
+    // the cost is no more than half of what a CTA gets
+    if (!s.parts) s.cost = min((int)((uint32_t)(total * kv_heads) / (uint32_t)(2 * grid)), rules.unit_cost);
+    const int all = s.parts ? units * s.parts : (total + s.cost * count) * kv_heads;
+    s.chunk = (int)((uint32_t)(all + grid - 1) / (uint32_t)grid);
+    if (!s.parts) s.chunk = max(s.chunk, rules.min_blocks);
+    s.at = (int)blockIdx.x * s.chunk;  // < 2^31: about all
+    if (s.at >= all) return false;
+    s.stop = min(s.at + s.chunk, all);
+    int before = 0;
+    for (int i0 = 0; i0 < items; i0 += NT) {
+        if (items > NT) {  // else the sums are still in registers
+            mine = a = blocks(i0 + threadIdx.x);
+            b = mine > 0;
+            int ta, tb, m;
+            share_scan<NT>(a, b, sh, ta, tb, m);
+            const int here = s.parts ? tb * s.parts : ta + s.cost * tb;
+            if (s.at >= (before + here) * kv_heads) {  // the same for all threads
+                before += here;
+                continue;
+            }
+        }
+        const int w = s.parts ? s.parts : mine + s.cost;
+        const int first = (before + (s.parts ? b * s.parts : a + s.cost * b) - w) * kv_heads;
+        if (mine > 0 && s.at >= first && s.at < first + w * kv_heads) sh.item = i0 + threadIdx.x, sh.first = first;
+        break;
+    }
+    __syncthreads();
+    s.item = sh.item, s.first = sh.first;
+    return true;
+}
+
 // One row by the definition, key by key, a warp to it: O[4 lane + x] in o (unnormalised over l > 0).
 // For what the tiles cannot do (infinities and NaN among values that only some rows see).
 template <typename T>

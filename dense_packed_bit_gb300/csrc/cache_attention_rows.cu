@@ -14,12 +14,9 @@
 // mma.sync.m16n8k16 (K rows read by ldmatrix are B as they lie, V rows by ldmatrix.trans); the probabilities
 // go from accumulator registers to A registers without shared memory.
 //
-// Split.  Two CTAs per SM.  With at least two of them to a unit (sequence, kv head), every unit is cut into
-// the same number of parts, one to a CTA.  With more to do, the blocks of all units are laid end to end and cut
-// evenly over the CTAs, so that ragged lengths cost no more than their sum; where all units are short the CTAs
-// take whole ones.  Every CTA finds its part from the lengths itself.  A unit that several CTAs share is joined by
-// the last of them to finish, in the order of its parts (a ticket per unit, reset by the last), so the result
-// does not depend on which one is last.
+// Split.  Two CTAs per SM, each with an even share of all units' blocks (share_of); ragged lengths cost no more
+// than their sum.  A unit that several CTAs share is joined by the last of them to finish, in the order of its
+// parts (a ticket per unit, reset by the last), so the result does not depend on which one is last.
 //
 // What a row does not see: its score is replaced, not added to.  In blocks that the mask cuts,
 // infinities and NaN in V are taken out of the product (0 x NaN) and added to the rows that do see them.
@@ -43,6 +40,7 @@ constexpr int HALF = B * 128;          // bytes of a block's 64 columns
 struct RowsArgs {
     CacheAttnArgs a;
     int box;           // keys of one TMA box
+    int force_whole;
     int32_t *tickets;  // [seqs][kv_heads]
     float2 *ml;        // [CTAs][2][16]
     float *part;       // [CTAs][2][16][head_dim]
@@ -105,35 +103,6 @@ __device__ __forceinline__ SeqKeys seq_keys(const CacheAttnArgs &a, int seq) {
     return k;
 }
 
-// Over the block's NT values: sums of a and of b (0 or 1), inclusive in the reference, totals returned; the
-// largest a
-struct Two {
-    int64_t a, b;
-    int most;
-};
-__device__ __forceinline__ Two scan(Two &v, Two *sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v.most = __reduce_max_sync(0xffffffffu, (int)v.a);
-    int n = (int)v.a;  // a sequence has at most 2^24 blocks: a warp's sum fits 32 bits
-    v.b = __popc(__ballot_sync(0xffffffffu, v.b != 0) & (0xffffffffu >> (31 - lane)));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += x;
-    }
-    v.a = n;
-    __syncthreads();
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    Two all = {0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) v.a += sh[w].a, v.b += sh[w].b;
-        all.a += sh[w].a, all.b += sh[w].b, all.most = max(all.most, sh[w].most);
-    }
-    return all;
-}
-
 // KS: 16-element steps of the head dimension held (head_dim <= 16 KS, the rest zero)
 template <typename T, int KS>
 __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -144,10 +113,8 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
     __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ float2 sm_ml[WARPS][16];
     __shared__ float sm_p[WARPS][16][SUB];  // probabilities of a block whose V holds an infinity or NaN
-    __shared__ Two sm_scan[NT / 32];
-    __shared__ int64_t sm_start;
-    __shared__ SeqKeys sm_k;
-    __shared__ int sm_seq, sm_last;
+    __shared__ ShareScratch sm_share;
+    __shared__ int sm_last;
     uint8_t *sm = smem_aligned<1024>(raw);
     const CacheAttnArgs &a = p.a;
     const CacheView &c = a.c;
@@ -161,59 +128,12 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
     pdl_launch_dependents();
     pdl_wait();
 
-    // This CTA's part [at, stop) of the call, in one of two measures laid end to end over the units that have
-    // blocks.  A unit measures `parts` (its blocks cut into as many, or whole: parts = 1), or, where parts is 0,
-    // cost + n for its n blocks (the blocks last); the cost is up to UNIT_COST, but no more than half of what a CTA gets.
-    SeqKeys k;
-    const auto blocks = [&](int s) {
-        if (s >= c.seqs) return Two{0, 0, 0};
-        k = seq_keys(a, s);
-        return Two{k.kb.count, k.kb.count > 0, 0};
-    };
-    Two mine, sum, total = {0, 0, 0};
-    for (int s0 = 0; s0 < c.seqs; s0 += NT) {
-        mine = sum = blocks(s0 + threadIdx.x);
-        const Two t = scan(sum, sm_scan);
-        total.a += t.a, total.b += t.b, total.most = max(total.most, t.most);
-    }
-    const int64_t units = total.b * c.kv_heads;
-    if (units == 0) return;
-    int parts = 0;
-    if (2 * units <= gridDim.x)
-        parts = min((int)(gridDim.x / (uint32_t)units), (total.most + MIN_BLOCKS - 1) / MIN_BLOCKS);
-    else if (total.most <= WHOLE_BLOCKS)
-        parts = 1;
-    const int cost = parts ? 0 : (int)min(total.a * c.kv_heads / gridDim.x / 2, (int64_t)UNIT_COST);
-    const auto weight = [&](const Two &t) { return parts ? t.b * parts : t.a + cost * t.b; };
-    const int64_t all = weight(total) * c.kv_heads;
-    const int64_t ctas = min((int64_t)gridDim.x, parts ? all : (all + MIN_BLOCKS - 1) / MIN_BLOCKS);
-    if (blockIdx.x >= ctas) return;
-    const auto part = [&](int64_t cta) {  // cta * all / ctas
-        const int64_t x = cta * all;
-        return x >> 32 ? x / ctas : (int64_t)((uint32_t)x / (uint32_t)ctas);
-    };
-    int64_t at = part(blockIdx.x);
-    const int64_t stop = part(blockIdx.x + 1);
-    {
-        int64_t before = 0;
-        for (int s0 = 0; s0 < c.seqs; s0 += NT) {
-            if (c.seqs > NT) {  // else the sums are still in registers
-                mine = sum = blocks(s0 + threadIdx.x);
-                const int64_t here = weight(scan(sum, sm_scan));
-                if (at >= (before + here) * c.kv_heads) {  // the same for all threads
-                    before += here;
-                    continue;
-                }
-            }
-            const int64_t w = weight(mine), first = (before + weight(sum) - w) * c.kv_heads;
-            if (w > 0 && at >= first && at < first + w * c.kv_heads) sm_seq = s0 + threadIdx.x, sm_start = first, sm_k = k;
-            break;
-        }
-        __syncthreads();
-    }
-    int seq = sm_seq;
-    int64_t seq_first = sm_start;  // where the sequence begins
-    k = sm_k;
+    Share share;
+    const auto blocks = [&](int s) { return s < c.seqs ? seq_keys(a, s).kb.count : 0; };
+    const ShareRules rules = {MIN_BLOCKS, WHOLE_BLOCKS, UNIT_COST, p.force_whole};
+    if (!share_of<NT>(c.seqs, c.kv_heads, rules, blocks, sm_share, share)) return;
+    int at = share.at, seq = share.item, seq_first = share.first;
+    SeqKeys k = seq_keys(a, seq);
 
     const uint32_t ring_s = smem_u32(sm);
     const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);  // > 0: a masked score stays -infinity
@@ -222,25 +142,10 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
     uint32_t it = 0;  // blocks that have passed through the ring
     bool ok = true;
 
-    while (at < stop) {
+    while (at < share.stop) {
         const int n = k.kb.count;
-        const int64_t size = parts ? parts : n + cost;  // of a unit of this sequence
-        const int head = (int)(((at - seq_first) | size) >> 32 ? (at - seq_first) / size
-                                                                : (uint32_t)(at - seq_first) / (uint32_t)size);
-        const int64_t u0 = seq_first + head * size, u1 = u0 + size;
-        // its blocks here [b0, b1), and the parts the unit is joined of: in CTA g0 and the next
-        int b0, b1, used;
-        int64_t g0;
-        if (parts) {
-            const int per = max((n + parts - 1) / parts, min(n, MIN_BLOCKS));
-            b0 = (int)(at - u0) * per, b1 = min(n, b0 + per);
-            used = (n + per - 1) / per;
-            g0 = u0;  // with more than one part, each CTA has one
-        } else {
-            b0 = max((int)(at - u0) - cost, 0), b1 = (int)(min(stop, u1) - u0) - cost;
-            g0 = ((u0 + cost + 1) * ctas - 1) / all;
-            used = (int)((u1 * ctas - 1) / all - g0) + 1;
-        }
+        const UnitPart u = unit_part(share, at, seq_first, n, MIN_BLOCKS);
+        const int head = u.head, b0 = u.b0, b1 = u.b1;
         if (b1 <= b0) break;  // nothing of the unit but its cost, or a part that a short unit does not have
         const SeqView sv = k.v;
         const int rows = sv.count * a.group;
@@ -448,8 +353,7 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
         __syncthreads();
 
         const bool alone = b0 == 0 && b1 == n;
-        // a part's slot: 0 for the CTA's first unit, 1 for one that it begins later and does not finish
-        const int64_t slot = ((int64_t)blockIdx.x * 2 + (b0 == 0 && part(blockIdx.x) < u0)) * 16;
+        const int64_t slot = ((int64_t)blockIdx.x * 2 + u.second) * 16;
         const auto out_at = [&](int r, int d) {
             const int i = r / a.group;
             return reinterpret_cast<uint32_t *>(
@@ -486,13 +390,14 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
             __syncthreads();
             if (threadIdx.x == 0) {
                 __threadfence();  // the block's partial results before its ticket, the others' after it
-                sm_last = atomicAdd(p.tickets + unit, 1) == used - 1;
+                sm_last = atomicAdd(p.tickets + unit, 1) == u.used - 1;
                 if (sm_last) p.tickets[unit] = 0;  // ready for the next call
                 __threadfence();
             }
             __syncthreads();
             if (sm_last) {
-                const int64_t slot0 = (g0 * 2 + (part(g0) < u0)) * 16;
+                const int used = u.used;
+                const int64_t slot0 = ((int64_t)u.g0 * 2 + u.first_second) * 16;
                 const int quads = D / 4;
                 for (int e = threadIdx.x; e < rows * quads; e += NT) {
                     const int r = e / quads, d = 4 * (e - r * quads);
@@ -503,7 +408,7 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
                         float4 x[JOIN];
 #pragma unroll
                         for (int i = 0; i < JOIN; ++i) {
-                            const int64_t sl = (y + i == 0 ? slot0 : (g0 + min(y + i, used - 1)) * 32) + r;
+                            const int64_t sl = (y + i == 0 ? slot0 : (int64_t)(u.g0 + min(y + i, used - 1)) * 32) + r;
                             ml[i] = __ldcg(&p.ml[sl]);
                             x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * D + d));
                             if (y + i >= used) ml[i].x = -INFINITY;
@@ -529,9 +434,9 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
                 }
             }
         }
-        at = parts ? at + 1 : min(stop, u1);
-        if (at >= stop) break;
-        if (at == seq_first + size * c.kv_heads) {  // on to the next sequence that has rows
+        at = share.parts ? at + 1 : min(share.stop, u.u1);
+        if (at >= share.stop) break;
+        if (at >= seq_first + (share.parts ? share.parts : n + share.cost) * c.kv_heads) {  // the next sequence that has rows
             seq_first = at;
             do k = seq_keys(a, ++seq);
             while (k.kb.count == 0);
@@ -576,7 +481,8 @@ int64_t cache_attention_rows_workspace(const CacheView &c, int ctas) {
 
 cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
     char *w = static_cast<char *>(a.ws);
-    RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, nullptr, nullptr, nullptr};
+    const int64_t most = (int64_t)a.c.seqs * a.c.kv_heads * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
+    RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), nullptr, nullptr, nullptr};
     p.tickets = reinterpret_cast<int32_t *>(w);
     w += round256((int64_t)a.c.seqs * a.c.kv_heads * 4);
     p.part = reinterpret_cast<float *>(w);

@@ -16,14 +16,14 @@
 // own).  O += P V takes P from TMEM as A and V from shared memory as an MN-major B (V rows lie as the
 // cache has them; nothing is transposed).
 //
-// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 the softmax of stream 0 and 1, warp 8 issues
-// the MMAs, warp 9 the TMA loads (one box per page and 64 columns; a page past the end reads as zeros), warps 10
-// and 11 look after V where the mask cuts.  The MMA order PV(i),
-// QK(i + 1) per stream lets the tensor core work on one stream while the other is in its softmax.
+// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 the softmax of stream 0 and 1, warp 8 issues the MMAs,
+// warp 9 the TMA loads (one box per page and 64 columns; a page past the end reads as zeros), warps 10 and 11 look
+// after V where the mask cuts.  The MMA order PV(i), QK(i + 1) per stream, streams in turn, lets the tensor core
+// work on one stream while the other is in its softmax.  (One issuing warp per stream was 9% slower: the streams'
+// products then share the tensor core instead of taking turns, and their softmaxes coincide.)
 //
-// Split.  One CTA per SM.  As in the rows kernel the blocks of all units are laid end to end and cut evenly
-// over the CTAs (or every unit into equal parts, when there are few); a CTA walks its units with the ring of K and
-// V blocks running through, and the last CTA of a shared unit to finish joins the partial results in order.
+// Split.  One CTA per SM, each with an even share of all units' blocks (share_of), the ring of K and V blocks
+// running through its units; the last CTA of a shared unit to finish joins the partial results in order.
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
 // memory (0 x NaN), and where the mask cuts between rows V is looked through: if it holds an infinity or NaN,
@@ -58,6 +58,8 @@ struct TilesArgs {
     CacheAttnArgs a;
     int tiles;  // 256-row units of a (sequence, kv head), at most
     int box;    // keys of one TMA box
+    int force_whole;
+    FastDiv by_group, by_tiles;
     int32_t *tickets, *poison;  // [seqs][tiles][kv_heads]
     float2 *ml;                 // [CTAs][2][256]
     float4 *part;               // [CTAs][2][head_dim / 4][256]
@@ -141,16 +143,17 @@ struct UnitKeys {
         return key0 + B > whole || (key0 < high && key0 + B > sinks);
     }
 };
-__device__ __forceinline__ UnitKeys unit_keys(const CacheAttnArgs &a, int item, int tiles) {
+__device__ __forceinline__ UnitKeys unit_keys(const TilesArgs &p, int item) {
     UnitKeys k;
-    const int seq = item / tiles;
+    const CacheAttnArgs &a = p.a;
+    const int seq = p.by_tiles.div(item);
     k.v = seq_view(a, seq, &g_tiles_err);
-    k.row0 = (item - seq * tiles) * ROWS;
+    k.row0 = (item - seq * p.tiles) * ROWS;
     k.rows = min(k.v.count * a.group - k.row0, ROWS);
     k.kb = {0, 0, 0};
     k.end = k.whole = k.low = k.high = 0;
     if (k.rows <= 0) return k;
-    const int i0 = k.row0 / a.group, i1 = (k.row0 + k.rows - 1) / a.group, len = k.v.len;
+    const int i0 = p.by_group.div(k.row0), i1 = p.by_group.div(k.row0 + k.rows - 1), len = k.v.len;
     if (a.mask) {  // a row's depth is between 0 and count drafted tokens
         k.end = len + k.v.count, k.whole = len;
         if (a.window) k.low = len - a.window, k.high = len + k.v.count - a.window;
@@ -162,88 +165,31 @@ __device__ __forceinline__ UnitKeys unit_keys(const CacheAttnArgs &a, int item, 
     return k;
 }
 
-// Over the block's NT values: sums of a and of b (0 or 1), inclusive in the reference, totals returned; the
-// largest a
-struct Two {
-    int64_t a, b;
-    int most;
-};
-__device__ __forceinline__ Two scan(Two &v, Two *sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v.most = __reduce_max_sync(0xffffffffu, (int)v.a);
-    int n = (int)v.a;  // a unit has at most 2^23 blocks: a warp's sum fits 32 bits
-    v.b = __popc(__ballot_sync(0xffffffffu, v.b != 0) & (0xffffffffu >> (31 - lane)));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += x;
-    }
-    v.a = n;
-    __syncthreads();
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    Two all = {0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) v.a += sh[w].a, v.b += sh[w].b;
-        all.a += sh[w].a, all.b += sh[w].b, all.most = max(all.most, sh[w].most);
-    }
-    return all;
-}
-
-// The units of one CTA, in order; every thread walks them by itself.  Units are measured and cut as in the rows
-// kernel: `parts` each, or cost + blocks where parts is 0.
+// The units of one CTA, in order; every role walks them by itself.
 struct Walk {
-    int64_t at, stop, all, ctas, item_first;
-    int item, parts, cost;
+    Share share;
+    int at, item, first;  // where the walk is, the item there and its beginning
     UnitKeys k;
     // the unit at hand: its head, the first of its blocks here and how many, the parts it is joined of
-    int head, b0, n, used;
-    int64_t g0;
-    bool alone, second;  // the whole unit; this CTA's partial result goes to its second slot
+    int head, b0, n, used, g0;
+    bool alone, second, first_second;
 
-    __device__ __forceinline__ int64_t part(int64_t cta) const {
-        const int64_t x = cta * all;
-        return x >> 32 ? x / ctas : (int64_t)((uint32_t)x / (uint32_t)ctas);
-    }
-    // false: no more
-    __device__ __forceinline__ bool here(int kv_heads, int tiles, const CacheAttnArgs &a) {
-        if (at >= stop) return false;
-        const int m = k.kb.count;
-        int64_t size = parts ? parts : m + cost;
-        if (at >= item_first + size * kv_heads) {
-            item_first += size * kv_heads;
-            do k = unit_keys(a, ++item, tiles);
+    __device__ __forceinline__ bool here(const TilesArgs &p) {  // false: no more
+        if (at >= share.stop) return false;
+        const int kv_heads = p.a.c.kv_heads;
+        const int size = share.parts ? share.parts : k.kb.count + share.cost;
+        if (at >= first + size * kv_heads) {
+            first += size * kv_heads;
+            do k = unit_keys(p, ++item);
             while (k.kb.count == 0);
-            return here2(kv_heads);
         }
-        return here2(kv_heads);
+        const UnitPart u = unit_part(share, at, first, k.kb.count, MIN_BLOCKS);
+        head = u.head, b0 = u.b0, n = u.b1 - u.b0, used = u.used, g0 = u.g0;
+        alone = u.b0 == 0 && u.b1 == k.kb.count;
+        second = u.second, first_second = u.first_second;
+        at = share.parts ? at + 1 : min(share.stop, u.u1);
+        return n > 0;  // else nothing of the unit but its cost, or a part that a short unit does not have
     }
-    __device__ __forceinline__ bool here2(int kv_heads) {
-        const int m = k.kb.count;
-        const int64_t size = parts ? parts : m + cost, off = at - item_first;
-        head = (int)((off | size) >> 32 ? off / size : (uint32_t)off / (uint32_t)size);
-        const int64_t u0 = item_first + head * size, u1 = u0 + size;
-        int b1;
-        if (parts) {
-            const int per = max((m + parts - 1) / parts, min(m, MIN_BLOCKS));
-            b0 = (int)(at - u0) * per, b1 = min(m, b0 + per);
-            used = (m + per - 1) / per;
-            g0 = u0;
-            at += 1;
-        } else {
-            b0 = max((int)(at - u0) - cost, 0), b1 = (int)(min(stop, u1) - u0) - cost;
-            g0 = ((u0 + cost + 1) * ctas - 1) / all;
-            used = (int)((u1 * ctas - 1) / all - g0) + 1;
-            at = min(stop, u1);
-        }
-        n = b1 - b0;
-        alone = b0 == 0 && b1 == m;
-        second = b0 == 0 && part(blockIdx.x) < u0;
-        first_second = part(g0) < u0;
-        return n > 0;  // else: nothing of the unit but its cost, or a part that a short unit does not have
-    }
-    bool first_second;  // the same for the unit's first part, in CTA g0
 };
 
 template <typename T, int HALVES>
@@ -252,16 +198,14 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     using P = Plan<HALVES>;
     constexpr int ST = P::STAGES;
     extern __shared__ uint8_t raw[];
-    __shared__ Two sm_scan[NT / 32];
-    __shared__ UnitKeys sm_k;
+    __shared__ ShareScratch sm_share;
     __shared__ Walk sm_walk;  // of the softmax warps, which have no registers for it
-    __shared__ int64_t sm_start;
-    __shared__ int sm_item, sm_last, sm_more;
+    __shared__ int sm_last, sm_more;
     uint8_t *sm = smem_aligned<1024>(raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + P::BARS);
     uint64_t *full = bars, *empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_done = s_full + 4,
-             *drain = s_full + 6, *fix = s_full + 7, *fixed = s_full + 8, *q_full = s_full + 9;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
+             *drain = s_full + 6, *fix = s_full + 8, *fixed = s_full + 10, *q_full = s_full + 12;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 13);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *poison = reinterpret_cast<volatile int *>(tmem_slot + 2);
 
@@ -287,65 +231,30 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     Walk w;
     {
         const int items = c.seqs * p.tiles;
-        const auto blocks = [&](int i) {
-            if (i >= items) return Two{0, 0, 0};
-            w.k = unit_keys(a, i, p.tiles);
-            return Two{w.k.kb.count, w.k.kb.count > 0, 0};
-        };
-        Two mine, sum, total = {0, 0, 0};
-        for (int i0 = 0; i0 < items; i0 += NT) {
-            mine = sum = blocks(i0 + tid);
-            const Two t = scan(sum, sm_scan);
-            total.a += t.a, total.b += t.b, total.most = max(total.most, t.most);
-        }
-        const int64_t units = total.b * c.kv_heads;
-        if (units == 0) return;
-        w.parts = 0;
-        if (2 * units <= gridDim.x)
-            w.parts = min((int)(gridDim.x / (uint32_t)units), (total.most + MIN_BLOCKS - 1) / MIN_BLOCKS);
-        else if (total.most <= WHOLE_BLOCKS)
-            w.parts = 1;
-        w.cost = w.parts ? 0 : (int)min(total.a * c.kv_heads / gridDim.x / 2, (int64_t)UNIT_COST);
-        const auto weight = [&](const Two &t) { return w.parts ? t.b * w.parts : t.a + w.cost * t.b; };
-        w.all = weight(total) * c.kv_heads;
-        w.ctas = min((int64_t)gridDim.x, w.parts ? w.all : (w.all + MIN_BLOCKS - 1) / MIN_BLOCKS);
-        if (blockIdx.x >= w.ctas) return;
-        w.at = w.part(blockIdx.x);
-        w.stop = w.part(blockIdx.x + 1);
-        int64_t before = 0;
-        for (int i0 = 0; i0 < items; i0 += NT) {
-            if (items > NT) {  // else the sums are still in registers
-                mine = sum = blocks(i0 + tid);
-                const int64_t here = weight(scan(sum, sm_scan));
-                if (w.at >= (before + here) * c.kv_heads) {  // the same for all threads
-                    before += here;
-                    continue;
-                }
-            }
-            const int64_t m = weight(mine), first = (before + weight(sum) - m) * c.kv_heads;
-            if (m > 0 && w.at >= first && w.at < first + m * c.kv_heads) sm_item = i0 + tid, sm_start = first, sm_k = w.k;
-            break;
-        }
+        const auto blocks = [&](int i) { return i < items ? unit_keys(p, i).kb.count : 0; };
+        const ShareRules rules = {MIN_BLOCKS, WHOLE_BLOCKS, UNIT_COST, p.force_whole};
+        if (!share_of<NT>(items, c.kv_heads, rules, blocks, sm_share, w.share)) return;
+        w.at = w.share.at, w.item = w.share.item, w.first = w.share.first;
+        w.k = unit_keys(p, w.item);
     }
     __syncwarp();
     if (warp == 8) tmem_alloc(tmem_slot, 512);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    w.item = sm_item, w.item_first = sm_start, w.k = sm_k;
     if (tid == 0) sm_walk = w;
     __syncthreads();
     const uint32_t tmem = *tmem_slot;
     const int steps = (c.head_dim + 15) / 16;  // 16-element steps of the head dimension
     const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
-        if (!*fail && mbar_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity) || (!*fail && mbar_wait(bar, parity))) return true;
         if (!*fail) atomicExch(&g_tiles_err, code);
         *fail = 1;
         return false;
     };
-    // a unit's loads in the order of their use: K 0, then K i + 1 and V i; x counts them over the CTA's units
-    const auto slot_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
-    const auto slot_v = [](int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+    // A unit's loads in the order of their use: K 0, V 0, K 1, ...; where the streams take turns K 0, then K i + 1
+    // and V i.  The slots of the ring count on over the CTA's units.
+    const auto slot_v = [](int i, int n, bool single) { return !single ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
     if (warp < 8) {
         const int s = warp >> 2, t = tid & 127;                 // stream, row of its tile
@@ -359,7 +268,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
         while (true) {
             if (tid == 0) {
                 Walk next = sm_walk;
-                sm_more = !*fail && next.here(c.kv_heads, p.tiles, a);
+                sm_more = !*fail && next.here(p);
                 sm_walk = next;
             }
             __syncwarp();
@@ -373,26 +282,27 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             const bool single = nrows <= 128;
             // Q into shared memory (both streams share a tile where one holds all rows), zeros past its rows and columns
             if (!single || s == 0) {
-                constexpr int PER = HALVES * 8, ROUNDS = 128 * PER / 128;
-#pragma unroll
-                for (int j0 = 0; j0 < ROUNDS; j0 += 8) {
+                constexpr int PER = HALVES * 8;  // 16-byte vectors of a row: this thread's is the same in all its rows
+                const int x = t % PER, r1 = t / PER;
+                const char *Q = static_cast<const char *>(a.Q) + ((int64_t)sv.first * a.q_stride + (int64_t)head * a.group * D + x * 8) * 2;
+                uint8_t *to_sm = sm + s * P::TILE + (x >> 3) * HALF;
+#pragma unroll 1
+                for (int j0 = 0; j0 < PER; j0 += 8) {
                     uint4 v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int e = t + (j0 + j) * 128, r = s * 128 + e / PER, x = e % PER;
+                        const int r = s * 128 + r1 + (j0 + j) * (128 / PER);
                         v[j] = make_uint4(0, 0, 0, 0);
                         if (r < nrows && x * 8 < D) {
-                            const int i = (row0 + r) / a.group, h = row0 + r - i * a.group;
-                            v[j] = __ldg(reinterpret_cast<const uint4 *>(
-                                static_cast<const char *>(a.Q) +
-                                ((int64_t)(sv.first + i) * a.q_stride + (int64_t)(head * a.group + h) * D + x * 8) * 2));
+                            const int i = p.by_group.div(row0 + r), h = row0 + r - i * a.group;
+                            v[j] = __ldg(reinterpret_cast<const uint4 *>(Q + ((int64_t)i * a.q_stride + h * D) * 2));
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int e = t + (j0 + j) * 128, r = e / PER, x = e % PER;
+                        const int r = r1 + (j0 + j) * (128 / PER);
                         v[j].x ^= flip, v[j].y ^= flip, v[j].z ^= flip, v[j].w ^= flip;
-                        *reinterpret_cast<uint4 *>(sm + s * P::TILE + (x >> 3) * HALF + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = v[j];
+                        *reinterpret_cast<uint4 *>(to_sm + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = v[j];
                     }
                 }
                 fence_proxy_async_smem();
@@ -401,7 +311,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             if (lane == 0) mbar_arrive(q_full);
 
             const int r = single ? t : s * 128 + t;  // row of the unit's 256
-            const int rc = min(r, nrows - 1), i = (row0 + rc) / a.group;
+            const int rc = min(r, nrows - 1), i = p.by_group.div(row0 + rc);
             const RowView rv = row_view(a, sv.len, sv.first, sv.count, i);
             float m = -INFINITY, l = 0.f;
             int done = 0;
@@ -552,7 +462,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     const int per = single ? 2 : 1, sources = per * u.used;
                     const auto slot_of = [&](int y) {  // source y: slot * 256 + its rows' first
                         const int g = y / per;
-                        return ((u.g0 + g) * 2 + (g == 0 && u.first_second)) * ROWS;
+                        return (int64_t)((u.g0 + g) * 2 + (g == 0 && u.first_second)) * ROWS;
                     };
                     const int64_t half = tid & 255;
                     if (half < nrows) {
@@ -565,27 +475,37 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                             mt = now;
                         }
                         const float inv = lt > 0.f ? 1.f / lt : 0.f;
-                        const int ri = (row0 + (int)half) / a.group, rh = row0 + (int)half - ri * a.group;
+                        const int ri = p.by_group.div(row0 + (int)half), rh = row0 + (int)half - ri * a.group;
                         uint4 *out = reinterpret_cast<uint4 *>(static_cast<char *>(a.O) +
                                                                ((int64_t)(sv.first + ri) * a.o_stride + (int64_t)(head * a.group + rh) * D) * 2);
-                        for (int x = 0; x < D / 8; x += 2) {  // 16 columns at a time, so that many loads are in flight
-                            float o[16] = {};
-#pragma unroll 2
-                            for (int y = 0; y < sources; ++y) {
-                                const int64_t at = slot_of(y);
-                                const int64_t row = (single ? (y & 1) * 128 : 0) + half;
-                                const float2 q = __ldcg(p.ml + at + row);
-                                const float f = q.x > -INFINITY ? ex2(q.x - mt) * inv : 0.f;
-                                const float4 *src = p.part + at * (D / 4) + (int64_t)(2 * x) * ROWS + row;
+#pragma unroll 1
+                        for (int x = 0; x < D / 8; x += 4) {  // 32 columns at a time, so that many loads are in flight
+                            float o[32] = {};
+#pragma unroll 1
+                            for (int y = 0; y < sources; y += 2) {
+                                float f[2];
+                                float4 g[2][8];
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    if (2 * x + z < D / 4) {
-                                        const float4 g = __ldcg(src + z * ROWS);
-                                        o[4 * z] += f * g.x, o[4 * z + 1] += f * g.y, o[4 * z + 2] += f * g.z, o[4 * z + 3] += f * g.w;
+                                for (int k = 0; k < 2; ++k) {
+                                    const int yk = min(y + k, sources - 1);
+                                    const int64_t at = slot_of(yk), row = (single ? (yk & 1) * 128 : 0) + half;
+                                    const float2 q = __ldcg(p.ml + at + row);
+                                    f[k] = q.x > -INFINITY && y + k < sources ? ex2(q.x - mt) * inv : 0.f;
+                                    const float4 *src = p.part + at * (D / 4) + (int64_t)(2 * x) * ROWS + row;
+#pragma unroll
+                                    for (int z = 0; z < 8; ++z)
+                                        g[k][z] = 2 * x + z < D / 4 ? __ldcg(src + z * ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                    for (int z = 0; z < 8; ++z) {
+                                        o[4 * z] += f[k] * g[k][z].x, o[4 * z + 1] += f[k] * g[k][z].y;
+                                        o[4 * z + 2] += f[k] * g[k][z].z, o[4 * z + 3] += f[k] * g[k][z].w;
                                     }
                             }
 #pragma unroll
-                            for (int z = 0; z < 2; ++z)
+                            for (int z = 0; z < 4; ++z)
                                 if (x + z < D / 8)
                                     out[x + z] = make_uint4(Pair<T>::pack(o[8 * z], o[8 * z + 1]), Pair<T>::pack(o[8 * z + 2], o[8 * z + 3]),
                                                             Pair<T>::pack(o[8 * z + 4], o[8 * z + 5]), Pair<T>::pack(o[8 * z + 6], o[8 * z + 7]));
@@ -644,8 +564,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             }
             if (again && ok)
                 for (int q = warp; q < nrows; q += 8) {
-                    const int qi = (row0 + q) / a.group;
-                    attend_row<T>(a, u.item / p.tiles, sv, qi, head * a.group + row0 + q - qi * a.group, &g_tiles_err);
+                    const int qi = p.by_group.div(row0 + q);
+                    attend_row<T>(a, p.by_tiles.div(u.item), sv, qi, head * a.group + row0 + q - qi * a.group, &g_tiles_err);
                 }
             __syncwarp();
             bar_sync(1, 256);  // the walk may go on
@@ -661,18 +581,14 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 // descriptors differ in their address alone (bytes / 16 in the low bits)
                 const uint64_t dk = sdesc_kmajor_sw128(0), dv = sdesc_make(0, HALF, 1024, kSdescSw128);
                 const uint32_t base = (smem_u32(sm) & 0x3FFFFu) >> 4, ring = base + P::RING / 16;
-                uint32_t x0 = 0, looked = 0, units = 0, task[2] = {0, 0};
+                uint32_t x = 0, looked = 0, units = 0, task[2] = {0, 0};  // x: the ring's next slot
                 bool ok = true;
-                while (ok && w.here(c.kv_heads, p.tiles, a)) {
+                while (ok && w.here(p)) {
                     const int n = w.n;
                     const bool single = w.k.rows <= 128;
-                    ok = wait(q_full, units++ & 1, kDevErrWaitFull);
-                    int begun[2] = {0, 0};
-                    const auto qk = [&](int s, int i) {
-                        const uint32_t x = x0 + slot_k(i), st = x % ST;
-                        if (!wait(full + st, (x / ST) & 1, kDevErrWaitFull)) return false;
-                        tc_fence_after_sync();
-                        const uint32_t q = base + (single ? 0 : s * P::TILE / 16), k = ring + st * (P::TILE / 16);
+                    const auto there = [&](uint32_t x) { return wait(full + x % ST, (x / ST) & 1, kDevErrWaitFull); };
+                    const auto qk = [&](int s, uint32_t x) {
+                        const uint32_t q = base + (single ? 0 : s * (P::TILE / 16)), k = ring + x % ST * (P::TILE / 16);
 #pragma unroll
                         for (int e = 0; e < HALVES * 4; ++e) {  // columns past head_dim are zeros in Q and K
                             const uint32_t off = (e >> 2) * (HALF / 16) + (e & 3) * 2;
@@ -681,35 +597,84 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                             umma_f16(tmem + s * 128, dk + q + off, dk + k + off, iqk, e > 0 || n <= 0);
                         }
                         umma_commit(s_full + s);
-                        if (single || s == 1) umma_commit(empty + st);
-                        return true;
                     };
-                    const auto pv = [&](int s, int i) {
-                        const uint32_t x = x0 + slot_v(i, n), st = x % ST;
-                        if (!wait(full + st, (x / ST) & 1, kDevErrWaitFull)) return false;
-                        const bool look = (single || s == 0) && w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks);
-                        if (look) mbar_arrive(fix);  // while the softmax runs
-                        if (!wait(p_full + s, task[s]++ & 1, kDevErrWaitFull)) return false;
-                        if (look && !wait(fixed, looked++ & 1, kDevErrWaitFull)) return false;
-                        tc_fence_after_sync();
-                        const uint32_t v = ring + st * (P::TILE / 16);
+                    const auto pv = [&](int s, uint32_t x, int begun) {
+                        const uint32_t v = ring + x % ST * (P::TILE / 16);
 #pragma unroll
                         for (int e = 0; e < B / 16; ++e)
-                            umma_f16_ta(tmem + 256 + s * 128, tmem + s * 128 + e * 8, dv + v + e * 128, ipv, begun[s] > 0 || e > 0);
-                        begun[s] = 1;
+                            umma_f16_ta(tmem + 256 + s * 128, tmem + s * 128 + e * 8, dv + v + e * 128, ipv, begun > 0 || e > 0);
                         umma_commit(o_done + s);
-                        if (single || s == 1) umma_commit(empty + st);
-                        return true;
                     };
-                    ok = ok && qk(0, 0);
-                    if (ok && (!single || n > 1)) ok = qk(1, single ? 1 : 0);
-                    if (single) {
-                        for (int i = 0; ok && i < n; ++i) ok = (i & 1 ? pv(1, i) : pv(0, i)) && (i + 2 >= n || (i & 1 ? qk(1, i + 2) : qk(0, i + 2)));
-                    } else {
-                        for (int i = 0; ok && i < n; ++i)
-                            ok = pv(0, i) && (i + 1 >= n || qk(0, i + 1)) && pv(1, i) && (i + 1 >= n || qk(1, i + 1));
+                    const auto cut = [&](int i) { return w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks); };
+                    const auto probs = [&](int s) { return wait(p_full + s, task[s]++ & 1, kDevErrWaitFull); };
+                    ok = wait(q_full, units++ & 1, kDevErrWaitFull) && there(x);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    qk(0, x);
+                    if (!single) qk(1, x);
+                    umma_commit(empty + x % ST);
+                    ++x;
+                    if (single && n > 1) {
+                        ok = there(x);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        qk(1, x);
+                        umma_commit(empty + x % ST);
+                        ++x;
                     }
-                    x0 += 2 * n;
+                    if (single) {  // blocks in turn: V i and K i + 2
+                        for (int i = 0; ok && i < n; ++i) {
+                            const bool look = cut(i);
+                            ok = there(x);
+                            if (look) mbar_arrive(fix);  // V is looked through while the softmax runs
+                            ok = ok && (i & 1 ? probs(1) : probs(0)) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (i & 1)
+                                pv(1, x, i > 1);
+                            else
+                                pv(0, x, i > 1);
+                            umma_commit(empty + x % ST);
+                            ++x;
+                            if (i + 2 < n) {
+                                ok = there(x);
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                if (i & 1)
+                                    qk(1, x);
+                                else
+                                    qk(0, x);
+                                umma_commit(empty + x % ST);
+                                ++x;
+                            }
+                        }
+                    } else {
+                        for (int i = 0; ok && i < n; ++i) {  // V i and K i + 1, for one stream and then the other
+                            const bool look = cut(i), more = i + 1 < n;
+                            ok = there(x);
+                            if (look) mbar_arrive(fix);
+                            ok = ok && probs(0) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            pv(0, x, i);
+                            if (more) {
+                                ok = there(x + 1);
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                qk(0, x + 1);
+                            }
+                            ok = probs(1);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            pv(1, x, i);
+                            umma_commit(empty + x % ST);
+                            if (more) {
+                                qk(1, x + 1);
+                                umma_commit(empty + (x + 1) % ST);
+                            }
+                            x += more ? 2 : 1;
+                        }
+                    }
                 }
                 umma_commit(drain);
                 if (!mbar_wait(drain, 0)) atomicExch(&g_tiles_err, kDevErrDrain);
@@ -722,7 +687,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             uint8_t *dst = sm + P::RING + (lane % HALVES) * HALF + row * 128;
             uint32_t x = 0;
             bool ok = true;
-            while (ok && w.here(c.kv_heads, p.tiles, a)) {
+            while (ok && w.here(p)) {
                 const int n = w.n, seq = w.item / p.tiles;
                 const auto page_at = [&](int blk) {
                     const int key = w.k.kb.block(w.b0 + blk) * B + row;
@@ -745,10 +710,12 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 // pages of block i, i + 1 and, ahead of their use, i + 2
                 int pg0 = page_at(0), pg1 = page_at(1);
                 ok = load(&kmap, 0, pg0);
+                const bool single = w.k.rows <= 128;
                 for (int i = 0; ok && i < n; ++i) {
                     const int pg2 = page_at(i + 2);
-                    if (i + 1 < n) ok = load(&kmap, i + 1, pg1);
-                    if (ok) ok = load(&vmap, i, pg0);
+                    if (!single) ok = load(&vmap, i, pg0);
+                    if (ok && i + 1 < n) ok = load(&kmap, i + 1, pg1);
+                    if (ok && single) ok = load(&vmap, i, pg0);
                     pg0 = pg1, pg1 = pg2;
                 }
             }
@@ -757,22 +724,22 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 if (!mbar_wait(full + y % ST, (y / ST) & 1)) atomicExch(&g_tiles_err, kDevErrDrain);
             __syncwarp();
         } else {
-            const int ft = tid - 320;
             uint32_t x0 = 0, looked = 0;
             bool ok = true;
-            while (ok && w.here(c.kv_heads, p.tiles, a)) {
+            while (ok && w.here(p)) {
                 const int n = w.n, end = w.k.end, low = w.k.low;
-                for (int i = 0; i < n; ++i) {
+                const bool single = w.k.rows <= 128;
+                for (int i = 0; ok && i < n; ++i) {
                     const int key0 = w.k.kb.block(w.b0 + i) * B;
                     if (!w.k.cut(key0, sinks)) continue;
-                    const uint32_t x = x0 + slot_v(i, n), st = x % ST;
+                    const uint32_t x = x0 + slot_v(i, n, single), st = x % ST;
                     ok = __all_sync(0xffffffffu, wait(fix, looked++ & 1, kDevErrWaitFull) &&
                                                      wait(full + st, (x / ST) & 1, kDevErrWaitFull));
                     if (!ok) break;
                     uint8_t *v = sm + P::RING + st * P::TILE;
                     bool special = false;
 #pragma unroll 4
-                    for (int e = ft; e < P::TILE / 16; e += 64) {
+                    for (int e = tid - 320; e < P::TILE / 16; e += 64) {
                         const int j = key0 + ((e & 1023) >> 3);
                         uint4 *at = reinterpret_cast<uint4 *>(v + e * 16);
                         if (j >= end || (j >= sinks && j < low)) {
@@ -830,9 +797,11 @@ int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t m
 }
 
 cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
-    TilesArgs p{a, tile_count(a.group, a.max_q), a.c.page_size < B ? a.c.page_size : B, nullptr, nullptr, nullptr, nullptr};
-    const int64_t units = (int64_t)p.tiles * a.c.seqs * a.c.kv_heads;
-    if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const int tiles = tile_count(a.group, a.max_q);
+    const int64_t units = (int64_t)tiles * a.c.seqs * a.c.kv_heads;
+    const int64_t most = units * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
+    TilesArgs p{a, tiles, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), fast_div(a.group), fast_div(tiles),
+                nullptr, nullptr, nullptr, nullptr};
     char *w = static_cast<char *>(a.ws);
     p.tickets = reinterpret_cast<int32_t *>(w);
     w += round256(units * 4);

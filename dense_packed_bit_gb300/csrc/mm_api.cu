@@ -986,6 +986,7 @@ mm_status check_cache(const mm_cache *c, int64_t layer, bool needs_refs, mm::Cac
         if (counts[i] > 1 && strides[i] < c->head_dim)
             return fail(MM_ERR_INVALID_ARG, "a cache stride is below head_dim: rows overlap");
     }
+    if (c->seqs * c->kv_heads > (1 << 24)) return fail(MM_ERR_INVALID_ARG, "seqs * kv_heads is above 2^24");
     if (c->max_pages * c->page_size > ((int64_t)1 << 30))
         return fail(MM_ERR_INVALID_ARG, "a sequence holds at most 2^30 tokens (max_pages * page_size)");
     for (int r : c->reserved)
@@ -1045,7 +1046,9 @@ mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, i
     if (heads < 1 || heads > 65535 || heads % cache->kv_heads)
         return fail(MM_ERR_INVALID_ARG, "heads (%lld) must be a multiple of kv_heads (%lld), at most 65535", (long long)heads,
                     (long long)cache->kv_heads);
-    if (max_q * (heads / cache->kv_heads) > ((int64_t)1 << 30)) return fail(MM_ERR_INVALID_ARG, "max_q * heads / kv_heads is above 2^30");
+    if (max_q * (heads / cache->kv_heads) > ((int64_t)1 << 30) ||
+        (max_q * (heads / cache->kv_heads) / 256 + 1) * cache->seqs * cache->kv_heads > ((int64_t)1 << 30))
+        return fail(MM_ERR_INVALID_ARG, "max_q is too large for so many heads and sequences");
     const int64_t width = heads * cache->head_dim;
     if ((tokens > 1 && (q_stride < width || o_stride < width)) || q_stride < 0 || o_stride < 0 || q_stride % 8 || o_stride % 8 ||
         q_stride > ((int64_t)1 << 31) || o_stride > ((int64_t)1 << 31))
