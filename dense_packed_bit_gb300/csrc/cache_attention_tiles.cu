@@ -581,14 +581,18 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 // descriptors differ in their address alone (bytes / 16 in the low bits)
                 const uint64_t dk = sdesc_kmajor_sw128(0), dv = sdesc_make(0, HALF, 1024, kSdescSw128);
                 const uint32_t base = (smem_u32(sm) & 0x3FFFFu) >> 4, ring = base + P::RING / 16;
-                uint32_t x = 0, looked = 0, units = 0, task[2] = {0, 0};  // x: the ring's next slot
+                uint32_t looked = 0, units = 0, task[2] = {0, 0};
+                uint32_t st = 0, ph = 0;  // the ring's next slot: its stage, the parity of its barrier
                 bool ok = true;
                 while (ok && w.here(p)) {
                     const int n = w.n;
                     const bool single = w.k.rows <= 128;
-                    const auto there = [&](uint32_t x) { return wait(full + x % ST, (x / ST) & 1, kDevErrWaitFull); };
-                    const auto qk = [&](int s, uint32_t x) {
-                        const uint32_t q = base + (single ? 0 : s * (P::TILE / 16)), k = ring + x % ST * (P::TILE / 16);
+                    const auto there = [&]() { return wait(full + st, ph, kDevErrWaitFull); };
+                    const auto on = [&]() {
+                        if (++st == ST) st = 0, ph ^= 1;
+                    };
+                    const auto qk = [&](int s, uint32_t stage) {
+                        const uint32_t q = base + (single ? 0 : s * (P::TILE / 16)), k = ring + stage * (P::TILE / 16);
 #pragma unroll
                         for (int e = 0; e < HALVES * 4; ++e) {  // columns past head_dim are zeros in Q and K
                             const uint32_t off = (e >> 2) * (HALF / 16) + (e & 3) * 2;
@@ -598,8 +602,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                         }
                         umma_commit(s_full + s);
                     };
-                    const auto pv = [&](int s, uint32_t x, int begun) {
-                        const uint32_t v = ring + x % ST * (P::TILE / 16);
+                    const auto pv = [&](int s, uint32_t stage, int begun) {
+                        const uint32_t v = ring + stage * (P::TILE / 16);
 #pragma unroll
                         for (int e = 0; e < B / 16; ++e)
                             umma_f16_ta(tmem + 256 + s * 128, tmem + s * 128 + e * 8, dv + v + e * 128, ipv, begun > 0 || e > 0);
@@ -607,72 +611,71 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     };
                     const auto cut = [&](int i) { return w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks); };
                     const auto probs = [&](int s) { return wait(p_full + s, task[s]++ & 1, kDevErrWaitFull); };
-                    ok = wait(q_full, units++ & 1, kDevErrWaitFull) && there(x);
+                    ok = wait(q_full, units++ & 1, kDevErrWaitFull) && there();
                     if (!ok) break;
                     tc_fence_after_sync();
-                    qk(0, x);
-                    if (!single) qk(1, x);
-                    umma_commit(empty + x % ST);
-                    ++x;
+                    qk(0, st);
+                    if (!single) qk(1, st);
+                    umma_commit(empty + st);
+                    on();
                     if (single && n > 1) {
-                        ok = there(x);
+                        ok = there();
                         if (!ok) break;
                         tc_fence_after_sync();
-                        qk(1, x);
-                        umma_commit(empty + x % ST);
-                        ++x;
+                        qk(1, st);
+                        umma_commit(empty + st);
+                        on();
                     }
                     if (single) {  // blocks in turn: V i and K i + 2
                         for (int i = 0; ok && i < n; ++i) {
                             const bool look = cut(i);
-                            ok = there(x);
+                            ok = there();
                             if (look) mbar_arrive(fix);  // V is looked through while the softmax runs
                             ok = ok && (i & 1 ? probs(1) : probs(0)) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
                             if (!ok) break;
                             tc_fence_after_sync();
                             if (i & 1)
-                                pv(1, x, i > 1);
+                                pv(1, st, i > 1);
                             else
-                                pv(0, x, i > 1);
-                            umma_commit(empty + x % ST);
-                            ++x;
+                                pv(0, st, i > 1);
+                            umma_commit(empty + st);
+                            on();
                             if (i + 2 < n) {
-                                ok = there(x);
+                                ok = there();
                                 if (!ok) break;
                                 tc_fence_after_sync();
                                 if (i & 1)
-                                    qk(1, x);
+                                    qk(1, st);
                                 else
-                                    qk(0, x);
-                                umma_commit(empty + x % ST);
-                                ++x;
+                                    qk(0, st);
+                                umma_commit(empty + st);
+                                on();
                             }
                         }
                     } else {
                         for (int i = 0; ok && i < n; ++i) {  // V i and K i + 1, for one stream and then the other
                             const bool look = cut(i), more = i + 1 < n;
-                            ok = there(x);
+                            ok = there();
+                            const uint32_t sv = st;
+                            on();
                             if (look) mbar_arrive(fix);
+                            if (more) ok = ok && there();  // nothing is left to wait for but the softmax
+                            const uint32_t sk = st;
                             ok = ok && probs(0) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
                             if (!ok) break;
                             tc_fence_after_sync();
-                            pv(0, x, i);
-                            if (more) {
-                                ok = there(x + 1);
-                                if (!ok) break;
-                                tc_fence_after_sync();
-                                qk(0, x + 1);
-                            }
+                            pv(0, sv, i);
+                            if (more) qk(0, sk);
                             ok = probs(1);
                             if (!ok) break;
                             tc_fence_after_sync();
-                            pv(1, x, i);
-                            umma_commit(empty + x % ST);
+                            pv(1, sv, i);
+                            if (more) qk(1, sk);
+                            umma_commit(empty + sv);
                             if (more) {
-                                qk(1, x + 1);
-                                umma_commit(empty + (x + 1) % ST);
+                                umma_commit(empty + sk);
+                                on();
                             }
-                            x += more ? 2 : 1;
                         }
                     }
                 }
