@@ -65,25 +65,23 @@ struct TilesArgs {
     float4 *part;               // [CTAs][2][head_dim / 4][256]
 };
 
-// 64 fp32 columns of this thread's TMEM lane; the wait is part of the statement, so that no register is read early
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+// 32 fp32 columns of this thread's TMEM lane, begun: v holds them after the next tmem_ld_done.
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, float (&v)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
           "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
           "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
-          "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
-          "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
-          "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
-          "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(taddr)
         : "memory");
+}
+// Waits for the loads begun.  What is then computed from them is computed with the values that pass through
+// here (a scale, two maxima, a key), so that none of it can be moved in front of the wait.
+__device__ __forceinline__ void tmem_ld_done(float2 &scale, float &m0, float &m1, int &key) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(scale.x), "+f"(scale.y), "+f"(m0), "+f"(m1), "+r"(key) : : "memory");
 }
 
 // 16 columns of this thread's lane (the caller waits with tmem_wait_st)
@@ -321,24 +319,21 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 tc_fence_after_sync();
                 const int key0 = kb.block(b0 + blk) * B;
                 const bool cut = key0 + B > whole || (key0 < high && key0 + B > sinks);  // as UnitKeys::cut()
-                const auto masked = [&](float (&v)[64], int h) {
+                const auto masked = [&](float (&v)[32], int key) {
                     if (!cut) return;
+                    const uint32_t bits = seen_bits(rv, key, sinks, sv.len, sv.count);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t bits = seen_bits(rv, key0 + 64 * h + 32 * w, sinks, sv.len, sv.count);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) v[32 * w + x] = bits >> x & 1u ? v[32 * w + x] : -INFINITY;
-                    }
+                    for (int x = 0; x < 32; ++x) v[x] = bits >> x & 1u ? v[x] : -INFINITY;
                 };
                 float mx = -INFINITY;
                 if (__any_sync(0xffffffffu, m == -INFINITY)) {  // the first block, or rows that have seen nothing yet
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        float v[64];
-                        tmem_ld64(ts + 64 * h, v);
-                        masked(v, h);
+                    for (int q = 0; q < 4; ++q) {
+                        float v[32];
+                        tmem_ld32(ts + 32 * q, v);
+                        masked(v, key0 + 32 * q);
 #pragma unroll
-                        for (int x = 0; x < 64; ++x) mx = fmaxf(mx, v[x]);
+                        for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
                     }
                     mx *= scale2;
                 }
@@ -371,23 +366,36 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     const float base = m == -INFINITY ? 0.f : -m;
                     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                     float a0 = -INFINITY, a1 = -INFINITY;
-                    const float2 one = make_float2(1.f, 1.f), sc = make_float2(scale2, scale2), bs = make_float2(base, base);
+                    const float2 one = make_float2(1.f, 1.f), bs = make_float2(base, base);
+                    float2 sc = make_float2(scale2, scale2);
+                    int key = key0;
+                    const auto probs = [&](float (&v)[32], int q) {
+                        masked(v, key + 32 * q);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v[64];
-                        tmem_ld64(ts + 64 * h, v);
-                        masked(v, h);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
+                        for (int x = 0; x < 16; ++x) {
                             float2 e = ffma2(make_float2(v[2 * x], v[2 * x + 1]), sc, bs);
                             e.x = ex2(e.x), e.y = ex2(e.y);
-                            pk[32 * h + x] = Pair<T>::pack(e.x, e.y);
+                            pk[16 * q + x] = Pair<T>::pack(e.x, e.y);
                             if (x & 1)
                                 sum1 = ffma2(e, one, sum1), a1 = fmaxf(fmaxf(a1, v[2 * x]), v[2 * x + 1]);
                             else
                                 sum0 = ffma2(e, one, sum0), a0 = fmaxf(fmaxf(a0, v[2 * x]), v[2 * x + 1]);
                         }
-                    }
+                    };
+                    // the next 32 columns are on their way while 32 are worked on
+                    float va[32], vb[32];
+                    tmem_ld32_begin(ts, va);
+                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld32_begin(ts + 32, vb);
+                    probs(va, 0);
+                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld32_begin(ts + 64, va);
+                    probs(vb, 1);
+                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld32_begin(ts + 96, vb);
+                    probs(va, 2);
+                    tmem_ld_done(sc, a0, a1, key);
+                    probs(vb, 3);
                     sum = make_float2(sum0.x + sum1.x, sum0.y + sum1.y);
                     mx = fmaxf(a0, a1) * scale2;
                     if (!__any_sync(0xffffffffu, mx > m + 8.f)) break;
