@@ -9,12 +9,14 @@
 // Bound: one pass over the logits.  With top-k on, that pass is all: the k-th largest of the maxima
 // of disjoint groups of 8 logits is a lower bound of the k-th largest logit (k groups hold a logit at
 // least as large), so a bound t from the row's first part lets the pass put the few logits >= t into a
-// shared-memory list, and everything else happens there.  What the list must hold is all tokens whose
+// shared-memory list, and everything else happens there.  (The bound is read off a histogram of the group
+// maxima; a bisection over the block took 9,000 to 13,000 cycles of barriers.)  What the list must hold is all tokens whose
 // weight reaches that of the k-th (equal weights can have different logits: t is lowered by 1/16 of a
 // temperature and the list is used only if the weight of the lowered bound is smaller).  Tokens more than
 // 22 temperatures below a logit weigh 0 and are left out.  The list is cut to the k-th largest by a
 // histogram of the weights, then every token's rank and the weight before it are counted against all
-// others (k^2 comparisons, no sort).
+// others (k^2 comparisons, no sort).  The two products in fp64 (the target of top-p, u S) are one thread's: this
+// GPU's fp64 units take thousands of cycles for a block of 1024.
 //
 // Rows that the list cannot serve (top-k off or above kMaxListK, a list that overflows) select by a
 // radix descent on the weights: 512 bins by exponent and 4 leading bits, then linear bins inside the
@@ -31,7 +33,7 @@ namespace mm {
 namespace {
 
 constexpr int CAP = 4096;       // list entries
-constexpr int CUT = 1024;       // entries left after the histogram's cut
+constexpr int CUT = 1024;       // entries left after the histogram's cut (3 CUT <= CAP)
 constexpr int kMaxListK = 512;  // top-k served by the list
 constexpr int BINS = 512;
 constexpr float kOne = 1073741824.0f;  // 2^30
@@ -77,8 +79,9 @@ struct Shared {
     unsigned long long key[CUT];  // w << 32 | ~index: larger is earlier in the order
     int count[BINS];
     unsigned long long part[32];
-    unsigned long long total;
-    float fpart[32];
+    unsigned long long target;
+    float2 fpart[32];
+    int wsum[32];
     int n, cut, picked, bin;
     unsigned long long acc_mass;
     int acc_count;
@@ -96,20 +99,55 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 __device__ __forceinline__ uint32_t weight(float x, float m, float rate) {
     if (!(x > -INFINITY)) return 0;  // NaN and -infinity
     const float z = x == m ? 0.f : (x - m) * rate;
-    return (uint32_t)__float2ll_rn(expf(z) * kOne);
+    return __float2uint_rn(expf(z) * kOne);
 }
 
+// maxima of two values over the block
 template <int NT>
-__device__ __forceinline__ float block_max(float v, Shared &sh) {
+__device__ __forceinline__ float2 block_max(float2 v, Shared &sh) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o; o >>= 1) {
+        v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+        v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+    }
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.fpart[threadIdx.x >> 5] = v;
     __syncthreads();
     v = sh.fpart[(threadIdx.x & 31) % (NT / 32)];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = NT / 64; o; o >>= 1) {
+        v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+        v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+    }
     return v;
+}
+
+// The first bin of sh.count at which the running count reaches `target`, BINS if none does.  The counts must be
+// complete (a barrier before); a barrier ends it.
+template <int NT>
+__device__ __forceinline__ int first_bin(Shared &sh, int target) {
+    constexpr int EACH = NT >= BINS ? 1 : BINS / NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = threadIdx.x * EACH;
+    int c[EACH], n = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) c[i] = b0 + i < BINS ? sh.count[b0 + i] : 0, n += c[i];
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += u;
+    }
+    if (lane == 31) sh.wsum[warp] = run;
+    if (threadIdx.x == 0) sh.bin = BINS;
+    __syncthreads();
+    run += __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane] : 0) - n;  // in front of this thread's bins
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (run < target && run + c[i] >= target) sh.bin = b0 + i;
+        run += c[i];
+    }
+    __syncthreads();
+    return sh.bin;
 }
 
 template <int NT>
@@ -245,8 +283,11 @@ __device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_
     unsigned long long taken = 0, mass = 0;
     if (r.k > 0 || r.top_p < 1.f) {
         mass = find_cut<T, NT>(x, n, m, r, sh, false, r.k > 0 ? (unsigned long long)r.k : ~0ull, &cut, &taken);
-        if (r.top_p < 1.f && mass > 0)
-            find_cut<T, NT>(x, n, m, r, sh, true, top_p_target(r.top_p, mass), &cut, &taken);
+        if (r.top_p < 1.f && mass > 0) {
+            if (threadIdx.x == 0) sh.target = top_p_target(r.top_p, mass);
+            __syncthreads();
+            find_cut<T, NT>(x, n, m, r, sh, true, sh.target, &cut, &taken);
+        }
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t share = ((n + NT / 32 - 1) / (NT / 32) + 31) / 32 * 32;
@@ -286,7 +327,9 @@ __device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_
         if (threadIdx.x == 0) put(a, row, -1, 1, 1);
         return;
     }
-    const unsigned long long want = wanted(r.u, total);
+    if (threadIdx.x == 0) sh.target = wanted(r.u, total);
+    __syncthreads();
+    const unsigned long long want = sh.target;
     if (want < before || want >= before + mine) return;
     tie = tie0;
     for (int64_t i = from; i < to; i += 32) {
@@ -336,51 +379,50 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     float t0 = -INFINITY;
     bool all_heavy = false;  // what is below `low` weighs 0
     if (listed) {
-        // the first part: four groups of 8 per thread
-        uint32_t g[4];
-        float mx = -INFINITY;
+        // The first part: GROUPS groups of 8 rep logits per thread, so long that the list holds about 2700 logits at most
+        constexpr int GROUPS = NT >= 1024 ? 4 : 2048 / NT;
+        const int rep = (int)min((long long)r.k * n / (2700ll * 8 * GROUPS * NT) + 1, 64ll);
+        float g[GROUPS], gx = -INFINITY, gl = -INFINITY;  // their maxima, the largest, minus the least finite one
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float gm = -INFINITY;
+        for (int q = 0; q < GROUPS; ++q) {
+            g[q] = -INFINITY;
+#pragma unroll 1
+            for (int i = 0; i < rep; ++i)
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int64_t v = (int64_t)(q * G + j) * NT + threadIdx.x;
-                if (v < vecs) {
-                    float f[N];
-                    Vec<T>::get(__ldg(body + v), f);
+                for (int j = 0; j < G; ++j) {
+                    const int64_t v = (int64_t)((q * rep + i) * G + j) * NT + threadIdx.x;
+                    if (v < vecs) {
+                        float f[N];
+                        Vec<T>::get(__ldg(body + v), f);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) gm = fmaxf(gm, f[e]);
+                        for (int e = 0; e < N; ++e) g[q] = fmaxf(g[q], f[e]);
+                    }
                 }
-            }
-            g[q] = order_key(gm + 0.f);
-            mx = fmaxf(mx, gm);
+            gx = fmaxf(gx, g[q]);
+            if (g[q] > -INFINITY) gl = fmaxf(gl, -g[q]);
         }
-        mx = block_max<NT>(mx, sh);
-        // a key that between k and a little more of the maxima reach
-        uint32_t lo = order_key(-INFINITY), hi = order_key(mx + 0.f) + 1;
-        while (hi - lo > 1) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            int c = 0;
+        for (int b = threadIdx.x; b < BINS; b += NT) sh.count[b] = 0;
+        const float2 ends = block_max<NT>(make_float2(gx, gl), sh);
+        const float mx = ends.x;
+        // bins of the maxima's distance from the largest, over the range that can weigh anything
+        const float range = fminf(22.f / r.rate, mx + ends.y), inv = range > 0.f ? (BINS - 1) / range : 0.f;
+        int bin[GROUPS];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) c += g[q] >= mid;
-            c = __reduce_add_sync(0xffffffffu, c);
-            if ((threadIdx.x & 31) == 0) sh.count[threadIdx.x >> 5] = c;
-            __syncthreads();
-            c = 0;
-#pragma unroll
-            for (int i = 0; i < NT / 32; ++i) c += sh.count[i];
-            __syncthreads();
-            if (c >= r.k) {
-                lo = mid;
-                if (c <= r.k + r.k / 8 + 2) break;
-            } else {
-                hi = mid;
-            }
+        for (int q = 0; q < GROUPS; ++q) {
+            bin[q] = g[q] == mx ? 0 : (int)fminf((mx - g[q]) * inv, (float)(BINS - 1));
+            atomicAdd(&sh.count[bin[q]], 1);
         }
-        t0 = from_key(lo);
+        __syncthreads();
+        const int last = first_bin<NT>(sh, r.k);
+        // the least of the maxima up to that bin: at least k of them are not below it
+        float least = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q)
+            if (bin[q] <= last) least = fmaxf(least, -g[q]);
+        t0 = -block_max<NT>(make_float2(least, -INFINITY), sh).x;
         // a sixteenth of a temperature lower, but not where every weight is 0 whatever the rest holds
         const float down = t0 - 0.0625f / r.rate;
-        low = down < t0 ? down : from_key(max(lo, order_key(-FLT_MAX)) - 1);
+        low = down < t0 ? down : from_key(max(order_key(t0 + 0.f), order_key(-FLT_MAX)) - 1);
         const float none = mx - 22.f / r.rate;
         all_heavy = none >= low;
         low = fmaxf(fmaxf(low, none), -FLT_MAX);
@@ -421,7 +463,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         m = fmaxf(m, f);
         offer(f, i);
     }
-    m = block_max<NT>(m, sh);
+    m = block_max<NT>(make_float2(m, 0.f), sh).x;
     if (m == -INFINITY) {  // nothing is left of the row
         if (threadIdx.x == 0) put(a, row, -1, 1, 1);
         return;
@@ -438,18 +480,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     }
 
     // the k heaviest of the list, by bins of their weights
-    for (int b = threadIdx.x; b < BINS; b += NT) sh.count[b] = 0, sh.mass[b] = 0;
-    if (threadIdx.x == 0) sh.acc_mass = 0, sh.acc_count = 0;
+    for (int b = threadIdx.x; b < BINS; b += NT) sh.count[b] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < have; i += NT) {
         const uint32_t w = weight(sh.x[i], m, r.rate);
         sh.x[i] = __uint_as_float(w);
-        if (w) atomicAdd(&sh.count[bin_of(w)], 1);
+        if (w) atomicAdd(&sh.count[BINS - 1 - bin_of(w)], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) find_bin(sh, false, (unsigned long long)r.k);
-    __syncthreads();
-    const uint32_t least = sh.bin < 0 ? 1u : bin_low(sh.bin);
+    const int last = first_bin<NT>(sh, r.k);
+    const uint32_t least = last == BINS ? 1u : bin_low(BINS - 1 - last);
     for (int i = threadIdx.x; i < have; i += NT) {
         const uint32_t w = __float_as_uint(sh.x[i]);
         if (w >= least) {
@@ -463,45 +503,45 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         general_row<T, NT>(a, row, x, n, m, r, sh);
         return;
     }
-    // rank and weight in front of each, four lanes per token
+    // rank and weight in front of each, four lanes per token (kept in the list's place, which is free)
+    unsigned long long *before = reinterpret_cast<unsigned long long *>(sh.x);
+    int *rank = sh.idx;
     const int sub = threadIdx.x & 3;
     unsigned long long mass = 0;
-    constexpr int ROUNDS = CUT * 4 / NT;
-    unsigned long long before[ROUNDS];
-    int rank[ROUNDS];
+    for (int e0 = 0; e0 < c; e0 += NT / 4) {
+        const int e = e0 + (threadIdx.x >> 2);
+        const unsigned long long key = e < c ? sh.key[e] : ~0ull;
+        unsigned long long in_front = 0;
+        int n_front = 0;
+#pragma unroll 4
+        for (int f = sub; f < c; f += 4) {
+            const unsigned long long o = sh.key[f];
+            if (o > key) in_front += o >> 32, ++n_front;
+        }
 #pragma unroll
-    for (int q = 0; q < ROUNDS; ++q) {
-        const int e = q * (NT / 4) + (threadIdx.x >> 2);
-        before[q] = 0, rank[q] = 0;
-        if (q * (NT / 4) < c) {  // the same for the whole block
-            const unsigned long long key = e < c ? sh.key[e] : ~0ull;
-            for (int f = sub; f < c; f += 4) {
-                const unsigned long long o = sh.key[f];
-                if (o > key) before[q] += o >> 32, ++rank[q];
-            }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                before[q] += __shfl_xor_sync(0xffffffffu, before[q], o);
-                rank[q] += __shfl_xor_sync(0xffffffffu, rank[q], o);
-            }
-            if (e < c && sub == 0 && rank[q] < r.k) mass += key >> 32;
+        for (int o = 1; o < 4; o <<= 1) {
+            in_front += __shfl_xor_sync(0xffffffffu, in_front, o);
+            n_front += __shfl_xor_sync(0xffffffffu, n_front, o);
+        }
+        if (e < c && sub == 0) {
+            before[e] = in_front, rank[e] = n_front;
+            if (n_front < r.k) mass += key >> 32;
         }
     }
     mass = block_sum<NT>(mass, sh);
-    const unsigned long long target = top_p_target(r.top_p, mass);
+    if (threadIdx.x == 0) sh.target = top_p_target(r.top_p, mass);
+    __syncthreads();
+    const unsigned long long target = sh.target;
+    float *kept_w = sh.x + 2 * CUT;
+    int *kept_i = sh.idx + CUT;
     unsigned long long total = 0;
-#pragma unroll
-    for (int q = 0; q < ROUNDS; ++q) {
-        const int e = q * (NT / 4) + (threadIdx.x >> 2);
-        if (e < c && sub == 0) {
-            const unsigned long long key = sh.key[e];
-            const bool in = rank[q] < r.k && (rank[q] == 0 || before[q] < target) && (uint32_t)(key >> 32) >= r.floor_w;
-            if (in) {
-                total += key >> 32;
-                const int at = atomicAdd(&sh.picked, 1);
-                sh.x[at] = __uint_as_float((uint32_t)(key >> 32));
-                sh.idx[at] = (int)~(uint32_t)key;
-            }
+    for (int e = threadIdx.x; e < c; e += NT) {
+        const unsigned long long key = sh.key[e];
+        if (rank[e] < r.k && (rank[e] == 0 || before[e] < target) && (uint32_t)(key >> 32) >= r.floor_w) {
+            total += key >> 32;
+            const int at = atomicAdd(&sh.picked, 1);
+            kept_w[at] = __uint_as_float((uint32_t)(key >> 32));
+            kept_i[at] = (int)~(uint32_t)key;
         }
     }
     total = block_sum<NT>(total, sh);
@@ -509,18 +549,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         if (threadIdx.x == 0) put(a, row, -1, 1, 1);
         return;
     }
-    const unsigned long long want = wanted(r.u, total);
+    if (threadIdx.x == 0) sh.target = wanted(r.u, total);
+    __syncthreads();
+    const unsigned long long want = sh.target;
     const int kept = sh.picked;
     for (int e0 = 0; e0 < kept; e0 += NT / 4) {
         const int e = e0 + (threadIdx.x >> 2);
         unsigned long long s = 0;
-        const int me = e < kept ? sh.idx[e] : 0;
+        const int me = e < kept ? kept_i[e] : 0;
+#pragma unroll 4
         for (int f = sub; f < kept; f += 4)
-            if (sh.idx[f] < me) s += __float_as_uint(sh.x[f]);
+            if (kept_i[f] < me) s += __float_as_uint(kept_w[f]);
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (e < kept && sub == 0) {
-            const uint32_t w = __float_as_uint(sh.x[e]);
+            const uint32_t w = __float_as_uint(kept_w[e]);
             if (s <= want && want < s + w) put(a, row, me, w, total);
         }
     }
@@ -536,9 +579,8 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_t(const SampleArgs &a, int sms, cudaStream_t s) {
-    // up to one row per SM: all its warps on the row; more rows: two to an SM, one streaming while the
-    // other chooses
-    return a.rows <= sms ? launch<T, 1024>(a, s) : launch<T, 512>(a, s);
+    // up to one row per SM: all its warps on the row; more rows: four to an SM, some streaming while others choose
+    return a.rows <= sms ? launch<T, 1024>(a, s) : launch<T, 256>(a, s);
 }
 
 }  // namespace
