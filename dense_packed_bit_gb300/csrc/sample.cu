@@ -15,8 +15,7 @@
 // temperature and the list is used only if the weight of the lowered bound is smaller).  Tokens more than
 // 22 temperatures below a logit weigh 0 and are left out.  The list is cut to the k-th largest by a
 // histogram of the weights, then every token's rank and the weight before it are counted against all
-// others (k^2 comparisons, no sort).  The two products in fp64 (the target of top-p, u S) are one thread's: this
-// GPU's fp64 units take thousands of cycles for a block of 1024.
+// others (k^2 comparisons, no sort).  256 threads do this, whatever the block: their barriers are cheaper.
 //
 // Rows that the list cannot serve (top-k off or above kMaxListK, a list that overflows) select by a
 // radix descent on the weights: 512 bins by exponent and 4 leading bits, then linear bins inside the
@@ -79,7 +78,6 @@ struct Shared {
     unsigned long long key[CUT];  // w << 32 | ~index: larger is earlier in the order
     int count[BINS];
     unsigned long long part[32];
-    unsigned long long target;
     float2 fpart[32];
     int wsum[32];
     int n, cut, picked, bin;
@@ -100,6 +98,17 @@ __device__ __forceinline__ uint32_t weight(float x, float m, float rate) {
     if (!(x > -INFINITY)) return 0;  // NaN and -infinity
     const float z = x == m ? 0.f : (x - m) * rate;
     return __float2uint_rn(expf(z) * kOne);
+}
+
+// All NT threads of the block, or (BAR 1) the first NT of it
+template <int NT, int BAR>
+__device__ __forceinline__ void sync() {
+    if (BAR == 0) {
+        __syncthreads();
+    } else {
+        __syncwarp();
+        bar_sync(BAR, NT);
+    }
 }
 
 // maxima of two values over the block
@@ -124,7 +133,7 @@ __device__ __forceinline__ float2 block_max(float2 v, Shared &sh) {
 
 // The first bin of sh.count at which the running count reaches `target`, BINS if none does.  The counts must be
 // complete (a barrier before); a barrier ends it.
-template <int NT>
+template <int NT, int BAR>
 __device__ __forceinline__ int first_bin(Shared &sh, int target) {
     constexpr int EACH = NT >= BINS ? 1 : BINS / NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = threadIdx.x * EACH;
@@ -139,24 +148,24 @@ __device__ __forceinline__ int first_bin(Shared &sh, int target) {
     }
     if (lane == 31) sh.wsum[warp] = run;
     if (threadIdx.x == 0) sh.bin = BINS;
-    __syncthreads();
+    sync<NT, BAR>();
     run += __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane] : 0) - n;  // in front of this thread's bins
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         if (run < target && run + c[i] >= target) sh.bin = b0 + i;
         run += c[i];
     }
-    __syncthreads();
+    sync<NT, BAR>();
     return sh.bin;
 }
 
-template <int NT>
+template <int NT, int BAR>
 __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, Shared &sh) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
+    sync<NT, BAR>();
     if ((threadIdx.x & 31) == 0) sh.part[threadIdx.x >> 5] = v;
-    __syncthreads();
+    sync<NT, BAR>();
     unsigned long long s = 0;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) s += sh.part[i];
@@ -170,15 +179,35 @@ struct Row {
     uint32_t floor_w;  // min-p
 };
 
+// floor(f n) and whether there is a rest, exactly, for 0 < f < 1 and n < 2^63 (in whole numbers: a block's worth
+// of fp64 products takes this GPU thousands of cycles)
+__device__ __forceinline__ unsigned long long times(float f, unsigned long long n, bool *rest) {
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+    const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);  // f = m 2^-shift
+    const int shift = 150 - (int)max(e, 1u);                                  // 24 .. 149
+    const unsigned long long lo = m * n, hi = __umul64hi(m, n);
+    if (shift >= 128) {
+        *rest = (lo | hi) != 0;
+        return 0;
+    }
+    if (shift >= 64) {
+        *rest = lo != 0 || (hi & ((1ull << (shift - 64)) - 1)) != 0;
+        return hi >> (shift - 64);
+    }
+    *rest = (lo & ((1ull << shift) - 1)) != 0;
+    return hi << (64 - shift) | lo >> shift;
+}
 __device__ __forceinline__ unsigned long long top_p_target(float p, unsigned long long mass) {
     if (!(p < 1.f)) return mass;
-    const double t = ceil((double)p * (double)mass);
-    return t < 1.0 ? 1ull : (unsigned long long)t;
+    if (!(p > 0.f)) return 1;
+    bool rest;
+    const unsigned long long t = times(p, mass, &rest);
+    return t + rest;
 }
 __device__ __forceinline__ unsigned long long wanted(float u, unsigned long long total) {
-    const double t = floor((double)u * (double)total);
-    const unsigned long long w = t > 0.0 ? (unsigned long long)t : 0ull;
-    return w < total ? w : total - 1;
+    if (!(u > 0.f)) return 0;
+    bool rest;
+    return u < 1.f ? times(u, total, &rest) : total - 1;
 }
 
 __device__ __forceinline__ void put(const SampleArgs &a, int64_t row, int token, uint32_t w, unsigned long long total) {
@@ -255,7 +284,7 @@ __device__ unsigned long long find_cut(const T *x, int64_t n, float m, const Row
             *cut_w = 0, *taken = 0;
             unsigned long long all = 0;
             for (int q = threadIdx.x; q < BINS; q += NT) all += sh.mass[q];
-            return block_sum<NT>(all, sh);
+            return block_sum<NT, 0>(all, sh);
         }
         if (shift < 0) {
             lo = bin_low(b), hi = bin_low(b + 1) - 1;
@@ -284,9 +313,7 @@ __device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_
     if (r.k > 0 || r.top_p < 1.f) {
         mass = find_cut<T, NT>(x, n, m, r, sh, false, r.k > 0 ? (unsigned long long)r.k : ~0ull, &cut, &taken);
         if (r.top_p < 1.f && mass > 0) {
-            if (threadIdx.x == 0) sh.target = top_p_target(r.top_p, mass);
-            __syncthreads();
-            find_cut<T, NT>(x, n, m, r, sh, true, sh.target, &cut, &taken);
+            find_cut<T, NT>(x, n, m, r, sh, true, top_p_target(r.top_p, mass), &cut, &taken);
         }
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -327,9 +354,7 @@ __device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_
         if (threadIdx.x == 0) put(a, row, -1, 1, 1);
         return;
     }
-    if (threadIdx.x == 0) sh.target = wanted(r.u, total);
-    __syncthreads();
-    const unsigned long long want = sh.target;
+    const unsigned long long want = wanted(r.u, total);
     if (want < before || want >= before + mine) return;
     tie = tie0;
     for (int64_t i = from; i < to; i += 32) {
@@ -345,6 +370,95 @@ __device__ void general_row(const SampleArgs &a, int64_t row, const T *x, int64_
         if (__any_sync(0xffffffffu, here)) return;
         before += __shfl_sync(0xffffffffu, s, 31);
     }
+}
+
+// The token from the list of `have` logits, by the first TAIL threads of the block; true: too many equal weights.
+template <int TAIL, int BAR>
+__device__ __forceinline__ bool from_list(const SampleArgs &a, int64_t row, int have, float m, const Row &r, Shared &sh) {
+    // the k heaviest of the list, by bins of their weights
+    for (int b = threadIdx.x; b < BINS; b += TAIL) sh.count[b] = 0;
+    sync<TAIL, BAR>();
+    for (int i = threadIdx.x; i < have; i += TAIL) {
+        const uint32_t w = weight(sh.x[i], m, r.rate);
+        sh.x[i] = __uint_as_float(w);
+        if (w) atomicAdd(&sh.count[BINS - 1 - bin_of(w)], 1);
+    }
+    sync<TAIL, BAR>();
+    const int last = first_bin<TAIL, BAR>(sh, r.k);
+    const uint32_t least = last == BINS ? 1u : bin_low(BINS - 1 - last);
+    for (int i = threadIdx.x; i < have; i += TAIL) {
+        const uint32_t w = __float_as_uint(sh.x[i]);
+        if (w >= least) {
+            const int at = atomicAdd(&sh.cut, 1);
+            if (at < CUT) sh.key[at] = (unsigned long long)w << 32 | (uint32_t)~sh.idx[i];
+        }
+    }
+    sync<TAIL, BAR>();
+    const int c = sh.cut;
+    if (c > CUT) {  // very many equal weights
+        return true;
+    }
+    // rank and weight in front of each, four lanes per token (kept in the list's place, which is free)
+    unsigned long long *before = reinterpret_cast<unsigned long long *>(sh.x);
+    int *rank = sh.idx;
+    const int sub = threadIdx.x & 3;
+    unsigned long long mass = 0;
+    for (int e0 = 0; e0 < c; e0 += TAIL / 4) {
+        const int e = e0 + (threadIdx.x >> 2);
+        const unsigned long long key = e < c ? sh.key[e] : ~0ull;
+        unsigned long long in_front = 0;
+        int n_front = 0;
+#pragma unroll 4
+        for (int f = sub; f < c; f += 4) {
+            const unsigned long long o = sh.key[f];
+            if (o > key) in_front += o >> 32, ++n_front;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            in_front += __shfl_xor_sync(0xffffffffu, in_front, o);
+            n_front += __shfl_xor_sync(0xffffffffu, n_front, o);
+        }
+        if (e < c && sub == 0) {
+            before[e] = in_front, rank[e] = n_front;
+            if (n_front < r.k) mass += key >> 32;
+        }
+    }
+    mass = block_sum<TAIL, BAR>(mass, sh);
+    const unsigned long long target = top_p_target(r.top_p, mass);
+    float *kept_w = sh.x + 2 * CUT;
+    int *kept_i = sh.idx + CUT;
+    unsigned long long total = 0;
+    for (int e = threadIdx.x; e < c; e += TAIL) {
+        const unsigned long long key = sh.key[e];
+        if (rank[e] < r.k && (rank[e] == 0 || before[e] < target) && (uint32_t)(key >> 32) >= r.floor_w) {
+            total += key >> 32;
+            const int at = atomicAdd(&sh.picked, 1);
+            kept_w[at] = __uint_as_float((uint32_t)(key >> 32));
+            kept_i[at] = (int)~(uint32_t)key;
+        }
+    }
+    total = block_sum<TAIL, BAR>(total, sh);
+    if (total == 0) {
+        if (threadIdx.x == 0) put(a, row, -1, 1, 1);
+        return false;
+    }
+    const unsigned long long want = wanted(r.u, total);
+    const int kept = sh.picked;
+    for (int e0 = 0; e0 < kept; e0 += TAIL / 4) {
+        const int e = e0 + (threadIdx.x >> 2);
+        unsigned long long s = 0;
+        const int me = e < kept ? kept_i[e] : 0;
+#pragma unroll 4
+        for (int f = sub; f < kept; f += 4)
+            if (kept_i[f] < me) s += __float_as_uint(kept_w[f]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (e < kept && sub == 0) {
+            const uint32_t w = __float_as_uint(kept_w[e]);
+            if (s <= want && want < s + w) put(a, row, me, w, total);
+        }
+    }
+    return false;
 }
 
 template <typename T, int NT>
@@ -413,7 +527,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
             atomicAdd(&sh.count[bin[q]], 1);
         }
         __syncthreads();
-        const int last = first_bin<NT>(sh, r.k);
+        const int last = first_bin<NT, 0>(sh, r.k);
         // the least of the maxima up to that bin: at least k of them are not below it
         float least = -INFINITY;
 #pragma unroll
@@ -479,94 +593,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         return;
     }
 
-    // the k heaviest of the list, by bins of their weights
-    for (int b = threadIdx.x; b < BINS; b += NT) sh.count[b] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < have; i += NT) {
-        const uint32_t w = weight(sh.x[i], m, r.rate);
-        sh.x[i] = __uint_as_float(w);
-        if (w) atomicAdd(&sh.count[BINS - 1 - bin_of(w)], 1);
-    }
-    __syncthreads();
-    const int last = first_bin<NT>(sh, r.k);
-    const uint32_t least = last == BINS ? 1u : bin_low(BINS - 1 - last);
-    for (int i = threadIdx.x; i < have; i += NT) {
-        const uint32_t w = __float_as_uint(sh.x[i]);
-        if (w >= least) {
-            const int at = atomicAdd(&sh.cut, 1);
-            if (at < CUT) sh.key[at] = (unsigned long long)w << 32 | (uint32_t)~sh.idx[i];
-        }
-    }
-    __syncthreads();
-    const int c = sh.cut;
-    if (c > CUT) {  // very many equal weights
-        general_row<T, NT>(a, row, x, n, m, r, sh);
+    constexpr int TAIL = 256;
+    if (NT == TAIL) {
+        if (from_list<TAIL, 0>(a, row, have, m, r, sh)) general_row<T, NT>(a, row, x, n, m, r, sh);
         return;
     }
-    // rank and weight in front of each, four lanes per token (kept in the list's place, which is free)
-    unsigned long long *before = reinterpret_cast<unsigned long long *>(sh.x);
-    int *rank = sh.idx;
-    const int sub = threadIdx.x & 3;
-    unsigned long long mass = 0;
-    for (int e0 = 0; e0 < c; e0 += NT / 4) {
-        const int e = e0 + (threadIdx.x >> 2);
-        const unsigned long long key = e < c ? sh.key[e] : ~0ull;
-        unsigned long long in_front = 0;
-        int n_front = 0;
-#pragma unroll 4
-        for (int f = sub; f < c; f += 4) {
-            const unsigned long long o = sh.key[f];
-            if (o > key) in_front += o >> 32, ++n_front;
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            in_front += __shfl_xor_sync(0xffffffffu, in_front, o);
-            n_front += __shfl_xor_sync(0xffffffffu, n_front, o);
-        }
-        if (e < c && sub == 0) {
-            before[e] = in_front, rank[e] = n_front;
-            if (n_front < r.k) mass += key >> 32;
-        }
+    if (threadIdx.x < TAIL) {
+        const bool many = from_list<TAIL, 1>(a, row, have, m, r, sh);
+        if (threadIdx.x == 0) sh.bin = many;
     }
-    mass = block_sum<NT>(mass, sh);
-    if (threadIdx.x == 0) sh.target = top_p_target(r.top_p, mass);
     __syncthreads();
-    const unsigned long long target = sh.target;
-    float *kept_w = sh.x + 2 * CUT;
-    int *kept_i = sh.idx + CUT;
-    unsigned long long total = 0;
-    for (int e = threadIdx.x; e < c; e += NT) {
-        const unsigned long long key = sh.key[e];
-        if (rank[e] < r.k && (rank[e] == 0 || before[e] < target) && (uint32_t)(key >> 32) >= r.floor_w) {
-            total += key >> 32;
-            const int at = atomicAdd(&sh.picked, 1);
-            kept_w[at] = __uint_as_float((uint32_t)(key >> 32));
-            kept_i[at] = (int)~(uint32_t)key;
-        }
-    }
-    total = block_sum<NT>(total, sh);
-    if (total == 0) {
-        if (threadIdx.x == 0) put(a, row, -1, 1, 1);
-        return;
-    }
-    if (threadIdx.x == 0) sh.target = wanted(r.u, total);
-    __syncthreads();
-    const unsigned long long want = sh.target;
-    const int kept = sh.picked;
-    for (int e0 = 0; e0 < kept; e0 += NT / 4) {
-        const int e = e0 + (threadIdx.x >> 2);
-        unsigned long long s = 0;
-        const int me = e < kept ? kept_i[e] : 0;
-#pragma unroll 4
-        for (int f = sub; f < kept; f += 4)
-            if (kept_i[f] < me) s += __float_as_uint(kept_w[f]);
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (e < kept && sub == 0) {
-            const uint32_t w = __float_as_uint(kept_w[e]);
-            if (s <= want && want < s + w) put(a, row, me, w, total);
-        }
-    }
+    if (sh.bin) general_row<T, NT>(a, row, x, n, m, r, sh);
 }
 
 template <typename T, int NT>
