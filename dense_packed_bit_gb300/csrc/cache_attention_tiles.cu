@@ -748,19 +748,28 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                                                      wait(full + st, (x / ST) & 1, kDevErrWaitFull));
                     if (!ok) break;
                     uint8_t *v = sm + P::RING + st * P::TILE;
-                    bool special = false;
-#pragma unroll 4
-                    for (int e = tid - 320; e < P::TILE / 16; e += 64) {
-                        const int j = key0 + ((e & 1023) >> 3);
-                        uint4 *at = reinterpret_cast<uint4 *>(v + e * 16);
-                        if (j >= end || (j >= sinks && j < low)) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            const uint4 u = *at;
-                            special |= any_special<T>(u.x) || any_special<T>(u.y) || any_special<T>(u.z) || any_special<T>(u.w);
+                    // infinite or NaN: the magnitude's bits are kExp or more, and adding this carries into bit 15
+                    constexpr uint32_t up = (0x8000u - Pair<T>::kExp) * 0x10001u;
+                    uint32_t special = 0;
+#pragma unroll 1
+                    for (int e0 = tid - 320; e0 < P::TILE / 16; e0 += 8 * 64) {
+                        uint4 u[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(v + (e0 + 64 * k) * 16);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int e = e0 + 64 * k, j = key0 + ((e & 1023) >> 3);
+                            if (j >= end || (j >= sinks && j < low)) {
+                                *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                            } else {
+                                special |= (u[k].x & 0x7fff7fffu) + up;
+                                special |= (u[k].y & 0x7fff7fffu) + up;
+                                special |= (u[k].z & 0x7fff7fffu) + up;
+                                special |= (u[k].w & 0x7fff7fffu) + up;
+                            }
                         }
                     }
-                    if (special) *poison = 1;
+                    if (special & 0x80008000u) *poison = 1;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(fixed);
