@@ -96,13 +96,37 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The MMA warp runs as one, and what its instructions take is the same in all lanes and known to be (a reduction's
+// result is): the lane that issues is a predicate, not a branch.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// D[tmem] (+)= A[smem] * B[smem], by the lane with `lead`.  The descriptors share their high word.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
         : "memory");
 }
 
@@ -582,114 +606,125 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
         __syncthreads();  // tensor memory has been read
     } else {
         if (warp == 8) {
-            if (lane == 0) {
-                const uint32_t fmt = c.dtype == 0 ? kFmtF16 : kFmtBF16;
-                const uint32_t iqk = make_idesc(fmt, fmt, B, 128);
-                const uint32_t ipv = make_idesc(fmt, fmt, (uint32_t)steps * 16, 128) | 1u << 16;  // V: MN-major
-                // descriptors differ in their address alone (bytes / 16 in the low bits)
-                const uint64_t dk = sdesc_kmajor_sw128(0), dv = sdesc_make(0, HALF, 1024, kSdescSw128);
-                const uint32_t base = (smem_u32(sm) & 0x3FFFFu) >> 4, ring = base + P::RING / 16;
-                uint32_t looked = 0, units = 0, task[2] = {0, 0};
-                uint32_t st = 0, ph = 0;  // the ring's next slot: its stage, the parity of its barrier
-                bool ok = true;
-                while (ok && w.here(p)) {
-                    const int n = w.n;
-                    const bool single = w.k.rows <= 128;
-                    const auto there = [&]() { return wait(full + st, ph, kDevErrWaitFull); };
-                    const auto on = [&]() {
-                        if (++st == ST) st = 0, ph ^= 1;
-                    };
-                    const auto qk = [&](int s, uint32_t stage) {
-                        const uint32_t q = base + (single ? 0 : s * (P::TILE / 16)), k = ring + stage * (P::TILE / 16);
+            const uint32_t lead = lane == 0, full_warp = 0xffffffffu;
+            const uint32_t fmt = c.dtype == 0 ? kFmtF16 : kFmtBF16;
+            const uint32_t iqk = make_idesc(fmt, fmt, B, 128);
+            const uint32_t ipv = make_idesc(fmt, fmt, (uint32_t)steps * 16, 128) | 1u << 16;  // V: MN-major
+            // descriptors differ in their address alone (bytes / 16 in the low bits)
+            const uint64_t dk = sdesc_kmajor_sw128(0), dv = sdesc_make(0, HALF, 1024, kSdescSw128);
+            const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+            const uint32_t base = uniform((smem_u32(sm) & 0x3FFFFu) >> 4), ring = base + P::RING / 16;
+            const uint32_t acc = uniform(tmem), bar = uniform(smem_u32(bars));
+            const auto signal = [&](const uint64_t *b) { commit(bar + (uint32_t)(b - bars) * 8, lead); };
+            const auto signal_empty = [&](uint32_t stage) { commit(bar + (ST + stage) * 8, lead); };
+            uint32_t looked = 0, units = 0, task0 = 0, task1 = 0;
+            uint32_t st = 0, ph = 0;  // the ring's next slot: its stage, the parity of its barrier
+            bool ok = true;
+            const auto all = [&](uint64_t *b, uint32_t parity) { return __all_sync(full_warp, wait(b, parity, kDevErrWaitFull)) != 0; };
+            while (ok && __all_sync(full_warp, w.here(p))) {
+                const int n = (int)uniform((uint32_t)w.n);
+                const bool single = __any_sync(full_warp, w.k.rows <= 128);
+                const auto there = [&]() { return all(full + st, ph); };
+                const auto on = [&]() {
+                    if (++st == ST) st = 0, ph ^= 1;
+                };
+                const auto qk = [&](int s, uint32_t stage) {
+                    const uint32_t q = (uint32_t)dk + base + (single ? 0 : s * (P::TILE / 16));
+                    const uint32_t k = (uint32_t)dk + ring + stage * (P::TILE / 16);
 #pragma unroll
-                        for (int e = 0; e < HALVES * 4; ++e) {  // columns past head_dim are zeros in Q and K
-                            const uint32_t off = (e >> 2) * (HALF / 16) + (e & 3) * 2;
-                            // n > 0: the flag of the first one has to be a value of the run.  As a constant 0, in the
-                            // unrolled loop, the product came out added to what was in tensor memory.
-                            umma_f16(tmem + s * 128, dk + q + off, dk + k + off, iqk, e > 0 || n <= 0);
-                        }
-                        umma_commit(s_full + s);
-                    };
-                    const auto pv = [&](int s, uint32_t stage, int begun) {
-                        const uint32_t v = ring + stage * (P::TILE / 16);
+                    for (int e = 0; e < HALVES * 4; ++e) {  // columns past head_dim are zeros in Q and K
+                        const uint32_t off = (e >> 2) * (HALF / 16) + (e & 3) * 2;
+                        // n > 0: the flag of the first one has to be a value of the run.  As a constant 0, in the
+                        // unrolled loop, the product came out added to what was in tensor memory.
+                        mma_ss(acc + s * 128, q + off, k + off, k_hi, iqk, e > 0 || n <= 0, lead);
+                    }
+                    signal(s_full + s);
+                };
+                const auto pv = [&](int s, uint32_t stage, int begun) {
+                    const uint32_t v = (uint32_t)dv + ring + stage * (P::TILE / 16);
 #pragma unroll
-                        for (int e = 0; e < B / 16; ++e)
-                            umma_f16_ta(tmem + 256 + s * 128, tmem + s * 128 + e * 8, dv + v + e * 128, ipv, begun > 0 || e > 0);
-                        umma_commit(o_done + s);
-                    };
-                    const auto cut = [&](int i) { return w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks); };
-                    const auto probs = [&](int s) { return wait(p_full + s, task[s]++ & 1, kDevErrWaitFull); };
-                    ok = wait(q_full, units++ & 1, kDevErrWaitFull) && there();
+                    for (int e = 0; e < B / 16; ++e)
+                        mma_ts(acc + 256 + s * 128, acc + s * 128 + e * 8, v + e * 128, v_hi, ipv, begun > 0 || e > 0, lead);
+                    signal(o_done + s);
+                };
+                const auto cut = [&](int i) {
+                    return __any_sync(full_warp, w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks)) != 0;
+                };
+                const auto look_through = [&]() {
+                    if (lead) mbar_arrive(fix);
+                    __syncwarp();
+                };
+                const auto probs = [&](int s) { return all(p_full + s, (s ? task1++ : task0++) & 1); };
+                ok = all(q_full, units++ & 1) && there();
+                if (!ok) break;
+                tc_fence_after_sync();
+                qk(0, st);
+                if (!single) qk(1, st);
+                signal_empty(st);
+                on();
+                if (single && n > 1) {
+                    ok = there();
                     if (!ok) break;
                     tc_fence_after_sync();
-                    qk(0, st);
-                    if (!single) qk(1, st);
-                    umma_commit(empty + st);
+                    qk(1, st);
+                    signal_empty(st);
                     on();
-                    if (single && n > 1) {
+                }
+                if (single) {  // blocks in turn: V i and K i + 2
+                    for (int i = 0; ok && i < n; ++i) {
+                        const bool look = cut(i);
                         ok = there();
+                        if (look) look_through();  // V is looked through while the softmax runs
+                        ok = ok && (i & 1 ? probs(1) : probs(0)) && (!look || all(fixed, looked++ & 1));
                         if (!ok) break;
                         tc_fence_after_sync();
-                        qk(1, st);
-                        umma_commit(empty + st);
+                        if (i & 1)
+                            pv(1, st, i > 1);
+                        else
+                            pv(0, st, i > 1);
+                        signal_empty(st);
                         on();
-                    }
-                    if (single) {  // blocks in turn: V i and K i + 2
-                        for (int i = 0; ok && i < n; ++i) {
-                            const bool look = cut(i);
+                        if (i + 2 < n) {
                             ok = there();
-                            if (look) mbar_arrive(fix);  // V is looked through while the softmax runs
-                            ok = ok && (i & 1 ? probs(1) : probs(0)) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
                             if (!ok) break;
                             tc_fence_after_sync();
                             if (i & 1)
-                                pv(1, st, i > 1);
+                                qk(1, st);
                             else
-                                pv(0, st, i > 1);
-                            umma_commit(empty + st);
+                                qk(0, st);
+                            signal_empty(st);
                             on();
-                            if (i + 2 < n) {
-                                ok = there();
-                                if (!ok) break;
-                                tc_fence_after_sync();
-                                if (i & 1)
-                                    qk(1, st);
-                                else
-                                    qk(0, st);
-                                umma_commit(empty + st);
-                                on();
-                            }
                         }
-                    } else {
-                        for (int i = 0; ok && i < n; ++i) {  // V i and K i + 1, for one stream and then the other
-                            const bool look = cut(i), more = i + 1 < n;
-                            ok = there();
-                            const uint32_t sv = st;
+                    }
+                } else {
+                    for (int i = 0; ok && i < n; ++i) {  // V i and K i + 1, for one stream and then the other
+                        const bool look = cut(i), more = i + 1 < n;
+                        ok = there();
+                        const uint32_t sv = st;
+                        on();
+                        if (look) look_through();
+                        if (more) ok = ok && there();  // nothing is left to wait for but the softmax
+                        const uint32_t sk = st;
+                        ok = ok && probs(0) && (!look || all(fixed, looked++ & 1));
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        pv(0, sv, i);
+                        if (more) qk(0, sk);
+                        ok = probs(1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        pv(1, sv, i);
+                        if (more) qk(1, sk);
+                        signal_empty(sv);
+                        if (more) {
+                            signal_empty(sk);
                             on();
-                            if (look) mbar_arrive(fix);
-                            if (more) ok = ok && there();  // nothing is left to wait for but the softmax
-                            const uint32_t sk = st;
-                            ok = ok && probs(0) && (!look || wait(fixed, looked++ & 1, kDevErrWaitFull));
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            pv(0, sv, i);
-                            if (more) qk(0, sk);
-                            ok = probs(1);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            pv(1, sv, i);
-                            if (more) qk(1, sk);
-                            umma_commit(empty + sv);
-                            if (more) {
-                                umma_commit(empty + sk);
-                                on();
-                            }
                         }
                     }
                 }
-                umma_commit(drain);
-                if (!mbar_wait(drain, 0)) atomicExch(&g_tiles_err, kDevErrDrain);
             }
+            signal(drain);
+            if (!mbar_wait(drain, 0) && lead) atomicExch(&g_tiles_err, kDevErrDrain);
             __syncwarp();
         } else if (warp == 9) {
             // a lane to each box: page lane / HALVES of the block, 64-column half lane % HALVES
