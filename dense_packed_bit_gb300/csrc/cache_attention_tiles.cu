@@ -49,9 +49,9 @@ struct Plan {
     static constexpr int STAGES = HALVES == 2 ? 5 : 8;
     static constexpr int RING = 2 * TILE;       // behind Q; Q's place also holds a stream's O when two are joined
     static constexpr int BARS = RING + STAGES * TILE;
-    static constexpr int ML = BARS + 256;       // (m, l) of a stream's rows for the join
+    static constexpr int ML = BARS + (3 * STAGES + 16) * 8;  // (m, l) of a stream's rows for the join
     static constexpr int BYTES = ML + 1024 + 1024;  // alignment slack
-    static_assert(BYTES + 512 <= 232448 && RING >= 128 * HALVES * 64 * 4, "shared memory");
+    static_assert(STAGES / 2 + 1 < 8 && BYTES + 512 <= 232448 && RING >= 128 * HALVES * 64 * 4, "shared memory");
 };
 
 struct TilesArgs {
@@ -225,11 +225,12 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     __shared__ int sm_last, sm_more;
     uint8_t *sm = smem_aligned<1024>(raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + P::BARS);
-    uint64_t *full = bars, *empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_done = s_full + 4,
-             *drain = s_full + 6, *fix = s_full + 8, *fixed = s_full + 10, *q_full = s_full + 12;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 13);
+    uint64_t *full = bars, *empty = bars + ST, *seen = bars + 2 * ST, *s_full = bars + 3 * ST, *p_full = s_full + 2,
+             *o_done = s_full + 4, *drain = s_full + 6, *q_full = s_full + 7;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 8);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *poison = reinterpret_cast<volatile int *>(tmem_slot + 2);
+    // V of the CTA's unit i holds an infinity or NaN: poisons[i % 8] (warps 10 and 11 are at most ST / 2 + 1 units ahead)
+    volatile int *poisons = reinterpret_cast<volatile int *>(tmem_slot + 2);
 
     const CacheAttnArgs &a = p.a;
     const CacheView &c = a.c;
@@ -239,10 +240,11 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int sinks = a.sinks;
     if (tid == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1);
+        for (int i = 0; i < ST; ++i) mbar_init(full + i, 1), mbar_init(empty + i, 1), mbar_init(seen + i, 2);
         for (int i = 0; i < 2; ++i) mbar_init(s_full + i, 1), mbar_init(p_full + i, 4), mbar_init(o_done + i, 1);
-        mbar_init(drain, 1), mbar_init(fix, 1), mbar_init(fixed, 2), mbar_init(q_full, 8);
-        *fail = 0, *poison = 0;
+        mbar_init(drain, 1), mbar_init(q_full, 8);
+        *fail = 0;
+        for (int i = 0; i < 8; ++i) poisons[i] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
@@ -268,15 +270,17 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     __syncthreads();
     const uint32_t tmem = *tmem_slot;
     const int steps = (c.head_dim + 15) / 16;  // 16-element steps of the head dimension
-    const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
-        if (mbar_try_wait(bar, parity) || (!*fail && mbar_wait(bar, parity))) return true;
+    const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code, bool asleep = false) {
+        if (mbar_try_wait(bar, parity) || (!*fail && (asleep ? mbar_wait_sleep(bar, parity) : mbar_wait(bar, parity)))) return true;
         if (!*fail) atomicExch(&g_tiles_err, code);
         *fail = 1;
         return false;
     };
     // A unit's loads in the order of their use: K 0, V 0, K 1, ...; where the streams take turns K 0, then K i + 1
-    // and V i.  The slots of the ring count on over the CTA's units.
-    const auto slot_v = [](int i, int n, bool single) { return !single ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+    // and V i.  The slots of the ring count on over the CTA's units.  The block whose V load y is, -1 for K:
+    const auto block_of_v = [](int y, int n, bool single) {
+        return !single ? (y & 1 ? y >> 1 : -1) : y == 2 * n - 1 ? n - 1 : y > 0 && !(y & 1) ? y / 2 - 1 : -1;
+    };
 
     if (warp < 8) {
         const int s = warp >> 2, t = tid & 127;                 // stream, row of its tile
@@ -287,7 +291,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
         const int D = c.head_dim;
         uint32_t task = 0;  // blocks this stream has done
         bool ok = true;
-        while (true) {
+        for (uint32_t units = 0;; ++units) {
+            volatile int *poison = poisons + (units & 7);
             if (tid == 0) {
                 Walk next = sm_walk;
                 sm_more = !*fail && next.here(p);
@@ -617,14 +622,15 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             const uint32_t acc = uniform(tmem), bar = uniform(smem_u32(bars));
             const auto signal = [&](const uint64_t *b) { commit(bar + (uint32_t)(b - bars) * 8, lead); };
             const auto signal_empty = [&](uint32_t stage) { commit(bar + (ST + stage) * 8, lead); };
-            uint32_t looked = 0, units = 0, task0 = 0, task1 = 0;
+            uint32_t units = 0, task0 = 0, task1 = 0;
             uint32_t st = 0, ph = 0;  // the ring's next slot: its stage, the parity of its barrier
             bool ok = true;
             const auto all = [&](uint64_t *b, uint32_t parity) { return __all_sync(full_warp, wait(b, parity, kDevErrWaitFull)) != 0; };
             while (ok && __all_sync(full_warp, w.here(p))) {
                 const int n = (int)uniform((uint32_t)w.n);
                 const bool single = __any_sync(full_warp, w.k.rows <= 128);
-                const auto there = [&]() { return all(full + st, ph); };
+                // a lane to each of what has to be there
+                const auto there = [&]() { return all(lane == 0 ? full + st : seen + st, ph); };
                 const auto on = [&]() {
                     if (++st == ST) st = 0, ph ^= 1;
                 };
@@ -647,13 +653,6 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                         mma_ts(acc + 256 + s * 128, acc + s * 128 + e * 8, v + e * 128, v_hi, ipv, begun > 0 || e > 0, lead);
                     signal(o_done + s);
                 };
-                const auto cut = [&](int i) {
-                    return __any_sync(full_warp, w.k.cut(w.k.kb.block(w.b0 + i) * B, sinks)) != 0;
-                };
-                const auto look_through = [&]() {
-                    if (lead) mbar_arrive(fix);
-                    __syncwarp();
-                };
                 const auto probs = [&](int s) { return all(p_full + s, (s ? task1++ : task0++) & 1); };
                 ok = all(q_full, units++ & 1) && there();
                 if (!ok) break;
@@ -672,10 +671,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 }
                 if (single) {  // blocks in turn: V i and K i + 2
                     for (int i = 0; ok && i < n; ++i) {
-                        const bool look = cut(i);
-                        ok = there();
-                        if (look) look_through();  // V is looked through while the softmax runs
-                        ok = ok && (i & 1 ? probs(1) : probs(0)) && (!look || all(fixed, looked++ & 1));
+                        ok = there() && (i & 1 ? probs(1) : probs(0));
                         if (!ok) break;
                         tc_fence_after_sync();
                         if (i & 1)
@@ -697,15 +693,17 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                         }
                     }
                 } else {
-                    for (int i = 0; ok && i < n; ++i) {  // V i and K i + 1, for one stream and then the other
-                        const bool look = cut(i), more = i + 1 < n;
-                        ok = there();
-                        const uint32_t sv = st;
+                    for (int i = 0; i < n; ++i) {  // V i and K i + 1, for one stream and then the other
+                        const bool more = i + 1 < n;
+                        const uint32_t sv = st, pv_there = ph;
                         on();
-                        if (look) look_through();
-                        if (more) ok = ok && there();  // nothing is left to wait for but the softmax
                         const uint32_t sk = st;
-                        ok = ok && probs(0) && (!look || all(fixed, looked++ & 1));
+                        // a lane to each of what has to be there: V i, K i + 1, P
+                        uint64_t *b = p_full;
+                        uint32_t parity = task0++ & 1;
+                        if (lane < 2) b = (lane ? seen : full) + sv, parity = pv_there;
+                        if ((lane == 2 || lane == 3) && more) b = (lane == 3 ? seen : full) + sk, parity = ph;
+                        ok = all(b, parity);
                         if (!ok) break;
                         tc_fence_after_sync();
                         pv(0, sv, i);
@@ -770,46 +768,46 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 if (!mbar_wait(full + y % ST, (y / ST) & 1)) atomicExch(&g_tiles_err, kDevErrDrain);
             __syncwarp();
         } else {
-            uint32_t x0 = 0, looked = 0;
+            // Every slot of the ring is waited for in order (a barrier's phase may not pass unseen), and passed on
+            uint32_t st = 0, ph = 0;
             bool ok = true;
-            while (ok && w.here(p)) {
+            for (uint32_t units = 0; ok && w.here(p); ++units) {
                 const int n = w.n, end = w.k.end, low = w.k.low;
                 const bool single = w.k.rows <= 128;
-                for (int i = 0; ok && i < n; ++i) {
-                    const int key0 = w.k.kb.block(w.b0 + i) * B;
-                    if (!w.k.cut(key0, sinks)) continue;
-                    const uint32_t x = x0 + slot_v(i, n, single), st = x % ST;
-                    ok = __all_sync(0xffffffffu, wait(fix, looked++ & 1, kDevErrWaitFull) &&
-                                                     wait(full + st, (x / ST) & 1, kDevErrWaitFull));
+                for (int y = 0; y < 2 * n; ++y) {
+                    ok = __all_sync(0xffffffffu, wait(full + st, ph, kDevErrWaitFull, true));
                     if (!ok) break;
-                    uint8_t *v = sm + P::RING + st * P::TILE;
-                    // infinite or NaN: the magnitude's bits are kExp or more, and adding this carries into bit 15
-                    constexpr uint32_t up = (0x8000u - Pair<T>::kExp) * 0x10001u;
-                    uint32_t special = 0;
+                    const int i = block_of_v(y, n, single), key0 = i < 0 ? 0 : w.k.kb.block(w.b0 + i) * B;
+                    if (i >= 0 && w.k.cut(key0, sinks)) {
+                        uint8_t *v = sm + P::RING + st * P::TILE;
+                        // infinite or NaN: the magnitude's bits are kExp or more, and adding this carries into bit 15
+                        constexpr uint32_t up = (0x8000u - Pair<T>::kExp) * 0x10001u;
+                        uint32_t special = 0;
 #pragma unroll 1
-                    for (int e0 = tid - 320; e0 < P::TILE / 16; e0 += 8 * 64) {
-                        uint4 u[8];
+                        for (int e0 = tid - 320; e0 < P::TILE / 16; e0 += 8 * 64) {
+                            uint4 u[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(v + (e0 + 64 * k) * 16);
+                            for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(v + (e0 + 64 * k) * 16);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int e = e0 + 64 * k, j = key0 + ((e & 1023) >> 3);
-                            if (j >= end || (j >= sinks && j < low)) {
-                                *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
-                            } else {
-                                special |= (u[k].x & 0x7fff7fffu) + up;
-                                special |= (u[k].y & 0x7fff7fffu) + up;
-                                special |= (u[k].z & 0x7fff7fffu) + up;
-                                special |= (u[k].w & 0x7fff7fffu) + up;
+                            for (int k = 0; k < 8; ++k) {
+                                const int e = e0 + 64 * k, j = key0 + ((e & 1023) >> 3);
+                                if (j >= end || (j >= sinks && j < low)) {
+                                    *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    special |= (u[k].x & 0x7fff7fffu) + up;
+                                    special |= (u[k].y & 0x7fff7fffu) + up;
+                                    special |= (u[k].z & 0x7fff7fffu) + up;
+                                    special |= (u[k].w & 0x7fff7fffu) + up;
+                                }
                             }
                         }
+                        if (special & 0x80008000u) poisons[units & 7] = 1;
+                        fence_proxy_async_smem();
                     }
-                    if (special & 0x80008000u) *poison = 1;
-                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(fixed);
+                    if (lane == 0) mbar_arrive(seen + st);
+                    if (++st == ST) st = 0, ph ^= 1;
                 }
-                x0 += 2 * n;
             }
             __syncwarp();
         }
