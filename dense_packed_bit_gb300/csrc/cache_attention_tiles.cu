@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 // a lane to each of what has to be there
                 const auto there = [&]() { return all(lane == 0 ? full + st : seen + st, ph); };
                 const auto on = [&]() {
-                    if (++st == ST) st = 0, ph ^= 1;
+                    const uint32_t wrap = st + 1 == ST;
+                    st = uniform(wrap ? 0 : st + 1), ph ^= wrap;
                 };
                 const auto qk = [&](int s, uint32_t stage) {
                     const uint32_t q = (uint32_t)dk + base + (single ? 0 : s * (P::TILE / 16));
