@@ -1,7 +1,9 @@
 // cache_attention.cu -- attention over a paged cache: which kernel a call runs, and its workspace.
 //
-// Up to 16 rows (new tokens x query heads of a kv head) of a sequence: the rows kernel.  More: the tiles
-// kernel.
+// Up to 16 rows (new tokens x query heads of a kv head) of a sequence: the rows kernel, whose one m16 tile they fill.
+// More: the tiles kernel, whose 128-row products are mostly zeros below that.  Measured, rows and tiles kernel: 48
+// sequences of 100 to 16,000 tokens, 8 kv heads of 128 columns, 4 rows 100 and 151 us, 16 rows 107 and 151; 8 x 100 to
+// 1,000 tokens, 12 heads of 64, 16 rows 11.8 and 16.6; one sequence of 513, 1 row 8.7 and 15.7.
 #include "cache_attention.cuh"
 
 namespace mm {

@@ -281,6 +281,10 @@ __device__ __forceinline__ bool share_of(int items, int kv_heads, const ShareRul
     return true;
 }
 
+// A block reaches into pages that a window has released.  A box of keys needs its page if it begins in the sinks or
+// behind this key; `low`: the lowest key that a row may see outside them (a drafted token sees itself, so one more).
+__device__ __forceinline__ int last_unheld(const CacheAttnArgs &a, int low, int box) { return low + (a.mask ? 1 : 0) - box; }
+
 // One row by the definition, key by key, a warp to it: O[4 lane + x] in o (unnormalised over l > 0).
 // For what the tiles cannot do (infinities and NaN among values that only some rows see).
 template <typename T>

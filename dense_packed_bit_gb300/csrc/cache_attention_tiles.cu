@@ -18,12 +18,22 @@
 //
 // Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 the softmax of stream 0 and 1, warp 8 issues the MMAs,
 // warp 9 the TMA loads (one box per page and 64 columns; a page past the end reads as zeros), warps 10 and 11 look
-// after V where the mask cuts.  The MMA order PV(i), QK(i + 1) per stream, streams in turn, lets the tensor core
-// work on one stream while the other is in its softmax.  (One issuing warp per stream was 9% slower: the streams'
-// products then share the tensor core instead of taking turns, and their softmaxes coincide.)
+// after V where the mask cuts, as it arrives: they see every slot of the ring before the MMA warp does.  The MMA order
+// PV(i), QK(i + 1) per stream, streams in turn, lets the tensor core work on one stream while the other is in its
+// softmax.  (One issuing warp per stream was 9% slower: the streams' products then share the tensor core instead of
+// taking turns, and their softmaxes coincide.  P handed over in halves was 15% slower: the MMA warp then waits inside
+// a product with the other stream's ready.)  The MMA warp runs as one, with operands the compiler knows to be uniform:
+// issued from one thread's branch the same products took 12% longer.
 //
 // Split.  One CTA per SM, each with an even share of all units' blocks (share_of), the ring of K and V blocks
 // running through its units; the last CTA of a shared unit to finish joins the partial results in order.
+//
+// Bound: the tensor core and the softmax in turn.  Per pair of blocks (two streams, 128 keys) the products take 2,050
+// cycles at the rated speed and about 2,250 as issued; the softmax of a stream is 1,150 (128 exponentials a thread,
+// an eighth of a warp a cycle) and with its waits 1,500; a pair takes 2,900 to 3,100.  Measured, one call: a chunk of 4,096
+// tokens on 12,289 under a window of 4,096, 32 heads over 8 of 128 columns, bf16: 261 us = 1,069 TFLOP/s, 57% of a
+// library product's rate; 16 trees of 64 tokens on 2,500 to 8,000: 92 us; 4 chunks of 150 to 1,024 tokens on up to 700,
+// 12 heads of 64: 23 us.
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
 // memory (0 x NaN), and where the mask cuts between rows V is looked through: if it holds an infinity or NaN,
@@ -39,8 +49,8 @@ __device__ unsigned int g_tiles_err;
 
 constexpr int NT = 384, B = 128, ROWS = 256;
 constexpr int MIN_BLOCKS = 4;    // blocks of a part, at least: two to a stream
-constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA
-constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA (4 chunks: 22.9 us, cut 29.7)
+constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 92 us, with 0 100, with 8 94)
 constexpr int HALF = 16384;      // 128 rows of 64 elements, 128-byte swizzle
 
 template <int HALVES>
@@ -734,11 +744,12 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             bool ok = true;
             while (ok && w.here(p)) {
                 const int n = w.n, seq = w.item / p.tiles;
+                const int unheld = last_unheld(a, w.k.low, p.box);
                 const auto page_at = [&](int blk) {
                     const int key = w.k.kb.block(w.b0 + blk) * B + row;
                     if (blk >= n || lane >= ops || key >= w.k.end) return -1;
                     const int page = page_of(c, seq, key >> c.page_shift);
-                    if (page < 0) g_tiles_err = kDevErrRange;
+                    if (page < 0 && (key < sinks || key > unheld)) g_tiles_err = kDevErrRange;
                     return page;
                 };
                 const auto load = [&](const CUtensorMap *map, int blk, int page) {

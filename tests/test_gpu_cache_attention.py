@@ -101,6 +101,29 @@ def test_tree_parity(case, dtype):
     print(f"worst error {worst:.3f} of the tolerance")
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("new", [[1, 3, 2], [40, 90, 33]])
+@pytest.mark.parametrize("lens,window,sinks", [([300, 45, 16], 24, 3), ([319, 64, 40], 16, 0), ([301, 48, 39], 40, 17)])
+def test_pages_released_under_a_window(lens, window, sinks, new, tree):
+    # a block of keys reaches into pages that mm_cache_free has taken: no error, and their contents do not show
+    dtype, rng = "f16", np.random.default_rng(17)
+    c, dk, dv = make_cache(31, lens, new, 2, 64, 16, dtype)
+    k, v, table, _, refs = c.tensors
+    before = int((table >= 0).sum())
+    seqs = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    mm.mm_cache_free(c, seqs, len(lens), window, sinks)
+    assert int((table >= 0).sum()) < before
+    k[:, refs == 0] = float("nan")
+    v[:, refs == 0] = float("nan")
+    q = queries(4, sum(new), 4, 64, dtype)
+    bits = [tree_bits(rng, n) for n in new] if tree else None
+    mask = None
+    if tree:
+        words = -(-max(new) // 32)
+        mask = pack_bits(np.concatenate([np.pad(b, ((0, 0), (0, words * 32 - b.shape[1]))) for b in bits]), words).cuda()
+    check_attention(c, dk, dv, 0, q, new, lens, window, sinks, 0.125, dtype, bits=bits, mask=mask)
+
+
 @pytest.mark.parametrize("layout", ["tokens", "padded", "both"])
 @pytest.mark.parametrize("new", [[1, 1], [50, 90]])
 def test_layouts_layers_and_strides(layout, new):
