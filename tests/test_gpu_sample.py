@@ -217,6 +217,28 @@ def test_large_vocabulary_and_distribution():
     assert abs(count - share).max() <= 2 / n and (np.diff(t) >= 0).all()
 
 
+@pytest.mark.parametrize("rows", [4, 400])  # a row to all of an SM's warps, and four rows to an SM
+@pytest.mark.parametrize("what", ["wide", "all equal", "nearly equal", "unaligned", "two values"])
+def test_without_the_list(what, rows):
+    # top-k off or above 512: sums that pass 32 bits, a bin with more weights than its list, ties over a whole row
+    rng = np.random.default_rng(len(what))
+    if what == "wide":
+        x = logits_of(31, rows, 9001, "f32", scale=6.0)
+    elif what == "all equal":
+        x = torch.zeros((rows, 140001 if rows < 9 else 5000), dtype=torch.float16, device="cuda")
+    elif what == "nearly equal":
+        n = 70001 if rows < 9 else 6001
+        x = torch.from_numpy(np.stack([-1e-5 * rng.permutation(n) for _ in range(rows)]).astype(np.float32)).cuda()
+    elif what == "unaligned":
+        x = logits_of(32, rows, 3333, "bf16")[:, 1:3330]
+    else:
+        x = torch.from_numpy((rng.integers(0, 2, (rows, 4097)) * -0.5).astype(np.float32)).cuda()
+    k = [(0, 0, 1000, 5000)[r % 4] for r in range(rows)]
+    p = [(0.7, 1.0, 0.9, 1.0)[r % 4] for r in range(rows)]
+    q = [(0.0, 0.1, 0.0, 0.2)[(r // 4) % 4] for r in range(rows)]
+    check(x, [0.9] * rows, k, p, q, rng.random(rows))
+
+
 def test_refusals():
     x = logits_of(1, 2, 100, "f32")
     u = torch.zeros(2, device="cuda")
