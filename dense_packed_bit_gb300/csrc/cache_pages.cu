@@ -260,16 +260,33 @@ __global__ void __launch_bounds__(NT, 1) fork_alloc_kernel(const CacheView c, co
     if (threadIdx.x == 0) *missing = (int)lacking;
 }
 
+// n / d for 0 <= n < 2^31, 1 <= d <= 128 (a page's tokens, a row's vectors), by a product: a division for each
+// 16-byte vector took more of the copy than its loads
+struct Inverses {
+    uint32_t m[129], s[129];
+    constexpr Inverses() : m(), s() {
+        for (uint32_t d = 2; d <= 128; ++d) {
+            uint32_t bits = 0;
+            while ((1u << bits) < d) ++bits;
+            m[d] = (uint32_t)(((1ull << (31 + bits)) + d - 1) / d), s[d] = bits - 1;
+        }
+    }
+};
+__constant__ Inverses inverses = Inverses();
+__device__ __forceinline__ int divided(int n, int d) {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, inverses.m[d]) >> inverses.s[d]);
+}
+
 // `tokens` rows of every head of one layer's page: 16-byte vectors, four in flight per thread
 __device__ __forceinline__ void copy_page(const CacheView &c, char *base, int64_t src, int64_t dst, int tokens, int part,
                                           int parts) {
     const int vecs = c.head_dim / 8;  // 16-byte vectors per row
-    const int per_head = tokens * vecs, all = per_head * c.kv_heads;
+    const int all = tokens * vecs * c.kv_heads;
     const char *s = base + src * c.page_stride * 2;
     char *d = base + dst * c.page_stride * 2;
     const auto at = [&](int e) {
-        const int h = e / per_head, r = e - h * per_head, t = r / vecs;
-        return (h * c.head_stride + t * c.token_stride + (r - t * vecs) * 8) * 2;
+        const int row = divided(e, vecs), h = divided(row, tokens), t = row - h * tokens;
+        return (h * c.head_stride + t * c.token_stride + (e - row * vecs) * 8) * 2;
     };
     for (int e = part * CT + threadIdx.x; e < all; e += 4 * parts * CT) {
         uint4 v[4];
@@ -288,21 +305,22 @@ __device__ __forceinline__ void copy_page(const CacheView &c, char *base, int64_
     }
 }
 
-// grid (parts, 2 layers, n): the partial page's tokens; the CTAs of layer 0's keys also share the
-// full pages and fill the child's row of the table
+// grid (n, 2 layers, parts): the partial page's tokens; the CTAs of layer 0's keys also share the
+// full pages and fill the child's row of the table.  The children of one part of a page follow each other, so that
+// what they share of it is read once and found in L2 by the others.
 __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const int32_t *parents,
                                                        const int32_t *children, const int32_t *missing) {
     pdl_launch_dependents();
     pdl_wait();
     int p, ch;
     int64_t len;
-    if (*missing != 0 || !fork_pair(c, parents, children, blockIdx.z, &p, &ch, &len)) return;
+    if (*missing != 0 || !fork_pair(c, parents, children, blockIdx.x, &p, &ch, &len)) return;
     const int64_t full = len >> c.page_shift;
     const int rest = (int)(len & (c.page_size - 1));
     const int32_t *from = c.table + (int64_t)p * c.max_pages;
     int32_t *to = c.table + (int64_t)ch * c.max_pages;
     if (blockIdx.y == 0) {
-        for (int64_t j = blockIdx.x * CT + threadIdx.x; j < c.max_pages; j += gridDim.x * CT) {
+        for (int64_t j = blockIdx.z * CT + threadIdx.x; j < c.max_pages; j += gridDim.z * CT) {
             if (j == full && rest) continue;
             int page = -1;
             if (j < full) {
@@ -324,19 +342,19 @@ __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const 
         return;
     }
     char *base = (blockIdx.y & 1 ? c.v : c.k) + (blockIdx.y >> 1) * c.layer_stride * 2;
-    copy_page(c, base, src, dst, rest, blockIdx.x, gridDim.x);
+    copy_page(c, base, src, dst, rest, blockIdx.z, gridDim.z);
 }
 
 __global__ void __launch_bounds__(CT) copy_pages_kernel(const CacheView c, const int32_t *src, const int32_t *dst) {
     pdl_launch_dependents();
     pdl_wait();
-    const int s = src[blockIdx.z], d = dst[blockIdx.z];
+    const int s = src[blockIdx.x], d = dst[blockIdx.x];
     if (s < 0 || s >= c.pages || d < 0 || d >= c.pages) {
         range_error();
         return;
     }
     char *base = (blockIdx.y & 1 ? c.v : c.k) + (blockIdx.y >> 1) * c.layer_stride * 2;
-    copy_page(c, base, s, d, c.page_size, blockIdx.x, gridDim.x);
+    copy_page(c, base, s, d, c.page_size, blockIdx.z, gridDim.z);
 }
 
 // takes the page out of a table entry and drops one reference to it
@@ -515,7 +533,7 @@ cudaError_t launch_cache_fork(const CacheView &c, const int32_t *parents, const 
                               int32_t *missing, cudaStream_t s) {
     const cudaError_t e = launch_pdl(fork_alloc_kernel, dim3(1), NT, 0, s, c, parents, children, n, missing);
     if (e != cudaSuccess) return e;
-    return launch_pdl(fork_copy_kernel, dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, 0, s, c, parents,
+    return launch_pdl(fork_copy_kernel, dim3((unsigned)n, (unsigned)(2 * c.layers), copy_parts(c)), CT, 0, s, c, parents,
                       children, missing);
 }
 
@@ -526,7 +544,7 @@ cudaError_t launch_cache_free(const CacheView &c, const int32_t *list, int64_t n
 
 cudaError_t launch_cache_copy_pages(const CacheView &c, const int32_t *src, const int32_t *dst, int64_t n,
                                     cudaStream_t s) {
-    return launch_pdl(copy_pages_kernel, dim3(copy_parts(c), (unsigned)(2 * c.layers), (unsigned)n), CT, 0, s, c, src, dst);
+    return launch_pdl(copy_pages_kernel, dim3((unsigned)n, (unsigned)(2 * c.layers), copy_parts(c)), CT, 0, s, c, src, dst);
 }
 
 unsigned int cache_pages_take_device_error(cudaError_t *err) {
