@@ -70,7 +70,7 @@ struct TilesArgs {
     int box;    // keys of one TMA box
     int force_whole;
     FastDiv by_group, by_tiles;
-    int32_t *tickets, *poison;  // [seqs][tiles][kv_heads]
+    uint32_t *tickets;  // [seqs][tiles][kv_heads]: parts done, and 2^16 for each whose V holds an infinity or NaN
     float2 *ml;                 // [CTAs][2][256]
     float4 *part;               // [CTAs][2][head_dim / 4][256]
 };
@@ -89,9 +89,9 @@ __device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, float (&v)[32]) 
         : "memory");
 }
 // Waits for the loads begun.  What is then computed from them is computed with the values that pass through
-// here (a scale, two maxima, a key), so that none of it can be moved in front of the wait.
-__device__ __forceinline__ void tmem_ld_done(float2 &scale, float &m0, float &m1, int &key) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(scale.x), "+f"(scale.y), "+f"(m0), "+f"(m1), "+r"(key) : : "memory");
+// here (a scale, two maxima), so that none of it can be moved in front of the wait.
+__device__ __forceinline__ void tmem_ld_done(float2 &scale, float &m0, float &m1) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(scale.x), "+f"(scale.y), "+f"(m0), "+f"(m1) : : "memory");
 }
 
 // 16 columns of this thread's lane (the caller waits with tmem_wait_st)
@@ -358,22 +358,29 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 tc_fence_after_sync();
                 const int key0 = kb.block(b0 + blk) * B;
                 const bool cut = key0 + B > whole || (key0 < high && key0 + B > sinks);  // as UnitKeys::cut()
-                const auto masked = [&](float (&v)[32], int key) {
-                    if (!cut) return;
-                    const uint32_t bits = seen_bits(rv, key, sinks, sv.len, sv.count);
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = bits >> x & 1u ? v[x] : -INFINITY;
-                };
                 float mx = -INFINITY;
-                if (__any_sync(0xffffffffu, m == -INFINITY)) {  // the first block, or rows that have seen nothing yet
+                // The first block, or rows that have seen nothing yet: the maximum.  Where the mask cuts: -infinity into
+                // S first.  (In the loop below the same took more code than the instruction cache likes, in every block.)
+                if (cut || __any_sync(0xffffffffu, m == -INFINITY)) {
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         float v[32];
                         tmem_ld32(ts + 32 * q, v);
-                        masked(v, key0 + 32 * q);
+                        if (cut) {
+                            const uint32_t bits = seen_bits(rv, key0 + 32 * q, sinks, sv.len, sv.count);
+                            uint32_t u0[16], u1[16];
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) v[x] = bits >> x & 1u ? v[x] : -INFINITY;
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) u0[x] = __float_as_uint(v[x]), u1[x] = __float_as_uint(v[16 + x]);
+                            __syncwarp();
+                            tmem_st16(ts + 32 * q, u0);
+                            tmem_st16(ts + 32 * q + 16, u1);
+                        }
 #pragma unroll
                         for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
                     }
+                    tmem_wait_st();
                     mx *= scale2;
                 }
                 // P in the cache's type, two to a register: S stays in TMEM until it is known to hold
@@ -407,9 +414,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     float a0 = -INFINITY, a1 = -INFINITY;
                     const float2 one = make_float2(1.f, 1.f), bs = make_float2(base, base);
                     float2 sc = make_float2(scale2, scale2);
-                    int key = key0;
                     const auto probs = [&](float (&v)[32], int q) {
-                        masked(v, key + 32 * q);
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             float2 e = ffma2(make_float2(v[2 * x], v[2 * x + 1]), sc, bs);
@@ -424,16 +429,16 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     // the next 32 columns are on their way while 32 are worked on
                     float va[32], vb[32];
                     tmem_ld32_begin(ts, va);
-                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld_done(sc, a0, a1);
                     tmem_ld32_begin(ts + 32, vb);
                     probs(va, 0);
-                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld_done(sc, a0, a1);
                     tmem_ld32_begin(ts + 64, va);
                     probs(vb, 1);
-                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld_done(sc, a0, a1);
                     tmem_ld32_begin(ts + 96, vb);
                     probs(va, 2);
-                    tmem_ld_done(sc, a0, a1, key);
+                    tmem_ld_done(sc, a0, a1);
                     probs(vb, 3);
                     sum = make_float2(sum0.x + sum1.x, sum0.y + sum1.y);
                     mx = fmaxf(a0, a1) * scale2;
@@ -489,15 +494,13 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 tc_fence_before_sync();
                 bar_sync(1, 256);
                 if (tid == 0) {
-                    if (*poison) atomicOr(p.poison + unit, 1);
                     __threadfence();  // the unit's partial results before its ticket, the others' after it
-                    const bool last = atomicAdd(p.tickets + unit, 1) == u.used - 1;
-                    sm_last = last ? 1 : 0;
+                    const uint32_t mine = *poison ? 0x10001u : 1u, all = atomicAdd(p.tickets + unit, mine) + mine;
+                    const bool last = (all & 0xffffu) == (uint32_t)u.used;
+                    sm_last = last ? (all >> 16 ? 2 : 1) : 0;
                     if (last) {
                         __threadfence();
-                        if (atomicExch(p.poison + unit, 0)) sm_last = 2;
                         p.tickets[unit] = 0;  // ready for the next call
-                        __threadfence();
                     }
                     *poison = 0;
                 }
@@ -858,7 +861,7 @@ int cache_attention_tiles_ctas(const CacheView &c, int group, int64_t max_q, int
 
 int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int ctas) {
     const int64_t units = (int64_t)tile_count(group, max_q) * c.seqs * c.kv_heads;
-    return 2 * round256(units * 4) + (int64_t)ctas * 2 * ROWS * (8 + (int64_t)c.head_dim * 4);
+    return round256(units * 4) + (int64_t)ctas * 2 * ROWS * (8 + (int64_t)c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
@@ -866,11 +869,9 @@ cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaS
     const int64_t units = (int64_t)tiles * a.c.seqs * a.c.kv_heads;
     const int64_t most = units * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
     TilesArgs p{a, tiles, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), fast_div(a.group), fast_div(tiles),
-                nullptr, nullptr, nullptr, nullptr};
+                nullptr, nullptr, nullptr};
     char *w = static_cast<char *>(a.ws);
-    p.tickets = reinterpret_cast<int32_t *>(w);
-    w += round256(units * 4);
-    p.poison = reinterpret_cast<int32_t *>(w);
+    p.tickets = reinterpret_cast<uint32_t *>(w);
     w += round256(units * 4);
     p.part = reinterpret_cast<float4 *>(w);
     w += (int64_t)ctas * 2 * ROWS * a.c.head_dim * 4;
