@@ -35,7 +35,7 @@ __device__ unsigned int g_rows_err;
 
 constexpr int WARPS = 4, NT = (WARPS + 1) * 32;  // four warps compute, the fifth loads
 constexpr int SUB = 16, B = WARPS * SUB;         // keys of a warp's part of a block, of a block
-constexpr int MIN_BLOCKS = 3;    // blocks of a part, at least (8 x window of 1,024: 12.4 us, with 1 13.4, with 8 15.7)
+constexpr int MIN_BLOCKS = 1;    // blocks of a part, at least (see least_part)
 constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA
 constexpr int JOIN = 8;          // parts joined at a time
 constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU (48 ragged: 100 us, with 0 137)
