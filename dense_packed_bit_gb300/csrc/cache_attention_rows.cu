@@ -20,7 +20,7 @@
 //
 // Measured, one call: 48 sequences of 100 to 16,000 tokens, one new, 32 heads over 8 of 128 columns, bf16, pages of
 // 64: 100 us = 6.07 TB/s, 89% of a plain copy's.  Small calls are a latency of launch, share, first loads and join:
-// 1 x 513 (12 heads of 64) 8.7 us, 8 sequences of 32,000 under a window of 1,024 12.4, trees of 4 x 7 tokens 9.3.
+// 1 x 513 (12 heads of 64) 8.3 us, 8 sequences of 32,000 under a window of 1,024 13.0, trees of 4 x 7 tokens 9.3.
 //
 // What a row does not see: its score is replaced, not added to.  In blocks that the mask cuts,
 // infinities and NaN in V are taken out of the product (0 x NaN) and added to the rows that do see them.
@@ -36,7 +36,7 @@ __device__ unsigned int g_rows_err;
 constexpr int WARPS = 4, NT = (WARPS + 1) * 32;  // four warps compute, the fifth loads
 constexpr int SUB = 16, B = WARPS * SUB;         // keys of a warp's part of a block, of a block
 constexpr int MIN_BLOCKS = 1;    // blocks of a part, at least (see least_part)
-constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (30 x 100 to 500 tokens: 13.7 us, cut 19.2)
 constexpr int JOIN = 8;          // parts joined at a time
 constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU (48 ragged: 100 us, with 0 137)
 constexpr int HALF = B * 128;          // bytes of a block's 64 columns

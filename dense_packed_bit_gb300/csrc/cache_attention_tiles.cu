@@ -29,11 +29,11 @@
 // running through its units; the last CTA of a shared unit to finish joins the partial results in order.
 //
 // Bound: the tensor core and the softmax in turn.  Per pair of blocks (two streams, 128 keys) the products take 2,050
-// cycles at the rated speed and about 2,250 as issued; the softmax of a stream is 1,150 (128 exponentials a thread,
-// an eighth of a warp a cycle) and with its waits 1,500; a pair takes 2,900 to 3,100.  Measured, one call: a chunk of 4,096
-// tokens on 12,289 under a window of 4,096, 32 heads over 8 of 128 columns, bf16: 261 us = 1,069 TFLOP/s, 57% of a
-// library product's rate; 16 trees of 64 tokens on 2,500 to 8,000: 92 us; 4 chunks of 150 to 1,024 tokens on up to 700,
-// 12 heads of 64: 23 us.
+// cycles at the rated speed and about 2,250 as issued; a stream's softmax is about 1,100 (128 exponentials a thread) and
+// with its waits 1,500; a pair takes 2,900 to 3,100, a unit's first blocks and its join about 25,000 once.  Measured, one
+// call: a chunk of 4,096 tokens on 12,289 under a window of 4,096, 32 heads over 8 of 128 columns, bf16: 255 us = 1,094
+// TFLOP/s, 59% of a library product's rate; 16 trees of 64 tokens on 2,500 to 8,000: 92 us; 4 chunks of 150 to 1,024
+// tokens on up to 700, 12 heads of 64: 22.5 us, a chunk of 64 on 500 19 (launch, first loads, softmax after softmax).
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
 // memory (0 x NaN), and where the mask cuts between rows V is looked through: if it holds an infinity or NaN,
@@ -51,7 +51,7 @@ constexpr int NT = 384, B = 128, ROWS = 256;
 // blocks of a part, at least: joining takes as long as several (a chunk of 64 tokens on 500, 5 blocks: cut 23.3 us, whole
 // 19.0; of 200 on 1,000, 10 blocks: 3 parts 19.5, 2 20.8, whole 24)
 constexpr int MIN_BLOCKS = 4;
-constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there is one for each CTA (4 chunks: 22.9 us, cut 29.7)
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (the 4 chunks: 22.5 us, cut 29.7)
 constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 92 us, with 0 100, with 8 94)
 constexpr int HALF = 16384;      // 128 rows of 64 elements, 128-byte swizzle
 

@@ -22,7 +22,7 @@
 // the weights of the chosen bin go to shared memory in a second one, and linear bins narrow them there.  The token
 // is then found by sums over ever smaller stretches (general_row).
 //
-// Measured, one call: 1 x 50257 fp32 11.7 us and 64 x 50257 bf16 15.5 us, both latency (a dozen phases of barriers);
+// Measured, one call: 1 x 50257 fp32 10 to 12 us and 64 x 50257 bf16 15.5 us, both latency (a dozen phases of barriers);
 // 512 x 128000 fp32 69 us = 3.8 TB/s, of which the pass is 43 us at 6.1 TB/s and finding the bound, ranks and
 // sums the rest.  General path, the same three sizes: temperature alone 20, 25 and 137 us; top-p 42, 48 and 333;
 // top-k 1000 and top-p 52, 58 and 416 (with one 64-bit addition per token in shared memory and every level a
