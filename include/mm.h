@@ -2,7 +2,7 @@
  * mm.h -- C ABI of libmm: fp32 dense GEMM and packed 2-bit GEMV / skinny GEMM
  * on one NVIDIA GB300 (sm_103a).
  *
- * The two operations:
+ * The operations:
  *
  *  1. Dense fp32 matrix multiply  C = op(A) . op(B), C overwritten.
  *     "I built a GPT-2 in the browser, then made it 2.6x-12.1x faster",
@@ -29,6 +29,11 @@
  *     whole token" (the model's 4-bit weight-reading kernels, the fastest the
  *     pages measure) and "More Stumbling..." (the packed NF4 path).
  *
+ *  4. Serving between the packed products: a paged cache of keys and values,
+ *     attention of single tokens, chunks and trees of drafts over it, and the
+ *     choice of the next token (declared at the end of this file, with their
+ *     own types, layouts and error bounds).
+ *
  * Layouts (all row-major, all pointers DEVICE memory owned by the caller):
  *  - A: M x K (lda >= K), or K x M when transA (lda >= M).
  *  - B: K x N (ldb >= N), or N x K when transB (ldb >= K).
@@ -45,7 +50,7 @@
  *  - codebook: 4 (2-bit) or 16 (4-bit) fp32 values in HOST memory, read
  *    during the call; every entry must be finite.
  *
- * Arithmetic: fp32 accumulation everywhere.  Every output satisfies
+ * Arithmetic (1 to 3): fp32 accumulation everywhere.  Every output satisfies
  * |y - y_exact| <= 1e-5 * sum_k |term_k|; decoding of 2-bit fields is exact.
  *
  * Calls are asynchronous on `stream` (NULL = the legacy default stream); the
