@@ -12,7 +12,7 @@ int64_t cache_attention_workspace(const CacheView &c, int heads, int64_t tokens,
     (void)tokens;
     const int group = heads / c.kv_heads;
     if (max_q * group <= kRowsMax) return cache_attention_rows_workspace(c, cache_attention_rows_ctas(c, sms));
-    return cache_attention_tiles_workspace(c, group, max_q, cache_attention_tiles_ctas(c, group, max_q, sms));
+    return cache_attention_tiles_workspace(c, cache_attention_tiles_ctas(c, group, max_q, sms));
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, int sms, cudaStream_t s) {

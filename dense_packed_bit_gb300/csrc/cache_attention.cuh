@@ -170,6 +170,10 @@ struct ShareRules {
     int force_whole;  // the sums could pass 31 bits: whole units only
 };
 
+// A shared unit's ticket is that of the CTA with its first part: a CTA begins one unit at most that it does not finish.  So
+// the tickets take the same place in the workspace whatever the call's sizes, and no call's partial results lie there.
+constexpr int kTickets = 1024;
+
 struct ShareScratch {
     int a[32], b[32], most[32];
     int item, first;
@@ -351,7 +355,7 @@ cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaSt
 unsigned int cache_attention_rows_take_device_error(cudaError_t *err);
 // CTAs of the tiles kernel, one per SM at most
 int cache_attention_tiles_ctas(const CacheView &c, int group, int64_t max_q, int sms);
-int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int ctas);
+int64_t cache_attention_tiles_workspace(const CacheView &c, int ctas);
 cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaStream_t s);
 unsigned int cache_attention_tiles_take_device_error(cudaError_t *err);
 constexpr int kRowsMax = 16;  // rows (new tokens x heads of a kv head) of one sequence in the rows kernel

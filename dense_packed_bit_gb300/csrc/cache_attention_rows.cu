@@ -45,7 +45,7 @@ struct RowsArgs {
     CacheAttnArgs a;
     int box;           // keys of one TMA box
     int force_whole;
-    int32_t *tickets;  // [seqs][kv_heads]
+    int32_t *tickets;  // [kTickets]
     float2 *ml;        // [CTAs][2][16]
     float *part;       // [CTAs][2][16][head_dim]
 };
@@ -391,12 +391,11 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
             }
         }
         if (!alone) {
-            const int unit = seq * c.kv_heads + head;
             __syncthreads();
             if (threadIdx.x == 0) {
                 __threadfence();  // the block's partial results before its ticket, the others' after it
-                sm_last = atomicAdd(p.tickets + unit, 1) == u.used - 1;
-                if (sm_last) p.tickets[unit] = 0;  // ready for the next call
+                sm_last = atomicAdd(p.tickets + u.g0, 1) == u.used - 1;
+                if (sm_last) p.tickets[u.g0] = 0;  // ready for the next call
                 __threadfence();
             }
             __syncthreads();
@@ -451,8 +450,6 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
     }
 }
 
-int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
-
 template <typename T, int KS>
 cudaError_t launch(const RowsArgs &p, int ctas, cudaStream_t s) {
     constexpr int SMEM = 6 * 2 * HALF + 1024;  // the ring, and alignment
@@ -477,11 +474,12 @@ cudaError_t launch_t(const RowsArgs &p, int ctas, cudaStream_t s) {
 int cache_attention_rows_ctas(const CacheView &c, int sms) {
     const int64_t most = (int64_t)c.seqs * c.kv_heads * (((c.max_pages << c.page_shift) + B - 1) / B);  // blocks
     const int64_t ctas = (most + MIN_BLOCKS - 1) / MIN_BLOCKS;
-    return (int)(ctas < 2 * (int64_t)sms ? ctas : 2 * (int64_t)sms);
+    const int64_t cap = 2 * sms < kTickets ? 2 * sms : kTickets;
+    return (int)(ctas < cap ? ctas : cap);
 }
 
 int64_t cache_attention_rows_workspace(const CacheView &c, int ctas) {
-    return round256((int64_t)c.seqs * c.kv_heads * 4) + (int64_t)ctas * 32 * (8 + (int64_t)c.head_dim * 4);
+    return kTickets * 4 + (int64_t)ctas * 32 * (8 + (int64_t)c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
@@ -489,7 +487,7 @@ cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaSt
     const int64_t most = (int64_t)a.c.seqs * a.c.kv_heads * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
     RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), nullptr, nullptr, nullptr};
     p.tickets = reinterpret_cast<int32_t *>(w);
-    w += round256((int64_t)a.c.seqs * a.c.kv_heads * 4);
+    w += kTickets * 4;
     p.part = reinterpret_cast<float *>(w);
     p.ml = reinterpret_cast<float2 *>(w + (int64_t)ctas * 32 * a.c.head_dim * 4);
     return a.c.dtype == 0 ? launch_t<__half>(p, ctas, s) : launch_t<__nv_bfloat16>(p, ctas, s);

@@ -72,7 +72,7 @@ struct TilesArgs {
     int box;    // keys of one TMA box
     int force_whole;
     FastDiv by_group, by_tiles;
-    uint32_t *tickets;  // [seqs][tiles][kv_heads]: parts done, and 2^16 for each whose V holds an infinity or NaN
+    uint32_t *tickets;  // [kTickets]: parts done, and 2^16 for each whose V holds an infinity or NaN
     float2 *ml;                 // [CTAs][2][256]
     float4 *part;               // [CTAs][2][head_dim / 4][256]
 };
@@ -473,7 +473,6 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                             make_uint4(Pair<T>::pack(o[8 * x] * f, o[8 * x + 1] * f), Pair<T>::pack(o[8 * x + 2] * f, o[8 * x + 3] * f),
                                        Pair<T>::pack(o[8 * x + 4] * f, o[8 * x + 5] * f), Pair<T>::pack(o[8 * x + 6] * f, o[8 * x + 7] * f));
             };
-            const int unit = u.item * c.kv_heads + head;
             bool again = false;  // rows to be computed by the definition
             if (!u.alone) {
                 // partial results: both streams' of the same rows where they share a tile
@@ -497,12 +496,12 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 bar_sync(1, 256);
                 if (tid == 0) {
                     __threadfence();  // the unit's partial results before its ticket, the others' after it
-                    const uint32_t mine = *poison ? 0x10001u : 1u, all = atomicAdd(p.tickets + unit, mine) + mine;
+                    const uint32_t mine = *poison ? 0x10001u : 1u, all = atomicAdd(p.tickets + u.g0, mine) + mine;
                     const bool last = (all & 0xffffu) == (uint32_t)u.used;
                     sm_last = last ? (all >> 16 ? 2 : 1) : 0;
                     if (last) {
                         __threadfence();
-                        p.tickets[unit] = 0;  // ready for the next call
+                        p.tickets[u.g0] = 0;  // ready for the next call
                     }
                     *poison = 0;
                 }
@@ -837,8 +836,6 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     }
 }
 
-int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
-
 int tile_count(int group, int64_t max_q) { return (int)((max_q * group + ROWS - 1) / ROWS); }
 
 template <typename T, int HALVES>
@@ -858,12 +855,12 @@ cudaError_t launch(const TilesArgs &p, int ctas, cudaStream_t s) {
 int cache_attention_tiles_ctas(const CacheView &c, int group, int64_t max_q, int sms) {
     const int64_t blocks = ((c.max_pages << c.page_shift) + B - 1) / B;
     const int64_t most = (int64_t)tile_count(group, max_q) * c.seqs * c.kv_heads * ((blocks + MIN_BLOCKS - 1) / MIN_BLOCKS);
-    return (int)(most < sms ? most : sms);
+    const int cap = sms < kTickets ? sms : kTickets;
+    return (int)(most < cap ? most : cap);
 }
 
-int64_t cache_attention_tiles_workspace(const CacheView &c, int group, int64_t max_q, int ctas) {
-    const int64_t units = (int64_t)tile_count(group, max_q) * c.seqs * c.kv_heads;
-    return round256(units * 4) + (int64_t)ctas * 2 * ROWS * (8 + (int64_t)c.head_dim * 4);
+int64_t cache_attention_tiles_workspace(const CacheView &c, int ctas) {
+    return kTickets * 4 + (int64_t)ctas * 2 * ROWS * (8 + (int64_t)c.head_dim * 4);
 }
 
 cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
@@ -874,7 +871,7 @@ cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaS
                 nullptr, nullptr, nullptr};
     char *w = static_cast<char *>(a.ws);
     p.tickets = reinterpret_cast<uint32_t *>(w);
-    w += round256(units * 4);
+    w += kTickets * 4;
     p.part = reinterpret_cast<float4 *>(w);
     w += (int64_t)ctas * 2 * ROWS * a.c.head_dim * 4;
     p.ml = reinterpret_cast<float2 *>(w);

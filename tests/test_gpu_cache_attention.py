@@ -101,6 +101,23 @@ def test_tree_parity(case, dtype):
     print(f"worst error {worst:.3f} of the tolerance")
 
 
+def test_one_workspace_for_calls_of_any_size():
+    # one after the other in both kernels, with more and with fewer units, heads and columns: each as with its own workspace
+    dtype = "f16"
+    calls = []
+    for seed, (lens, new, heads, kv_heads, dim) in enumerate([([3000, 900], [1, 1], 8, 2, 128), ([5000], [1], 1, 1, 64),
+                                                              ([40, 1700, 300], [600, 300, 90], 8, 4, 64), ([700] * 40, [1] * 40, 16, 8, 64),
+                                                              ([2500], [40], 4, 1, 128), ([100] * 30, [300] * 30, 8, 8, 64)]):
+        c, _, _ = make_cache(seed, lens, new, kv_heads, dim, 64, dtype)
+        q = queries(seed, sum(new), heads, dim, dtype)
+        calls.append((c, q, new, run_attention(c, 0, q, new, 0, 0, 0.1),
+                      mm.mm_cache_attention_workspace(c, heads, sum(new), max(new))))
+    ws = torch.zeros(max(need for *_, need in calls), dtype=torch.uint8, device="cuda")
+    for i in (0, 5, 1, 2, 3, 4, 0, 2, 5, 3, 1, 0, 4, 2):
+        c, q, new, alone, _ = calls[i]
+        assert torch.equal(alone.view(torch.int16), run_attention(c, 0, q, new, 0, 0, 0.1, ws=ws).view(torch.int16)), i
+
+
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("new", [[1, 3, 2], [40, 90, 33]])
 @pytest.mark.parametrize("lens,window,sinks", [([300, 45, 16], 24, 3), ([319, 64, 40], 16, 0), ([301, 48, 39], 40, 17)])
