@@ -51,8 +51,8 @@ constexpr int NT = 384, B = 128, ROWS = 256;
 // blocks of a part, at least: joining takes as long as several (a chunk of 64 tokens on 500, 5 blocks: cut 23.3 us, whole
 // 19.0; of 200 on 1,000, 10 blocks: 3 parts 19.5, 2 20.8, whole 24)
 constexpr int MIN_BLOCKS = 4;
-constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (the 4 chunks: 22.5 us, cut 29.7)
-constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 92 us, with 0 100, with 8 94)
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (the 4 chunks: 22.2 us, cut 28.0)
+constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 92 us, with 0 101, with 8 94)
 constexpr int HALF = 16384;      // 128 rows of 64 elements, 128-byte swizzle
 
 template <int HALVES>
