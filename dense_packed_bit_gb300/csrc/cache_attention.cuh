@@ -135,6 +135,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A warp's, stream's or part's share (m, l) of a row that saw no key, so that it adds nothing.  m alone does not tell: a
+// maximum passes over NaN, so a share whose scores are all NaN has m = -infinity too, and its l, which is NaN, has to
+// reach the row.  Joined, ex2(-infinity - m) l is NaN for it whatever m is.
+__device__ __forceinline__ bool saw_nothing(float2 ml) { return ml.x == -INFINITY && ml.y == 0.f; }
+
 // Division by a number that is known at the launch: n / d = (n m) >> (31 + s) for 0 <= n < 2^31, with 2^s >= d
 // and m = ceil(2^(31 + s) / d) <= 2^32 - 1 (d = 1: m 0).
 struct FastDiv {

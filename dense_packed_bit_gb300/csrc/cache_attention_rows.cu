@@ -371,19 +371,17 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) mt = fmaxf(mt, sm_ml[w][r].x);
-            if (mt > -INFINITY) {
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const float2 ml = sm_ml[w][r];
-                    if (ml.x == -INFINITY) continue;
-                    const float f = ex2(ml.x - mt);
-                    const float2 x = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * OS + d);
-                    lt += f * ml.y;
-                    v.x += f * x.x, v.y += f * x.y;
-                }
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 ml = sm_ml[w][r];
+                if (saw_nothing(ml)) continue;
+                const float f = ex2(ml.x - mt);
+                const float2 x = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * OS + d);
+                lt += f * ml.y;
+                v.x += f * x.x, v.y += f * x.y;
             }
             if (alone) {
-                const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
+                const float inv = lt != 0.f ? 1.f / lt : 0.f;
                 *out_at(r, d) = Pair<T>::pack(v.x * inv, v.y * inv);
             } else {
                 *reinterpret_cast<float2 *>(p.part + (slot + r) * D + d) = v;
@@ -415,24 +413,23 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
                             const int64_t sl = (y + i == 0 ? slot0 : (int64_t)(u.g0 + min(y + i, used - 1)) * 32) + r;
                             ml[i] = __ldcg(&p.ml[sl]);
                             x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * D + d));
-                            if (y + i >= used) ml[i].x = -INFINITY;
+                            if (y + i >= used) ml[i] = make_float2(-INFINITY, 0.f);
                         }
                         float now = mt;
 #pragma unroll
                         for (int i = 0; i < JOIN; ++i) now = fmaxf(now, ml[i].x);
-                        if (now == -INFINITY) continue;
-                        const float f = ex2(mt - now);
+                        const float f = now == -INFINITY ? 1.f : ex2(mt - now);
                         mt = now;
                         lt *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
                         for (int i = 0; i < JOIN; ++i) {
+                            if (saw_nothing(ml[i])) continue;
                             const float w = ex2(ml[i].x - now);
-                            if (ml[i].x == -INFINITY) continue;
                             lt += w * ml[i].y;
                             v.x += w * x[i].x, v.y += w * x[i].y, v.z += w * x[i].z, v.w += w * x[i].w;
                         }
                     }
-                    const float inv = mt > -INFINITY ? 1.f / lt : 0.f;
+                    const float inv = lt != 0.f ? 1.f / lt : 0.f;
                     *reinterpret_cast<uint2 *>(out_at(r, d)) =
                         make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
                 }

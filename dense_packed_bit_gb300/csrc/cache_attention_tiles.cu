@@ -520,12 +520,12 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                         float mt = -INFINITY, lt = 0.f;
                         for (int y = 0; y < sources; ++y) {
                             const float2 q = __ldcg(p.ml + slot_of(y) + (single ? (y & 1) * 128 : 0) + half);
+                            if (saw_nothing(q)) continue;
                             const float now = fmaxf(mt, q.x);
-                            if (now == -INFINITY) continue;
-                            lt = lt * ex2(mt - now) + (q.x > -INFINITY ? q.y * ex2(q.x - now) : 0.f);
+                            lt = lt * (mt == -INFINITY ? 1.f : ex2(mt - now)) + q.y * ex2(q.x - now);
                             mt = now;
                         }
-                        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+                        const float inv = lt != 0.f ? 1.f / lt : 0.f;
                         const int ri = p.by_group.div(row0 + (int)half), rh = row0 + (int)half - ri * a.group;
                         uint4 *out = reinterpret_cast<uint4 *>(static_cast<char *>(a.O) +
                                                                ((int64_t)(sv.first + ri) * a.o_stride + (int64_t)(head * a.group + rh) * D) * 2);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     const float2 other = sm_ml[t];
                     const float mt = fmaxf(m, other.x);
                     const float f0 = m == -INFINITY ? 0.f : ex2(m - mt), f1 = other.x == -INFINITY ? 0.f : ex2(other.x - mt);
-                    const float lt = l * f0 + other.y * f1, inv = lt > 0.f ? 1.f / lt : 0.f;
+                    const float lt = l * f0 + other.y * f1, inv = lt != 0.f ? 1.f / lt : 0.f;
                     for (int d = 0; d < D; d += 32) {
                         float o[32];
                         tmem_ld32(to + d, o);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 bar_sync(1, 256);  // before Q's place is written again
                 if (tid == 0) *poison = 0;
             } else {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l != 0.f ? 1.f / l : 0.f;
                 for (int d = 0; d < D; d += 32) {
                     float o[32];
                     tmem_ld32(to + d, o);
