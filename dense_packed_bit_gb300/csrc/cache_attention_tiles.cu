@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                                     const float4 *src = p.part + at * (D / 4) + (int64_t)(2 * x) * ROWS + row;
 #pragma unroll
                                     for (int z = 0; z < 8; ++z)
-                                        g[k][z] = 2 * x + z < D / 4 ? __ldcg(src + z * ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                        // a part past the last adds 0, not 0 times what the last one holds (an infinity, say)
+                                        g[k][z] = 2 * x + z < D / 4 && y + k < sources ? __ldcg(src + z * ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
                                 }
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
