@@ -56,6 +56,17 @@ __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
     return v + (warp ? part[warp - 1] : 0);
 }
 
+// Sum over the block's NT values, each at most 2^24 (a row of the table): a warp's fits 32 bits, the block's does not.
+__device__ __forceinline__ int64_t block_sum(int v, int *part) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();  // part may still be read from the sum before
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int64_t s = 0;
+    for (int i = 0; i < NT / 32; ++i) s += part[i];
+    return s;
+}
+
 constexpr int PER = 16;  // refs per thread and step of the search: four 16-byte loads in flight
 
 // From page `from` on: puts the free pages of rank 0 .. want - 1 into list (want <= LIST) and
@@ -118,11 +129,10 @@ __device__ __forceinline__ int64_t allocate(const CacheView &c, int64_t n, Alloc
     for (int64_t i0 = 0; i0 < n; i0 += NT) {
         count(i0);
         __syncthreads();
-        int sum;
-        block_scan(sh.count[threadIdx.x], sh.part, &sum);
-        total += sum;
+        total += block_sum(sh.count[threadIdx.x], sh.part);
     }
     if (total == 0) return 0;
+    // (from here on total is at most the number of pages, so that the ranks below fit 32 bits)
     const int64_t have = free_pages(c, 0, min(total, (int64_t)LIST), sh.list, sh.part, &next);
     if (have < total) {
         int64_t more = 0, end;
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(NT, 1) reserve_kernel(const CacheView c, const
             });
         }
     };
-    const int64_t lacking = allocate(c, c.seqs, sh, count, give);
+    const int64_t lacking = min(allocate(c, c.seqs, sh, count, give), (int64_t)0x7fffffff);
     __syncthreads();
     if (lacking == 0)
         for (int64_t s = warp; s < c.seqs; s += NT / 32)

@@ -609,8 +609,8 @@ typedef struct {
  *
  * mm_cache_reserve: gives every sequence the pages of lens[s] + need[s] tokens, in the order
  *   of the sequences, keeping the pages it has.  Where the free pages do not suffice nothing
- *   is changed and *missing is how many are lacking (else 0).  A sequence whose tokens do not
- *   fit max_pages gets max_pages and is reported as out of range.
+ *   is changed and *missing is how many are lacking, at most 2^31 - 1 (else 0).  A sequence
+ *   whose tokens do not fit max_pages gets max_pages and is reported as out of range.
  * mm_cache_append: K, V [tokens][kv_heads][head_dim], tokens kv_token_stride elements apart:
  *   row q_start[s] + i goes to token lens[s] + i of layer `layer`.  q_start: [seqs + 1],
  *   ascending from 0 to tokens; max_new: an upper bound of q_start[s + 1] - q_start[s].
