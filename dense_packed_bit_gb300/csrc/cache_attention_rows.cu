@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
 
     Share share;
     const auto blocks = [&](int s) { return s < c.seqs ? seq_keys(a, s).kb.count : 0; };

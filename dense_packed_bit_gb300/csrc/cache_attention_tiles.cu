@@ -261,7 +261,6 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
-    pdl_launch_dependents();
     pdl_wait();
 
     Walk w;
@@ -280,6 +279,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
     tc_fence_after_sync();
     if (tid == 0) sm_walk = w;
     __syncthreads();
+    pdl_launch_dependents();  // not before: the next kernel's CTAs may take tensor memory, and then wait for this one
     const uint32_t tmem = *tmem_slot;
     const int steps = (c.head_dim + 15) / 16;  // 16-element steps of the head dimension
     const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code, bool asleep = false) {

@@ -182,8 +182,8 @@ __device__ __forceinline__ void reserve_range(const CacheView &c, const int32_t 
 // counts as wanted and the ranks stay; the marks are turned into pages at the end.
 __global__ void __launch_bounds__(NT, 1) reserve_kernel(const CacheView c, const int32_t *need, int32_t *missing) {
     __shared__ AllocShared sh;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // f(seq, entry, rank of the entry among the sequence's wanted ones)
     const auto each_wanted = [&](int64_t s, const auto &f) {
@@ -239,8 +239,8 @@ __device__ __forceinline__ bool fork_pair(const CacheView &c, const int32_t *par
 __global__ void __launch_bounds__(NT, 1) fork_alloc_kernel(const CacheView c, const int32_t *parents,
                                                            const int32_t *children, int64_t n, int32_t *missing) {
     __shared__ AllocShared sh;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const auto count = [&](int64_t i0) {
         const int64_t i = i0 + threadIdx.x;
         int p, ch, want = 0;
@@ -325,8 +325,8 @@ __device__ __forceinline__ void copy_page(const CacheView &c, char *base, int64_
 // what they share of it is read once and found in L2 by the others.
 __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const int32_t *parents,
                                                        const int32_t *children, const int32_t *missing) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     int p, ch;
     int64_t len;
     if (*missing != 0 || !fork_pair(c, parents, children, blockIdx.x, &p, &ch, &len)) return;
@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(CT) fork_copy_kernel(const CacheView c, const 
 }
 
 __global__ void __launch_bounds__(CT) copy_pages_kernel(const CacheView c, const int32_t *src, const int32_t *dst) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int s = src[blockIdx.x], d = dst[blockIdx.x];
     if (s < 0 || s >= c.pages || d < 0 || d >= c.pages) {
         range_error();
@@ -384,8 +384,8 @@ __device__ __forceinline__ void release(const CacheView &c, int32_t *entry) {
 
 __global__ void __launch_bounds__(CT) free_kernel(const CacheView c, const int32_t *list, int64_t window,
                                                   int64_t sinks) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int s = list[blockIdx.x];
     if (s < 0 || s >= c.seqs) {
         range_error();
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(CT) free_kernel(const CacheView c, const int32
 __global__ void __launch_bounds__(CT) append_kernel(const CacheView c, const char *K, const char *V,
                                                     int64_t token_stride, const int32_t *q_start, int64_t tokens,
                                                     int64_t max_new) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int s = blockIdx.y;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
     const int64_t len = c.lens[s];
@@ -448,8 +448,8 @@ __device__ __forceinline__ int kept_of(const int32_t *kept, int s, int count) {
 __global__ void __launch_bounds__(CT) compact_move_kernel(const CacheView c, const int32_t *q_start,
                                                           const int32_t *keep, const int32_t *kept, int64_t tokens,
                                                           int64_t max_new) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int s = blockIdx.y;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
     const int n = kept_of(kept, s, r.count);
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(CT) compact_move_kernel(const CacheView c, con
 
 __global__ void __launch_bounds__(CT) compact_table_kernel(const CacheView c, const int32_t *q_start,
                                                            const int32_t *kept, int64_t tokens, int64_t max_new) {
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int s = blockIdx.x;
     const RowRange r = rows_of(q_start, s, tokens, max_new, &g_pages_err);
     const int64_t len = c.lens[s];

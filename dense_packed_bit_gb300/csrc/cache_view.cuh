@@ -37,7 +37,8 @@ __device__ __forceinline__ RowRange rows_of(const int32_t *q_start, int seq, int
 }
 
 // Launches a kernel whose first step is pdl_wait(): it may become resident while the kernel before it in
-// the stream ends (that one's results are visible after the wait), which hides the launch itself.
+// the stream ends (that one's results are visible after the wait), which hides the launch itself.  The kernel calls
+// pdl_launch_dependents() behind its wait, so that one that starts without a wait of its own has only this one beside it.
 template <typename... P, typename... A>
 cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t lc = {};

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(512) gemv2_vec_kernel(const PackedArgs a, cons
             a.y[row] = scale * v;
         }
     }
+    pdl_wait_at_end(prefetch);
 }
 
 // Any cols, any alignment: one warp per row, lanes stride over the row's bytes.

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(512) gemv2_fp8_kernel(const __grid_constant__ 
         for (int j = waited; j < issued; ++j)
             if (!mbar_wait(&bars[j % ring], (j / ring) & 1)) atomicExch(&g_gemv_fp8_err, kDevErrDrain);
     }
+    pdl_wait_at_end(prefetch);
 }
 
 }  // namespace

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(RB == 1 ? 512 : 256) gemv2_mma_kernel(const Pa
                         a.y[row] = h2f(a.scales[row]) * __fadd_rn(__fmul_rn(c0, sx), __fmul_rn(dd, v[b][h]));
                 }
         }
+        pdl_wait_at_end(prefetch);
         return;
     }
     // ---- combine the KW partial sums in a fixed order
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(RB == 1 ? 512 : 256) gemv2_mma_kernel(const Pa
             if (row < a.rows) a.y[row] = h2f(a.scales[row]) * __fadd_rn(__fmul_rn(c0, sxa), __fmul_rn(dd, s1));
         }
     }
+    pdl_wait_at_end(prefetch);
 }
 
 constexpr int kMaxMmaCols = 32768;

@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) gemv2_mxf4_kernel(const __grid_co
     tc_fence_before_sync();
     __syncthreads();
     if (warp == PRODUCER_WARP) tmem_dealloc(tmem, TMEM_COLS);
+    pdl_wait_at_end(prefetch);
 }
 
 size_t mxf4_smem_bytes(int64_t cols, int ring) {

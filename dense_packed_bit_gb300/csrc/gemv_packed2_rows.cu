@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(NTHREADS) gemv2_rows_kernel(const __grid_const
         for (int j = waited; j < issued; ++j)
             if (!mbar_wait(&full[j % ring], (j / ring) & 1)) atomicExch(&g_gemv_rows_err, kDevErrDrain);
     }
+    pdl_wait_at_end(prefetch);
 }
 
 // ---------------------------------------------------------------- batches of matrices

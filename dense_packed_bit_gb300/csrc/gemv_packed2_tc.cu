@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(NTHREADS) gemv2_tc_kernel(const __grid_constan
     tc_fence_before_sync();
     __syncthreads();
     if (warp == PRODUCER_WARP) tmem_dealloc(tmem, TMEM_COLS);
+    pdl_wait_at_end(prefetch);
 }
 
 }  // namespace

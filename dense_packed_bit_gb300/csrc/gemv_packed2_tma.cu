@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(512) gemv2_tma_kernel(const __grid_constant__ 
     if (!ok && threadIdx.x == 0)
         for (int i = 0; i < RING && i < my_blocks; ++i)
             if (!mbar_wait(&full[i], 0) && !mbar_wait(&full[i], 1)) atomicExch(&g_gemv_tma_err, kDevErrDrain);
+    pdl_wait_at_end(prefetch);
 }
 
 }  // namespace

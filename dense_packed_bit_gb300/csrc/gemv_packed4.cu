@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(32 * NW) gemv4_lut_kernel(const __grid_constan
         for (int j = waited; j < issued; ++j)
             if (!mbar_wait(&full[j % ring], (j / ring) & 1)) atomicExch(&g_gemv4_err, kDevErrDrain);
     }
+    pdl_wait_at_end(prefetch);
 }
 
 // dynamic shared memory (the 32 KiB byte table is static)

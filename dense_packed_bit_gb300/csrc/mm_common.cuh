@@ -243,6 +243,13 @@ __device__ __forceinline__ void tma_prefetch_desc(const void *tmap) {
 // are visible.  A no-op when the grid was not launched as a dependent.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The end of a kernel that may run as an independent call (prefetch 2), without having waited: the grid completes after
+// the one it follows.  A grid that waits waits for the one in front of it alone, so without this one that follows an
+// independent call could run beside work from before that call.  One CTA is enough, and by then there is little to wait for.
+__device__ __forceinline__ void pdl_wait_at_end(int prefetch) {
+    if (prefetch == 2 && blockIdx.x == 0) pdl_wait();
+}
+
 // Allow the next dependent grid in the stream to begin launching.
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

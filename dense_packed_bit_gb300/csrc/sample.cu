@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     extern __shared__ __align__(16) uint8_t raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     constexpr int N = Vec<T>::N, G = 8 / N;  // vectors per group of 8
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const int64_t row = blockIdx.x, n = a.vocab;
     const T *x = static_cast<const T *>(a.logits) + row * a.stride;
     Row r;

@@ -435,8 +435,10 @@ typedef struct {
                             before the wait on the previous kernel (needs pdl) */
     int independent;     /* 1: promise that no work queued before this call writes
                             codes, scales or x, or reads y: the kernel then never
-                            waits for the previous kernel (needs pdl), so back-to-back
-                            calls over different matrices overlap completely */
+                            waits for the previous kernel before it starts (needs pdl), so
+                            back-to-back calls over different matrices overlap completely;
+                            it completes after that kernel, so work that waits for this call
+                            has waited for all queued before it */
     int staging;         /* MM_DEQ_MMA and MM_DEQ_AFFINE: 1 = code rows arrive in shared
                             memory by TMA (cols % 512 == 0, cols <= 4096; split and warps must
                             be 0).  MM_DEQ_MMA: 64-row blocks through a 2-deep ring per CTA,
@@ -519,7 +521,8 @@ mm_status mm_gemv_packed2_strided_batched(const uint8_t *codes, int64_t codes_st
  * time, 0 = spread evenly over the SMs).  With the fp4 decode, pdl, weights_static and
  * independent mean what they mean for one mm_gemv_packed2_ex call, the batch being one
  * kernel: independent = 1 promises that nothing this launch reads or writes is written by
- * the kernel before it in the stream, so that launch runs without waiting for it and
+ * the kernel before it in the stream (nor, where that is an independent call too, by the one
+ * before that, and so on), so that launch runs without waiting for it and
  * back-to-back batched launches overlap their first and last CTAs.  Every other field 0
  * (staging may be -1).  Each y_b then equals bit for bit the single MM_DEQ_MXF4 call's.
  * Errors: as mm_gemv_packed2_strided_batched, plus MM_ERR_INVALID_ARG for other options,
