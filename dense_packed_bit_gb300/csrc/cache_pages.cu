@@ -431,13 +431,13 @@ __global__ void __launch_bounds__(CT) append_kernel(const CacheView c, const cha
     }
 }
 
-// kept new tokens of sequence s, clamped to the new ones
+// kept new tokens of sequence s; -1: out of range, and the sequence is left as it is
 __device__ __forceinline__ int kept_of(const int32_t *kept, int s, int count) {
     if (!kept) return count;
     const int k = kept[s];
     if (k < 0 || k > count) {
         range_error();
-        return 0;
+        return -1;
     }
     return k;
 }
@@ -505,7 +505,9 @@ __global__ void __launch_bounds__(CT) compact_table_kernel(const CacheView c, co
         range_error();
         return;
     }
-    const int64_t now = len + kept_of(kept, s, r.count);
+    const int n = r.ok ? kept_of(kept, s, r.count) : -1;
+    if (n < 0) return;
+    const int64_t now = len + n;
     __syncthreads();  // before lens changes
     if (threadIdx.x == 0) c.lens[s] = (int)now;
     for (int64_t j = ((now + c.page_size - 1) >> c.page_shift) + threadIdx.x; j < c.max_pages; j += CT)

@@ -22,18 +22,19 @@ __device__ __forceinline__ int page_of(const CacheView &c, int seq, int64_t slot
 // tokens sequence `seq` can hold in its table row
 __device__ __forceinline__ int64_t row_capacity(const CacheView &c) { return c.max_pages << c.page_shift; }
 
-// [first, first + count) of sequence seq's rows of Q, clamped to [0, tokens) and max_q
+// [first, first + count) of sequence seq's rows of Q; out of range: no rows, and not ok
 struct RowRange {
     int first, count;
+    bool ok;
 };
 __device__ __forceinline__ RowRange rows_of(const int32_t *q_start, int seq, int64_t tokens, int64_t max_q,
                                             unsigned int *err) {
     const int64_t a = __ldg(q_start + seq), b = __ldg(q_start + seq + 1);
     if (a < 0 || b < a || b > tokens || b - a > max_q) {
         *err = kDevErrRange;
-        return {0, 0};
+        return {0, 0, false};
     }
-    return {(int)a, (int)(b - a)};
+    return {(int)a, (int)(b - a), true};
 }
 
 // Launches a kernel whose first step is pdl_wait(): it may become resident while the kernel before it in

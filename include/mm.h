@@ -622,6 +622,8 @@ typedef struct {
  *   lens[s] grows by kept[s], and pages that hold no token any more are released.
  *   keep: [tokens]; NULL: the first kept[s] stay where they are; kept NULL: all of them.
  *   The pages of new tokens must not be shared (fork copies the last page, so they are not).
+ *   A sequence whose rows or kept[s] are out of range is left as it is; a token whose entry
+ *   of keep does not rise or names no new token stays where it is.
  * mm_cache_fork: sequence children[i] becomes a copy of parents[i], i < n: the full pages are
  *   shared, the tokens of a last partial page copied to a page of its own, in all layers.
  *   Children hold no pages before (mm_cache_free) and are not parents.  *missing as above.
