@@ -299,6 +299,11 @@ __device__ __forceinline__ bool share_of(int items, int kv_heads, const ShareRul
 // A block reaches into pages that a window has released.  A box of keys needs its page if it begins in the sinks or
 // behind this key; `low`: the lowest key that a row may see outside them (a drafted token sees itself, so one more).
 __device__ __forceinline__ int last_unheld(const CacheAttnArgs &a, int low, int box) { return low + (a.mask ? 1 : 0) - box; }
+// The exception, a row of a tree with no bit at all: it sits at len - 1 and sees key len - window, whose page may be gone.
+__device__ __forceinline__ void check_held(const CacheAttnArgs &a, int seq, const SeqView &sv, const RowView &r, unsigned int *err) {
+    if (a.mask && a.window > 0 && r.low == sv.len - a.window && r.low >= a.sinks && page_of(a.c, seq, r.low >> a.c.page_shift) < 0)
+        *err = kDevErrRange;
+}
 
 // One row by the definition, key by key, a warp to it: O[4 lane + x] in o (unnormalised over l > 0).
 // For what the tiles cannot do (infinities and NaN among values that only some rows see).

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(NT, 2) rows_kernel(const __grid_constant__ CUt
             for (int h = 0; h < 2; ++h) {
                 const int r = min((lane >> 2) + 8 * h, rows - 1), i = r / a.group;
                 rv[h] = row_view(a, sv.len, sv.first, sv.count, i);
+                check_held(a, seq, sv, rv[h], &g_rows_err);
                 tree[h] = rv[h].bits ? __ldg(rv[h].bits) & ((1u << sv.count) - 1u) : 0u;  // count <= 16
                 src[h] = reinterpret_cast<const uint32_t *>(
                     static_cast<const char *>(a.Q) +

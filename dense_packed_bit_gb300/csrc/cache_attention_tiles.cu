@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
             const int r = single ? t : s * 128 + t;  // row of the unit's 256
             const int rc = min(r, nrows - 1), i = p.by_group.div(row0 + rc);
             const RowView rv = row_view(a, sv.len, sv.first, sv.count, i);
+            check_held(a, p.by_tiles.div(u.item), sv, rv, &g_tiles_err);
             float m = -INFINITY, l = 0.f;
             int done = 0;
             for (int blk = single ? s : 0; blk < n; blk += single ? 2 : 1, ++done, ++task) {

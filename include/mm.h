@@ -662,6 +662,8 @@ mm_status mm_cache_copy_pages(const mm_cache *cache, const int32_t *src, const i
  *   set, and of the keys before lens[s] those that the window and sinks leave to position
  *   p = lens[s] + (bits set) - 1, its depth.  Bits at or past the sequence's count of new
  *   tokens are ignored.
+ *   A row without a bit sits at lens[s] - 1 and sees one token more than any other, which
+ *   mm_cache_free under the same window may have released; the call then reports it.
  * A row that sees no key gives 0; a NaN in a score that it does see makes it NaN.  Keys and
  * values that a row does not see have no influence on it, whatever they hold (NaN and
  * infinities in released or never written rows included).
