@@ -986,6 +986,10 @@ mm_status check_cache(const mm_cache *c, int64_t layer, bool needs_refs, mm::Cac
         if (counts[i] > 1 && strides[i] < c->head_dim)
             return fail(MM_ERR_INVALID_ARG, "a cache stride is below head_dim: rows overlap");
     }
+    // from the first element to the last, in numbers that cannot overflow: every offset fits 64 bits with room
+    double elements = (double)c->head_dim;
+    for (int i = 0; i < 4; ++i) elements += (double)(counts[i] - 1) * (double)strides[i];
+    if (elements > (double)((int64_t)1 << 46)) return fail(MM_ERR_INVALID_ARG, "k and v span more than 2^47 bytes");
     if (c->seqs * c->kv_heads > (1 << 24)) return fail(MM_ERR_INVALID_ARG, "seqs * kv_heads is above 2^24");
     if (c->max_pages * c->page_size > ((int64_t)1 << 30))
         return fail(MM_ERR_INVALID_ARG, "a sequence holds at most 2^30 tokens (max_pages * page_size)");

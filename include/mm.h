@@ -589,7 +589,8 @@ typedef enum { MM_F16 = 0, MM_BF16 = 1, MM_F32 = 2 } mm_dtype;
  *   attention are called.  A page is allocated by the calls below lowest number first.
  * page_size: 16, 32, 64 or 128; head_dim: a multiple of 8 up to 128; dtype: MM_F16 or
  *   MM_BF16; k, v 16-byte aligned and every stride a multiple of 8 elements.
- * At most 32767 layers, 2^31 - 1 pages, 65535 seqs and kv_heads, 2^24 seqs * kv_heads.
+ * At most 32767 layers, 2^31 - 1 pages, 65535 seqs and kv_heads, 2^24 seqs * kv_heads, and
+ * 2^47 bytes from the first element of k (or v) to its last.
  * The struct is host memory, read during each call.
  */
 typedef struct {

@@ -1,0 +1,35 @@
+"""Sizes, strides and workspaces that the cache calls refuse before any CUDA call (no GPU needed; no pointer passed is ever
+dereferenced)."""
+import ctypes
+
+import pytest
+
+import dense_packed_bit_gb300 as mm
+from dense_packed_bit_gb300 import build as mmbuild
+from test_abi_cache import P, cache, refused
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mmbuild.build()
+    return mm.load_library()
+
+
+BIG = 1 << 38  # the largest stride
+
+
+@pytest.mark.parametrize("far", [dict(pages=(1 << 31) - 1, page_stride=BIG), dict(pages=1 << 20, page_stride=BIG),
+                                 dict(layers=32767, layer_stride=BIG), dict(kv_heads=65535, seqs=1, head_stride=BIG)], ids=str)
+def test_a_cache_past_any_memory(lib, far):
+    # pages 2^38 elements apart, 2^31 of them: the last one's offset passes 64 bits
+    c = cache(**far)
+    refused(lib, lib.mm_cache_free(c, P[5], 1, 0, 0, None))
+    refused(lib, lib.mm_cache_append(c, 0, P[5], P[6], c.kv_heads * 64, P[7], 5, 3, None))
+    refused(lib, lib.mm_cache_attention(c, 0, P[5], c.kv_heads * 64, c.kv_heads, P[6], 5, 3, 0, 0, 0.125, P[7], c.kv_heads * 64, P[8], 1 << 40, None))
+    assert "bytes" in lib.mm_last_error().decode()
+
+
+def test_a_large_cache_is_not(lib):
+    # 2^45 elements from end to end: more than there is, but every offset is a number
+    n = ctypes.c_int64(-1)
+    assert lib.mm_cache_attention_workspace(cache(pages=1 << 20, page_stride=1 << 25), 4, 5, 3, ctypes.byref(n)) == mm.MM_OK and n.value > 0
