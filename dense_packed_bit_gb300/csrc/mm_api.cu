@@ -1031,6 +1031,14 @@ int sm_count() {
     return sms;
 }
 
+// 32 bits number the rows of a sequence and the units (256 of them) of all sequences and kv heads
+mm_status check_units(const mm_cache *c, int64_t heads, int64_t max_q) {
+    const int64_t rows = max_q * (heads / c->kv_heads), most = (int64_t)1 << 30;
+    if (rows > most || (rows / 256 + 1) * c->seqs * c->kv_heads > most)
+        return fail(MM_ERR_INVALID_ARG, "max_q is too large for so many heads and sequences");
+    return MM_OK;
+}
+
 uint64_t page_bytes_span(const mm_cache *c) {
     return (uint64_t)((c->layers - 1) * c->layer_stride + (c->pages - 1) * c->page_stride +
                       (c->kv_heads - 1) * c->head_stride + (c->page_size - 1) * c->token_stride + c->head_dim) * 2;
@@ -1050,9 +1058,8 @@ mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, i
     if (heads < 1 || heads > 65535 || heads % cache->kv_heads)
         return fail(MM_ERR_INVALID_ARG, "heads (%lld) must be a multiple of kv_heads (%lld), at most 65535", (long long)heads,
                     (long long)cache->kv_heads);
-    if (max_q * (heads / cache->kv_heads) > ((int64_t)1 << 30) ||
-        (max_q * (heads / cache->kv_heads) / 256 + 1) * cache->seqs * cache->kv_heads > ((int64_t)1 << 30))
-        return fail(MM_ERR_INVALID_ARG, "max_q is too large for so many heads and sequences");
+    s = check_units(cache, heads, max_q);
+    if (s != MM_OK) return s;
     const int64_t width = heads * cache->head_dim;
     if ((tokens > 1 && (q_stride < width || o_stride < width)) || q_stride < 0 || o_stride < 0 || q_stride % 8 || o_stride % 8 ||
         q_stride > ((int64_t)1 << 31) || o_stride > ((int64_t)1 << 31))
@@ -1191,10 +1198,12 @@ mm_status mm_cache_attention_workspace(const mm_cache *cache, int64_t heads, int
                                        int64_t *bytes) {
     mm::CacheView c;
     if (!bytes) return fail(MM_ERR_INVALID_ARG, "bytes is NULL");
-    const mm_status s = check_cache(cache, -1, false, &c);
+    mm_status s = check_cache(cache, -1, false, &c);
     if (s != MM_OK) return s;
     if (heads < 1 || heads > 65535 || heads % cache->kv_heads || tokens < 1 || tokens > 0x7fffffff || max_q < 1 || max_q > tokens)
         return fail(MM_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, 1 <= max_q <= tokens");
+    s = check_units(cache, heads, max_q);
+    if (s != MM_OK) return s;
     *bytes = mm::cache_attention_workspace(c, (int)heads, tokens, max_q, sm_count());
     return ok();
 }

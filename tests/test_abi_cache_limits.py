@@ -33,3 +33,12 @@ def test_a_large_cache_is_not(lib):
     # 2^45 elements from end to end: more than there is, but every offset is a number
     n = ctypes.c_int64(-1)
     assert lib.mm_cache_attention_workspace(cache(pages=1 << 20, page_stride=1 << 25), 4, 5, 3, ctypes.byref(n)) == mm.MM_OK and n.value > 0
+
+
+@pytest.mark.parametrize("heads,tokens,most", [(65534, (1 << 31) - 1, (1 << 31) - 1), (2 << 14, 1 << 20, 1 << 20), (4, (1 << 31) - 1, 1 << 30)])
+def test_workspace_of_sizes_that_no_call_takes(lib, heads, tokens, most):
+    # the rows of one sequence (new tokens times query heads of a kv head) pass 2^30: attention refuses, and so does this
+    c, n = cache(), ctypes.c_int64(-1)
+    refused(lib, lib.mm_cache_attention_workspace(c, heads, tokens, most, ctypes.byref(n)))
+    assert n.value == -1
+    refused(lib, lib.mm_cache_attention(c, 0, P[5], heads * 64, heads, P[6], tokens, most, 0, 0, 0.125, P[7], heads * 64, P[8], 1 << 40, None))
