@@ -1081,14 +1081,18 @@ mm_status cache_attention(const mm_cache *cache, int64_t layer, const void *Q, i
     a.mask_words = mask_words;
     a.heads = (int)heads, a.group = (int)(heads / cache->kv_heads);
     a.scale = scale, a.ws = workspace;
-    s = check_device();
-    if (s != MM_OK) return s;
     const int sms = sm_count();
     const int64_t need = mm::cache_attention_workspace(a.c, a.heads, tokens, max_q, sms);
     if (need > 0 && (!workspace || !is_aligned(workspace, 16) || workspace_bytes < need))
         return fail(MM_ERR_INVALID_ARG, "the workspace is NULL, not 16-byte aligned or below %lld bytes", (long long)need);
-    if (need > 0 && (overlap(O, ob, workspace, (uint64_t)need) || overlap(Q, qb, workspace, (uint64_t)need)))
-        return fail(MM_ERR_INVALID_ARG, "the workspace overlaps Q or O");
+    const auto in_workspace = [&](const void *p, uint64_t bytes) { return need > 0 && overlap(p, bytes, workspace, (uint64_t)need); };
+    if (in_workspace(O, ob) || in_workspace(Q, qb) || in_workspace(cache->k, cb) || in_workspace(cache->v, cb) ||
+        in_workspace(q_start, (uint64_t)(cache->seqs + 1) * 4) || in_workspace(cache->table, (uint64_t)(cache->seqs * cache->max_pages) * 4) ||
+        in_workspace(cache->lens, (uint64_t)cache->seqs * 4) || (cache->refs && in_workspace(cache->refs, (uint64_t)cache->pages * 4)) ||
+        (mask && in_workspace(mask, (uint64_t)(tokens * mask_words) * 4)))
+        return fail(MM_ERR_INVALID_ARG, "the workspace overlaps Q, O, the cache, q_start or the mask");
+    s = check_device();
+    if (s != MM_OK) return s;
     const cudaError_t e = mm::launch_cache_attention(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
     return ok();

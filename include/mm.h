@@ -677,7 +677,7 @@ mm_status mm_cache_copy_pages(const mm_cache *cache, const int32_t *src, const i
  * 16-byte aligned, zeroed once before its first use; every call leaves it ready for the
  * next one in stream order, whatever the sizes of either.  Two calls at once need two workspaces.
  * Errors: MM_ERR_INVALID_ARG as above, for heads not a multiple of kv_heads, a non-finite
- * scale, O overlapping an input or a workspace that is too small.
+ * scale, O overlapping an input, or a workspace that is too small or overlaps anything else.
  */
 mm_status mm_cache_attention_workspace(const mm_cache *cache, int64_t heads, int64_t tokens, int64_t max_q,
                                        int64_t *bytes);

@@ -42,3 +42,17 @@ def test_workspace_of_sizes_that_no_call_takes(lib, heads, tokens, most):
     refused(lib, lib.mm_cache_attention_workspace(c, heads, tokens, most, ctypes.byref(n)))
     assert n.value == -1
     refused(lib, lib.mm_cache_attention(c, 0, P[5], heads * 64, heads, P[6], tokens, most, 0, 0, 0.125, P[7], heads * 64, P[8], 1 << 40, None))
+
+
+@pytest.mark.parametrize("what", ["k", "v", "the end of v", "table", "lens", "refs", "q_start", "mask", "Q", "O"])
+def test_workspace_over_what_the_call_reads_or_keeps(lib, what):
+    # the split's partial results would be written over it
+    c, last = cache(), 10 * 2048 * 2 * 2 - 16
+    at = {"k": P[0], "v": P[1] - 4096 * 2, "the end of v": P[1] + last, "table": P[2], "lens": P[3], "refs": P[4], "q_start": P[6],
+          "mask": P[9], "Q": P[5] - 16, "O": P[7] + 256}[what]
+    front = (c, 0, P[5], 256, 4, P[6], 5, 3)
+    back = (0, 0, 0.125, P[7], 256, at, 1 << 40, None)
+    refused(lib, lib.mm_cache_attention_tree(*front, P[9], 1, *back))
+    assert "workspace overlaps" in lib.mm_last_error().decode()
+    if what != "mask":
+        refused(lib, lib.mm_cache_attention(*front, *back))
