@@ -174,6 +174,8 @@ struct ShareRules {
     int min_blocks, whole_blocks, unit_cost;
     int force_whole;  // the sums could pass 31 bits: whole units only
 };
+// All units end to end, at most: the last CTA's end, before it is cut, passes the sum by less than one for each CTA
+constexpr int64_t kShareLimit = ((int64_t)1 << 31) - 4096;
 
 // A shared unit's ticket is that of the CTA with its first part: a CTA begins one unit at most that it does not finish.  So
 // the tickets take the same place in the workspace whatever the call's sizes, and no call's partial results lie there.
@@ -270,7 +272,7 @@ __device__ __forceinline__ bool share_of(int items, int kv_heads, const ShareRul
     const int all = s.parts ? units * s.parts : (total + s.cost * count) * kv_heads;
     s.chunk = (int)((uint32_t)(all + grid - 1) / (uint32_t)grid);
     if (!s.parts) s.chunk = max(s.chunk, rules.min_blocks);
-    s.at = (int)blockIdx.x * s.chunk;  // < 2^31: about all
+    s.at = (int)blockIdx.x * s.chunk;  // this and the end below: < 2^31 (kShareLimit)
     if (s.at >= all) return false;
     s.stop = min(s.at + s.chunk, all);
     int before = 0;

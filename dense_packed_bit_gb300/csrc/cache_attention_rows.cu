@@ -483,7 +483,7 @@ int64_t cache_attention_rows_workspace(const CacheView &c, int ctas) {
 cudaError_t launch_cache_attention_rows(const CacheAttnArgs &a, int ctas, cudaStream_t s) {
     char *w = static_cast<char *>(a.ws);
     const int64_t most = (int64_t)a.c.seqs * a.c.kv_heads * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
-    RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), nullptr, nullptr, nullptr};
+    RowsArgs p{a, a.c.page_size < B ? a.c.page_size : B, most >= kShareLimit, nullptr, nullptr, nullptr};
     p.tickets = reinterpret_cast<int32_t *>(w);
     w += kTickets * 4;
     p.part = reinterpret_cast<float *>(w);

@@ -869,7 +869,7 @@ cudaError_t launch_cache_attention_tiles(const CacheAttnArgs &a, int ctas, cudaS
     const int tiles = tile_count(a.group, a.max_q);
     const int64_t units = (int64_t)tiles * a.c.seqs * a.c.kv_heads;
     const int64_t most = units * (((a.c.max_pages << a.c.page_shift) + B - 1) / B + UNIT_COST);
-    TilesArgs p{a, tiles, a.c.page_size < B ? a.c.page_size : B, most >= ((int64_t)1 << 31), fast_div(a.group), fast_div(tiles),
+    TilesArgs p{a, tiles, a.c.page_size < B ? a.c.page_size : B, most >= kShareLimit, fast_div(a.group), fast_div(tiles),
                 nullptr, nullptr, nullptr};
     char *w = static_cast<char *>(a.ws);
     p.tickets = reinterpret_cast<uint32_t *>(w);
