@@ -452,11 +452,11 @@ template <typename T, int KS>
 cudaError_t launch(const RowsArgs &p, int ctas, cudaStream_t s) {
     constexpr int SMEM = 6 * 2 * HALF + 1024;  // the ring, and alignment
     static_assert(SMEM - 1024 >= WARPS * 16 * (KS * 16 + 4) * 4, "the warps' O fit in the rings");
-    static const cudaError_t once =
-        cudaFuncSetAttribute(rows_kernel<T, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (once != cudaSuccess) return once;
+    static SmemLimit limit;
+    cudaError_t e = limit.allow((const void *)rows_kernel<T, KS>, SMEM);
+    if (e != cudaSuccess) return e;
     CUtensorMap k, v;
-    cudaError_t e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
+    e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
     if (e == cudaSuccess) e = cache_tmap(&v, p.a.c, p.a.c.v, p.box);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_kernel<T, KS>, dim3((unsigned)ctas), NT, SMEM, s, k, v, p);

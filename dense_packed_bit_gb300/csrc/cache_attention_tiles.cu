@@ -842,11 +842,11 @@ int tile_count(int group, int64_t max_q) { return (int)((max_q * group + ROWS - 
 
 template <typename T, int HALVES>
 cudaError_t launch(const TilesArgs &p, int ctas, cudaStream_t s) {
-    static const cudaError_t once = cudaFuncSetAttribute(
-        tiles_kernel<T, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<HALVES>::BYTES);
-    if (once != cudaSuccess) return once;
+    static SmemLimit limit;
+    cudaError_t e = limit.allow((const void *)tiles_kernel<T, HALVES>, Plan<HALVES>::BYTES);
+    if (e != cudaSuccess) return e;
     CUtensorMap k, v;
-    cudaError_t e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
+    e = cache_tmap(&k, p.a.c, p.a.c.k, p.box);
     if (e == cudaSuccess) e = cache_tmap(&v, p.a.c, p.a.c.v, p.box);
     if (e != cudaSuccess) return e;
     return launch_pdl(tiles_kernel<T, HALVES>, dim3((unsigned)ctas), NT, Plan<HALVES>::BYTES, s, k, v, p);

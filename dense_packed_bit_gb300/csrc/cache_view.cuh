@@ -8,6 +8,7 @@
 
 #include "mm_common.cuh"
 #include "mm_internal.h"
+#include "smem_limit.h"
 
 namespace mm {
 

@@ -702,9 +702,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
 
 template <typename T, int NT>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
-    static const cudaError_t once =
-        cudaFuncSetAttribute(sample_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-    if (once != cudaSuccess) return once;
+    static SmemLimit limit;
+    const cudaError_t e = limit.allow((const void *)sample_kernel<T, NT>, (int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
     return launch_pdl(sample_kernel<T, NT>, dim3((unsigned)a.rows), NT, sizeof(Shared), s, a);
 }
 
