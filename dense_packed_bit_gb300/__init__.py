@@ -42,6 +42,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
 _torch = None
+_cuda = False  # CUDA was seen to be initialised
 
 # symbol -> (argtypes, restype); mirrors include/mm.h
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -170,13 +171,12 @@ def _ptr(t) -> int | None:
 
 def _stream(stream):
     if stream is None:
-        global _torch
-        if _torch is None:
-            import torch
-            _torch = torch
-        if _torch.cuda.is_initialized():  # the current stream's handle without an object around it
-            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
-        return _torch.cuda.current_stream().cuda_stream
+        torch = _torch_module()
+        global _cuda
+        if _cuda or torch.cuda.is_initialized():  # the current stream's handle without an object around it
+            _cuda = True
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -366,16 +366,88 @@ def mm_attention_bwd(Q, K, V, O, dO, L, dQ, dK, dV, heads, T, D, causal, scale, 
 
 
 def _dtype(t) -> int:
-    name = str(t.dtype)
-    try:
-        return {"torch.float16": MM_F16, "torch.bfloat16": MM_BF16, "torch.float32": MM_F32}[name]
-    except KeyError:
-        raise ValueError(f"no kernel takes {name}") from None
+    dtype, torch = t.dtype, _torch_module()
+    if dtype is torch.float32:
+        return MM_F32
+    if dtype is torch.float16:
+        return MM_F16
+    if dtype is torch.bfloat16:
+        return MM_BF16
+    raise ValueError(f"no kernel takes {dtype}")
 
 
 def _int32(t, what, shape):
     if str(t.dtype) != "torch.int32" or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+# What the library cannot see of a tensor whose address it gets: its type, its strides, its length, where it lies.  None and
+# plain addresses are passed on as they are.
+
+def _torch_module():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _refuse(what):
+    raise MMError(MM_ERR_INVALID_ARG, what)
+
+
+def _array(t, what, dtype, n, also=None):
+    """Address of at least n contiguous elements of `dtype` (or `also`) on the GPU."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    if t.dtype is not dtype and (also is None or t.dtype is not also):
+        _refuse(f"{what} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        _refuse(f"{what} must be contiguous")
+    if t.numel() < n:
+        _refuse(f"{what} has {t.numel()} elements, not {n}")
+    if not t.is_cuda:
+        _refuse(f"{what} is not on the GPU")
+    return t.data_ptr()
+
+
+def _tokens(t, what, cache, tokens, row, heads):
+    """Address of `tokens` rows, `row` elements apart, of heads side by side: 16-bit elements of the cache's type, or bit
+    patterns of it."""
+    if t is None or t.__class__ is int:
+        return t
+    dim, torch = cache.head_dim, _torch_module()
+    n = (tokens - 1) * row + heads * dim
+    if t.dtype is not (torch.bfloat16 if cache.dtype == MM_BF16 else torch.float16) and t.dtype is not torch.int16:
+        _refuse(f"{what} must have the cache's type, not {t.dtype}")
+    if t.is_contiguous() and t.is_cuda and t.numel() >= n:
+        return t.data_ptr()
+    shape, stride = t.shape, t.stride()
+    if stride and stride[-1] != 1 and shape[-1] > 1 or len(shape) == 3 and shape[1] == heads > 1 and shape[2] == dim != stride[1]:
+        _refuse(f"{what} must have the heads of a token side by side")
+    _reach(t, what, n)
+    return t.data_ptr()
+
+
+def _reach(t, what, n):
+    """t holds n elements from its first to its last, on the GPU."""
+    if t.numel() < n and 1 + sum((a - 1) * b for a, b in zip(t.shape, t.stride())) < n:
+        _refuse(f"{what} ends before the {n} elements that the call's sizes span")
+    if not t.is_cuda:
+        _refuse(f"{what} is not on the GPU")
+
+
+def _bytes(t, what, n):
+    """Address of n bytes on the GPU."""
+    if t is None or t.__class__ is int:
+        return t
+    if not t.is_contiguous() or t.nbytes < n:
+        _refuse(f"{what} must be {n} contiguous bytes")
+    if not t.is_cuda:
+        _refuse(f"{what} is not on the GPU")
+    return t.data_ptr()
 
 
 def mm_cache(k, v, table, lens, refs=None) -> Cache:
@@ -389,6 +461,8 @@ def mm_cache(k, v, table, lens, refs=None) -> Cache:
     _int32(lens, "lens", (seqs,))
     if refs is not None:
         _int32(refs, "refs", (k.shape[1],))
+    if not all(t.is_cuda for t in (k, v, table, lens, refs) if t is not None):
+        raise ValueError("k, v, table, lens and refs must be on the GPU")
     c = Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(refs), *k.shape, seqs, max_pages,
               *k.stride()[:4], _dtype(k))
     c.tensors = (k, v, table, lens, refs)
@@ -397,35 +471,46 @@ def mm_cache(k, v, table, lens, refs=None) -> Cache:
 
 def mm_cache_reserve(cache, need, missing, stream=None):
     """Pages for lens[s] + need[s] tokens of every sequence; missing[0]: pages lacking (nothing is changed then)."""
-    _check(load_library().mm_cache_reserve(cache, _ptr(need), _ptr(missing), _stream(stream)))
+    i32 = _torch_module().int32
+    _check(load_library().mm_cache_reserve(cache, _array(need, "need", i32, cache.seqs), _array(missing, "missing", i32, 1),
+                                           _stream(stream)))
 
 
 def mm_cache_append(cache, layer, K, V, kv_token_stride, q_start, tokens, max_new, stream=None):
     """New tokens' keys and values [tokens][kv_heads][head_dim] into the slots behind lens."""
-    _check(load_library().mm_cache_append(cache, layer, _ptr(K), _ptr(V), kv_token_stride, _ptr(q_start), tokens,
+    heads = cache.kv_heads
+    _check(load_library().mm_cache_append(cache, layer, _tokens(K, "K", cache, tokens, kv_token_stride, heads),
+                                          _tokens(V, "V", cache, tokens, kv_token_stride, heads), kv_token_stride,
+                                          _array(q_start, "q_start", _torch_module().int32, cache.seqs + 1), tokens,
                                           max_new, _stream(stream)))
 
 
 def mm_cache_compact(cache, q_start, keep, kept, tokens, max_new, stream=None):
     """Keeps kept[s] of each sequence's new tokens (keep: which, ascending; None: the first ones), moved
     together; lens grows by kept, pages without a token are released."""
-    _check(load_library().mm_cache_compact(cache, _ptr(q_start), _ptr(keep), _ptr(kept), tokens, max_new,
-                                           _stream(stream)))
+    i32, seqs = _torch_module().int32, cache.seqs
+    _check(load_library().mm_cache_compact(cache, _array(q_start, "q_start", i32, seqs + 1), _array(keep, "keep", i32, tokens),
+                                           _array(kept, "kept", i32, seqs), tokens, max_new, _stream(stream)))
 
 
 def mm_cache_fork(cache, parents, children, n, missing, stream=None):
     """children[i] becomes a copy of parents[i]: full pages shared, the last partial page copied."""
-    _check(load_library().mm_cache_fork(cache, _ptr(parents), _ptr(children), n, _ptr(missing), _stream(stream)))
+    i32 = _torch_module().int32
+    _check(load_library().mm_cache_fork(cache, _array(parents, "parents", i32, n), _array(children, "children", i32, n), n,
+                                        _array(missing, "missing", i32, 1), _stream(stream)))
 
 
 def mm_cache_free(cache, list, n, window=0, sinks=0, stream=None):
     """Releases the pages of sequences list[:n]: all of them, or with a window those no later query sees."""
-    _check(load_library().mm_cache_free(cache, _ptr(list), n, window, sinks, _stream(stream)))
+    _check(load_library().mm_cache_free(cache, _array(list, "list", _torch_module().int32, n), n, window, sinks,
+                                        _stream(stream)))
 
 
 def mm_cache_copy_pages(cache, src, dst, n, stream=None):
     """Page src[i] into page dst[i], i < n, in all layers."""
-    _check(load_library().mm_cache_copy_pages(cache, _ptr(src), _ptr(dst), n, _stream(stream)))
+    i32 = _torch_module().int32
+    _check(load_library().mm_cache_copy_pages(cache, _array(src, "src", i32, n), _array(dst, "dst", i32, n), n,
+                                              _stream(stream)))
 
 
 def mm_cache_attention_workspace(cache, heads, tokens, max_q) -> int:
@@ -438,21 +523,35 @@ def mm_cache_attention_workspace(cache, heads, tokens, max_q) -> int:
 def mm_cache_attention(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, window, sinks, scale, O, o_stride,
                        workspace, workspace_bytes, stream=None):
     """O = attention of new tokens Q [tokens][heads][head_dim] over the cache, with a window and sinks."""
-    _check(load_library().mm_cache_attention(cache, layer, _ptr(Q), q_stride, heads, _ptr(q_start), tokens, max_q,
-                                             window, sinks, scale, _ptr(O), o_stride, _ptr(workspace), workspace_bytes,
+    _check(load_library().mm_cache_attention(cache, layer, _tokens(Q, "Q", cache, tokens, q_stride, heads), q_stride, heads,
+                                             _array(q_start, "q_start", _torch_module().int32, cache.seqs + 1), tokens,
+                                             max_q, window, sinks, scale, _tokens(O, "O", cache, tokens, o_stride, heads), o_stride,
+                                             _bytes(workspace, "workspace", workspace_bytes), workspace_bytes,
                                              _stream(stream)))
 
 
 def mm_cache_attention_tree(cache, layer, Q, q_stride, heads, q_start, tokens, max_q, mask, mask_words, window, sinks,
                             scale, O, o_stride, workspace, workspace_bytes, stream=None):
     """mm_cache_attention for a tree of drafted tokens: mask [tokens][mask_words], bit t: sees drafted token t."""
-    _check(load_library().mm_cache_attention_tree(cache, layer, _ptr(Q), q_stride, heads, _ptr(q_start), tokens, max_q,
-                                                  _ptr(mask), mask_words, window, sinks, scale, _ptr(O), o_stride,
-                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+    torch = _torch_module()
+    _check(load_library().mm_cache_attention_tree(cache, layer, _tokens(Q, "Q", cache, tokens, q_stride, heads), q_stride, heads,
+                                                  _array(q_start, "q_start", torch.int32, cache.seqs + 1), tokens, max_q,
+                                                  _array(mask, "mask", torch.int32, tokens * mask_words, torch.uint32),
+                                                  mask_words, window, sinks, scale, _tokens(O, "O", cache, tokens, o_stride, heads),
+                                                  o_stride, _bytes(workspace, "workspace", workspace_bytes),
+                                                  workspace_bytes, _stream(stream)))
 
 
 def mm_sample(logits, rows, vocab, stride, temperature, top_k, top_p, min_p, u, tokens, logprobs=None, stream=None):
     """tokens[r]: the next token of row r by temperature, top-k, top-p and min-p from the uniform number u[r]
     (each parameter a [rows] tensor or None: off); logprobs[r]: log of its probability among those kept."""
-    _check(load_library().mm_sample(_ptr(logits), _dtype(logits), rows, vocab, stride, _ptr(temperature), _ptr(top_k),
-                                    _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(tokens), _ptr(logprobs), _stream(stream)))
+    dtype, torch = _dtype(logits), _torch_module()
+    f32, i32 = torch.float32, torch.int32
+    if not logits.is_contiguous() and logits.stride(-1) != 1 and vocab > 1:
+        _refuse("the logits of a row must be contiguous")
+    _reach(logits, "logits", (rows - 1) * stride + vocab)
+    _check(load_library().mm_sample(logits.data_ptr(), dtype, rows, vocab, stride,
+                                    _array(temperature, "temperature", f32, rows), _array(top_k, "top_k", i32, rows),
+                                    _array(top_p, "top_p", f32, rows), _array(min_p, "min_p", f32, rows),
+                                    _array(u, "u", f32, rows), _array(tokens, "tokens", i32, rows),
+                                    _array(logprobs, "logprobs", f32, rows), _stream(stream)))
