@@ -119,7 +119,14 @@ class Server:
     def step(self, new, places, window=0, sinks=0, trees=None):
         """Logits of the new tokens new[s] (a list per sequence, [] for none) at places[s].  trees[s][i]: the drafted
         tokens that token i sees (itself included); None: all up to it."""
-        s, c = self.model.shape, self.cache
+        s = self.model.shape
+        if any(not 0 <= p < s.positions for seq in places for p in seq):
+            raise ValueError(f"the model has {s.positions} positions")
+        if any(not 0 <= t < s.vocab for seq in new for t in seq):
+            raise ValueError(f"a token is not in the vocabulary of {s.vocab}")
+        if window and trees is not None and any(len(row) > window for tree in trees for row in tree):
+            raise ValueError("a drafted token with more ancestors than the window holds sees more than it would if decoded")
+        c = self.cache
         counts = [len(t) for t in new]
         tokens, most = sum(counts), max(counts)
         starts = self.ints(np.concatenate([[0], np.cumsum(counts)]).tolist())
@@ -187,6 +194,13 @@ def generate(server, prompts, answers, tokens, temperature=0.8, top_k=40, top_p=
     first = [P + i for i in range(A)]  # sequences: the prompts, then the answers
     if server.seqs < P + A:
         raise ValueError("the server has too few sequences")
+    if not prompts or not all(prompts):
+        raise ValueError("a prompt needs a token")
+    if window and depth and depth + 1 > window:
+        raise ValueError(f"drafts of {depth} tokens do not fit a window of {window}: they would see more than decoded tokens do")
+    # an answer's last token is not processed; drafts follow the one before it
+    if max(len(p) for p in prompts) - 1 + (tokens - 1 + depth if tokens > 1 else 0) >= server.model.shape.positions:
+        raise ValueError(f"the model has {server.model.shape.positions} positions")
     generator = torch.Generator().manual_seed(seed)
     longest = max(len(p) for p in prompts)
     u = torch.rand(longest + tokens + depth + 2, A, generator=generator).T  # by position, so the same for any depth
