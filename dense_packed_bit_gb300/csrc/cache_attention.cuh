@@ -307,59 +307,6 @@ __device__ __forceinline__ void check_held(const CacheAttnArgs &a, int seq, cons
         *err = kDevErrRange;
 }
 
-// One row by the definition, key by key, a warp to it: O[4 lane + x] in o (unnormalised over l > 0).
-// For what the tiles cannot do (infinities and NaN among values that only some rows see).
-template <typename T>
-__device__ void attend_row(const CacheAttnArgs &a, int seq, const SeqView &sv, int i, int qhead, unsigned int *err) {
-    const CacheView &c = a.c;
-    const int lane = threadIdx.x & 31, kv_head = qhead / a.group;
-    const RowView r = row_view(a, sv.len, sv.first, sv.count, i);
-    const bool mine = 4 * lane < c.head_dim;
-    const auto get4 = [&](const char *p, float (&f)[4]) {
-        uint2 u = make_uint2(0, 0);
-        if (mine) u = *reinterpret_cast<const uint2 *>(p + 8 * lane);
-        f[0] = Pair<T>::one((uint16_t)u.x), f[1] = Pair<T>::one((uint16_t)(u.x >> 16));
-        f[2] = Pair<T>::one((uint16_t)u.y), f[3] = Pair<T>::one((uint16_t)(u.y >> 16));
-    };
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    get4(static_cast<const char *>(a.Q) + ((int64_t)(sv.first + i) * a.q_stride + (int64_t)qhead * c.head_dim) * 2, q);
-    const float scale2 = a.scale * kLog2e;
-    const int end = sv.len + sv.count;
-    const KeyBlocks kb = key_blocks<16>(a.mask ? min(r.low, sv.len) : r.low, a.sinks, end);
-    for (int b = 0; b < kb.count; ++b) {
-        const int key0 = kb.block(b) * 16;
-        const int page = page_of(c, seq, key0 >> c.page_shift);
-        if (page < 0) {
-            *err = kDevErrRange;
-            continue;
-        }
-        for (int j = key0; j < min(key0 + 16, end); ++j) {
-            if (!sees(r, j, a.sinks, sv.len, sv.count)) continue;
-            const int64_t at =
-                ((int64_t)page * c.page_stride + kv_head * c.head_stride + (j & (c.page_size - 1)) * c.token_stride) * 2;
-            float k[4], v[4];
-            get4(c.k + at, k);
-            get4(c.v + at, v);
-            float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            s *= scale2;
-            const float now = fmaxf(m, s), f = m == now ? 1.f : ex2(m - now), p = s == -INFINITY ? 0.f : ex2(s - now);
-            m = now;
-            l = l * f + p;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = o[x] * f + p * v[x];
-        }
-    }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    if (mine) {
-        uint2 u = make_uint2(Pair<T>::pack(o[0] * inv, o[1] * inv), Pair<T>::pack(o[2] * inv, o[3] * inv));
-        if (m == -INFINITY && l == 0.f) u = make_uint2(0, 0);
-        *reinterpret_cast<uint2 *>(static_cast<char *>(a.O) +
-                                   ((int64_t)(sv.first + i) * a.o_stride + (int64_t)qhead * c.head_dim) * 2 + 8 * lane) = u;
-    }
-}
-
 // CTAs of the rows kernel (the blocks of all units are cut evenly over them)
 int cache_attention_rows_ctas(const CacheView &c, int sms);
 int64_t cache_attention_rows_workspace(const CacheView &c, int ctas);

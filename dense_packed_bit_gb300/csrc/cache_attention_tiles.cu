@@ -36,8 +36,8 @@
 // tokens on up to 700, 12 heads of 64: 22.5 us, a chunk of 64 on 500 19 (launch, first loads, softmax after softmax).
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
-// memory (0 x NaN), and where the mask cuts between rows V is looked through: if it holds an infinity or NaN,
-// the unit's rows are computed again by the definition, key by key.
+// memory (0 x NaN), and where the mask cuts between rows V is looked through: infinities and NaN are taken out of the
+// product and, when the unit's O is stored, added to the rows that see them (add_special).
 #include "cache_attention.cuh"
 #include "tcgen05.cuh"
 
@@ -197,6 +197,66 @@ __device__ __forceinline__ UnitKeys unit_keys(const TilesArgs &p, int item) {
     }
     k.kb = key_blocks<B>(k.low, a.sinks, k.end);
     return k;
+}
+
+// The infinities and NaN that were taken out of V, added to the stored O of the unit's rows that see them.  The weight
+// of a key that a row sees is above 0, so an infinity stays one whatever it is multiplied with.  By the 256 threads of
+// the softmax; the keys are looked for again, a block at a time, into list[0 .. 127] (list[128]: how many).
+template <typename T>
+__device__ __noinline__ void add_special(const CacheAttnArgs &a, const UnitKeys &k, const FastDiv &by_group, int seq, int head,
+                                         volatile int *list) {
+    const CacheView &c = a.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool mine = 4 * lane < c.head_dim;
+    const auto values = [&](int j) {  // of key j, this lane's four
+        uint2 v = make_uint2(0, 0);
+        const int page = page_of(c, seq, j >> c.page_shift);
+        if (mine && page >= 0)
+            v = *reinterpret_cast<const uint2 *>(c.v + ((int64_t)page * c.page_stride + head * c.head_stride +
+                                                        (j & (c.page_size - 1)) * c.token_stride + 4 * lane) * 2);
+        return v;
+    };
+    for (int b = 0; b < k.kb.count; ++b) {
+        const int key0 = k.kb.block(b) * B;
+        if (!k.cut(key0, a.sinks)) continue;
+        if (threadIdx.x == 0) list[128] = 0;
+        __syncwarp();
+        bar_sync(1, 256);
+        for (int j = key0 + warp; j < min(key0 + B, k.end); j += 8) {
+            if (j >= a.sinks && j < k.low) continue;
+            const uint2 v = values(j);
+            if (__any_sync(0xffffffffu, any_special<T>(v.x) || any_special<T>(v.y)) && lane == 0)
+                list[atomicAdd(const_cast<int *>(list) + 128, 1)] = j;
+        }
+        __syncwarp();
+        bar_sync(1, 256);
+        const int n = list[128];
+        for (int r = warp; n > 0 && r < k.rows; r += 8) {
+            const int i = by_group.div(k.row0 + r);
+            const RowView rv = row_view(a, k.v.len, k.v.first, k.v.count, i);
+            float add[4] = {-0.f, -0.f, -0.f, -0.f};  // what leaves every other value as it is
+            bool any = false;
+            for (int x = 0; x < n; ++x) {
+                const int j = list[x];
+                if (!sees(rv, j, a.sinks, k.v.len, k.v.count)) continue;
+                const uint2 v = values(j);
+                const uint16_t h[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if ((h[y] & Pair<T>::kExp) == Pair<T>::kExp) add[y] += Pair<T>::one(h[y]), any = true;
+            }
+            if (any) {  // never a lane past head_dim, whose values are 0
+                uint2 *out = reinterpret_cast<uint2 *>(
+                    static_cast<char *>(a.O) + ((int64_t)(k.v.first + i) * a.o_stride +
+                                                (int64_t)(head * a.group + k.row0 + r - i * a.group) * c.head_dim + 4 * lane) * 2);
+                const uint2 o = *out;
+                *out = make_uint2(Pair<T>::pack(Pair<T>::one((uint16_t)o.x) + add[0], Pair<T>::one((uint16_t)(o.x >> 16)) + add[1]),
+                                  Pair<T>::pack(Pair<T>::one((uint16_t)o.y) + add[2], Pair<T>::one((uint16_t)(o.y >> 16)) + add[3]));
+            }
+        }
+        __syncwarp();
+        bar_sync(1, 256);  // before the list is written again
+    }
 }
 
 // The units of one CTA, in order; every role walks them by itself.
@@ -474,7 +534,7 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                             make_uint4(Pair<T>::pack(o[8 * x] * f, o[8 * x + 1] * f), Pair<T>::pack(o[8 * x + 2] * f, o[8 * x + 3] * f),
                                        Pair<T>::pack(o[8 * x + 4] * f, o[8 * x + 5] * f), Pair<T>::pack(o[8 * x + 6] * f, o[8 * x + 7] * f));
             };
-            bool again = false;  // rows to be computed by the definition
+            bool special = false;  // V of the unit holds infinities or NaN that were taken out of it
             if (!u.alone) {
                 // partial results: both streams' of the same rows where they share a tile
                 const int64_t slot = (int64_t)blockIdx.x * 2 + u.second;
@@ -509,8 +569,8 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 __syncwarp();
                 bar_sync(1, 256);
                 const int last = sm_last;
-                again = last == 2;
-                if (last == 1) {
+                special = last == 2;
+                if (last) {
                     const int per = single ? 2 : 1, sources = per * u.used;
                     const auto slot_of = [&](int y) {  // source y: slot * 256 + its rows' first
                         const int g = y / per;
@@ -582,7 +642,6 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                 }
                 tc_fence_before_sync();
                 bar_sync(1, 256);
-                again = *poison != 0;
                 if (s == 0) {
                     const float2 other = sm_ml[t];
                     const float mt = fmaxf(m, other.x);
@@ -599,8 +658,10 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     }
                     tc_fence_before_sync();
                 }
+                if (tid == 0) sm_last = *poison, *poison = 0;
+                __syncwarp();
                 bar_sync(1, 256);  // before Q's place is written again
-                if (tid == 0) *poison = 0;
+                special = sm_last != 0;
             } else {
                 const float inv = l != 0.f ? 1.f / l : 0.f;
                 for (int d = 0; d < D; d += 32) {
@@ -610,16 +671,13 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                     __syncwarp();
                 }
                 tc_fence_before_sync();
+                if (tid == 0) sm_last = *poison, *poison = 0;
+                __syncwarp();
                 bar_sync(1, 256);
-                again = *poison != 0;
-                bar_sync(1, 256);
-                if (tid == 0) *poison = 0;
+                special = sm_last != 0;
             }
-            if (again && ok)
-                for (int q = warp; q < nrows; q += 8) {
-                    const int qi = p.by_group.div(row0 + q);
-                    attend_row<T>(a, p.by_tiles.div(u.item), sv, qi, head * a.group + row0 + q - qi * a.group, &g_tiles_err);
-                }
+            // (the same for all 256 threads, also where a wait has failed: there are barriers inside)
+            if (special) add_special<T>(a, u.k, p.by_group, p.by_tiles.div(u.item), head, reinterpret_cast<volatile int *>(sm));
             __syncwarp();
             bar_sync(1, 256);  // the walk may go on
         }
@@ -800,10 +858,10 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                         uint8_t *v = sm + P::RING + st * P::TILE;
                         // infinite or NaN: the magnitude's bits are kExp or more, and adding this carries into bit 15
                         constexpr uint32_t up = (0x8000u - Pair<T>::kExp) * 0x10001u;
-                        uint32_t special = 0;
 #pragma unroll 1
                         for (int e0 = tid - 320; e0 < P::TILE / 16; e0 += 8 * 64) {
                             uint4 u[8];
+                            uint32_t special = 0;
 #pragma unroll
                             for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4 *>(v + (e0 + 64 * k) * 16);
 #pragma unroll
@@ -818,8 +876,18 @@ __global__ void __launch_bounds__(NT, 1) tiles_kernel(const __grid_constant__ CU
                                     special |= (u[k].w & 0x7fff7fffu) + up;
                                 }
                             }
+                            if (special & 0x80008000u) {
+                                poisons[units & 7] = 1;
+#pragma unroll 1
+                                for (int e = e0; e < e0 + 8 * 64; e += 64) {
+                                    uint4 *at = reinterpret_cast<uint4 *>(v + e * 16);
+                                    uint4 x = *at;
+                                    x.x = without_special<T>(x.x), x.y = without_special<T>(x.y);
+                                    x.z = without_special<T>(x.z), x.w = without_special<T>(x.w);
+                                    *at = x;
+                                }
+                            }
                         }
-                        if (special & 0x80008000u) poisons[units & 7] = 1;
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
