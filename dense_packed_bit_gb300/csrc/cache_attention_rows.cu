@@ -20,7 +20,7 @@
 //
 // Measured, one call: 48 sequences of 100 to 16,000 tokens, one new, 32 heads over 8 of 128 columns, bf16, pages of
 // 64: 100 us = 6.07 TB/s, 89% of a plain copy's.  Small calls are a latency of launch, share, first loads and join:
-// 1 x 513 (12 heads of 64) 8.3 us, 8 sequences of 32,000 under a window of 1,024 13.0, trees of 4 x 7 tokens 9.3.
+// 1 x 513 (12 heads of 64) 7.9 us, 8 sequences of 32,000 under a window of 1,024 12.6, trees of 4 x 7 tokens 9.1.
 //
 // What a row does not see: its score is replaced, not added to.  In blocks that the mask cuts,
 // infinities and NaN in V are taken out of the product (0 x NaN) and added to the rows that do see them.

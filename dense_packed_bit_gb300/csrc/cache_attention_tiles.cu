@@ -28,12 +28,15 @@
 // Split.  One CTA per SM, each with an even share of all units' blocks (share_of), the ring of K and V blocks
 // running through its units; the last CTA of a shared unit to finish joins the partial results in order.
 //
-// Bound: the tensor core and the softmax in turn.  Per pair of blocks (two streams, 128 keys) the products take 2,050
-// cycles at the rated speed and about 2,250 as issued; a stream's softmax is about 1,100 (128 exponentials a thread) and
-// with its waits 1,500; a pair takes 2,900 to 3,100, a unit's first blocks and its join about 25,000 once.  Measured, one
-// call: a chunk of 4,096 tokens on 12,289 under a window of 4,096, 32 heads over 8 of 128 columns, bf16: 255 us = 1,094
-// TFLOP/s, 59% of a library product's rate; 16 trees of 64 tokens on 2,500 to 8,000: 92 us; 4 chunks of 150 to 1,024
-// tokens on up to 700, 12 heads of 64: 22.5 us, a chunk of 64 on 500 19 (launch, first loads, softmax after softmax).
+// Bound: the tensor core and the softmax in turn, and the beginning and end of each unit.  Per pair of blocks (two
+// streams, 128 keys) the products take 2,050 cycles at the rated speed; a stream's softmax is about 1,100 (128
+// exponentials a thread) and with its waits 1,500.  Measured, one call: a chunk of 4,096 tokens on 12,289 under a window
+// of 4,096, 32 heads over 8 of 128 columns, bf16: 254 us = 1,100 TFLOP/s, 59% of a library product's rate.  Of a CTA's
+// 500,000 cycles there (by time stamps of one warp, which made the call 3% longer) 68% are 102 pairs at 3,330, 9% ten
+// pairs that the mask cuts at 4,620, 7% the beginning of 4.2 units (the walk, Q, the first scores), 11% their last blocks,
+// O and joins, 5% the launch, its wait and the share.  16 trees of 64 tokens on 2,500 to 8,000: 89 us, of which the
+// pairs are 60%, beginnings 10%, ends 16%, the launch 14%; 4 chunks of 150 to 1,024 tokens on up to 700, 12 heads of 64:
+// 22.5 us (47%, 10%, 15%, 27%); a chunk of 64 on 500: 19.
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
 // memory (0 x NaN), and where the mask cuts between rows V is looked through: infinities and NaN are taken out of the

@@ -15,7 +15,7 @@
 // Measured, a call: 8 sequences forked into 64 (16 layers, 8 heads of 128, a partial page each: 170 MB written) 46 us with
 // the children's release, of which the copy is 39 (131 MB of DRAM traffic: a parent's page is read once, part of what is
 // written stays in L2) and the rest two kernels of one CTA in a row; 4,096 tokens of 8 heads of 128 appended 8.3 us,
-// reserved 4.8; reserve, append and compact for 16 sequences of 12 drafts 21 us, four launches' host time.
+// reserved 4.8; reserve, append and compact for 16 sequences of 12 drafts 22 us, four launches' host time.
 #include "cache_view.cuh"
 
 namespace mm {

@@ -675,7 +675,8 @@ mm_status mm_cache_copy_pages(const mm_cache *cache, const int32_t *src, const i
  * end.  max_q: an upper bound of the new tokens of one sequence.
  * workspace: mm_cache_attention_workspace bytes for these sizes (at least; 0 is possible),
  * 16-byte aligned, zeroed once before its first use; every call leaves it ready for the
- * next one in stream order, whatever the sizes of either.  Two calls at once need two workspaces.
+ * next one in stream order, whatever the sizes of either, unless mm_check_device_error
+ * reports MM_ERR_TIMEOUT: zero it again then.  Two calls at once need two workspaces.
  * Errors: MM_ERR_INVALID_ARG as above, for heads not a multiple of kv_heads, a non-finite
  * scale, O overlapping an input, or a workspace that is too small or overlaps anything else.
  */
