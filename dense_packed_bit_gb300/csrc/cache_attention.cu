@@ -2,8 +2,8 @@
 //
 // Up to 16 rows (new tokens x query heads of a kv head) of a sequence: the rows kernel, whose one m16 tile they fill.
 // More: the tiles kernel, whose 128-row products are mostly zeros below that.  Measured, rows and tiles kernel: 48
-// sequences of 100 to 16,000 tokens, 8 kv heads of 128 columns, 1 new token (4 rows) 101 and 130 us, 4 new (16 rows) 107 and 130; 8 x 100 to
-// 1,000 tokens, 12 heads of 64, 16 rows 12.0 and 17.4; one sequence of 513, 1 row 8.2 and 13.3.
+// sequences of 100 to 16,000 tokens, 8 kv heads of 128 columns, 1 new token (4 rows) 100 and 131 us, 4 new (16 rows) 106 and 131; 8 x 100 to
+// 1,000 tokens, 12 heads of 64, 16 rows 12.1 and 17.7; one sequence of 513, 1 row 7.9 and 13.4.
 #include "cache_attention.cuh"
 
 namespace mm {

@@ -38,7 +38,7 @@ constexpr int SUB = 16, B = WARPS * SUB;         // keys of a warp's part of a b
 constexpr int MIN_BLOCKS = 1;    // blocks of a part, at least (see least_part)
 constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (30 x 100 to 500 tokens: 13.7 us, cut 19.2)
 constexpr int JOIN = 8;          // parts joined at a time
-constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU (48 ragged: 100 us, with 0 137)
+constexpr int UNIT_COST = 12;    // what beginning and ending a unit takes, in blocks of a full GPU (48 ragged: 100 us, with 0 135)
 constexpr int HALF = B * 128;          // bytes of a block's 64 columns
 
 struct RowsArgs {

@@ -31,12 +31,12 @@
 // Bound: the tensor core and the softmax in turn, and the beginning and end of each unit.  Per pair of blocks (two
 // streams, 128 keys) the products take 2,050 cycles at the rated speed; a stream's softmax is about 1,100 (128
 // exponentials a thread) and with its waits 1,500.  Measured, one call: a chunk of 4,096 tokens on 12,289 under a window
-// of 4,096, 32 heads over 8 of 128 columns, bf16: 254 us = 1,100 TFLOP/s, 59% of a library product's rate.  Of a CTA's
-// 500,000 cycles there (by time stamps of one warp, which made the call 3% longer) 68% are 102 pairs at 3,330, 9% ten
-// pairs that the mask cuts at 4,620, 7% the beginning of 4.2 units (the walk, Q, the first scores), 11% their last blocks,
-// O and joins, 5% the launch, its wait and the share.  16 trees of 64 tokens on 2,500 to 8,000: 89 us, of which the
-// pairs are 60%, beginnings 10%, ends 16%, the launch 14%; 4 chunks of 150 to 1,024 tokens on up to 700, 12 heads of 64:
-// 22.5 us (47%, 10%, 15%, 27%); a chunk of 64 on 500: 19.
+// of 4,096, 32 heads over 8 of 128 columns, bf16: 256 us = 1,090 TFLOP/s, 58% of a library product's rate.  Of a CTA's
+// 500,000 cycles there (by time stamps of one warp, which made the call 3% longer) 66% are 102 pairs at 3,280, 9% ten
+// pairs that the mask cuts at 4,650, 7% the beginning of 4.2 units (the walk, Q, the first scores), 11% their last blocks,
+// O and joins, 6% the launch, its wait and the share.  16 trees of 64 tokens on 2,500 to 8,000: 89 us, of which the
+// pairs are 58%, beginnings 10%, ends 15%, the launch 15%; 4 chunks of 150 to 1,024 tokens on up to 700, 12 heads of 64:
+// 22.3 us (45%, 10%, 15%, 28%); a chunk of 64 on 500: 18.5.
 //
 // What a row does not see: its score is replaced.  V rows that no row of the unit sees are zeroed in shared
 // memory (0 x NaN), and where the mask cuts between rows V is looked through: infinities and NaN are taken out of the
@@ -54,8 +54,8 @@ constexpr int NT = 384, B = 128, ROWS = 256;
 // blocks of a part, at least: joining takes as long as several (a chunk of 64 tokens on 500, 5 blocks: cut 23.3 us, whole
 // 19.0; of 200 on 1,000, 10 blocks: 3 parts 19.5, 2 20.8, whole 24)
 constexpr int MIN_BLOCKS = 4;
-constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (the 4 chunks: 22.2 us, cut 28.0)
-constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 92 us, with 0 101, with 8 94)
+constexpr int WHOLE_BLOCKS = 8;  // units up to this are not cut when there are many (the 4 chunks: 22.3 us, cut 28.3)
+constexpr int UNIT_COST = 4;     // what beginning and ending a unit takes, in blocks (16 trees: 89 us, with 0 98, with 8 92)
 constexpr int HALF = 16384;      // 128 rows of 64 elements, 128-byte swizzle
 
 template <int HALVES>
@@ -205,8 +205,10 @@ __device__ __forceinline__ UnitKeys unit_keys(const TilesArgs &p, int item) {
 // The infinities and NaN that were taken out of V, added to the stored O of the unit's rows that see them.  The weight
 // of a key that a row sees is above 0, so an infinity stays one whatever it is multiplied with.  By the 256 threads of
 // the softmax; the keys are looked for again, a block at a time, into list[0 .. 127] (list[128]: how many).
+// (As a function of its own it cost the kernel registers over the call: 48 sequences of 100 to 16,000 tokens, 8 new each,
+// 142 us, inlined 132.)
 template <typename T>
-__device__ __noinline__ void add_special(const CacheAttnArgs &a, const UnitKeys &k, const FastDiv &by_group, int seq, int head,
+__device__ __forceinline__ void add_special(const CacheAttnArgs &a, const UnitKeys &k, const FastDiv &by_group, int seq, int head,
                                          volatile int *list) {
     const CacheView &c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
