@@ -180,7 +180,7 @@ def _own(s):
         return s["out"]
     w = s.get("w")
     if w is None:
-        w = s["w"] = mm.mm_packed4(s["codes"], s["scales"], s["zeros"], s["cols"], s["group"])
+        w = s["w"] = mm.mm_packed4(s["codes"], s["scales"], s["zeros"], s["cols"], s["group"], weights_static=True)
     if op == "linear":
         mm.mm_gemm_packed4(w, s["x"], s["x"].stride(0), t, mm.MM_ACT_NONE, s["y"], s["y"].stride(0))
     elif op == "up":
