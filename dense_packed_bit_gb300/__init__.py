@@ -1,5 +1,5 @@
-"""dense_packed_bit_gb300 -- fp32 dense GEMM, packed 2-bit GEMV / skinny GEMM and packed
-4-bit GEMV on GB300.
+"""dense_packed_bit_gb300 -- fp32 dense GEMM, packed 2-bit GEMV / skinny GEMM, packed 4-bit
+products and what serves a model's tokens between them, on GB300.
 
 Thin ctypes binding over libmm.so (the C ABI declared in include/mm.h).  The
 functions keep the C names and argument order; tensors are torch CUDA tensors
@@ -26,6 +26,8 @@ __all__ = [
     "mm_cache", "mm_cache_reserve", "mm_cache_append", "mm_cache_compact", "mm_cache_fork", "mm_cache_free",
     "mm_cache_copy_pages", "mm_cache_attention_workspace", "mm_cache_attention", "mm_cache_attention_tree",
     "mm_sample", "MM_F16", "MM_BF16", "MM_F32",
+    "mm_packed4", "mm_gemm_packed4", "mm_experts_route_workspace", "mm_experts_route", "mm_experts_gemm_packed4",
+    "mm_experts_combine", "MM_ACT_SWIGLU", "MM_ROUTE_SOFTMAX", "MM_ROUTE_SIGMOID",
     "MM_OK", "MM_ERR_INVALID_ARG", "MM_ERR_UNSUPPORTED", "MM_ERR_CUDA", "MM_ERR_TIMEOUT",
     "MM_GEMM_AUTO", "MM_GEMM_FFMA", "MM_GEMM_TF32X3",
     "MM_DEQ_AUTO", "MM_DEQ_SELECT", "MM_DEQ_AFFINE", "MM_DEQ_MMA", "MM_DEQ_FP8", "MM_DEQ_TC", "MM_DEQ_MXF4",
@@ -35,7 +37,8 @@ MM_OK, MM_ERR_INVALID_ARG, MM_ERR_UNSUPPORTED, MM_ERR_CUDA, MM_ERR_TIMEOUT = 0, 
 MM_GEMM_AUTO, MM_GEMM_FFMA, MM_GEMM_TF32X3 = 0, 1, 2
 MM_DEQ_AUTO, MM_DEQ_SELECT, MM_DEQ_AFFINE, MM_DEQ_MMA, MM_DEQ_FP8, MM_DEQ_TC, MM_DEQ_MXF4 = 0, 1, 2, 3, 4, 5, 6
 MM_SPLITK_NOALLOC_MAX_FLOATS = 4194304  # floats of the static split-K scratch (16 MiB), as in mm.h
-MM_ACT_NONE, MM_ACT_GELU_TANH = 0, 1
+MM_ACT_NONE, MM_ACT_GELU_TANH, MM_ACT_SWIGLU = 0, 1, 2
+MM_ROUTE_SOFTMAX, MM_ROUTE_SIGMOID = 0, 1
 MM_F16, MM_BF16, MM_F32 = 0, 1, 2
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,7 +81,16 @@ class Cache(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("reserved", ctypes.c_int * 5)]
 
 
-_PC, _PI64, _F = ctypes.POINTER(Cache), ctypes.POINTER(ctypes.c_int64), ctypes.c_float
+class Packed4(ctypes.Structure):
+    """mm_packed4 of mm.h; mm_packed4() makes one from tensors."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("experts", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("codes_row", ctypes.c_int64), ("codes_expert", ctypes.c_int64), ("scales_row", ctypes.c_int64),
+                ("scales_expert", ctypes.c_int64), ("dtype", ctypes.c_int), ("weights_static", ctypes.c_int),
+                ("reserved", ctypes.c_int * 4)]
+
+
+_PC, _PW, _PI64, _F = ctypes.POINTER(Cache), ctypes.POINTER(Packed4), ctypes.POINTER(ctypes.c_int64), ctypes.c_float
 
 SIGNATURES = {
     "mm_version": ([], ctypes.c_int),
@@ -128,6 +140,11 @@ SIGNATURES = {
     "mm_attention_fwd": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P], ctypes.c_int),
     "mm_attention_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, ctypes.c_float, _P],
                          ctypes.c_int),
+    "mm_gemm_packed4": ([_PW, _P, _I64, _I64, _I, _P, _I, _I64, _P], ctypes.c_int),
+    "mm_experts_route_workspace": ([_I64, _I64, _I64, _PI64], ctypes.c_int),
+    "mm_experts_route": ([_P, _I, _I64, _I64, _I64, _I64, _I, _I, _F, _P, _P, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "mm_experts_gemm_packed4": ([_PW, _P, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _I, _I64, _P], ctypes.c_int),
+    "mm_experts_combine": ([_P, _I, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I, _I64, _P], ctypes.c_int),
 }
 
 
@@ -555,3 +572,106 @@ def mm_sample(logits, rows, vocab, stride, temperature, top_k, top_p, min_p, u, 
                                     _array(top_p, "top_p", f32, rows), _array(min_p, "min_p", f32, rows),
                                     _array(u, "u", f32, rows), _array(tokens, "tokens", i32, rows),
                                     _array(logprobs, "logprobs", f32, rows), _stream(stream)))
+
+
+def _rows(t, what, dtypes, n, stride, cols):
+    """Address of n rows of `cols` contiguous elements, `stride` apart, of one of `dtypes`."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype not in dtypes:
+        _refuse(f"{what} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    span = (n - 1) * stride + cols
+    if not (t.is_cuda and t.is_contiguous() and t.numel() >= span):
+        if t.stride() and t.stride(-1) != 1 and t.shape[-1] > 1 and cols > 1:
+            _refuse(f"the elements of a row of {what} must be contiguous")
+        _reach(t, what, span)
+    return t.data_ptr()
+
+
+def mm_packed4(codes, scales, zeros=None, cols=None, group=128, weights_static=False) -> Packed4:
+    """The description of 4-bit matrices: codes uint8 [experts][rows][bytes] (or [rows][bytes], one matrix), 2 to a byte, a
+    multiple of 16 bytes to a row; scales f16 or bf16 [experts][rows][groups]; zeros None or uint8 laid out like scales; cols
+    columns (default: all that the bytes hold).  It holds the tensors, so it is made once and kept as long as they are used."""
+    torch = _torch_module()
+    if codes.dim() == 2:
+        codes, scales = codes[None], scales[None]
+        zeros = None if zeros is None else zeros[None]
+    if codes.dim() != 3 or codes.dtype is not torch.uint8 or scales.dim() != 3 or scales.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("codes must be uint8 [experts][rows][bytes] and scales float16 or bfloat16 [experts][rows][groups]")
+    experts, rows, held = codes.shape
+    cols = 2 * held if cols is None else int(cols)
+    if not 1 <= cols <= 2 * held or 16 * -(-cols // 32) > held:
+        raise ValueError(f"rows of {held} bytes do not hold {cols} columns in whole 16 bytes")
+    if scales.shape != (experts, rows, -(-cols // group)):
+        raise ValueError(f"scales must be of shape {(experts, rows, -(-cols // group))}")
+    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != scales.shape or zeros.stride() != scales.stride()):
+        raise ValueError("zeros must be uint8, of the shape and strides of scales")
+    if codes.stride(2) != 1 or scales.shape[2] > 1 and scales.stride(2) != 1:
+        raise ValueError("the bytes and the scales of a row must be contiguous")
+    if not all(t.is_cuda for t in (codes, scales, zeros) if t is not None):
+        raise ValueError("codes, scales and zeros must be on the GPU")
+    groups, many = scales.shape[2], experts > 1
+    w = Packed4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), experts, rows, cols, group,
+                codes.stride(1) if rows > 1 else 16 * -(-cols // 32), codes.stride(0) if many else 0,
+                scales.stride(1) if rows > 1 else groups, scales.stride(0) if many else 0, _dtype(scales), int(bool(weights_static)))
+    w.tensors = (codes, scales, zeros)
+    return w
+
+
+def _product(W, X, x_stride, x_rows, act, Y, y_stride, n):
+    """Addresses of X and Y and Y's type for a product with W."""
+    torch = _torch_module()
+    kind = torch.bfloat16 if W.dtype == MM_BF16 else torch.float16
+    if Y is None or Y.__class__ is int:
+        raise ValueError("Y must be a tensor: its type is that of the result")
+    return (_rows(X, "X", (kind,), x_rows, x_stride, W.cols),
+            _rows(Y, "Y", (torch.float32, kind), n, y_stride, W.rows // 2 if act == MM_ACT_SWIGLU else W.rows), _dtype(Y))
+
+
+def mm_gemm_packed4(W, X, x_stride, M, act, Y, y_stride, stream=None):
+    """Y = act(X W^T) for a 4-bit matrix W (mm_packed4), X [M][cols] of its type, Y fp32 or of its type."""
+    x, y, dtype = _product(W, X, x_stride, M, act, Y, y_stride, M)
+    _check(load_library().mm_gemm_packed4(W, x, x_stride, M, act, y, dtype, y_stride, _stream(stream)))
+
+
+def mm_experts_route_workspace(tokens, experts, top_k) -> int:
+    """Bytes of workspace mm_experts_route needs."""
+    out = ctypes.c_int64(0)
+    _check(load_library().mm_experts_route_workspace(tokens, experts, top_k, ctypes.byref(out)))
+    return out.value
+
+
+def mm_experts_route(logits, tokens, experts, stride, top_k, score, renorm, scale, ids, weights, offsets, order, slots,
+                     workspace=None, workspace_bytes=0, stream=None):
+    """The top_k experts of each token (ids, weights [tokens][top_k]) and the picks in order of expert: order[slot] = token *
+    top_k + j, expert e's slots offsets[e] .. offsets[e + 1], slots [tokens][top_k] the slot of each pick."""
+    torch = _torch_module()
+    i32, picks = torch.int32, tokens * top_k
+    x = _rows(logits, "logits", (torch.float32, torch.float16, torch.bfloat16), tokens, stride, experts)
+    _check(load_library().mm_experts_route(x, _dtype(logits), tokens, experts, stride, top_k, score, int(renorm), scale,
+                                           _array(ids, "ids", i32, picks), _array(weights, "weights", torch.float32, picks),
+                                           _array(offsets, "offsets", i32, experts + 1), _array(order, "order", i32, picks),
+                                           _array(slots, "slots", i32, picks), _bytes(workspace, "workspace", workspace_bytes),
+                                           workspace_bytes, _stream(stream)))
+
+
+def mm_experts_gemm_packed4(W, X, x_stride, x_rows, order, per_row, offsets, slots, act, Y, y_stride, stream=None):
+    """Y[i] = act(W_e X[order[i] / per_row]) (X[i] with order None) for the slots offsets[e] <= i < offsets[e + 1] of every
+    expert e of W; other rows of Y stay as they were."""
+    i32 = _torch_module().int32
+    x, y, dtype = _product(W, X, x_stride, x_rows, act, Y, y_stride, slots)
+    _check(load_library().mm_experts_gemm_packed4(W, x, x_stride, x_rows, _array(order, "order", i32, slots), per_row,
+                                                  _array(offsets, "offsets", i32, W.experts + 1), slots, act, y, dtype,
+                                                  y_stride, _stream(stream)))
+
+
+def mm_experts_combine(Y, y_stride, y_rows, slots, weights, tokens, top_k, cols, residual, residual_stride, out, out_stride,
+                       stream=None):
+    """out[t] = residual[t] + sum_j weights[t][j] Y[slots[t][j]] (residual None: 0; it may be out itself)."""
+    torch = _torch_module()
+    kinds, picks = (torch.float32, torch.float16, torch.bfloat16), tokens * top_k
+    y, o = _rows(Y, "Y", kinds, y_rows, y_stride, cols), _rows(out, "out", kinds, tokens, out_stride, cols)
+    r = _rows(residual, "residual", (out.dtype,), tokens, residual_stride, cols)
+    _check(load_library().mm_experts_combine(y, _dtype(Y), y_stride, y_rows, _array(slots, "slots", torch.int32, picks),
+                                             _array(weights, "weights", torch.float32, picks), tokens, top_k, cols, r,
+                                             residual_stride, o, _dtype(out), out_stride, _stream(stream)))

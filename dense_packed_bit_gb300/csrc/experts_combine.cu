@@ -1,0 +1,129 @@
+// experts_combine.cu -- the weighted sum of a token's expert rows, added to the residual stream:
+//
+//     out[t] = residual[t] + sum_j weights[t][j] * Y[slots[t][j]]
+//
+// in fp32, j ascending, rounded once.  Bound by memory: a call reads tokens x top_k rows of Y, one of the residual and
+// writes one.  A thread takes 16 bytes of Y's columns with up to 8 rows' loads on their way at once.
+#include "cache_view.cuh"
+#include "mm_common.cuh"
+#include "mm_internal.h"
+#include "packed4.cuh"
+
+namespace mm {
+
+__device__ unsigned int g_combine_err;
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float widen<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+    T v[N];
+};
+
+constexpr int THREADS = 256, AHEAD = 8;
+
+// N columns to a thread (1 where strides or pointers do not allow vectors)
+template <typename TY, typename TO, int N>
+__global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t vecs = a.cols / N, n = a.tokens * vecs;
+    unsigned int err = 0;
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
+        const int64_t t = i / vecs, c = (i - t * vecs) * N;
+        float sum[N];
+        if (a.residual) {
+            const Pack<TO, N> r = *reinterpret_cast<const Pack<TO, N> *>(static_cast<const TO *>(a.residual) + t * a.r_stride + c);
+#pragma unroll
+            for (int x = 0; x < N; ++x) sum[x] = widen<TO>(r.v[x]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < N; ++x) sum[x] = 0.f;
+        }
+        for (int j0 = 0; j0 < a.top_k; j0 += AHEAD) {
+            Pack<TY, N> y[AHEAD];
+            float w[AHEAD];
+            bool have[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                have[j] = false;
+                if (j0 + j >= a.top_k) continue;
+                const int slot = __ldg(a.slots + t * a.top_k + j0 + j);
+                if (slot >= a.y_rows || slot < -1) err = kDevErrRange;
+                else have[j] = slot >= 0;
+                if (!have[j]) continue;
+                w[j] = __ldg(a.weights + t * a.top_k + j0 + j);
+                y[j] = *reinterpret_cast<const Pack<TY, N> *>(static_cast<const TY *>(a.Y) + slot * a.y_stride + c);
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                if (have[j])
+#pragma unroll
+                    for (int x = 0; x < N; ++x) sum[x] = fmaf(w[j], widen<TY>(y[j].v[x]), sum[x]);
+        }
+        Pack<TO, N> o;
+#pragma unroll
+        for (int x = 0; x < N; ++x) o.v[x] = narrow<TO>(sum[x]);
+        *reinterpret_cast<Pack<TO, N> *>(static_cast<TO *>(a.out) + t * a.out_stride + c) = o;
+    }
+    if (err) atomicExch(&g_combine_err, err);
+}
+
+bool fits(const void *p, int64_t stride, int64_t size, int n) {
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(size * n) == 0 && stride % n == 0;
+}
+
+template <typename TY, typename TO>
+cudaError_t launch(const CombineArgs &a, cudaStream_t s) {
+    constexpr int N = 16 / sizeof(TY);
+    const bool vec = a.cols % N == 0 && fits(a.Y, a.y_stride, sizeof(TY), N) && fits(a.out, a.out_stride, sizeof(TO), N) &&
+                     (!a.residual || fits(a.residual, a.r_stride, sizeof(TO), N));
+    const int64_t work = a.tokens * (a.cols / (vec ? N : 1)), blocks = (work + THREADS - 1) / THREADS;
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
+    if (vec) return launch_pdl(combine_kernel<TY, TO, N>, grid, THREADS, 0, s, a);
+    return launch_pdl(combine_kernel<TY, TO, 1>, grid, THREADS, 0, s, a);
+}
+
+template <typename TY>
+cudaError_t launch_o(const CombineArgs &a, cudaStream_t s) {
+    if (a.out_dtype == 0) return launch<TY, __half>(a, s);
+    if (a.out_dtype == 1) return launch<TY, __nv_bfloat16>(a, s);
+    return launch<TY, float>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_experts_combine(const CombineArgs &a, cudaStream_t s) {
+    if (a.y_dtype == 0) return launch_o<__half>(a, s);
+    if (a.y_dtype == 1) return launch_o<__nv_bfloat16>(a, s);
+    return launch_o<float>(a, s);
+}
+
+unsigned int experts_combine_take_device_error(cudaError_t *err) {
+    unsigned int v = 0;
+    *err = cudaMemcpyFromSymbol(&v, g_combine_err, sizeof(v));
+    if (*err == cudaSuccess && v != 0) {
+        const unsigned int zero = 0;
+        *err = cudaMemcpyToSymbol(g_combine_err, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace mm

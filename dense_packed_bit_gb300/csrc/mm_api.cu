@@ -889,6 +889,12 @@ mm_status mm_check_device_error(mm_stream_t stream) {
     if (ca == mm::kCacheErrRange)
         return fail(MM_ERR_INVALID_ARG, "cache attention: a page, length or row range in device memory is out of range");
     if (ca != 0) return fail(MM_ERR_TIMEOUT, "a bounded device wait ran out in the cache attention (code %u)", ca);
+    const unsigned int pw = mm::packed4_rows_take_device_error(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
+    if (pw != 0) return fail(MM_ERR_INVALID_ARG, "4-bit products: an expert's slots or a row of X in device memory is out of range");
+    const unsigned int co = mm::experts_combine_take_device_error(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
+    if (co != 0) return fail(MM_ERR_INVALID_ARG, "experts combine: a slot in device memory is out of range");
     return ok();
 }
 
@@ -1261,6 +1267,168 @@ mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, 
     const mm::SampleArgs a{logits, dtype, rows, vocab, stride, temperature, top_k, top_p, min_p, u, tokens, logprobs};
     const cudaError_t e = mm::launch_sample(a, sm_count(), reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "sample launch");
+    return ok();
+}
+
+namespace {
+
+// Types, sizes and layout of the weights; `a`: the same for the kernels.
+mm_status check_packed4_weights(const mm_packed4 *W, mm::Packed4MmArgs *a) {
+    if (!W) return fail(MM_ERR_INVALID_ARG, "W is NULL");
+    if (!W->codes || !W->scales) return fail(MM_ERR_INVALID_ARG, "NULL pointer in W");
+    if (!is_aligned(W->codes, 16) || !is_aligned(W->scales, 2)) return fail(MM_ERR_INVALID_ARG, "misaligned pointer in W (codes: 16 bytes)");
+    if (W->dtype != MM_F16 && W->dtype != MM_BF16) return fail(MM_ERR_INVALID_ARG, "W's dtype must be MM_F16 or MM_BF16");
+    if (W->group != 32 && W->group != 64 && W->group != 128)
+        return fail(MM_ERR_INVALID_ARG, "group must be 32, 64 or 128 (got %lld)", (long long)W->group);
+    const int64_t most = (int64_t)1 << 28;
+    if (W->experts < 1 || W->experts > 1024 || W->rows < 1 || W->rows > most || W->cols < 1 || W->cols > most)
+        return fail(MM_ERR_INVALID_ARG, "experts must be 1 .. 1024, rows and cols 1 .. 2^28");
+    const int64_t bytes = (W->cols + 31) / 32 * 16, groups = (W->cols + W->group - 1) / W->group, far = (int64_t)1 << 47;
+    if (W->codes_row < bytes || W->codes_row % 16 || W->codes_expert < 0 || W->codes_expert % 16 || W->codes_row > far ||
+        W->codes_expert > far)
+        return fail(MM_ERR_INVALID_ARG, "codes_row must be a multiple of 16, at least %lld, and codes_expert a multiple of 16", (long long)bytes);
+    if (W->scales_row < groups || W->scales_expert < 0 || W->scales_row > far || W->scales_expert > far)
+        return fail(MM_ERR_INVALID_ARG, "scales_row must be at least %lld", (long long)groups);
+    if ((double)(W->rows - 1) * (double)W->codes_row + (double)(W->experts - 1) * (double)W->codes_expert + (double)bytes > (double)far ||
+        (double)(W->rows - 1) * (double)W->scales_row + (double)(W->experts - 1) * (double)W->scales_expert + (double)groups > (double)(far / 2))
+        return fail(MM_ERR_INVALID_ARG, "codes or scales span more than 2^47 bytes");
+    if (W->experts > 1 && (W->codes_expert < (W->rows - 1) * W->codes_row + bytes || W->scales_expert < (W->rows - 1) * W->scales_row + groups))
+        return fail(MM_ERR_INVALID_ARG, "codes_expert or scales_expert does not hold a matrix");
+    if (W->weights_static != 0 && W->weights_static != 1) return fail(MM_ERR_INVALID_ARG, "weights_static must be 0 or 1");
+    for (int r : W->reserved)
+        if (r != 0) return fail(MM_ERR_INVALID_ARG, "reserved fields of W must be 0");
+    a->codes = W->codes, a->scales = W->scales, a->zeros = W->zeros;
+    a->codes_row = W->codes_row, a->codes_expert = W->codes_expert;
+    a->scales_row = W->scales_row, a->scales_expert = W->scales_expert;
+    a->experts = (int)W->experts, a->rows = (int)W->rows, a->cols = (int)W->cols, a->group = (int)W->group;
+    a->groups = (int)groups;
+    a->dtype = W->dtype, a->weights_static = W->weights_static;
+    return MM_OK;
+}
+
+mm_status packed4_product(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t x_rows, const int32_t *order,
+                          int64_t per_row, const int32_t *offsets, int64_t slots, int act, void *Y, int y_dtype,
+                          int64_t y_stride, mm_stream_t stream) {
+    mm::Packed4MmArgs a;
+    mm_status s = check_packed4_weights(W, &a);
+    if (s != MM_OK) return s;
+    const int64_t most = (int64_t)1 << 30, wide = (int64_t)1 << 30;
+    if (slots < 1 || slots > most || x_rows < 1 || x_rows > most) return fail(MM_ERR_INVALID_ARG, "rows of X and Y must be 1 .. 2^30");
+    if (!order && (x_rows < slots || per_row != 1)) return fail(MM_ERR_INVALID_ARG, "without order X has a row for each of Y, and per_row is 1");
+    if (per_row < 1 || per_row > most) return fail(MM_ERR_INVALID_ARG, "per_row must be 1 .. 2^30");
+    if (!X || !is_aligned(X, 16)) return fail(MM_ERR_INVALID_ARG, "X is NULL or not 16-byte aligned");
+    if (x_stride < 0 || x_stride % 8 || x_stride > wide || (x_rows > 1 && x_stride < W->cols))
+        return fail(MM_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least cols");
+    if (y_dtype != MM_F32 && y_dtype != W->dtype) return fail(MM_ERR_INVALID_ARG, "y_dtype must be MM_F32 or W's dtype");
+    const int64_t size = y_dtype == MM_F32 ? 4 : 2;
+    if (!Y || !is_aligned(Y, (uintptr_t)size)) return fail(MM_ERR_INVALID_ARG, "Y is NULL or misaligned");
+    if (act != MM_ACT_NONE && act != MM_ACT_SWIGLU) return fail(MM_ERR_INVALID_ARG, "act must be MM_ACT_NONE or MM_ACT_SWIGLU");
+    if (act == MM_ACT_SWIGLU && W->rows % 2) return fail(MM_ERR_INVALID_ARG, "MM_ACT_SWIGLU takes rows in pairs");
+    const int64_t columns = act == MM_ACT_SWIGLU ? W->rows / 2 : W->rows;
+    if (y_stride < 0 || y_stride > wide || (slots > 1 && y_stride < columns)) return fail(MM_ERR_INVALID_ARG, "y_stride is below Y's columns");
+    const uint64_t yb = span(slots, columns, y_stride, size), xb = span(x_rows, W->cols, x_stride, 2);
+    const uint64_t cb = (uint64_t)((W->experts - 1) * W->codes_expert + (W->rows - 1) * W->codes_row + (W->cols + 31) / 32 * 16);
+    const uint64_t sn = (uint64_t)((W->experts - 1) * W->scales_expert + (W->rows - 1) * W->scales_row + a.groups);
+    if (overlap(Y, yb, X, xb) || overlap(Y, yb, W->codes, cb) || overlap(Y, yb, W->scales, sn * 2) ||
+        (W->zeros && overlap(Y, yb, W->zeros, sn)) || (order && overlap(Y, yb, order, (uint64_t)slots * 4)) ||
+        (offsets && overlap(Y, yb, offsets, (uint64_t)(W->experts + 1) * 4)))
+        return fail(MM_ERR_INVALID_ARG, "Y overlaps an input");
+    s = check_device();
+    if (s != MM_OK) return s;
+    a.X = X, a.x_stride = x_stride, a.x_rows = x_rows, a.order = order, a.per_row = (int)per_row, a.offsets = offsets;
+    a.slots = slots, a.swiglu = act == MM_ACT_SWIGLU, a.Y = Y, a.y_dtype = y_dtype, a.y_stride = y_stride;
+    const cudaError_t e = mm::launch_packed4_rows(a, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
+    return ok();
+}
+
+}  // namespace
+
+mm_status mm_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t M, int act, void *Y, int y_dtype,
+                          int64_t y_stride, mm_stream_t stream) {
+    if (W && W->experts != 1) return fail(MM_ERR_INVALID_ARG, "mm_gemm_packed4 takes one matrix (experts = 1)");
+    return packed4_product(W, X, x_stride, M, nullptr, 1, nullptr, M, act, Y, y_dtype, y_stride, stream);
+}
+
+mm_status mm_experts_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t x_rows, const int32_t *order,
+                                  int64_t per_row, const int32_t *offsets, int64_t slots, int act, void *Y, int y_dtype,
+                                  int64_t y_stride, mm_stream_t stream) {
+    mm_status s = check_ints(offsets, "offsets");
+    if (s == MM_OK && order) s = check_ints(order, "order");
+    if (s != MM_OK) return s;
+    return packed4_product(W, X, x_stride, x_rows, order, per_row, offsets, slots, act, Y, y_dtype, y_stride, stream);
+}
+
+mm_status mm_experts_route_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t *bytes) {
+    if (!bytes) return fail(MM_ERR_INVALID_ARG, "bytes is NULL");
+    if (experts < 1 || experts > 1024 || top_k < 1 || top_k > 32 || top_k > experts || tokens < 1 || tokens > ((int64_t)1 << 30) / top_k)
+        return fail(MM_ERR_INVALID_ARG, "1 <= top_k <= 32, top_k <= experts <= 1024, 1 <= tokens * top_k <= 2^30");
+    *bytes = mm::experts_route_workspace(tokens, (int)experts);
+    return ok();
+}
+
+mm_status mm_experts_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride, int64_t top_k,
+                           int score, int renorm, float scale, int32_t *ids, float *weights, int32_t *offsets,
+                           int32_t *order, int32_t *slots, void *workspace, int64_t workspace_bytes, mm_stream_t stream) {
+    int64_t need = 0;
+    mm_status s = mm_experts_route_workspace(tokens, experts, top_k, &need);
+    if (s != MM_OK) return s;
+    if (dtype != MM_F16 && dtype != MM_BF16 && dtype != MM_F32) return fail(MM_ERR_INVALID_ARG, "dtype must be MM_F16, MM_BF16 or MM_F32");
+    const int64_t size = dtype == MM_F32 ? 4 : 2;
+    if (!logits || !is_aligned(logits, (uintptr_t)size)) return fail(MM_ERR_INVALID_ARG, "logits is NULL or misaligned");
+    if ((tokens > 1 && stride < experts) || stride < 0 || stride > ((int64_t)1 << 30)) return fail(MM_ERR_INVALID_ARG, "stride is below experts, or above 2^30");
+    if (score != MM_ROUTE_SOFTMAX && score != MM_ROUTE_SIGMOID) return fail(MM_ERR_INVALID_ARG, "score must be MM_ROUTE_SOFTMAX or MM_ROUTE_SIGMOID");
+    if (renorm != 0 && renorm != 1) return fail(MM_ERR_INVALID_ARG, "renorm must be 0 or 1");
+    if (!std::isfinite(scale)) return fail(MM_ERR_INVALID_ARG, "scale is not finite");
+    const uint64_t picks = (uint64_t)(tokens * top_k) * 4, lb = span(tokens, experts, stride, size);
+    const void *const outs[6] = {ids, weights, offsets, order, slots, workspace};
+    const uint64_t out_bytes[6] = {picks, picks, (uint64_t)(experts + 1) * 4, picks, picks, (uint64_t)need};
+    const char *const names[6] = {"ids", "weights", "offsets", "order", "slots", "workspace"};
+    for (int i = 0; i < 6; ++i) {
+        if (out_bytes[i] == 0) continue;
+        s = check_ints(outs[i], names[i]);
+        if (s != MM_OK) return s;
+        if (overlap(outs[i], out_bytes[i], logits, lb)) return fail(MM_ERR_INVALID_ARG, "%s overlaps the logits", names[i]);
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_bytes[i], outs[j], out_bytes[j])) return fail(MM_ERR_INVALID_ARG, "%s and %s overlap", names[j], names[i]);
+    }
+    if (workspace_bytes < need) return fail(MM_ERR_INVALID_ARG, "the workspace is below %lld bytes", (long long)need);
+    s = check_device();
+    if (s != MM_OK) return s;
+    const mm::RouteArgs a{logits, dtype, tokens, stride, (int)experts, (int)top_k, score == MM_ROUTE_SIGMOID, renorm, scale,
+                          ids, weights, offsets, order, slots, static_cast<int32_t *>(workspace)};
+    const cudaError_t e = mm::launch_experts_route(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "experts route launch");
+    return ok();
+}
+
+mm_status mm_experts_combine(const void *Y, int y_dtype, int64_t y_stride, int64_t y_rows, const int32_t *slots,
+                             const float *weights, int64_t tokens, int64_t top_k, int64_t cols, const void *residual,
+                             int64_t residual_stride, void *out, int out_dtype, int64_t out_stride, mm_stream_t stream) {
+    const auto size_of = [](int dtype) { return dtype == MM_F32 ? 4 : dtype == MM_F16 || dtype == MM_BF16 ? 2 : 0; };
+    const int64_t ys = size_of(y_dtype), os = size_of(out_dtype), most = (int64_t)1 << 30, wide = (int64_t)1 << 30;
+    if (!ys || !os) return fail(MM_ERR_INVALID_ARG, "y_dtype and out_dtype must be MM_F16, MM_BF16 or MM_F32");
+    if (tokens < 1 || top_k < 1 || top_k > 1024 || tokens > most / top_k || cols < 1 || cols > ((int64_t)1 << 28) || y_rows < 1 || y_rows > most)
+        return fail(MM_ERR_INVALID_ARG, "1 <= tokens * top_k <= 2^30, top_k <= 1024, cols <= 2^28, y_rows <= 2^30");
+    if (!Y || !is_aligned(Y, (uintptr_t)ys) || !out || !is_aligned(out, (uintptr_t)os) || !is_aligned(residual, (uintptr_t)os))
+        return fail(MM_ERR_INVALID_ARG, "Y, residual or out is NULL or misaligned");
+    mm_status s = check_ints(slots, "slots");
+    if (s == MM_OK) s = check_ints(weights, "weights");
+    if (s != MM_OK) return s;
+    if (y_stride < 0 || out_stride < 0 || y_stride > wide || out_stride > wide || (y_rows > 1 && y_stride < cols) ||
+        (tokens > 1 && out_stride < cols) || (residual && (residual_stride < 0 || residual_stride > wide || (tokens > 1 && residual_stride < cols))))
+        return fail(MM_ERR_INVALID_ARG, "a stride is below cols");
+    const uint64_t ob = span(tokens, cols, out_stride, os), picks = (uint64_t)(tokens * top_k) * 4;
+    const bool in_place = residual == out && (residual_stride == out_stride || tokens == 1);
+    if (overlap(out, ob, Y, span(y_rows, cols, y_stride, ys)) || overlap(out, ob, slots, picks) || overlap(out, ob, weights, picks) ||
+        (residual && !in_place && overlap(out, ob, residual, span(tokens, cols, residual_stride, os))))
+        return fail(MM_ERR_INVALID_ARG, "out overlaps an input");
+    s = check_device();
+    if (s != MM_OK) return s;
+    const mm::CombineArgs a{Y, y_dtype, y_stride, y_rows, slots, weights, tokens, cols, (int)top_k, residual, residual_stride,
+                            out, out_dtype, out_stride};
+    const cudaError_t e = mm::launch_experts_combine(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "experts combine launch");
     return ok();
 }
 

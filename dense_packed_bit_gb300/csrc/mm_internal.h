@@ -311,4 +311,61 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t s);
 
+// ------------------------------------------------------------------ 4-bit weights with group scales, experts
+
+// Y[slot][r] = sum_k scale (code - zero) X[row of slot][k], slot by slot with the matrix of its expert.
+struct Packed4MmArgs {
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;  // null: 8
+    int64_t codes_row, codes_expert;    // bytes
+    int64_t scales_row, scales_expert;  // elements, of zeros too
+    int experts, rows, cols, group, groups;
+    int dtype;         // 0 f16, 1 bf16: X and scales
+    int weights_static;
+    const void *X;
+    int64_t x_stride, x_rows;
+    const int32_t *order;    // null: slot i multiplies row i of X; else row order[i] / per_row
+    int per_row;
+    const int32_t *offsets;  // null: one expert, all slots
+    int64_t slots;
+    int swiglu;              // rows 2i, 2i + 1 give silu(gate) * up in column i
+    void *Y;
+    int y_dtype;             // 0 f16, 1 bf16, 2 f32
+    int64_t y_stride;
+};
+cudaError_t launch_packed4_rows(const Packed4MmArgs &a, int sms, cudaStream_t s);
+unsigned int packed4_rows_take_device_error(cudaError_t *err);
+
+struct RouteArgs {
+    const void *logits;
+    int dtype;
+    int64_t tokens, stride;
+    int experts, top_k, sigmoid, renorm;
+    float scale;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *order, *slots;
+    int32_t *counts;  // workspace: [blocks][experts]
+};
+int64_t experts_route_workspace(int64_t tokens, int experts);
+cudaError_t launch_experts_route(const RouteArgs &a, cudaStream_t s);
+
+struct CombineArgs {
+    const void *Y;
+    int y_dtype;
+    int64_t y_stride, y_rows;
+    const int32_t *slots;
+    const float *weights;
+    int64_t tokens, cols;
+    int top_k;
+    const void *residual;  // null: none
+    int64_t r_stride;
+    void *out;
+    int out_dtype;
+    int64_t out_stride;
+};
+cudaError_t launch_experts_combine(const CombineArgs &a, cudaStream_t s);
+unsigned int experts_combine_take_device_error(cudaError_t *err);
+
 }  // namespace mm

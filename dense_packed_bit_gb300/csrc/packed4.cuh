@@ -1,0 +1,96 @@
+// packed4.cuh -- 4-bit weights with group scales as the kernels see them: whose rows a unit of work
+// multiplies, and codes turned into 16-bit whole numbers.
+//
+// Everything read from device memory that becomes an address (expert offsets, rows of X) is checked
+// before its use: what is out of range is treated as absent and recorded in the translation unit's
+// device error word (kDevErrRange).
+#pragma once
+
+#include "cache_view.cuh"  // launch_pdl, kDevErrRange
+#include "mm_common.cuh"
+#include "mm_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace mm {
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+// (a & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
+// Codes become weights by placing them in the mantissa of a 16-bit number whose last place is 1 (1024 in fp16,
+// 128 in bf16) and taking that number and the zero off again: c - z is a whole number of -15 .. 15, exact in
+// both types, and the difference of two exact numbers is rounded nowhere.
+template <typename T>
+struct Code4;
+template <>
+struct Code4<__half> {
+    static constexpr uint32_t kBase = 0x64006400u;  // 1024
+    static __device__ __forceinline__ uint32_t zero(uint32_t z) { return 0x64006400u + z * 0x10001u; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&d);
+    }
+    static __device__ __forceinline__ float f32(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+    static __device__ __forceinline__ uint16_t round(float v) { return __half_as_ushort(__float2half_rn(v)); }
+};
+template <>
+struct Code4<__nv_bfloat16> {
+    static constexpr uint32_t kBase = 0x43004300u;  // 128
+    static __device__ __forceinline__ uint32_t zero(uint32_t z) { return 0x43004300u + z * 0x10001u; }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 d =
+            __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&d);
+    }
+    static __device__ __forceinline__ float f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+    static __device__ __forceinline__ uint16_t round(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// Slots [first, first + count) of expert e.
+struct Slots {
+    int first, count;
+};
+__device__ __forceinline__ Slots slots_of(const Packed4MmArgs &a, int e, unsigned int *err) {
+    if (!a.offsets) return {0, (int)a.slots};
+    const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+    if (lo < 0 || hi < lo || hi > a.slots) {
+        *err = kDevErrRange;
+        return {0, 0};
+    }
+    return {lo, hi - lo};
+}
+
+// The row of X that slot i multiplies, -1 where order names none.
+__device__ __forceinline__ int64_t x_row(const Packed4MmArgs &a, int64_t i, unsigned int *err) {
+    if (!a.order) return i;
+    const int pick = __ldg(a.order + i);
+    const int row = pick < 0 ? -1 : pick / a.per_row;
+    if (row < 0 || row >= a.x_rows) {
+        *err = kDevErrRange;
+        return -1;
+    }
+    return row;
+}
+
+// Y[slot][col] = v in Y's type (0 f16, 1 bf16, 2 f32)
+__device__ __forceinline__ void store_y(const Packed4MmArgs &a, int64_t slot, int col, float v) {
+    const int64_t i = slot * a.y_stride + col;
+    if (a.y_dtype == 2) static_cast<float *>(a.Y)[i] = v;
+    else if (a.y_dtype == 1) static_cast<uint16_t *>(a.Y)[i] = Code4<__nv_bfloat16>::round(v);
+    else static_cast<uint16_t *>(a.Y)[i] = Code4<__half>::round(v);
+}
+
+}  // namespace mm

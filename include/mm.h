@@ -34,6 +34,10 @@
  *     choice of the next token (declared at the end of this file, with their
  *     own types, layouts and error bounds).
  *
+ *  5. 4-bit weights with a scale and a zero per group of a row's elements, times
+ *     any number of rows, and a mixture of experts on such weights: routing,
+ *     ragged products by expert, combination (declared last, as 4).
+ *
  * Layouts (all row-major, all pointers DEVICE memory owned by the caller):
  *  - A: M x K (lda >= K), or K x M when transA (lda >= M).
  *  - B: K x N (ldb >= N), or N x K when transB (ldb >= K).
@@ -195,7 +199,7 @@ mm_status mm_attention_bwd(const float *Q, const float *K, const float *V, const
  * 16-byte aligned, the general kernel otherwise.  Errors: as mm_gemm_f32, plus
  * MM_ERR_INVALID_ARG for an unknown act or C overlapping bias.
  */
-enum { MM_ACT_NONE = 0, MM_ACT_GELU_TANH = 1 };
+enum { MM_ACT_NONE = 0, MM_ACT_GELU_TANH = 1, MM_ACT_SWIGLU = 2 /* mm_gemm_packed4 and experts only */ };
 mm_status mm_gemm_f32_bias_act(int transA, int transB, int64_t M, int64_t N, int64_t K,
                                const float *A, int64_t lda, const float *B, int64_t ldb,
                                const float *bias, int act, float *C, int64_t ldc,
@@ -714,6 +718,106 @@ mm_status mm_cache_attention_tree(const mm_cache *cache, int64_t layer, const vo
 mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                     const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                     const float *u, int32_t *tokens, float *logprobs, mm_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit weights with group scales, experts
+ *
+ * "Kernel 0112", section "What the kernel costs in a whole token": a token's products read 4-bit weights.
+ * mm_gemv_packed4 above takes one scale per row and one vector; here a row has a scale, and if wanted a zero, per
+ * group of its elements, there are any number of rows of X, and there may be a matrix per expert.
+ */
+
+/*
+ * Matrices W_e of `rows` x `cols`, e < experts (1 for a plain one), in device memory owned by the caller:
+ *     W_e[r][k] = scale[e][r][k / group] * (code[e][r][k] - zero[e][r][k / group])
+ * codes: element k of a row in byte k / 2, low four bits first; rows codes_row bytes apart, matrices codes_expert
+ *   bytes: both multiples of 16, codes_row at least 16 * ceil(cols / 32); those 16 * ceil(cols / 32) bytes of every row
+ *   are read, fields past cols ignored.  codes 16-byte aligned.
+ * scales: of `dtype`, rows scales_row elements apart, matrices scales_expert; ceil(cols / group) to a row.
+ * zeros: a byte each, laid out (strides in elements) like scales, the low four bits count; NULL: 8 throughout.
+ * group: 32, 64 or 128.  dtype: MM_F16 or MM_BF16, that of scales and X.
+ * weights_static: 1 promises that codes, scales and zeros are not written by work that is still queued or running when
+ *   a call is made (weights laid out once), so their loads may start before the kernel in front of it has ended.
+ * rows, cols at most 2^28, experts at most 1024, 2^47 bytes from the first code to the last; strides of X, Y, logits,
+ * residual and out below at most 2^30.
+ * The struct is host memory, read during each call.
+ */
+typedef struct {
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;
+    int64_t experts, rows, cols, group;
+    int64_t codes_row, codes_expert;
+    int64_t scales_row, scales_expert;
+    int dtype;
+    int weights_static;
+    int reserved[4];  /* 0 */
+} mm_packed4;
+
+/*
+ * Y = X W^T for W->experts = 1: Y[m][r] = sum_k W[r][k] X[m][k], m < M.
+ * X: [M][cols] of W's dtype, rows x_stride elements apart (a multiple of 8; X 16-byte aligned).
+ * act: MM_ACT_NONE; MM_ACT_SWIGLU (rows even): column i of Y is silu(z[2 i]) * z[2 i + 1], z the product, silu(z) = z /
+ *   (1 + exp(-z)): a gate's and an up-projection's rows taken in turn; Y then has rows / 2 columns.
+ * Y: y_dtype MM_F32 or W's dtype, rows y_stride elements apart, aligned to its elements; every element is written.
+ * Codes less their zeros are exact, products and sums are fp32, the scale is applied to a group's fp32 sum, Y is rounded
+ * once: |z - z_exact| <= 1e-5 * sum_k |W[r][k] X[m][k]| before that.  Results repeat bit for bit.
+ * 1 <= M <= 2^30.
+ * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, strides, types or options out of range, Y
+ * overlapping an input.
+ */
+mm_status mm_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t M, int act, void *Y, int y_dtype,
+                          int64_t y_stride, mm_stream_t stream);
+
+/*
+ * The experts of each token from its router's logits.
+ * logits: [tokens][experts] of `dtype` (MM_F16, MM_BF16, MM_F32), rows `stride` elements apart.
+ * Token t's picks are the top_k largest of its logits, larger first, equal ones by index; NaN and -infinity are never
+ * picked.  ids: [tokens][top_k], -1 where there are fewer.  weights: [tokens][top_k] fp32, `scale` times the scores of the
+ * picks: score MM_ROUTE_SOFTMAX exp(x) / sum over all experts, MM_ROUTE_SIGMOID 1 / (1 + exp(-x)); renorm = 1: divided by
+ * their sum over the token's picks.  A pick of -1 has weight 0.  A logit of +infinity makes the weights that depend on it
+ * NaN (MM_ROUTE_SIGMOID without renorm: 1).
+ * The picks in order of expert, within an expert of token: order[i] = token * top_k + j is the pick in slot i, the slots
+ * of expert e are offsets[e] .. offsets[e + 1] - 1 (offsets: [experts + 1]), and slots[token * top_k + j] is a pick's slot,
+ * -1 for none.  order: [tokens * top_k], of which the first offsets[experts] are written.
+ * workspace: mm_experts_route_workspace bytes (0 is possible), 4-byte aligned, its contents on entry do not matter; two
+ * calls at once need two.
+ * 1 <= top_k <= 32, top_k <= experts <= 1024, tokens * top_k at most 2^30.
+ * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, types or options out of range, a non-finite scale, a
+ * workspace that is too small, outputs that overlap each other, the logits or the workspace.
+ */
+enum { MM_ROUTE_SOFTMAX = 0, MM_ROUTE_SIGMOID = 1 };
+mm_status mm_experts_route_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t *bytes);
+mm_status mm_experts_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride, int64_t top_k,
+                           int score, int renorm, float scale, int32_t *ids, float *weights, int32_t *offsets,
+                           int32_t *order, int32_t *slots, void *workspace, int64_t workspace_bytes, mm_stream_t stream);
+
+/*
+ * The products of a ragged batch, slot by slot with the matrix of its expert: for e < W->experts and slots i of
+ * offsets[e] .. offsets[e + 1] - 1,
+ *     Y[i] = act(W_e . X[row of i]),   row of i = order[i] / per_row, or i where order is NULL (per_row must then be 1).
+ * X: [x_rows][cols].  With mm_experts_route's order and per_row = top_k, row t of X is token t's; a product that follows
+ * takes the slots in place (order NULL, x_rows = slots).  slots: the rows of Y and entries of order, an upper bound of
+ * offsets[experts]; rows of Y in no expert's range are left as they were.  offsets and order are checked on the device: a
+ * range that is not ascending within 0 .. slots is skipped, a row out of range counts as 0s, and mm_check_device_error
+ * then returns MM_ERR_INVALID_ARG.  Types, act, layout and error bound as mm_gemm_packed4.  1 <= slots <= 2^30.
+ * Errors: as mm_gemm_packed4, plus x_rows < 1, or < slots where order is NULL.
+ */
+mm_status mm_experts_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t x_rows,
+                                  const int32_t *order, int64_t per_row, const int32_t *offsets, int64_t slots, int act,
+                                  void *Y, int y_dtype, int64_t y_stride, mm_stream_t stream);
+
+/*
+ * out[t] = residual[t] + sum_j weights[t][j] * Y[slots[t][j]], t < tokens, j < top_k ascending, in fp32, rounded once; a slot
+ * of -1 adds nothing (whatever its weight), one that is not below y_rows neither, and mm_check_device_error then returns
+ * MM_ERR_INVALID_ARG.
+ * Y: [y_rows][cols] of y_dtype; residual (NULL: 0) and out: [tokens][cols] of out_dtype; any of MM_F16, MM_BF16, MM_F32,
+ * rows their strides apart, aligned to their elements (16-byte aligned rows of a multiple of 16 bytes are faster).  out may
+ * be the residual itself with the same stride, and overlaps nothing else.
+ * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, strides or types out of range, overlaps.
+ */
+mm_status mm_experts_combine(const void *Y, int y_dtype, int64_t y_stride, int64_t y_rows, const int32_t *slots,
+                             const float *weights, int64_t tokens, int64_t top_k, int64_t cols, const void *residual,
+                             int64_t residual_stride, void *out, int out_dtype, int64_t out_stride, mm_stream_t stream);
 
 #ifdef __cplusplus
 }
