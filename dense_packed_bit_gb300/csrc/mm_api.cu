@@ -892,6 +892,11 @@ mm_status mm_check_device_error(mm_stream_t stream) {
     const unsigned int pw = mm::packed4_rows_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
     if (pw != 0) return fail(MM_ERR_INVALID_ARG, "4-bit products: an expert's slots or a row of X in device memory is out of range");
+    const unsigned int pt = mm::packed4_tiles_take_device_error(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
+    if (pt == mm::kCacheErrRange)
+        return fail(MM_ERR_INVALID_ARG, "4-bit products: an expert's slots or a row of X in device memory is out of range");
+    if (pt != 0) return fail(MM_ERR_TIMEOUT, "a bounded device wait ran out in the 4-bit products (code %u)", pt);
     const unsigned int co = mm::experts_combine_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
     if (co != 0) return fail(MM_ERR_INVALID_ARG, "experts combine: a slot in device memory is out of range");
@@ -1337,7 +1342,8 @@ mm_status packed4_product(const mm_packed4 *W, const void *X, int64_t x_stride, 
     if (s != MM_OK) return s;
     a.X = X, a.x_stride = x_stride, a.x_rows = x_rows, a.order = order, a.per_row = (int)per_row, a.offsets = offsets;
     a.slots = slots, a.swiglu = act == MM_ACT_SWIGLU, a.Y = Y, a.y_dtype = y_dtype, a.y_stride = y_stride;
-    const cudaError_t e = mm::launch_packed4_rows(a, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = slots > 16 * W->experts ? mm::launch_packed4_tiles(a, sm_count(), st) : mm::launch_packed4_rows(a, sm_count(), st);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
     return ok();
 }

@@ -336,6 +336,8 @@ struct Packed4MmArgs {
 };
 cudaError_t launch_packed4_rows(const Packed4MmArgs &a, int sms, cudaStream_t s);
 unsigned int packed4_rows_take_device_error(cudaError_t *err);
+cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s);
+unsigned int packed4_tiles_take_device_error(cudaError_t *err);
 
 struct RouteArgs {
     const void *logits;
