@@ -9,14 +9,14 @@
 // tensor memory and an FMA for each of its elements against G MMA steps of each: with groups of 128 a quarter of the time
 // of the MMAs, beside which it runs (two accumulators of 256 columns), with groups of 32 all of it.
 //
-// Roles of a CTA's 16 warps, over a ring of stages of 64 columns:
+// Roles of a CTA's 20 warps, over a ring of stages of 64 columns:
 //   warp 0          X by TMA, 16 rows to a box, or four gathered rows at a time where `order` names them;
 //   warp 1          issues the MMAs (in a pair: the even CTA's, for both);
-//   warps 4 - 7     a thread to a row of W: codes AHEAD stages ahead from memory into registers, made 16-bit numbers and
-//                   stored as the MMA's A (128-byte swizzle).  Three instructions for two codes: a byte and the same byte
-//                   shifted are put into the halves of a register, masked into the mantissa of 1024 (bf16: 128), and that
-//                   number and the zero are subtracted;
-//   warps 8 - 15    a thread to a row of D and half of its columns: scale and add, at the end the activation and the store
+//   warp 2          codes by TMA, 128 rows x 128 codes to a box, into a ring of their own that is CRING boxes deep;
+//   warps 4 - 11    make 16-bit numbers of them and store them as the MMA's A (128-byte swizzle), a thread to 32 codes of a
+//                   row.  Three instructions for two codes: a byte and the same byte shifted are put into the halves of
+//                   a register, masked into the mantissa of 1024 (bf16: 128), and that number and the zero are subtracted;
+//   warps 12 - 19   a thread to a row of D and half of its columns: scale and add, at the end the activation and the store
 //                   (at a fixed row of X a warp writes 32 neighbouring columns of Y).
 // Persistent: the units of work -- a chunk of an expert's slots times a tile of rows of W -- are dealt to the CTAs in
 // turn, tiles of rows first, so that X is read once and the codes, 4 bits a weight, come from L2.  The slots of an expert
@@ -35,24 +35,28 @@ namespace {
 constexpr int BM = 128;        // rows of W per CTA: the TMEM lanes
 constexpr int BK = 64;         // columns per stage: 128 bytes of X's type
 constexpr int BN = 256;        // rows of X per unit, at most: columns of an accumulator
-constexpr int AHEAD = 4;       // stages of codes on their way to registers
-constexpr int NTHREADS = 512;
-constexpr int WARP_TMA = 0, WARP_MMA = 1, WARP_DEC0 = 4, WARP_EPI0 = 8;
-constexpr int DEC_WARPS = 4, EPI_WARPS = 8;
+constexpr int CRING = 6;       // boxes of codes on their way to shared memory, 8 KB each
+constexpr int CBOX = BM * 64;  // bytes of a box: 128 rows of two stages' codes
+constexpr int NTHREADS = 640;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_CODES = 2, WARP_DEC0 = 4, WARP_EPI0 = 12;
+constexpr int DEC_WARPS = 8, EPI_WARPS = 8;
 constexpr int MAX_EXPERTS = 1024;
 constexpr int BOX = 16;        // rows of X per TMA box
 
-// Registers of a thread after the roles part, of the 128 at launch: 256 x 80 + 256 x 176 = 512 x 128.
-#define MM_PACKED4_REGS_FEW "80"
-#define MM_PACKED4_REGS_EPI "176"
+// Registers of a thread once the roles part, of the 96 at launch: 384 x 48 + 256 x 168 = 640 x 96.
+#define MM_PACKED4_REGS_FEW "48"
+#define MM_PACKED4_REGS_EPI "168"
 
 template <int CG>
 struct Plan {
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = CG == 2 ? 6 : 4;
-    static constexpr int BAR = STAGES * STAGE;                 // 3 barriers a stage, 4 of the accumulators, 1 at the end
+    static constexpr int STAGES = CG == 2 ? 5 : 3;
+    static constexpr int CODES = STAGES * STAGE;
+    static constexpr int BAR = CODES + CRING * CBOX;
     static constexpr int PRE = BAR + 256;                      // chunks before each expert
     static constexpr int TOTAL = PRE + (MAX_EXPERTS + 1) * 4 + 12 + 1024;  // + alignment of the dynamic allocation
+    static_assert((3 * STAGES + 2 * CRING + 5) * 8 + 8 <= 256, "barriers");
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
 struct Shared {  // what follows the barriers
@@ -70,14 +74,14 @@ struct Work {
     const int *pre;    // chunks before expert e; pre[experts]: all
     int experts, tiles;
     int longest;       // slots of a chunk, at most
-    int64_t units;
+    int units;
 };
 
 __device__ __forceinline__ int chunks_of(int n, int longest) { return (n + longest - 1) / longest; }
 
 template <int CG>
-__device__ __forceinline__ Unit unit_at(const Packed4MmArgs &a, const Work &w, int64_t u, unsigned int *err) {
-    const int chunk = (int)(u / w.tiles), tile = (int)(u - (int64_t)chunk * w.tiles);
+__device__ __forceinline__ Unit unit_at(const Packed4MmArgs &a, const Work &w, int u, unsigned int *err) {
+    const int chunk = u / w.tiles, tile = u - chunk * w.tiles;
     int lo = 0, hi = w.experts;  // pre[lo] <= chunk < pre[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -103,29 +107,45 @@ __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code
         st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
 }
 
+// One thread of a warp that runs as one issues (the operands stay uniform)
+template <int CG>
+__device__ __forceinline__ void mma_if(bool issue, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
+            "r"(accumulate), "r"((uint32_t)issue)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
+            "r"(accumulate), "r"((uint32_t)issue)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void commit_if(bool issue, uint64_t *bar) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.b32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+                smem_u32(bar)),
+            "r"((uint32_t)issue)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+            "r"((uint32_t)issue)
+            : "memory");
+}
+// What is the same in all lanes, and known to be: a reduction's result
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(~0u, x); }
+
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
     if constexpr (CG == 2) mbar_arrive_cluster(cluster_map(smem_u32(bar), 0));
     else mbar_arrive(bar);
-}
-
-// 64 codes of one row and their zeros (one, or of groups of 32 two)
-struct Codes {
-    uint4 lo, hi;
-    uint32_t z;  // low half: of the first 32 columns, high half: of the others
-};
-
-__device__ __forceinline__ void load_codes(const Packed4MmArgs &a, const uint8_t *codes, const uint8_t *zeros, int s, Codes &c) {
-    const int col = s * BK;
-    c.lo = ld_stream_v4(codes + s * (BK / 2));
-    c.hi = col + 32 < a.cols ? ld_stream_v4(codes + s * (BK / 2) + 16) : make_uint4(0, 0, 0, 0);
-    if (zeros) {
-        const uint32_t z0 = __ldg(zeros + col / a.group) & 15;
-        const uint32_t z1 = a.group == 32 && col + 32 < a.cols ? __ldg(zeros + col / 32 + 1) & 15 : z0;
-        c.z = z0 | z1 << 16;
-    } else {
-        c.z = 0x00080008u;
-    }
 }
 
 // 32 codes as 16-bit numbers in order, 16 bytes for each word: chunks first .. first + 3 of the row's 128 bytes
@@ -156,47 +176,58 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// Column `row` of Y, slots first .. first + n - 1: this thread's values of one row of D
-template <typename T, typename Y>
-__device__ __forceinline__ void store_rows(const Packed4MmArgs &a, int64_t first, int row, int n, const float (&v)[32]) {
-    if (row >= a.rows) return;
-    Y *p = static_cast<Y *>(a.Y) + first * a.y_stride + row;
-#pragma unroll
-    for (int j = 0; j < 32; ++j, p += a.y_stride) {
-        if (j >= n) break;
-        if constexpr (sizeof(Y) == 4) *p = v[j];
-        else *p = Code4<T>::round(v[j]);
-    }
-}
+// silu in few instructions, for results of 16 bits: an exponential and a quotient of a few ulp each (at a gate of -20 about
+// 2^-19, of which a half-ulp of fp16 is 2^7)
+__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// silu(gate) * up of the rows of neighbouring lanes: the even lane takes the even slots, the odd lane the others
+// Slots first .. first + n - 1 of Y from this thread's row of D.  Neighbouring lanes hold neighbouring rows: the even one
+// takes the even slots, the odd one the others, so that a thread stores pairs (or silu(gate) * up of a pair).
 template <typename T, typename Y>
-__device__ __forceinline__ void store_pairs(const Packed4MmArgs &a, int64_t first, int row, int n, const float (&v)[32]) {
-    const int odd = row & 1;
-    Y *p = static_cast<Y *>(a.Y) + (first + odd) * a.y_stride + (row >> 1);
+__device__ __forceinline__ void store32(const Packed4MmArgs &a, int first, int row, int n, const float *v) {
+    const int odd = row & 1, width = a.swiglu ? a.rows >> 1 : a.rows;
+    if (sizeof(Y) == 4 && !a.swiglu) {
+        Y *p = static_cast<Y *>(a.Y) + first * a.y_stride + row;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, p += a.y_stride)
+            if (j < n && row < a.rows) *p = v[j];
+        return;
+    }
+    const int col = a.swiglu ? row >> 1 : row - odd;
+    Y *p = static_cast<Y *>(a.Y) + (first + odd) * a.y_stride + col;
+    const bool pair = !a.swiglu && col + 1 < width && (reinterpret_cast<uintptr_t>(a.Y) & 3) == 0 && a.y_stride % 2 == 0;
 #pragma unroll
     for (int j = 0; j < 32; j += 2, p += 2 * a.y_stride) {
         if (j >= n) break;
         const float got = __shfl_xor_sync(~0u, odd ? v[j] : v[j + 1], 1);
-        const float gate = odd ? got : v[j], up = odd ? v[j + 1] : got;
-        if (j + odd >= n || row >= a.rows) continue;
-        const float z = silu(gate) * up;
-        if constexpr (sizeof(Y) == 4) *p = z;
-        else *p = Code4<T>::round(z);
+        const float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
+        if (j + odd >= n || col >= width) continue;
+        if (a.swiglu) {
+            if constexpr (sizeof(Y) == 4) *p = silu(lo) * hi;
+            else *p = Code4<T>::round(silu_fast(lo) * hi);
+        } else if constexpr (sizeof(Y) == 2) {
+            if (pair) *reinterpret_cast<uint32_t *>(p) = Code4<T>::round(lo) | (uint32_t)Code4<T>::round(hi) << 16;
+            else {
+                p[0] = Code4<T>::round(lo);
+                if (col + 1 < width) p[1] = Code4<T>::round(hi);
+            }
+        }
     }
 }
 
 template <typename T, int CG>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ Packed4MmArgs a) {
+    packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                         const __grid_constant__ Packed4MmArgs a) {
     using P = Plan<CG>;
     constexpr int STAGES = P::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_aligned<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR);  // X has arrived (this CTA's)
-    uint64_t *ready = full + STAGES;   // codes and X are there (the leader's)
+    uint64_t *ready = full + STAGES;   // numbers and X are there (the leader's)
     uint64_t *empty = ready + STAGES;  // the stage's MMAs are done (every CTA's)
-    uint64_t *accf = empty + STAGES;   // a group's sum is complete (every CTA's)
+    uint64_t *cfull = empty + STAGES;  // codes have arrived (this CTA's)
+    uint64_t *cempty = cfull + CRING;  // they have been read (this CTA's)
+    uint64_t *accf = cempty + CRING;   // a group's sum is complete (every CTA's)
     uint64_t *acce = accf + 2;         // it has been taken (the leader's)
     uint64_t *last = acce + 2;
     Shared *sh = reinterpret_cast<Shared *>(last + 1);
@@ -205,7 +236,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
-    const int64_t cid = blockIdx.x / CG, ncl = gridDim.x / CG;
+    const int cid = blockIdx.x / CG, ncl = gridDim.x / CG;
 
     if (warp == WARP_MMA) {
         if constexpr (CG == 2) {
@@ -222,6 +253,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(&ready[s], DEC_WARPS * CG);
             mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < CRING; ++s) {
+            mbar_init(&cfull[s], 1);
+            mbar_init(&cempty[s], DEC_WARPS);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
             mbar_init(&acce[b], EPI_WARPS * CG);
@@ -230,9 +265,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
     }
-    pdl_wait();
-    pdl_launch_dependents();
+    // weights laid out long ago are asked for before the kernel in front has ended, where that one does not say whose they are
+    const bool early = a.weights_static && !a.offsets;
+    if (!early) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 
     // chunks before each expert, for the longest chunk that leaves no SM idle
     unsigned int err = 0;
@@ -272,7 +312,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (e0 < a.experts) pre[e0] = before;
         if (e0 + 1 < a.experts) pre[e0 + 1] = before + c0;
         if (threadIdx.x == 0) pre[a.experts] = all;
-        wk.units = (int64_t)all * wk.tiles;
+        wk.units = all * wk.tiles;
     }
     tc_fence_before_sync();
     if constexpr (CG == 2) cluster_sync();
@@ -281,12 +321,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t tmem = sh->tmem;
     const int stages = (a.cols + BK - 1) / BK;
 
+    const auto late_wait = [&] {
+        if (early) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+    };
     if (warp < WARP_DEC0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " MM_PACKED4_REGS_FEW ";");
-        if (warp == WARP_TMA) {
-            int it = 0;
+        if (warp == WARP_X) {
+            late_wait();
+            int b = 0, it = 0;
+            uint32_t use = 0;
             bool stop = false;
-            for (int64_t u = cid; u < wk.units && !stop; u += ncl) {
+            for (int u = cid; u < wk.units && !stop; u += ncl) {
                 const Unit t = unit_at<CG>(a, wk, u, &err);
                 const int mine = t.N / CG, from = (int)rank * mine;  // this CTA's rows of X
                 int rows[2][4];
@@ -301,10 +349,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                 }
                 for (int s = 0; s < stages; ++s, ++it) {
-                    const int b = it % STAGES;
-                    const uint32_t use = it / STAGES;
                     if (*abort_flag) { stop = true; break; }
-                    if (use > 0 && !mbar_wait(&empty[b], (use - 1) & 1)) {
+                    if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
                         fail<CG>(abort_flag, kDevErrWaitEmpty);
                         stop = true;
                         break;
@@ -320,139 +366,178 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     } else if (lane * BOX < mine) {
                         tma_load_2d(dst + lane * BOX * 128, &tmX, &full[b], s * BK, t.first + from + lane * BOX);
                     }
+                    if (++b == STAGES) b = 0, ++use;
                 }
             }
             // every copy issued must land before this CTA's shared memory is released
-            for (int b = 0; b < STAGES && b < it; ++b) {
-                const int lastit = b + ((it - 1 - b) / STAGES) * STAGES;
-                if (!mbar_wait(&full[b], (uint32_t)(lastit / STAGES) & 1)) {
+            for (int i = 0; i < STAGES && i < it; ++i) {
+                const int lastit = i + ((it - 1 - i) / STAGES) * STAGES;
+                if (!mbar_wait(&full[i], (uint32_t)(lastit / STAGES) & 1)) {
                     atomicExch(&g_packed4_tiles_err, kDevErrDrain);
                     break;
                 }
             }
-        } else if (warp == WARP_MMA && rank == 0) {
+        } else if (warp == WARP_CODES) {
             if (lane == 0) {
-                constexpr uint32_t fmt = sizeof(T) && __is_same(T, __half) ? kFmtF16 : kFmtBF16;
-                constexpr uint16_t both = (uint16_t)((1u << CG) - 1u);
-                const int steps = a.group / 16;  // MMAs of a group
-                int it = 0, gi = 0;              // stages, groups so far
+                int b = 0, it = 0;
+                uint32_t use = 0;
                 bool stop = false;
-                for (int64_t u = cid; u < wk.units && !stop; u += ncl) {
+                for (int u = cid; u < wk.units && !stop; u += ncl) {
                     const Unit t = unit_at<CG>(a, wk, u, &err);
-                    const uint32_t idesc = make_idesc(fmt, fmt, (uint32_t)t.N, BM * CG);
-                    const int total = (a.cols + 15) / 16;  // MMAs of the unit
-                    int done = 0;                          // of them, those of whole or begun groups so far
-                    for (int s = 0; s < stages && !stop; ++s, ++it) {
-                        const int b = it % STAGES;
-                        const uint32_t use = it / STAGES;
+                    for (int s = 0; s < stages; s += 2, ++it) {
                         if (*abort_flag) { stop = true; break; }
-                        if (!mbar_wait(&ready[b], use & 1)) {
-                            fail<CG>(abort_flag, kDevErrWaitFull);
+                        if (use > 0 && !mbar_wait_sleep(&cempty[b], (use - 1) & 1)) {
+                            fail<CG>(abort_flag, kDevErrWaitEmpty);
                             stop = true;
                             break;
                         }
-                        tc_fence_after_sync();
-                        const uint32_t at = smem_u32(smem + b * P::STAGE);
-#pragma unroll 1
-                        for (int k = 0; k < BK / 16 && done < total; ++k, ++done) {
-                            const int in_group = done & (steps - 1);
-                            if (in_group == 0 && gi >= 2 && !mbar_wait(&acce[gi & 1], (uint32_t)(gi / 2 - 1) & 1)) {
-                                fail<CG>(abort_flag, kDevErrWaitEmpty);
-                                stop = true;
-                                break;
-                            }
-                            if (in_group == 0) tc_fence_after_sync();
-                            const uint32_t d = tmem + (uint32_t)((gi & 1) * BN);
-                            const uint64_t da = sdesc_kmajor_sw128(at + 32u * k), db = sdesc_kmajor_sw128(at + P::A_BYTES + 32u * k);
-                            if constexpr (CG == 2) umma_f16_pair(d, da, db, idesc, in_group > 0);
-                            else umma_f16(d, da, db, idesc, in_group > 0);
-                            if (in_group == steps - 1 || done == total - 1) {
-                                if constexpr (CG == 2) umma_commit_pair(&accf[gi & 1], both);
-                                else umma_commit(&accf[gi & 1]);
-                                ++gi;
-                            }
-                        }
-                        if constexpr (CG == 2) umma_commit_pair(&empty[b], both);
-                        else umma_commit(&empty[b]);
+                        mbar_arrive_expect_tx(&cfull[b], CBOX);
+                        tma_load_3d(smem + P::CODES + b * CBOX, &tmW, &cfull[b], s * (BK / 2), t.r0 + (int)rank * BM, t.e);
+                        if (++b == CRING) b = 0, ++use;
                     }
                 }
-                // every MMA issued must be complete before the tensor memory is freed
-                if constexpr (CG == 2) umma_commit_pair(last, 1);
-                else umma_commit(last);
-                if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
+                for (int i = 0; i < CRING && i < it; ++i) {
+                    const int lastit = i + ((it - 1 - i) / CRING) * CRING;
+                    if (!mbar_wait(&cfull[i], (uint32_t)(lastit / CRING) & 1)) {
+                        atomicExch(&g_packed4_tiles_err, kDevErrDrain);
+                        break;
+                    }
+                }
             }
+            __syncwarp();
+            late_wait();
+        } else if (warp == WARP_MMA && rank == 0) {
+            late_wait();
+            constexpr uint32_t fmt = __is_same(T, __half) ? kFmtF16 : kFmtBF16;
+            const bool issue = lane == 0;
+            int b = 0, gi = 0;  // stage of the ring, groups so far
+            uint32_t use = 0;
+            bool stop = false;
+            const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned int code) {
+                if (!mbar_wait(bar, parity)) {
+                    if (issue) fail<CG>(abort_flag, code);
+                    stop = true;
+                }
+                tc_fence_after_sync();
+            };
+            const auto begin = [&] {  // a group's accumulator is free
+                if (gi >= 2) wait(&acce[gi & 1], (uint32_t)(gi / 2 - 1) & 1, kDevErrWaitEmpty);
+            };
+            const auto end = [&] {
+                commit_if<CG>(issue && !stop, &accf[gi & 1]);
+                ++gi;
+            };
+            const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem)), db0 = sdesc_kmajor_sw128(smem_u32(smem) + P::A_BYTES);
+            for (int u = cid; u < wk.units && !stop; u += ncl) {
+                const Unit t = unit_at<CG>(a, wk, u, &err);
+                const uint32_t idesc = uniform(make_idesc(fmt, fmt, (uint32_t)t.N, BM * CG));
+                for (int s = 0; s < stages && !stop; ++s) {
+                    if (*abort_flag) { stop = true; break; }
+                    // the first MMA of a group clears the accumulator: of 128 columns every other stage's, of 64 every
+                    // stage's, of 32 two in a stage
+                    const bool first = a.group <= BK || (s & 1) == 0;
+                    if (first) begin();
+                    if (!stop) wait(&ready[b], use & 1, kDevErrWaitFull);
+                    const uint32_t at = uniform((uint32_t)b * (P::STAGE >> 4)), dd = uniform(tmem);
+                    const uint64_t da = da0 + at, db = db0 + at;
+                    uint32_t d = dd + (uint32_t)((gi & 1) * BN);
+                    const bool go = issue && !stop;
+                    mma_if<CG>(go, d, da, db, idesc, !first);
+                    mma_if<CG>(go, d, da + 2, db + 2, idesc, 1);
+                    const bool halves = a.group == 32 && s * BK + 32 < a.cols;
+                    if (halves) {
+                        end();
+                        begin();
+                        d = dd + (uint32_t)((gi & 1) * BN);
+                    }
+                    const bool go2 = issue && !stop;
+                    mma_if<CG>(go2, d, da + 4, db + 4, idesc, !halves);
+                    mma_if<CG>(go2, d, da + 6, db + 6, idesc, 1);
+                    commit_if<CG>(go2, &empty[b]);
+                    if (a.group <= BK || (s & 1) || s == stages - 1) end();
+                    if (++b == STAGES) b = 0, ++use;
+                }
+            }
+            // every MMA issued must be complete before the tensor memory is freed
+            commit_if<CG>(issue, last);
+            if (!mbar_wait(last, 0) && issue) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
+        } else {
+            late_wait();
         }
     } else if (warp < WARP_EPI0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " MM_PACKED4_REGS_FEW ";");
-        const int r = threadIdx.x - 32 * WARP_DEC0;  // the row of the tile
-        // the cursor of the loads runs AHEAD stages before the one that decodes, over the ends of units
-        int64_t lu = cid;
-        int ls = 0;
-        const uint8_t *lc = nullptr, *lz = nullptr;
-        const auto point = [&] {
-            if (lu >= wk.units) return;
-            const Unit t = unit_at<CG>(a, wk, lu, &err);
-            const int row = min(t.r0 + (int)rank * BM + r, a.rows - 1);
-            lc = a.codes + t.e * a.codes_expert + row * a.codes_row;
-            lz = a.zeros ? a.zeros + t.e * a.scales_expert + row * a.scales_row : nullptr;
-        };
-        const auto load = [&](Codes &c) {
-            if (lu >= wk.units) return;
-            load_codes(a, lc, lz, ls, c);
-            if (++ls == stages) ls = 0, lu += ncl, point();
-        };
-        Codes c[AHEAD];
-        point();
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) load(c[i]);
-        const int64_t mine = cid < wk.units ? (wk.units - cid + ncl - 1) / ncl : 0, all = mine * stages;
+        late_wait();
+        const int half = (warp - WARP_DEC0) >> 2, r = ((warp - WARP_DEC0) & 3) * 32 + lane;  // 32 codes of the stage, row of the tile
+        uint8_t *const row = smem + r * 128;
+        const uint8_t *const box = smem + P::CODES + r * 64;
+        int b = 0, cb = 0;
+        uint32_t use = 0, cuse = 0;
         bool stop = false;
-        int b = 0;
-        uint32_t use = 0;
-        for (int64_t it = 0; it < all && !stop; it += AHEAD) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                if (it + i >= all || stop) break;
+        for (int u = cid; u < wk.units && !stop; u += ncl) {
+            const uint8_t *zeros = nullptr;
+            int zlast = 0, shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
+            if (a.zeros) {
+                const Unit t = unit_at<CG>(a, wk, u, &err);
+                zeros = a.zeros + t.e * a.scales_expert + min(t.r0 + (int)rank * BM + r, a.rows - 1) * a.scales_row;
+                zlast = a.groups - 1;
+            }
+            const auto zero_at = [&](int s) { return zeros ? __ldg(zeros + min((s * BK + half * 32) >> shift, zlast)) & 15u : 8u; };
+            uint32_t z0 = zero_at(0), z1 = zero_at(1);  // two stages ahead
+            for (int s = 0; s < stages; ++s) {
+                const uint32_t z = z0;
+                z0 = z1;
+                z1 = zero_at(s + 2);
                 if (*abort_flag) { stop = true; break; }
-                if (use > 0 && !mbar_wait(&empty[b], (use - 1) & 1)) {
+                if ((s & 1) == 0 && !mbar_wait_sleep(&cfull[cb], cuse & 1)) {
+                    fail<CG>(abort_flag, kDevErrWaitFull);
+                    stop = true;
+                    break;
+                }
+                // chunk j of row r lies at j ^ (r / 2 % 4) of its 64 bytes
+                const uint4 v = *reinterpret_cast<const uint4 *>(box + cb * CBOX + ((((s & 1) * 2 + half) ^ ((r >> 1) & 3)) << 4));
+                if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
                     fail<CG>(abort_flag, kDevErrWaitEmpty);
                     stop = true;
                     break;
                 }
-                uint8_t *row = smem + b * P::STAGE + r * 128;
-                store_codes<T>(row, r, 0, c[i].lo, c[i].z & 0xFFFFu);
-                store_codes<T>(row, r, 4, c[i].hi, c[i].z >> 16);
-                load(c[i]);
+                store_codes<T>(row + b * P::STAGE, r, half * 4, v, z);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     // the stage is ready when X is there too: one warp of each CTA waits for it
-                    if (warp == WARP_DEC0 && !mbar_wait(&full[b], use & 1)) {
-                        fail<CG>(abort_flag, kDevErrWaitFull);
-                    }
+                    if (warp == WARP_DEC0 && !mbar_wait(&full[b], use & 1)) fail<CG>(abort_flag, kDevErrWaitFull);
                     arrive_leader<CG>(&ready[b]);
+                    if ((s & 1) || s == stages - 1) mbar_arrive(&cempty[cb]);
                 }
                 if (++b == STAGES) b = 0, ++use;
+                if (((s & 1) || s == stages - 1) && ++cb == CRING) cb = 0, ++cuse;
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 " MM_PACKED4_REGS_EPI ";");
+        late_wait();
         const int quarter = warp & 3, half = (warp - WARP_EPI0) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        constexpr int SC = 4;  // scales on their way
         int gi = 0;
         bool stop = false;
-        for (int64_t u = cid; u < wk.units && !stop; u += ncl) {
-            const Unit t = unit_at<CG>(a, wk, u, &err);
+        Unit t = {0, 0, 0, 0, 0};
+        const uint16_t *sc = nullptr;
+        uint16_t next[SC];
+        const auto enter = [&](int u) {  // the unit's first scales
+            if (u >= wk.units) return;
+            t = unit_at<CG>(a, wk, u, &err);
+            sc = static_cast<const uint16_t *>(a.scales) + t.e * a.scales_expert +
+                 min(t.r0 + (int)rank * BM + 32 * quarter + lane, a.rows - 1) * a.scales_row;
+#pragma unroll
+            for (int i = 0; i < SC; ++i) next[i] = i < a.groups ? __ldg(sc + i) : 0;
+        };
+        enter(cid);
+        for (int u = cid; u < wk.units; u += ncl) {
             const int cols = (t.N + 63) / 64 * 32, c0 = half * cols;  // this half's columns of D
-            const int row = t.r0 + (int)rank * BM + 32 * quarter + lane;
-            const uint16_t *sc = static_cast<const uint16_t *>(a.scales) + t.e * a.scales_expert + (int64_t)min(row, a.rows - 1) * a.scales_row;
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            constexpr int SC = 4;  // scales on their way
-            uint16_t next[SC];
-#pragma unroll
-            for (int i = 0; i < SC; ++i) next[i] = i < a.groups ? __ldg(sc + i) : 0;
             for (int g0 = 0; g0 < a.groups && !stop; g0 += SC) {
                 float now[SC];
 #pragma unroll
@@ -465,7 +550,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (g0 + i >= a.groups) break;
                     const float f = i == 0 ? now[0] : i == 1 ? now[1] : i == 2 ? now[2] : now[3];
                     if (*abort_flag) { stop = true; break; }
-                    if (!mbar_wait(&accf[gi & 1], (uint32_t)(gi / 2) & 1)) {
+                    if (!mbar_wait_sleep(&accf[gi & 1], (uint32_t)(gi / 2) & 1)) {
                         fail<CG>(abort_flag, kDevErrWaitMma);
                         stop = true;
                         break;
@@ -490,27 +575,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             }
             if (stop) break;
+            const Unit done = t;
+            enter(u + ncl);  // its scales come while this one is stored
+            const int row = done.r0 + (int)rank * BM + 32 * quarter + lane;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int base = c0 + c * 32;
-                if (c * 32 >= cols || base >= t.n) break;
+                if (c * 32 >= cols || base >= done.n) break;
                 if (a.order) {  // a slot whose row of X does not exist (reported where X was loaded) counts as 0s
                     unsigned int seen = 0;
-                    const uint32_t ok = __ballot_sync(~0u, base + lane >= t.n || x_row(a, t.first + base + lane, &seen) >= 0);
+                    const uint32_t ok = __ballot_sync(~0u, base + lane >= done.n || x_row(a, done.first + base + lane, &seen) >= 0);
                     if (ok != ~0u)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!(ok >> j & 1)) acc[c * 32 + j] = 0.f;
                 }
-                const int n = min(32, t.n - base);
-                const float(&v)[32] = *reinterpret_cast<const float(*)[32]>(&acc[c * 32]);
-                if (a.y_dtype == 2) {
-                    if (a.swiglu) store_pairs<T, float>(a, t.first + base, row, n, v);
-                    else store_rows<T, float>(a, t.first + base, row, n, v);
-                } else {
-                    if (a.swiglu) store_pairs<T, uint16_t>(a, t.first + base, row, n, v);
-                    else store_rows<T, uint16_t>(a, t.first + base, row, n, v);
-                }
+                const int n = min(32, done.n - base);
+                if (a.y_dtype == 2) store32<T, float>(a, done.first + base, row, n, acc + c * 32);
+                else store32<T, uint16_t>(a, done.first + base, row, n, acc + c * 32);
             }
         }
     }
@@ -538,6 +620,12 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     e = make_tmap_2d(&tm, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, (uint64_t)a.cols,
                      (uint64_t)a.x_rows, stride, BK, a.order ? 1 : BOX, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
+    CUtensorMap tw;
+    const uint64_t bytes = ((uint64_t)a.cols + 31) / 32 * 16;
+    const uint64_t row = a.rows > 1 ? (uint64_t)a.codes_row : bytes, matrix = a.experts > 1 ? (uint64_t)a.codes_expert : row * a.rows;
+    e = make_tmap_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, &tw, a.codes, bytes, (uint64_t)a.rows, (uint64_t)a.experts, row, matrix, BK,
+                     BM, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != cudaSuccess) return e;
     // no more CTAs than units of the shortest chunks
     const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG);
     const int64_t most = ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
@@ -554,7 +642,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.x = CG, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = CG == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tm, a);
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tm, tw, a);
 }
 
 }  // namespace
