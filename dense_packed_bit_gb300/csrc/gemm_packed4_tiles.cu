@@ -41,7 +41,7 @@ constexpr int NTHREADS = 640;
 constexpr int WARP_X = 0, WARP_MMA = 1, WARP_CODES = 2, WARP_DEC0 = 4, WARP_EPI0 = 12;
 constexpr int DEC_WARPS = 8, EPI_WARPS = 8;
 constexpr int MAX_EXPERTS = 1024;
-constexpr int BOX = 16;        // rows of X per TMA box
+constexpr int BOX = 64;        // rows of X per TMA box
 
 // Registers of a thread once the roles part, of the 96 at launch: 384 x 48 + 256 x 168 = 640 x 96.
 #define MM_PACKED4_REGS_FEW "48"
@@ -53,9 +53,9 @@ struct Plan {
     static constexpr int STAGES = CG == 2 ? 5 : 3;
     static constexpr int CODES = STAGES * STAGE;
     static constexpr int BAR = CODES + CRING * CBOX;
-    static constexpr int PRE = BAR + 256;                      // chunks before each expert
+    static constexpr int PRE = BAR + 320;                      // chunks before each expert
     static constexpr int TOTAL = PRE + (MAX_EXPERTS + 1) * 4 + 12 + 1024;  // + alignment of the dynamic allocation
-    static_assert((3 * STAGES + 2 * CRING + 5) * 8 + 8 <= 256, "barriers");
+    static_assert((3 * STAGES + 2 * CRING + 5) * 8 + 8 <= 320, "barriers");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
@@ -337,6 +337,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int u = cid; u < wk.units && !stop; u += ncl) {
                 const Unit t = unit_at<CG>(a, wk, u, &err);
                 const int mine = t.N / CG, from = (int)rank * mine;  // this CTA's rows of X
+                // whole boxes: the rows behind the unit's are loaded too, into the rest of the stage
+                const uint32_t bytes = 128u * (uint32_t)(a.order ? mine : (mine + BOX - 1) / BOX * BOX);
                 int rows[2][4];
                 if (a.order) {
 #pragma unroll
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         break;
                     }
                     uint8_t *dst = smem + b * P::STAGE + P::A_BYTES;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[b], (uint32_t)mine * 128u);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[b], bytes);
                     __syncwarp();
                     if (a.order) {
 #pragma unroll
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (issue) fail<CG>(abort_flag, code);
                     stop = true;
                 }
+                __syncwarp();
                 tc_fence_after_sync();
             };
             const auto begin = [&] {  // a group's accumulator is free
@@ -555,6 +558,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         stop = true;
                         break;
                     }
+                    __syncwarp();  // the reads below are the whole warp's
                     tc_fence_after_sync();
                     const uint32_t d = lanes + (uint32_t)((gi & 1) * BN + c0);
                     // 8 columns are read while the 8 before them are added
@@ -648,6 +652,8 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s) {
+    const int64_t pairs = ((a.slots + BN - 1) / BN) * ((a.rows + 2 * BM - 1) / (2 * BM));
+    if (pairs >= sms / 2) return a.dtype == 0 ? launch<__half, 2>(a, sms, s) : launch<__nv_bfloat16, 2>(a, sms, s);
     return a.dtype == 0 ? launch<__half, 1>(a, sms, s) : launch<__nv_bfloat16, 1>(a, sms, s);
 }
 
