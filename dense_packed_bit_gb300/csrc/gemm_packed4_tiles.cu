@@ -10,7 +10,7 @@
 // of the MMAs, beside which it runs (two accumulators of 256 columns), with groups of 32 all of it.
 //
 // Roles of a CTA's 20 warps, over a ring of stages of 64 columns:
-//   warp 0          X by TMA, 16 rows to a box, or four gathered rows at a time where `order` names them;
+//   warp 0          X by TMA, 64 rows to a box; where `order` names the rows, warps 0 and 3 copy them 16 bytes at a time;
 //   warp 1          issues the MMAs (in a pair: the even CTA's, for both);
 //   warp 2          codes by TMA, 128 rows x 128 codes to a box, into a ring of their own that is CRING boxes deep;
 //   warps 4 - 11    make 16-bit numbers of them and store them as the MMA's A (128-byte swizzle), a thread to 32 codes of a
@@ -35,10 +35,9 @@ namespace {
 constexpr int BM = 128;        // rows of W per CTA: the TMEM lanes
 constexpr int BK = 64;         // columns per stage: 128 bytes of X's type
 constexpr int BN = 256;        // rows of X per unit, at most: columns of an accumulator
-constexpr int CRING = 6;       // boxes of codes on their way to shared memory, 8 KB each
 constexpr int CBOX = BM * 64;  // bytes of a box: 128 rows of two stages' codes
 constexpr int NTHREADS = 640;
-constexpr int WARP_X = 0, WARP_MMA = 1, WARP_CODES = 2, WARP_DEC0 = 4, WARP_EPI0 = 12;
+constexpr int WARP_X = 0, WARP_MMA = 1, WARP_CODES = 2, WARP_X2 = 3, WARP_DEC0 = 4, WARP_EPI0 = 12;
 constexpr int DEC_WARPS = 8, EPI_WARPS = 8;
 constexpr int MAX_EXPERTS = 1024;
 constexpr int BOX = 64;        // rows of X per TMA box
@@ -50,13 +49,16 @@ constexpr int BOX = 64;        // rows of X per TMA box
 template <int CG>
 struct Plan {
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = CG == 2 ? 5 : 3;
+    static constexpr int STAGES = CG == 2 ? 4 : 3;
+    static constexpr int CRING = CG == 2 ? 6 : 5;              // boxes of codes on their way to shared memory
     static constexpr int CODES = STAGES * STAGE;
-    static constexpr int BAR = CODES + CRING * CBOX;
+    static constexpr int OUT = CODES + CRING * CBOX;           // 32 x 32 results of each epilogue warp
+    static constexpr int ROWS = OUT + EPI_WARPS * 4096;        // rows of X of two units, where they are gathered
+    static constexpr int BAR = ROWS + 2 * BN * 4;
     static constexpr int PRE = BAR + 320;                      // chunks before each expert
     static constexpr int TOTAL = PRE + (MAX_EXPERTS + 1) * 4 + 12 + 1024;  // + alignment of the dynamic allocation
     static_assert((3 * STAGES + 2 * CRING + 5) * 8 + 8 <= 320, "barriers");
-    static_assert(TOTAL <= 227 * 1024, "shared memory");
+    static_assert(TOTAL + 512 <= 227 * 1024, "shared memory");
 };
 
 struct Shared {  // what follows the barriers
@@ -107,40 +109,28 @@ __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code
         st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
 }
 
-// One thread of a warp that runs as one issues (the operands stay uniform)
-template <int CG>
-__device__ __forceinline__ void mma_if(bool issue, uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (CG == 2)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
-            "r"(accumulate), "r"((uint32_t)issue)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(da), "l"(db), "r"(idesc),
-            "r"(accumulate), "r"((uint32_t)issue)
-            : "memory");
+// 16 bytes to shared memory, of which those past `have` are 0
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t have) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
+}
+
+// True in one thread of the warp.  The compiler knows that of elect.sync, and puts the operands of the MMAs behind it straight
+// into uniform registers: four MMAs and a commit are issued in 160 clocks, behind a test of the lane in 700.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 template <int CG>
-__device__ __forceinline__ void commit_if(bool issue, uint64_t *bar) {
-    if constexpr (CG == 2)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.b32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
-            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
-                smem_u32(bar)),
-            "r"((uint32_t)issue)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-            "r"((uint32_t)issue)
-            : "memory");
+__device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 2) umma_f16_pair(d, da, db, idesc, accumulate);
+    else umma_f16(d, da, db, idesc, accumulate);
 }
-// What is the same in all lanes, and known to be: a reduction's result
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(~0u, x); }
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (CG == 2) umma_commit_pair(bar, 3);
+    else umma_commit(bar);
+}
 
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
@@ -180,37 +170,51 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
 // 2^-19, of which a half-ulp of fp16 is 2^7)
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// Slots first .. first + n - 1 of Y from this thread's row of D.  Neighbouring lanes hold neighbouring rows: the even one
-// takes the even slots, the odd one the others, so that a thread stores pairs (or silu(gate) * up of a pair).
-template <typename T, typename Y>
-__device__ __forceinline__ void store32(const Packed4MmArgs &a, int first, int row, int n, const float *v) {
-    const int odd = row & 1, width = a.swiglu ? a.rows >> 1 : a.rows;
-    if (sizeof(Y) == 4 && !a.swiglu) {
-        Y *p = static_cast<Y *>(a.Y) + first * a.y_stride + row;
-#pragma unroll
-        for (int j = 0; j < 32; ++j, p += a.y_stride)
-            if (j < n && row < a.rows) *p = v[j];
-        return;
-    }
-    const int col = a.swiglu ? row >> 1 : row - odd;
-    Y *p = static_cast<Y *>(a.Y) + (first + odd) * a.y_stride + col;
-    const bool pair = !a.swiglu && col + 1 < width && (reinterpret_cast<uintptr_t>(a.Y) & 3) == 0 && a.y_stride % 2 == 0;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2, p += 2 * a.y_stride) {
-        if (j >= n) break;
-        const float got = __shfl_xor_sync(~0u, odd ? v[j] : v[j + 1], 1);
-        const float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
-        if (j + odd >= n || col >= width) continue;
-        if (a.swiglu) {
-            if constexpr (sizeof(Y) == 4) *p = silu(lo) * hi;
-            else *p = Code4<T>::round(silu_fast(lo) * hi);
-        } else if constexpr (sizeof(Y) == 2) {
-            if (pair) *reinterpret_cast<uint32_t *>(p) = Code4<T>::round(lo) | (uint32_t)Code4<T>::round(hi) << 16;
-            else {
-                p[0] = Code4<T>::round(lo);
-                if (col + 1 < width) p[1] = Code4<T>::round(hi);
+// Slots first .. first + n - 1 and rows r0 .. r0 + 31 of Y from `out`, [32 slots][32 rows] of a warp: 16 bytes to a lane where
+// Y allows it (vec), else element by element.
+template <typename T>
+__device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float *out, int first, int n, int r0, int lane, bool vec) {
+    const int left = min(32, a.rows - r0);
+    if (a.swiglu) {
+        const int per = 16;  // columns of Y
+        if (vec && left == 32) {
+            const int c = (lane & 3) * 4;
+            for (int j = lane >> 2; j < n; j += 8) {
+                const float4 p = *reinterpret_cast<const float4 *>(out + j * 32 + 2 * c), q = *reinterpret_cast<const float4 *>(out + j * 32 + 2 * c + 4);
+                const int64_t at = (int64_t)(first + j) * a.y_stride + (r0 >> 1) + c;
+                if (a.y_dtype == 2) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.Y) + at) =
+                        make_float4(silu(p.x) * p.y, silu(p.z) * p.w, silu(q.x) * q.y, silu(q.z) * q.w);
+                } else {
+                    const uint32_t lo = Code4<T>::round(silu_fast(p.x) * p.y) | (uint32_t)Code4<T>::round(silu_fast(p.z) * p.w) << 16;
+                    const uint32_t hi = Code4<T>::round(silu_fast(q.x) * q.y) | (uint32_t)Code4<T>::round(silu_fast(q.z) * q.w) << 16;
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.Y) + at) = make_uint2(lo, hi);
+                }
+            }
+        } else {
+            for (int i = lane; i < n * per; i += 32) {
+                const int j = i / per, c = i % per;
+                if (2 * c < left) store_y(a, first + j, (r0 >> 1) + c, silu(out[j * 32 + 2 * c]) * out[j * 32 + 2 * c + 1]);
             }
         }
+    } else if (vec && left == 32) {
+        if (a.y_dtype == 2) {
+            const int c = (lane & 7) * 4;
+            for (int j = lane >> 3; j < n; j += 4)
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.Y) + (int64_t)(first + j) * a.y_stride + r0 + c) =
+                    *reinterpret_cast<const float4 *>(out + j * 32 + c);
+        } else {
+            const int c = (lane & 3) * 8;
+            for (int j = lane >> 2; j < n; j += 8) {
+                const float4 p = *reinterpret_cast<const float4 *>(out + j * 32 + c), q = *reinterpret_cast<const float4 *>(out + j * 32 + c + 4);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.Y) + (int64_t)(first + j) * a.y_stride + r0 + c) =
+                    make_uint4(Code4<T>::round(p.x) | (uint32_t)Code4<T>::round(p.y) << 16, Code4<T>::round(p.z) | (uint32_t)Code4<T>::round(p.w) << 16,
+                               Code4<T>::round(q.x) | (uint32_t)Code4<T>::round(q.y) << 16, Code4<T>::round(q.z) | (uint32_t)Code4<T>::round(q.w) << 16);
+            }
+        }
+    } else {
+        for (int j = 0; j < n; ++j)
+            if (lane < left) store_y(a, first + j, r0 + lane, out[j * 32 + lane]);
     }
 }
 
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ Packed4MmArgs a) {
     using P = Plan<CG>;
-    constexpr int STAGES = P::STAGES;
+    constexpr int STAGES = P::STAGES, CRING = P::CRING;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_aligned<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR);  // X has arrived (this CTA's)
@@ -249,8 +253,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&ready[s], DEC_WARPS * CG);
+            mbar_init(&full[s], a.order ? 64 : 1);
+            mbar_init(&ready[s], DEC_WARPS / 2 * CG);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < CRING; ++s) {
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     if (warp < WARP_DEC0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " MM_PACKED4_REGS_FEW ";");
-        if (warp == WARP_X) {
+        if (warp == WARP_X && !a.order) {
             late_wait();
             int b = 0, it = 0;
             uint32_t use = 0;
@@ -338,18 +342,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const Unit t = unit_at<CG>(a, wk, u, &err);
                 const int mine = t.N / CG, from = (int)rank * mine;  // this CTA's rows of X
                 // whole boxes: the rows behind the unit's are loaded too, into the rest of the stage
-                const uint32_t bytes = 128u * (uint32_t)(a.order ? mine : (mine + BOX - 1) / BOX * BOX);
-                int rows[2][4];
-                if (a.order) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // rows that are none, or behind the chunk: any row, not stored
-                            const int i = from + (h * 32 + lane) * 4 + j;
-                            const int64_t row = i < t.n ? x_row(a, t.first + i, &err) : 0;
-                            rows[h][j] = row < 0 ? 0 : (int)row;
-                        }
-                }
+                const int boxes = (mine + BOX - 1) / BOX;
                 for (int s = 0; s < stages; ++s, ++it) {
                     if (*abort_flag) { stop = true; break; }
                     if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
@@ -357,17 +350,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         stop = true;
                         break;
                     }
-                    uint8_t *dst = smem + b * P::STAGE + P::A_BYTES;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[b], bytes);
-                    __syncwarp();
-                    if (a.order) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if ((h * 32 + lane) * 4 < mine)
-                                tma_gather4(dst + (h * 32 + lane) * 512, &tmX, &full[b], s * BK, rows[h][0], rows[h][1], rows[h][2], rows[h][3]);
-                    } else if (lane * BOX < mine) {
-                        tma_load_2d(dst + lane * BOX * 128, &tmX, &full[b], s * BK, t.first + from + lane * BOX);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&full[b], (uint32_t)boxes * BOX * 128u);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &full[b], s * BK, t.first + from + i * BOX);
                     }
+                    __syncwarp();
                     if (++b == STAGES) b = 0, ++use;
                 }
             }
@@ -379,6 +367,51 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     break;
                 }
             }
+        } else if (warp == WARP_X || (warp == WARP_X2 && a.order)) {
+            // Gathered rows: half of them to each of two warps, 8 lanes to a row's 128 bytes.  (Four rows to a TMA gather
+            // took 70 clocks an instruction: 2.2 times as long as the MMAs of a stage.)  The copies arrive at the stage's
+            // barrier by themselves; who waits for it makes them visible to the tensor cores.  (A fence here waits for every
+            // copy on its way: 3500 clocks a stage.)
+            const int half = warp == WARP_X2, c = lane & 7, sub = lane >> 3;
+            const uint32_t stride = (uint32_t)a.x_stride * 2;
+            int b = 0;
+            uint32_t use = 0;
+            bool stop = false;
+            for (int u = cid, turn = 0; u < wk.units && !stop; u += ncl, turn ^= 1) {
+                const Unit t = unit_at<CG>(a, wk, u, &err);
+                const int mine = t.N / CG, from = (int)rank * mine, n = mine / 2;  // a multiple of 8
+                int *rows = reinterpret_cast<int *>(smem + P::ROWS) + turn * BN + half * n;
+                for (int i = lane; i < n; i += 32) {  // rows that are none, or behind the chunk: any row, not stored
+                    const int at = from + half * n + i;
+                    const int64_t row = at < t.n ? x_row(a, t.first + at, &err) : 0;
+                    rows[i] = row < 0 ? 0 : (int)row;
+                }
+                __syncwarp();
+                rows += sub;
+                for (int s = 0; s < stages; ++s) {
+                    if (*abort_flag) { stop = true; break; }
+                    if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
+                        fail<CG>(abort_flag, kDevErrWaitEmpty);
+                        stop = true;
+                        break;
+                    }
+                    // of the rows of this lane, every fourth, the place modulo 8 alternates between two
+                    const uint32_t dst = smem_u32(smem + b * P::STAGE + P::A_BYTES + (half * n + sub) * 128);
+                    const uint32_t d0 = dst + ((c ^ sub) << 4), d1 = dst + ((c ^ sub ^ 4) << 4);
+                    const int col = s * BK + c * 8;
+                    const uint32_t have = (uint32_t)max(0, min(8, a.cols - col)) * 2;  // bytes of its chunk that a row has; the rest is 0
+                    const uint8_t *x = static_cast<const uint8_t *>(a.X) + (have ? col * 2 : 0);
+#pragma unroll 2
+                    for (int i = 0; i < n; i += 32) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (i + 4 * k < n) copy16((k & 1 ? d1 : d0) + (i + 4 * k) * 128, x + (uint64_t)(uint32_t)rows[i + 4 * k] * stride, have);
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[b])) : "memory");
+                    if (++b == STAGES) b = 0, ++use;
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == WARP_CODES) {
             if (lane == 0) {
                 int b = 0, it = 0;
@@ -411,109 +444,134 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         } else if (warp == WARP_MMA && rank == 0) {
             late_wait();
             constexpr uint32_t fmt = __is_same(T, __half) ? kFmtF16 : kFmtBF16;
-            const bool issue = lane == 0;
-            int b = 0, gi = 0;  // stage of the ring, groups so far
-            uint32_t use = 0;
-            bool stop = false;
-            const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned int code) {
-                if (!mbar_wait(bar, parity)) {
-                    if (issue) fail<CG>(abort_flag, code);
-                    stop = true;
-                }
-                __syncwarp();
-                tc_fence_after_sync();
-            };
-            const auto begin = [&] {  // a group's accumulator is free
-                if (gi >= 2) wait(&acce[gi & 1], (uint32_t)(gi / 2 - 1) & 1, kDevErrWaitEmpty);
-            };
-            const auto end = [&] {
-                commit_if<CG>(issue && !stop, &accf[gi & 1]);
-                ++gi;
-            };
-            const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem)), db0 = sdesc_kmajor_sw128(smem_u32(smem) + P::A_BYTES);
-            for (int u = cid; u < wk.units && !stop; u += ncl) {
-                const Unit t = unit_at<CG>(a, wk, u, &err);
-                const uint32_t idesc = uniform(make_idesc(fmt, fmt, (uint32_t)t.N, BM * CG));
-                for (int s = 0; s < stages && !stop; ++s) {
-                    if (*abort_flag) { stop = true; break; }
-                    // the first MMA of a group clears the accumulator: of 128 columns every other stage's, of 64 every
-                    // stage's, of 32 two in a stage
-                    const bool first = a.group <= BK || (s & 1) == 0;
-                    if (first) begin();
-                    if (!stop) wait(&ready[b], use & 1, kDevErrWaitFull);
-                    const uint32_t at = uniform((uint32_t)b * (P::STAGE >> 4)), dd = uniform(tmem);
-                    const uint64_t da = da0 + at, db = db0 + at;
-                    uint32_t d = dd + (uint32_t)((gi & 1) * BN);
-                    const bool go = issue && !stop;
-                    mma_if<CG>(go, d, da, db, idesc, !first);
-                    mma_if<CG>(go, d, da + 2, db + 2, idesc, 1);
-                    const bool halves = a.group == 32 && s * BK + 32 < a.cols;
-                    if (halves) {
-                        end();
-                        begin();
-                        d = dd + (uint32_t)((gi & 1) * BN);
+            if (elected()) {
+                int b = 0, gi = 0;  // stage of the ring, groups so far
+                uint32_t use = 0;
+                bool stop = false;
+                const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned int code) {
+                    if (!mbar_wait(bar, parity)) {
+                        fail<CG>(abort_flag, code);
+                        stop = true;
                     }
-                    const bool go2 = issue && !stop;
-                    mma_if<CG>(go2, d, da + 4, db + 4, idesc, !halves);
-                    mma_if<CG>(go2, d, da + 6, db + 6, idesc, 1);
-                    commit_if<CG>(go2, &empty[b]);
-                    if (a.group <= BK || (s & 1) || s == stages - 1) end();
-                    if (++b == STAGES) b = 0, ++use;
+                    tc_fence_after_sync();
+                };
+                const auto begin = [&] {  // a group's accumulator is free
+                    if (gi >= 2) wait(&acce[gi & 1], (uint32_t)(gi / 2 - 1) & 1, kDevErrWaitEmpty);
+                };
+                const auto end = [&] {
+                    commit<CG>(&accf[gi & 1]);
+                    ++gi;
+                };
+                for (int u = cid; u < wk.units && !stop; u += ncl) {
+                    const Unit t = unit_at<CG>(a, wk, u, &err);
+                    const uint32_t idesc = make_idesc(fmt, fmt, (uint32_t)t.N, BM * CG);
+                    for (int s = 0; s < stages; ++s) {
+                        // the first MMA of a group clears the accumulator: of 128 columns every other stage's, of 64 every
+                        // stage's, of 32 two in a stage
+                        const bool first = a.group <= BK || (s & 1) == 0;
+                        if (first) begin();
+                        wait(&ready[b], use & 1, kDevErrWaitFull);
+                        if (stop) break;
+                        const uint32_t at = smem_u32(smem + b * P::STAGE);
+                        const uint64_t da = sdesc_kmajor_sw128(at), db = sdesc_kmajor_sw128(at + P::A_BYTES);
+                        uint32_t d = tmem + (uint32_t)((gi & 1) * BN);
+                        mma<CG>(d, da, db, idesc, !first);
+                        mma<CG>(d, da + 2, db + 2, idesc, 1);
+                        const bool halves = a.group == 32 && s * BK + 32 < a.cols;
+                        if (halves) {
+                            end();
+                            begin();
+                            if (stop) break;
+                            d = tmem + (uint32_t)((gi & 1) * BN);
+                        }
+                        mma<CG>(d, da + 4, db + 4, idesc, !halves);
+                        mma<CG>(d, da + 6, db + 6, idesc, 1);
+                        commit<CG>(&empty[b]);
+                        if (a.group <= BK || (s & 1) || s == stages - 1) end();
+                        if (++b == STAGES) b = 0, ++use;
+                    }
+                    if (*abort_flag) stop = true;
                 }
+                // every MMA issued must be complete before the tensor memory is freed
+                commit<CG>(last);
+                if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
             }
-            // every MMA issued must be complete before the tensor memory is freed
-            commit_if<CG>(issue, last);
-            if (!mbar_wait(last, 0) && issue) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
+            __syncwarp();
         } else {
             late_wait();
         }
     } else if (warp < WARP_EPI0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " MM_PACKED4_REGS_FEW ";");
         late_wait();
-        const int half = (warp - WARP_DEC0) >> 2, r = ((warp - WARP_DEC0) & 3) * 32 + lane;  // 32 codes of the stage, row of the tile
+        // four warps take the even stages, four the odd ones: a box of codes holds one of each
+        const int odd = (warp - WARP_DEC0) >> 2, r = ((warp - WARP_DEC0) & 3) * 32 + lane;  // row of the tile
         uint8_t *const row = smem + r * 128;
         const uint8_t *const box = smem + P::CODES + r * 64;
+        // chunk j of row r lies at j ^ (r / 2 % 4) of its 64 bytes
+        const int lo = (odd * 2 ^ ((r >> 1) & 3)) << 4, hi = lo ^ 16;
         int b = 0, cb = 0;
         uint32_t use = 0, cuse = 0;
         bool stop = false;
+        const auto next_stage = [&] { if (++b == STAGES) b = 0, ++use; };
+        if (odd) next_stage();
+        const int shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
         for (int u = cid; u < wk.units && !stop; u += ncl) {
             const uint8_t *zeros = nullptr;
-            int zlast = 0, shift = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
             if (a.zeros) {
                 const Unit t = unit_at<CG>(a, wk, u, &err);
                 zeros = a.zeros + t.e * a.scales_expert + min(t.r0 + (int)rank * BM + r, a.rows - 1) * a.scales_row;
-                zlast = a.groups - 1;
             }
-            const auto zero_at = [&](int s) { return zeros ? __ldg(zeros + min((s * BK + half * 32) >> shift, zlast)) & 15u : 8u; };
-            uint32_t z0 = zero_at(0), z1 = zero_at(1);  // two stages ahead
-            for (int s = 0; s < stages; ++s) {
+            const auto zeros_at = [&](int s) {  // low half: of the stage's first 32 columns, high half: of the others
+                if (!zeros || s >= stages) return 0x00080008u;
+                const int j = (s * BK) >> shift;
+                const uint32_t z = __ldg(zeros + j) & 15u;
+                return z | (a.group == 32 ? __ldg(zeros + min(j + 1, a.groups - 1)) & 15u : z) << 16;
+            };
+            uint32_t z0 = zeros_at(odd), z1 = zeros_at(odd + 2);  // two stages ahead
+            for (int s = odd;; s += 2) {
+                const bool box_only = s >= stages;  // an odd number of stages: the last box is passed over
+                if (box_only && !(odd && s == stages)) break;
                 const uint32_t z = z0;
                 z0 = z1;
-                z1 = zero_at(s + 2);
-                if (*abort_flag) { stop = true; break; }
-                if ((s & 1) == 0 && !mbar_wait_sleep(&cfull[cb], cuse & 1)) {
-                    fail<CG>(abort_flag, kDevErrWaitFull);
+                z1 = zeros_at(s + 4);
+                if (*abort_flag || !mbar_wait_sleep(&cfull[cb], cuse & 1)) {
+                    if (!*abort_flag) fail<CG>(abort_flag, kDevErrWaitFull);
                     stop = true;
                     break;
                 }
-                // chunk j of row r lies at j ^ (r / 2 % 4) of its 64 bytes
-                const uint4 v = *reinterpret_cast<const uint4 *>(box + cb * CBOX + ((((s & 1) * 2 + half) ^ ((r >> 1) & 3)) << 4));
-                if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
-                    fail<CG>(abort_flag, kDevErrWaitEmpty);
-                    stop = true;
-                    break;
+                if (!box_only) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(box + cb * CBOX + lo), w = *reinterpret_cast<const uint4 *>(box + cb * CBOX + hi);
+                    if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
+                        fail<CG>(abort_flag, kDevErrWaitEmpty);
+                        stop = true;
+                        break;
+                    }
+                    store_codes<T>(row + b * P::STAGE, r, 0, v, z & 0xFFFFu);
+                    store_codes<T>(row + b * P::STAGE, r, 4, w, z >> 16);
+                    fence_proxy_async_smem();
                 }
-                store_codes<T>(row + b * P::STAGE, r, half * 4, v, z);
-                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    // the stage is ready when X is there too: one warp of each CTA waits for it
-                    if (warp == WARP_DEC0 && !mbar_wait(&full[b], use & 1)) fail<CG>(abort_flag, kDevErrWaitFull);
-                    arrive_leader<CG>(&ready[b]);
-                    if ((s & 1) || s == stages - 1) mbar_arrive(&cempty[cb]);
+                    mbar_arrive(&cempty[cb]);
+                    if (!box_only) {
+                        // the stage is ready when X is there too: one warp of each CTA waits for it
+                        if (warp == WARP_DEC0 + 4 * odd) {
+                            if (!mbar_wait(&full[b], use & 1)) fail<CG>(abort_flag, kDevErrWaitFull);
+                            if (a.order) fence_proxy_async_smem();
+                        }
+                        arrive_leader<CG>(&ready[b]);
+                    }
                 }
-                if (++b == STAGES) b = 0, ++use;
-                if (((s & 1) || s == stages - 1) && ++cb == CRING) cb = 0, ++cuse;
+                if (!box_only) next_stage(), next_stage();
+                if (++cb == CRING) cb = 0, ++cuse;
+            }
+            // with an odd number of stages a unit's first one falls to the other place of the ring
+            if (stages & 1) {
+                if (odd) next_stage();
+                else {
+                    b = b == 0 ? STAGES - 1 : b - 1;
+                    if (b == STAGES - 1) --use;
+                }
             }
         }
     } else {
@@ -524,6 +582,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         constexpr int SC = 4;  // scales on their way
         int gi = 0;
         bool stop = false;
+        const int size = a.y_dtype == 2 ? 4 : 2;
+        const bool vec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.y_stride * size % 16 == 0;
         Unit t = {0, 0, 0, 0, 0};
         const uint16_t *sc = nullptr;
         uint16_t next[SC];
@@ -581,11 +641,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (stop) break;
             const Unit done = t;
             enter(u + ncl);  // its scales come while this one is stored
-            const int row = done.r0 + (int)rank * BM + 32 * quarter + lane;
+            float *const out = reinterpret_cast<float *>(smem + P::OUT) + (warp - WARP_EPI0) * 1024;
+            const int r0 = done.r0 + (int)rank * BM + 32 * quarter;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int base = c0 + c * 32;
-                if (c * 32 >= cols || base >= done.n) break;
+                if (c * 32 >= cols || base >= done.n || r0 >= a.rows) break;
                 if (a.order) {  // a slot whose row of X does not exist (reported where X was loaded) counts as 0s
                     unsigned int seen = 0;
                     const uint32_t ok = __ballot_sync(~0u, base + lane >= done.n || x_row(a, done.first + base + lane, &seen) >= 0);
@@ -594,9 +655,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         for (int j = 0; j < 32; ++j)
                             if (!(ok >> j & 1)) acc[c * 32 + j] = 0.f;
                 }
-                const int n = min(32, done.n - base);
-                if (a.y_dtype == 2) store32<T, float>(a, done.first + base, row, n, acc + c * 32);
-                else store32<T, uint16_t>(a, done.first + base, row, n, acc + c * 32);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) out[j * 32 + lane] = acc[c * 32 + j];
+                __syncwarp();
+                store_block<T>(a, out, done.first + base, min(32, done.n - base), r0, lane, vec);
+                __syncwarp();
             }
         }
     }
@@ -622,7 +685,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     // a single row may have any stride: the map wants one of whole 16 bytes that holds the row
     const uint64_t stride = a.x_rows > 1 ? (uint64_t)a.x_stride * 2 : ((uint64_t)a.cols * 2 + 15) / 16 * 16;
     e = make_tmap_2d(&tm, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, (uint64_t)a.cols,
-                     (uint64_t)a.x_rows, stride, BK, a.order ? 1 : BOX, CU_TENSOR_MAP_SWIZZLE_128B);
+                     (uint64_t)a.x_rows, stride, BK, BOX, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     CUtensorMap tw;
     const uint64_t bytes = ((uint64_t)a.cols + 31) / 32 * 16;
