@@ -109,11 +109,6 @@ __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code
         st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
 }
 
-// 16 bytes to shared memory, of which those past `have` are 0
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t have) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
-}
-
 // True in one thread of the warp.  The compiler knows that of elect.sync, and puts the operands of the MMAs behind it straight
 // into uniform registers: four MMAs and a commit are issued in 160 clocks, behind a test of the lane in 700.
 __device__ __forceinline__ bool elected() {
@@ -253,7 +248,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], a.order ? 64 : 1);
+            mbar_init(&full[s], a.order ? 2 : 1);
             mbar_init(&ready[s], DEC_WARPS / 2 * CG);
             mbar_init(&empty[s], 1);
         }
@@ -333,6 +328,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     if (warp < WARP_DEC0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 " MM_PACKED4_REGS_FEW ";");
+        // every copy issued must land before this CTA's shared memory is released
+        const auto drain = [&](int it) {
+            for (int i = 0; i < STAGES && i < it; ++i) {
+                const int lastit = i + ((it - 1 - i) / STAGES) * STAGES;
+                if (!mbar_wait(&full[i], (uint32_t)(lastit / STAGES) & 1)) {
+                    atomicExch(&g_packed4_tiles_err, kDevErrDrain);
+                    break;
+                }
+            }
+        };
         if (warp == WARP_X && !a.order) {
             late_wait();
             int b = 0, it = 0;
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         stop = true;
                         break;
                     }
-                    if (lane == 0) {
+                    if (elected()) {
                         mbar_arrive_expect_tx(&full[b], (uint32_t)boxes * BOX * 128u);
                         for (int i = 0; i < boxes; ++i)
                             tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &full[b], s * BK, t.first + from + i * BOX);
@@ -359,22 +364,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (++b == STAGES) b = 0, ++use;
                 }
             }
-            // every copy issued must land before this CTA's shared memory is released
-            for (int i = 0; i < STAGES && i < it; ++i) {
-                const int lastit = i + ((it - 1 - i) / STAGES) * STAGES;
-                if (!mbar_wait(&full[i], (uint32_t)(lastit / STAGES) & 1)) {
-                    atomicExch(&g_packed4_tiles_err, kDevErrDrain);
-                    break;
-                }
-            }
+            drain(it);
         } else if (warp == WARP_X || (warp == WARP_X2 && a.order)) {
-            // Gathered rows: half of them to each of two warps, 8 lanes to a row's 128 bytes.  (Four rows to a TMA gather
-            // took 70 clocks an instruction: 2.2 times as long as the MMAs of a stage.)  The copies arrive at the stage's
-            // barrier by themselves; who waits for it makes them visible to the tensor cores.  (A fence here waits for every
-            // copy on its way: 3500 clocks a stage.)
-            const int half = warp == WARP_X2, c = lane & 7, sub = lane >> 3;
-            const uint32_t stride = (uint32_t)a.x_stride * 2;
-            int b = 0;
+            // Gathered rows, four to an instruction, half of them to each of two warps.  (Issued by a lane for each four, 70
+            // clocks an instruction; copied by the warps 16 bytes at a time, 60 clocks for four rows.)
+            const int half = warp == WARP_X2;
+            int b = 0, it = 0;
             uint32_t use = 0;
             bool stop = false;
             for (int u = cid, turn = 0; u < wk.units && !stop; u += ncl, turn ^= 1) {
@@ -387,31 +382,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     rows[i] = row < 0 ? 0 : (int)row;
                 }
                 __syncwarp();
-                rows += sub;
-                for (int s = 0; s < stages; ++s) {
+                for (int s = 0; s < stages; ++s, ++it) {
                     if (*abort_flag) { stop = true; break; }
                     if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
                         fail<CG>(abort_flag, kDevErrWaitEmpty);
                         stop = true;
                         break;
                     }
-                    // of the rows of this lane, every fourth, the place modulo 8 alternates between two
-                    const uint32_t dst = smem_u32(smem + b * P::STAGE + P::A_BYTES + (half * n + sub) * 128);
-                    const uint32_t d0 = dst + ((c ^ sub) << 4), d1 = dst + ((c ^ sub ^ 4) << 4);
-                    const int col = s * BK + c * 8;
-                    const uint32_t have = (uint32_t)max(0, min(8, a.cols - col)) * 2;  // bytes of its chunk that a row has; the rest is 0
-                    const uint8_t *x = static_cast<const uint8_t *>(a.X) + (have ? col * 2 : 0);
-#pragma unroll 2
-                    for (int i = 0; i < n; i += 32) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (i + 4 * k < n) copy16((k & 1 ? d1 : d0) + (i + 4 * k) * 128, x + (uint64_t)(uint32_t)rows[i + 4 * k] * stride, have);
+                    __syncwarp();
+                    if (elected()) {
+                        uint8_t *dst = smem + b * P::STAGE + P::A_BYTES + half * n * 128;
+                        mbar_arrive_expect_tx(&full[b], (uint32_t)n * 128u);
+#pragma unroll 4
+                        for (int i = 0; i < n; i += 4) {
+                            const int4 r = *reinterpret_cast<const int4 *>(rows + i);
+                            tma_gather4(dst + i * 128, &tmX, &full[b], s * BK, r.x, r.y, r.z, r.w);
+                        }
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[b])) : "memory");
+                    __syncwarp();
                     if (++b == STAGES) b = 0, ++use;
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (half == 0) drain(it);
         } else if (warp == WARP_CODES) {
             if (lane == 0) {
                 int b = 0, it = 0;
@@ -557,7 +549,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         // the stage is ready when X is there too: one warp of each CTA waits for it
                         if (warp == WARP_DEC0 + 4 * odd) {
                             if (!mbar_wait(&full[b], use & 1)) fail<CG>(abort_flag, kDevErrWaitFull);
-                            if (a.order) fence_proxy_async_smem();
                         }
                         arrive_leader<CG>(&ready[b]);
                     }
@@ -685,7 +676,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     // a single row may have any stride: the map wants one of whole 16 bytes that holds the row
     const uint64_t stride = a.x_rows > 1 ? (uint64_t)a.x_stride * 2 : ((uint64_t)a.cols * 2 + 15) / 16 * 16;
     e = make_tmap_2d(&tm, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, (uint64_t)a.cols,
-                     (uint64_t)a.x_rows, stride, BK, BOX, CU_TENSOR_MAP_SWIZZLE_128B);
+                     (uint64_t)a.x_rows, stride, BK, a.order ? 1 : BOX, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     CUtensorMap tw;
     const uint64_t bytes = ((uint64_t)a.cols + 31) / 32 * 16;
