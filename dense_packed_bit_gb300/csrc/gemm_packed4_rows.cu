@@ -5,19 +5,20 @@
 // "Kernel 0112", section "What the kernel costs in a whole token": the products of a token are bound by reading
 // 4-bit weights.  What a call cannot do without is the codes, half a byte each, and 2 or 3 bytes a group.
 //
-// A warp takes 16 rows of W and a part of K and streams it from memory into registers, 128 columns at a time: lane
-// (g, q) = (lane / 4, lane % 4) loads 16 bytes (32 codes) of row g and of row g + 8, eight such loads ahead of their
-// use.  The codes become exact 16-bit whole numbers in registers and are the A operand of mma.sync m16n8k16, whose
-// k slots are dealt so that no data moves: a word of 8 codes holds in one masked step the codes 0 and 4, in the next 1
-// and 5, and X is paired the same way.  The tensor cores add the products of one group in fp32; the group's scale is
-// applied to that sum in fp32, so neither scaled weights nor partial sums are ever rounded to 16 bits.  Groups below
-// 128 need the lanes of a row on the same group: they exchange words among the four lanes of a row first.
+// A unit of work is 64 rows of W times 8 (or 16) rows of X.  One warp of a CTA brings it by TMA, 256 columns at a time,
+// through a ring that does not stop at a unit's end: the codes, and as many columns of the rows of X (gathered where
+// `order` names them).  Eight warps multiply, four tiles of 16 rows by two halves of the 256 columns.  The codes become
+// exact 16-bit whole numbers in registers and are the A operand of mma.sync m16n8k16, whose k slots are dealt so that no
+// data moves between lanes: a word of 8 codes holds in one masked step the codes 0 and 4, in the next 1 and 5, and X is
+// paired the same way.  The tensor cores add the products of one group in fp32; the group's scale is applied to that sum
+// in fp32, so neither scaled weights nor partial sums are ever rounded to 16 bits.
 //
-// K is cut over the warps of a CTA, and over a cluster of CTAs where the rows alone would leave SMs idle; the parts
-// are added in a fixed order through shared memory, so results repeat bit for bit.  8 or 16 rows of X at a time (the
-// MMA's n, once or twice); more of them go around again with the codes read from L2.
+// K is cut over a cluster of CTAs where the rows alone would leave SMs idle; all parts are added in a fixed order through
+// shared memory, so results repeat bit for bit.  More rows of X than 8 (16) go around again with the codes read from L2.
 #include "packed4.cuh"
 #include "smem_limit.h"
+#include "tcgen05.cuh"
+#include "tmap.h"
 
 namespace mm {
 
@@ -25,11 +26,28 @@ __device__ unsigned int g_packed4_rows_err;
 
 namespace {
 
-constexpr int TILE = 16;      // rows of W per warp
-constexpr int KBLOCK = 128;   // columns per step
-constexpr int DEEP = 4;       // steps loaded ahead
-constexpr int STRIDE = 20;    // floats between tokens of a staged partial tile: lanes' stores meet no bank twice
-constexpr int MAX_WARPS = 8, MAX_CLUSTER = 8, MAX_EXPERTS = 1024;
+constexpr int TILE = 16;       // rows of W per warp
+constexpr int ROWS = 64;       // per unit
+constexpr int BK = 256;        // columns per stage
+constexpr int HALF = 128;      // per warp
+constexpr int CODES = ROWS * BK / 2;
+constexpr int CONSUMERS = 256, NTHREADS = CONSUMERS + 32;
+constexpr int AHEAD = 4;       // stages of scales on their way to registers
+constexpr int MAX_CLUSTER = 8, MAX_EXPERTS = 1024;
+
+template <int NT>
+struct Plan {
+    static constexpr int TOKENS = 8 * NT;
+    static constexpr int X = TOKENS * BK * 2, STAGE = CODES + X;   // X: four boxes of 64 columns
+    static constexpr int DEPTH = 5;
+    static constexpr int CTAS = NT == 1 ? 3 : 2;                   // of an SM: 3 x 60 KB, 2 x 80 KB and the partial tiles
+    static constexpr int STRIDE = ROWS + 4;                        // floats between tokens of a partial tile
+    static constexpr int RED = DEPTH * STAGE;                      // [2 turns][2 halves][TOKENS][STRIDE]
+    static constexpr int PART = RED + 4 * TOKENS * STRIDE * 4;     // [TOKENS][ROWS], of a cluster's CTA
+    static constexpr int BAR = PART + TOKENS * ROWS * 4;
+    static constexpr int TOTAL = BAR + 2 * DEPTH * 8 + 16 + 1024;  // + alignment of the dynamic allocation
+    static_assert(CTAS * (TOTAL + MAX_EXPERTS * 2 + 1024 + 64) <= 227 * 1024, "shared memory");
+};
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -46,82 +64,6 @@ __device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// What a lane waits for of one step: its codes come to shared memory (its own 2 x 16 bytes of the warp's 1 KB), these to
-// registers: the scale (low half) and zero (high half) of rows g and g + 8.
-struct Scales {
-    uint32_t g, h;
-};
-
-__device__ __forceinline__ void copy16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// This lane's part of 16 rows of W.
-struct Source {
-    const uint8_t *g, *h;  // codes of rows g and g + 8, at this lane's 16 bytes of the first step
-    const uint16_t *sg, *sh;
-    const uint8_t *zg, *zh;
-
-    __device__ __forceinline__ void point(const Packed4MmArgs &a, int e, int r0, int lane) {
-        // rows past the last one read the last one and are not stored
-        const int rg = min(r0 + (lane >> 2), a.rows - 1), rh = min(r0 + (lane >> 2) + 8, a.rows - 1);
-        const uint8_t *c = a.codes + e * a.codes_expert + (lane & 3) * 16;
-        g = c + rg * a.codes_row, h = c + rh * a.codes_row;
-        const uint16_t *s = static_cast<const uint16_t *>(a.scales) + e * a.scales_expert;
-        sg = s + rg * a.scales_row, sh = s + rh * a.scales_row;
-        const uint8_t *z = a.zeros ? a.zeros + e * a.scales_expert : nullptr;
-        zg = z ? z + rg * a.scales_row : nullptr, zh = z ? z + rh * a.scales_row : nullptr;
-    }
-
-    template <int G>
-    __device__ __forceinline__ void load(int b, int cols, int q, uint4 *dst, Scales &s) const {
-        const int col = b * KBLOCK + q * 32;
-        if (col < cols) {
-            copy16(dst, g + (int64_t)b * (KBLOCK / 2));
-            copy16(dst + 32, h + (int64_t)b * (KBLOCK / 2));
-        } else {
-            dst[0] = dst[32] = make_uint4(0, 0, 0, 0);
-        }
-        if (G == KBLOCK || col < cols) {  // of a group of 128 every lane applies the scale, whether it has codes or not
-            const int j = G == KBLOCK ? b : col / G;
-            s.g = __ldg(sg + j) | (zg ? (uint32_t)(__ldg(zg + j) & 15) : 8u) << 16;
-            s.h = __ldg(sh + j) | (zh ? (uint32_t)(__ldg(zh + j) & 15) : 8u) << 16;
-        } else {
-            s.g = s.h = 8u << 16;
-        }
-    }
-};
-
-// The words of a row's 128 codes (four to a lane, lane q those of columns 32 q on) redistributed so that word i of every
-// lane lies in group i / (4 G / 128); chunk_of tells which 8 columns the word then holds.
-template <int G>
-__device__ __forceinline__ void exchange(uint4 &w, int q) {
-    if constexpr (G == 64) {
-        const bool low = q < 2;
-        const uint32_t r0 = __shfl_xor_sync(~0u, low ? w.z : w.x, 2), r1 = __shfl_xor_sync(~0u, low ? w.w : w.y, 2);
-        if (low) w.z = r0, w.w = r1;
-        else w.x = r0, w.y = r1;
-    } else if constexpr (G == 32) {
-        const bool even = (q & 1) == 0, low = q < 2;
-        uint32_t r0 = __shfl_xor_sync(~0u, even ? w.y : w.x, 1), r1 = __shfl_xor_sync(~0u, even ? w.w : w.z, 1);
-        if (even) w.y = r0, w.w = r1;
-        else w.x = r0, w.z = r1;
-        r0 = __shfl_xor_sync(~0u, low ? w.z : w.x, 2), r1 = __shfl_xor_sync(~0u, low ? w.w : w.y, 2);
-        if (low) w.z = r0, w.w = r1;
-        else w.x = r0, w.y = r1;
-    }
-}
-// 64: a lane below 2 keeps its words 0, 1 and gets those of lane q + 2; the others keep 2, 3 and get those of q - 2.
-template <int G>
-__device__ __forceinline__ int chunk_of(int i, int q) {
-    if constexpr (G == 128) return q * 4 + i;
-    if constexpr (G == 64) return (i >> 1) * 8 + (q & 1) * 4 + (q >> 1) * 2 + (i & 1);
-    return i * 4 + q;
 }
 
 // The 8 codes of w less z as pairs (0, 4), (1, 5), (2, 6), (3, 7); zero: Zero4<T>::of(z).  In fp16 the second field of a
@@ -157,55 +99,54 @@ struct Zero4<__half> {
     }
 };
 
-// 8 columns from `col` of a row of X as the same pairs; columns at or past cols are 0
-__device__ __forceinline__ void load_x(const uint16_t *x, int col, int cols, uint32_t (&p)[4]) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (x && col + 8 <= cols) {
-        v = __ldg(reinterpret_cast<const uint4 *>(x + col));
-    } else if (x && col < cols) {
-        uint32_t t[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < cols) t[i >> 1] |= (uint32_t)__ldg(x + col + i) << (16 * (i & 1));
-        v = make_uint4(t[0], t[1], t[2], t[3]);
-    }
-    p[0] = prmt(v.x, v.z, 0x5410), p[1] = prmt(v.x, v.z, 0x7632);
-    p[2] = prmt(v.y, v.w, 0x5410), p[3] = prmt(v.y, v.w, 0x7632);
+// Which 8 columns of a half (of 16 such) the lanes with q = lane % 4 take in the i-th of four turns.  A group of 32 columns
+// takes all lanes; wider ones let a lane have two neighbours, so that eight lanes reading X meet no bank twice.
+template <int G>
+__device__ __forceinline__ int chunk_of(int i, int q) {
+    if constexpr (G == 32) return i * 4 + q;
+    return (i >> 1) * 8 + q * 2 + (i & 1);
 }
 
+// A half of a stage: 16 rows times 128 columns.  codes: the unit's rows, 128 bytes each, 16 bytes j of row r at j ^ r % 8; x: the
+// tokens' rows in boxes of 64 columns, 128 bytes each, the same way.  sz: scale (low half) and zero (high half) of rows g and
+// g + 8, in a lane of group (its q) of the half.  left: columns of the half that exist.
 template <typename T, int NT, int G>
-__device__ __forceinline__ void step(uint4 vg, uint4 vh, const Scales &in, int b, int cols, const uint16_t *const (&x)[NT], int lane,
-                                     float (&acc)[NT][4]) {
-    constexpr int GROUPS = KBLOCK / G, WORDS = 4 / GROUPS;
-    const int q = lane & 3;
-    exchange<G>(vg, q);
-    exchange<G>(vh, q);
-    const uint32_t wg[4] = {vg.x, vg.y, vg.z, vg.w}, wh[4] = {vh.x, vh.y, vh.z, vh.w};
+__device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *x, uint32_t szg, uint32_t szh, int half, int left,
+                                           int lane, float (&acc)[NT][4]) {
+    constexpr int GROUPS = HALF / G, TURNS = 4 / GROUPS;
+    const int g = lane >> 2, q = lane & 3;
+    uint32_t wg[4], wh[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = chunk_of<G>(i, q);
+        const uint8_t *at = codes + g * 128 + (((half * 4 + (c >> 2)) ^ g) << 4) + (c & 3) * 4;
+        wg[i] = *reinterpret_cast<const uint32_t *>(at);
+        wh[i] = *reinterpret_cast<const uint32_t *>(at + 8 * 128);
+    }
 #pragma unroll
     for (int j = 0; j < GROUPS; ++j) {
-        uint32_t sg = in.g, sh = in.h;
+        uint32_t sg = szg, sh = szh;
         if constexpr (GROUPS > 1) {
-            const int from = (lane & ~3) | j * (G / 32);
-            sg = __shfl_sync(~0u, sg, from);
-            sh = __shfl_sync(~0u, sh, from);
+            sg = __shfl_sync(~0u, szg, (lane & ~3) | j);
+            sh = __shfl_sync(~0u, szh, (lane & ~3) | j);
         }
         const Zero4<T> zg = Zero4<T>::of(sg >> 16), zh = Zero4<T>::of(sh >> 16);
         float d[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
 #pragma unroll
-        for (int i = j * WORDS; i < (j + 1) * WORDS; ++i) {
+        for (int i = j * TURNS; i < (j + 1) * TURNS; ++i) {
             uint32_t pg[4], ph[4];
             zg.decode(wg[i], pg);
             zh.decode(wh[i], ph);
             const uint32_t a0[4] = {pg[0], ph[0], pg[1], ph[1]}, a1[4] = {pg[2], ph[2], pg[3], ph[3]};
-            const int col = b * KBLOCK + chunk_of<G>(i, q) * 8;
+            const int c = chunk_of<G>(i, q), box = half * 2 + (c >> 3);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint32_t p[4];
-                load_x(x[n], col, cols, p);
-                mma<T>(d[n], a0, p[0], p[1]);
-                mma<T>(d[n], a1, p[2], p[3]);
+                uint4 v = *reinterpret_cast<const uint4 *>(x + box * (NT * 1024) + n * 1024 + g * 128 + (((c & 7) ^ g) << 4));
+                if (left < HALF && (c >> 3) * 64 >= left) v = make_uint4(0, 0, 0, 0);  // a box that was not loaded
+                mma<T>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
+                mma<T>(d[n], a1, prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
             }
         }
         const float fg = Code4<T>::f32((uint16_t)sg), fh = Code4<T>::f32((uint16_t)sh);
@@ -219,73 +160,49 @@ __device__ __forceinline__ void step(uint4 vg, uint4 vh, const Scales &in, int b
     }
 }
 
-// Where a warp is: its part of K of a unit (16 rows of an expert's matrix), for 8 NT of the expert's slots after the other.
+// Where a warp is in the CTA's work: units in turn, of each its slots TOKENS at a time, of those its stages.
 struct Cursor {
-    int64_t unit;
+    int unit;
     int e, r0, first, count;  // the unit's expert, rows and slots
-    int t0, b;                // slots already done, step
+    int t0, s;                // slots already done, stage
 };
 
-// Grid: clusters that take units in turn; a cluster's CTAs and their warps take consecutive parts of K.  The loads run DEEP
-// steps ahead of the products and do not stop at a unit's end.
+// Grid: clusters that take units in turn; a cluster's CTAs take consecutive parts of K.
 template <typename T, int NT, int G>
-__global__ void __launch_bounds__(32 * MAX_WARPS, NT == 1 ? 3 : 2)
-    packed4_rows_kernel(const __grid_constant__ Packed4MmArgs a, const int cluster) {
-    extern __shared__ uint4 smem[];  // a ring of DEEP KB to each warp, and twice a partial tile
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    uint4(*ring)[64] = reinterpret_cast<uint4(*)[64]>(smem) + warp * DEEP;
-    float(*red)[8 * NT * STRIDE] = reinterpret_cast<float(*)[8 * NT * STRIDE]>(smem + warps * DEEP * 64);  // [2][warps]
-    __shared__ float part[8 * NT * TILE];
+__global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
+    packed4_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ Packed4MmArgs a, const int cluster, const int xbox) {
+    using P = Plan<NT>;
+    constexpr int DEPTH = P::DEPTH, TOKENS = P::TOKENS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_aligned<1024>(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR), *empty = full + DEPTH;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + DEPTH);
     __shared__ int16_t listed[MAX_EXPERTS];  // the experts that have slots
     __shared__ int listed_n;
-    const int g = lane >> 2, q = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
-    const int64_t cid = blockIdx.x / cluster, clusters = gridDim.x / cluster;
-    const int tiles = (a.rows + TILE - 1) / TILE, steps = (a.cols + KBLOCK - 1) / KBLOCK;
-    const int parts = warps * cluster, mine = rank * warps + warp;
-    const int b0 = (int)((int64_t)steps * mine / parts), b1 = (int)((int64_t)steps * (mine + 1) / parts);
+    const int cid = blockIdx.x / cluster, clusters = gridDim.x / cluster;
+    const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
+    const int s0 = stages * rank / cluster, s1 = stages * (rank + 1) / cluster;
     unsigned int err = 0;
-    int64_t units = tiles;
+    int units = tiles;
 
-    const auto enter = [&](Cursor &c) {  // c.unit is set
-        c.t0 = 0, c.b = b0;
-        if (c.unit >= units) return;
-        const int at = a.offsets ? (int)(c.unit / tiles) : 0;
-        c.e = a.offsets ? listed[at] : 0;
-        c.r0 = (int)(c.unit - (int64_t)at * tiles) * TILE;
-        const Slots s = slots_of(a, c.e, &err);
-        c.first = s.first, c.count = s.count;
-    };
-    const auto past_chunk = [&](Cursor &c) {  // to the next slots, or the next unit
-        c.b = b0, c.t0 += 8 * NT;
-        if (c.t0 >= c.count) c.unit += clusters, enter(c);
-    };
-    Cursor ld;
-    Source src;
-    Scales sc[DEEP];
-    ld.unit = cid;
-    const auto load = [&](int u) {
-        if (ld.unit < units && b0 < b1) {
-            src.load<G>(ld.b, a.cols, q, &ring[u][lane], sc[u]);
-            if (++ld.b == b1) {
-                const int64_t unit = ld.unit;
-                past_chunk(ld);
-                if (ld.unit != unit && ld.unit < units) src.point(a, ld.e, ld.r0, lane);
-            }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < DEPTH; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], CONSUMERS / 32);
         }
-        copies_commit();
-    };
-    const auto start = [&] {
-        enter(ld);
-        if (ld.unit < units) src.point(a, ld.e, ld.r0, lane);
-#pragma unroll
-        for (int u = 0; u < DEEP; ++u) load(u);
-    };
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    // weights laid out long ago are asked for before the kernel in front has ended, where that one does not say whose they are
     const bool early = a.weights_static && !a.offsets;
-    if (early) start();
-    pdl_wait();
-    pdl_launch_dependents();
     if (a.offsets) {
+        pdl_wait();
+        pdl_launch_dependents();
         if (warp == 0) {
             int n = 0;
             for (int e0 = 0; e0 < a.experts; e0 += 32) {
@@ -296,106 +213,255 @@ __global__ void __launch_bounds__(32 * MAX_WARPS, NT == 1 ? 3 : 2)
             }
             if (lane == 0) listed_n = n;
         }
-        __syncthreads();
-        units = (int64_t)listed_n * tiles;
     }
-    if (!early) start();
+    __syncthreads();
+    if (a.offsets) units = listed_n * tiles;
 
-    int slot = 0, turn = 0;
-    Cursor at;
-    at.unit = cid;
-    enter(at);
-    while (at.unit < units) {
-        const uint16_t *x[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int t = at.t0 + 8 * n + g;
-            const int64_t row = t < at.count ? x_row(a, at.first + t, &err) : -1;
-            x[n] = row < 0 ? nullptr : static_cast<const uint16_t *>(a.X) + row * a.x_stride;
-        }
-        float acc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        for (int b = b0; b < b1;) {
-#pragma unroll
-            for (int u = 0; u < DEEP; ++u) {
-                if (u < slot || b >= b1) continue;
-                copies_wait<DEEP - 1>();
-                const uint4 vg = ring[u][lane], vh = ring[u][lane + 32];
-                const Scales now = sc[u];
-                load(u);
-                step<T, NT, G>(vg, vh, now, b, a.cols, x, lane, acc);
-                ++b;
-                slot = u + 1;
-            }
-            if (slot == DEEP) slot = 0;
-        }
-        float(&mine_red)[8 * NT * STRIDE] = red[turn * warps + warp];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mine_red[(8 * n + 2 * q + (i & 1)) * STRIDE + g + 8 * (i >> 1)] = acc[n][i];
-        __syncthreads();
-        if (cluster > 1) {
-            for (int i = threadIdx.x; i < 8 * NT * TILE; i += blockDim.x) {
-                float v = 0.f;
-                for (int w = 0; w < warps; ++w) v += red[turn * warps + w][(i / TILE) * STRIDE + i % TILE];
-                part[i] = v;
-            }
-            cluster_sync();
-        }
-        if (rank == 0) {
-            for (int i = threadIdx.x; i < 8 * NT * TILE; i += blockDim.x) {
-                const int t = at.t0 + i / TILE, r = at.r0 + i % TILE;
-                float v = 0.f;
-                if (cluster > 1) {
-                    const uint32_t from = smem_u32(&part[i]);
-                    float p[MAX_CLUSTER];
-#pragma unroll
-                    for (int c = 0; c < MAX_CLUSTER; ++c)
-                        if (c < cluster)
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[c]) : "r"(cluster_map(from, c)) : "memory");
-#pragma unroll
-                    for (int c = 0; c < MAX_CLUSTER; ++c)
-                        if (c < cluster) v += p[c];
-                } else {
-                    for (int w = 0; w < warps; ++w) v += red[turn * warps + w][(i / TILE) * STRIDE + i % TILE];
+    const auto enter = [&](Cursor &c) {  // c.unit is set
+        c.t0 = 0, c.s = s0;
+        if (c.unit >= units) return;
+        const int at = a.offsets ? c.unit / tiles : 0;
+        c.e = a.offsets ? listed[at] : 0;
+        c.r0 = (c.unit - at * tiles) * ROWS;
+        const Slots s = slots_of(a, c.e, &err);
+        c.first = s.first, c.count = s.count;
+    };
+    const auto next_chunk = [&](Cursor &c) {
+        c.s = s0, c.t0 += TOKENS;
+        if (c.t0 >= c.count) c.unit += clusters, enter(c);
+    };
+
+    if (warp == CONSUMERS / 32) {
+        // the producer: lane i holds the row of X of slot t0 + i
+        Cursor c;
+        c.unit = cid;
+        enter(c);
+        int row = 0;
+        const auto rows_of_chunk = [&] {
+            if (!a.order || c.unit >= units) return;
+            const int64_t r = lane < TOKENS && c.t0 + lane < c.count ? x_row(a, c.first + c.t0 + lane, &err) : 0;
+            row = r < 0 ? 0 : (int)r;
+        };
+        const auto boxes_of = [&](int s) { return min(4, (a.cols - s * BK + 63) / 64); };
+        const auto codes = [&](const Cursor &k, int b) {
+            const int rows = a.order ? min(TOKENS, (k.count - k.t0 + 3) & ~3) : xbox;
+            mbar_arrive_expect_tx(&full[b], CODES + (uint32_t)(boxes_of(k.s) * rows) * 128u);
+            tma_load_3d(smem + b * P::STAGE, &tmW, &full[b], k.s * (BK / 2), k.r0, k.e);
+        };
+        const auto xs = [&](const Cursor &k, int b) {
+            uint8_t *dst = smem + b * P::STAGE + CODES;
+            const int boxes = boxes_of(k.s);
+            if (a.order) {
+                const int rows = min(TOKENS, (k.count - k.t0 + 3) & ~3);
+                for (int i = 0; i < rows; i += 4) {
+                    const int r0 = __shfl_sync(~0u, row, i), r1 = __shfl_sync(~0u, row, i + 1), r2 = __shfl_sync(~0u, row, i + 2),
+                              r3 = __shfl_sync(~0u, row, i + 3);
+                    if (elected())
+                        for (int j = 0; j < boxes; ++j) tma_gather4(dst + j * (NT * 1024) + i * 128, &tmX, &full[b], k.s * BK + j * 64, r0, r1, r2, r3);
                 }
-                // a row's neighbour is the lane beside it, and the loop's length a multiple of 32: whole warps are here
-                const float up = __shfl_down_sync(~0u, v, 1);
-                if (t < at.count && r < a.rows) {
-                    if (!a.swiglu) store_y(a, at.first + t, r, v);
-                    else if ((r & 1) == 0) store_y(a, at.first + t, r >> 1, silu(v) * up);
+            } else if (elected()) {
+                for (int j = 0; j < boxes; ++j) tma_load_2d(dst + j * (NT * 1024), &tmX, &full[b], k.s * BK + j * 64, k.first + k.t0);
+            }
+        };
+        int b = 0, n = 0;
+        uint32_t use = 0;
+        bool stop = false;
+        const auto more = [&] { return c.unit < units && s0 < s1; };
+        if (early) {
+            // the first stages' codes, then what waits for the kernel in front
+            Cursor f = c;
+            for (int i = 0; i < DEPTH && f.unit < units && s0 < s1; ++i) {
+                if (elected()) codes(f, i);
+                __syncwarp();
+                if (++f.s == s1) next_chunk(f);
+            }
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+        rows_of_chunk();
+        while (more() && !stop) {
+            if (use > 0) {
+                if (*abort_flag || !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
+                    if (lane == 0 && !*abort_flag) atomicExch(&g_packed4_rows_err, kDevErrWaitEmpty);
+                    *abort_flag = 1;
+                    stop = true;
+                    break;
                 }
             }
+            __syncwarp();
+            if (!early || use > 0) {
+                if (elected()) codes(c, b);
+                __syncwarp();
+            }
+            xs(c, b);
+            __syncwarp();
+            ++n;
+            if (++b == DEPTH) b = 0, ++use;
+            if (++c.s == s1) {
+                if (cluster > 1) {  // the consumers' barriers count every thread; a cluster seldom has a second chunk
+                    cluster_sync();
+                    cluster_sync();
+                }
+                next_chunk(c);
+                rows_of_chunk();
+            }
         }
-        if (cluster > 1) cluster_sync();  // nobody leaves, or writes part again, before it has been read
-        turn ^= 1;  // of two buffers the other is free: the barrier above was behind its last reader
-        past_chunk(at);
+        // every copy issued must land before this CTA's shared memory is released
+        for (int i = 0; i < DEPTH && i < n; ++i) {
+            const int lastn = i + ((n - 1 - i) / DEPTH) * DEPTH;
+            if (!mbar_wait(&full[i], (uint32_t)(lastn / DEPTH) & 1)) {
+                if (lane == 0) atomicExch(&g_packed4_rows_err, kDevErrDrain);
+                break;
+            }
+        }
+    } else {
+        const int g = lane >> 2, q = lane & 3, tile = warp & 3, half = warp >> 2;
+        // scales and zeros AHEAD stages ahead, with a cursor of their own
+        Cursor sc;
+        const uint16_t *sg = nullptr, *sh = nullptr;
+        const uint8_t *zg = nullptr, *zh = nullptr;
+        sc.unit = cid;
+        const auto point = [&] {
+            if (sc.unit >= units) return;
+            const int rg = min(sc.r0 + tile * TILE + g, a.rows - 1), rh = min(sc.r0 + tile * TILE + g + 8, a.rows - 1);
+            const uint16_t *s = static_cast<const uint16_t *>(a.scales) + sc.e * a.scales_expert;
+            sg = s + rg * a.scales_row, sh = s + rh * a.scales_row;
+            if (a.zeros) {
+                const uint8_t *z = a.zeros + sc.e * a.scales_expert;
+                zg = z + rg * a.scales_row, zh = z + rh * a.scales_row;
+            }
+        };
+        uint32_t szg[AHEAD], szh[AHEAD];
+        const auto fetch = [&](uint32_t &x, uint32_t &y) {
+            x = y = 8u << 16;
+            if (sc.unit >= units || s0 >= s1) return;
+            const int j = (sc.s * BK + half * HALF) / G + (q & (HALF / G - 1));
+            if (j < a.groups) {
+                x = __ldg(sg + j) | (zg ? (uint32_t)(__ldg(zg + j) & 15) : 8u) << 16;
+                y = __ldg(sh + j) | (zh ? (uint32_t)(__ldg(zh + j) & 15) : 8u) << 16;
+            }
+            if (++sc.s == s1) {
+                const int unit = sc.unit;
+                next_chunk(sc);
+                if (sc.unit != unit) point();
+            }
+        };
+        enter(sc);
+        point();
+        if (early) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) fetch(szg[i], szh[i]);
+        }
+        if (!a.offsets) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+        if (!early) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) fetch(szg[i], szh[i]);
+        }
+        float *const red = reinterpret_cast<float *>(smem + P::RED), *const part = reinterpret_cast<float *>(smem + P::PART);
+        int b = 0, turn = 0, ahead = 0;
+        uint32_t use = 0;
+        Cursor c;
+        c.unit = cid;
+        enter(c);
+        while (c.unit < units) {
+            float acc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+            for (int s = s0; s < s1;) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (i < ahead || s >= s1) continue;
+                    const uint32_t x = szg[i], y = szh[i];
+                    fetch(szg[i], szh[i]);
+                    if (!*abort_flag && !mbar_wait(&full[b], use & 1)) {
+                        if (lane == 0) atomicExch(&g_packed4_rows_err, kDevErrWaitFull);
+                        *abort_flag = 1;
+                    }
+                    __syncwarp();
+                    const int left = a.cols - s * BK - half * HALF;
+                    const uint8_t *st = smem + b * P::STAGE;
+                    if (left > 0 && !*abort_flag) half_stage<T, NT, G>(st + tile * (TILE * 128), st + CODES, x, y, half, left, lane, acc);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[b]);
+                    if (++b == DEPTH) b = 0, ++use;
+                    ++s;
+                    ahead = i + 1;
+                }
+                if (ahead == AHEAD) ahead = 0;
+            }
+            float *mine = red + (turn * 2 + half) * (TOKENS * P::STRIDE) + tile * TILE;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mine[(8 * n + 2 * q + (i & 1)) * P::STRIDE + g + 8 * (i >> 1)] = acc[n][i];
+            bar_sync(1, CONSUMERS);
+            const float *sum = red + turn * 2 * (TOKENS * P::STRIDE);
+            const auto total = [&](int t, int r) { return sum[t * P::STRIDE + r] + sum[(TOKENS + t) * P::STRIDE + r]; };
+            if (cluster > 1) {
+                for (int i = threadIdx.x; i < TOKENS * ROWS; i += CONSUMERS) part[i] = total(i / ROWS, i % ROWS);
+                cluster_sync();
+            }
+            if (rank == 0) {
+                const int n = min(TOKENS, c.count - c.t0) * ROWS;
+                for (int i = threadIdx.x; i < n; i += CONSUMERS) {
+                    const int t = c.t0 + i / ROWS, r = c.r0 + i % ROWS;
+                    float v = 0.f;
+                    if (cluster > 1) {
+                        const uint32_t from = smem_u32(&part[i]);
+                        float p[MAX_CLUSTER];
+#pragma unroll
+                        for (int k = 0; k < MAX_CLUSTER; ++k)
+                            if (k < cluster)
+                                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[k]) : "r"(cluster_map(from, k)) : "memory");
+#pragma unroll
+                        for (int k = 0; k < MAX_CLUSTER; ++k)
+                            if (k < cluster) v += p[k];
+                    } else {
+                        v = total(i / ROWS, i % ROWS);
+                    }
+                    // a slot whose row of X does not exist (reported where X was loaded) counts as 0s
+                    unsigned int seen = 0;
+                    if (a.order && x_row(a, c.first + t, &seen) < 0) v = 0.f;
+                    // a row's neighbour is the lane beside it: n and the CTA's threads are multiples of 32, whole warps are here
+                    const float up = __shfl_down_sync(~0u, v, 1);
+                    if (r < a.rows) {
+                        if (!a.swiglu) store_y(a, c.first + t, r, v);
+                        else if ((r & 1) == 0) store_y(a, c.first + t, r >> 1, silu(v) * up);
+                    }
+                }
+            }
+            if (cluster > 1) cluster_sync();  // nobody leaves, or writes part again, before it has been read
+            turn ^= 1;  // of two buffers the other is free: the barrier above was behind its last reader
+            next_chunk(c);
+        }
     }
-    copies_wait<0>();
     if (err) atomicExch(&g_packed4_rows_err, err);
 }
 
 template <typename T, int NT, int G>
 cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    // K is cut into as many parts as keep all warps resident at once, but into no less than four (where it has as many
-    // steps), so that a tile's parts are a CTA's warps; beyond a CTA's eight warps a cluster's CTAs share it.
-    constexpr int RESIDENT = NT == 1 ? 24 : 16;  // warps of an SM: the launch bounds
-    constexpr int bytes = DEEP * 1024 + 2 * 8 * NT * STRIDE * 4;  // of shared memory to a warp
+    using P = Plan<NT>;
     static SmemLimit limit;
-    const cudaError_t e = limit.allow((const void *)packed4_rows_kernel<T, NT, G>, MAX_WARPS * bytes);
+    cudaError_t e = limit.allow((const void *)packed4_rows_kernel<T, NT, G>, P::TOTAL);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.rows + TILE - 1) / TILE, steps = (a.cols + KBLOCK - 1) / KBLOCK;
+    const int xbox = a.slots < P::TOKENS ? (int)a.slots : P::TOKENS;
+    CUtensorMap tx, tw;
+    e = packed4_tmap_x(&tx, a, a.order ? 1 : xbox);
+    if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    // K is cut over as many CTAs of a cluster as the GPU holds beside each other
+    const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
     const int64_t units = tiles * (a.offsets ? (a.slots < a.experts ? a.slots : a.experts) : 1);
-    int parts = 1;
-    while (parts * 2 <= steps && parts < MAX_WARPS * MAX_CLUSTER && (units * parts * 2 <= sms * RESIDENT || parts < 4)) parts *= 2;
-    const int warps = parts < MAX_WARPS ? parts : MAX_WARPS, cluster = parts / warps;
-    const int64_t fit = (int64_t)sms * (RESIDENT / warps) / cluster, clusters = units < fit ? units : fit;
+    int cluster = 1;
+    while (cluster < MAX_CLUSTER && cluster * 2 <= stages && units * cluster * 2 <= sms * P::CTAS) cluster *= 2;
+    const int64_t fit = (int64_t)sms * P::CTAS / cluster, clusters = units < fit ? units : fit;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(clusters * cluster));
-    lc.blockDim = dim3(32u * warps);
-    lc.dynamicSmemBytes = (size_t)warps * bytes;
+    lc.blockDim = dim3(NTHREADS);
+    lc.dynamicSmemBytes = P::TOTAL;
     lc.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -404,7 +470,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.x = (unsigned)cluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_rows_kernel<T, NT, G>, a, cluster);
+    return cudaLaunchKernelEx(&lc, packed4_rows_kernel<T, NT, G>, tx, tw, a, cluster, xbox);
 }
 
 template <typename T, int NT>

@@ -109,13 +109,6 @@ __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code
         st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
 }
 
-// True in one thread of the warp.  The compiler knows that of elect.sync, and puts the operands of the MMAs behind it straight
-// into uniform registers: four MMAs and a commit are issued in 160 clocks, behind a test of the lane in 700.
-__device__ __forceinline__ bool elected() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
-}
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
     if constexpr (CG == 2) umma_f16_pair(d, da, db, idesc, accumulate);
@@ -672,17 +665,9 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     static SmemLimit limit;
     cudaError_t e = limit.allow((const void *)packed4_tiles_kernel<T, CG>, P::TOTAL);
     if (e != cudaSuccess) return e;
-    CUtensorMap tm;
-    // a single row may have any stride: the map wants one of whole 16 bytes that holds the row
-    const uint64_t stride = a.x_rows > 1 ? (uint64_t)a.x_stride * 2 : ((uint64_t)a.cols * 2 + 15) / 16 * 16;
-    e = make_tmap_2d(&tm, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, (uint64_t)a.cols,
-                     (uint64_t)a.x_rows, stride, BK, a.order ? 1 : BOX, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
-    CUtensorMap tw;
-    const uint64_t bytes = ((uint64_t)a.cols + 31) / 32 * 16;
-    const uint64_t row = a.rows > 1 ? (uint64_t)a.codes_row : bytes, matrix = a.experts > 1 ? (uint64_t)a.codes_expert : row * a.rows;
-    e = make_tmap_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, &tw, a.codes, bytes, (uint64_t)a.rows, (uint64_t)a.experts, row, matrix, BK,
-                     BM, CU_TENSOR_MAP_SWIZZLE_64B);
+    CUtensorMap tx, tw;
+    e = packed4_tmap_x(&tx, a, a.order ? 1 : BOX);
+    if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK, BM, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
     // no more CTAs than units of the shortest chunks
     const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG);
@@ -700,7 +685,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.x = CG, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = CG == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tm, tw, a);
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tx, tw, a);
 }
 
 }  // namespace

@@ -9,6 +9,7 @@
 #include "cache_view.cuh"  // launch_pdl, kDevErrRange
 #include "mm_common.cuh"
 #include "mm_internal.h"
+#include "tmap.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -91,6 +92,28 @@ __device__ __forceinline__ void store_y(const Packed4MmArgs &a, int64_t slot, in
     if (a.y_dtype == 2) static_cast<float *>(a.Y)[i] = v;
     else if (a.y_dtype == 1) static_cast<uint16_t *>(a.Y)[i] = Code4<__nv_bfloat16>::round(v);
     else static_cast<uint16_t *>(a.Y)[i] = Code4<__half>::round(v);
+}
+
+// True in one thread of the warp.  The compiler knows that of elect.sync, and puts the operands of TMA copies and MMAs behind
+// it straight into uniform registers: four MMAs and a commit are issued in 160 clocks, behind a test of the lane in 700; a
+// gather of four rows in a third of the 70 clocks that a lane for each takes.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// X in boxes of 64 columns (128 bytes, swizzled) and `rows` rows, W's codes in boxes of `bytes` by `rows`.  A matrix of one row
+// may have any stride: the map is given one that holds it.
+inline cudaError_t packed4_tmap_x(CUtensorMap *map, const Packed4MmArgs &a, int rows) {
+    const uint64_t stride = a.x_rows > 1 ? (uint64_t)a.x_stride * 2 : ((uint64_t)a.cols * 2 + 15) / 16 * 16;
+    return make_tmap_2d(map, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.X, (uint64_t)a.cols,
+                        (uint64_t)a.x_rows, stride, 64, (uint32_t)rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+inline cudaError_t packed4_tmap_w(CUtensorMap *map, const Packed4MmArgs &a, int bytes, int rows, CUtensorMapSwizzle swizzle) {
+    const uint64_t held = ((uint64_t)a.cols + 31) / 32 * 16, row = a.rows > 1 ? (uint64_t)a.codes_row : held;
+    return make_tmap_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, map, a.codes, held, (uint64_t)a.rows, (uint64_t)a.experts, row,
+                        a.experts > 1 ? (uint64_t)a.codes_expert : row * a.rows, (uint32_t)bytes, (uint32_t)rows, swizzle);
 }
 
 }  // namespace mm
