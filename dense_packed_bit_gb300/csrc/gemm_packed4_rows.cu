@@ -5,9 +5,9 @@
 // "Kernel 0112", section "What the kernel costs in a whole token": the products of a token are bound by reading
 // 4-bit weights.  What a call cannot do without is the codes, half a byte each, and 2 or 3 bytes a group.
 //
-// A unit of work is 64 rows of W times 8 (or 16) rows of X.  One warp of a CTA brings it by TMA, 256 columns at a time,
+// A unit of work is 64 rows of W times 8 (or 16) rows of X.  One warp of a CTA brings it by TMA, 512 columns at a time,
 // through a ring that does not stop at a unit's end: the codes, and as many columns of the rows of X (gathered where
-// `order` names them).  Eight warps multiply, four tiles of 16 rows by two halves of the 256 columns.  The codes become
+// `order` names them).  Eight warps multiply, four tiles of 16 rows by two halves of the columns.  The codes become
 // exact 16-bit whole numbers in registers and are the A operand of mma.sync m16n8k16, whose k slots are dealt so that no
 // data moves between lanes: a word of 8 codes holds in one masked step the codes 0 and 4, in the next 1 and 5, and X is
 // paired the same way.  The tensor cores add the products of one group in fp32; the group's scale is applied to that sum
@@ -28,19 +28,19 @@ namespace {
 
 constexpr int TILE = 16;       // rows of W per warp
 constexpr int ROWS = 64;       // per unit
-constexpr int BK = 256;        // columns per stage
-constexpr int HALF = 128;      // per warp
+constexpr int BK = 512;        // columns per stage
+constexpr int HALF = 256;      // per warp
 constexpr int CODES = ROWS * BK / 2;
 constexpr int CONSUMERS = 256, NTHREADS = CONSUMERS + 32;
-constexpr int AHEAD = 4;       // stages of scales on their way to registers
+constexpr int AHEAD = 2;       // stages of scales on their way to registers
 constexpr int MAX_CLUSTER = 8, MAX_EXPERTS = 1024;
 
 template <int NT>
 struct Plan {
     static constexpr int TOKENS = 8 * NT;
-    static constexpr int X = TOKENS * BK * 2, STAGE = CODES + X;   // X: four boxes of 64 columns
-    static constexpr int DEPTH = 5;
-    static constexpr int CTAS = NT == 1 ? 3 : 2;                   // of an SM: 3 x 60 KB, 2 x 80 KB and the partial tiles
+    static constexpr int X = TOKENS * BK * 2, STAGE = CODES + X;   // codes: two boxes of 256 columns, X: eight of 64
+    static constexpr int DEPTH = NT == 1 ? 3 : 2;
+    static constexpr int CTAS = 2;                                 // of an SM: 2 x 72 KB, 2 x 64 KB and the partial tiles
     static constexpr int STRIDE = ROWS + 4;                        // floats between tokens of a partial tile
     static constexpr int RED = DEPTH * STAGE;                      // [2 turns][2 halves][TOKENS][STRIDE]
     static constexpr int PART = RED + 4 * TOKENS * STRIDE * 4;     // [TOKENS][ROWS], of a cluster's CTA
@@ -99,63 +99,85 @@ struct Zero4<__half> {
     }
 };
 
-// Which 8 columns of a half (of 16 such) the lanes with q = lane % 4 take in the i-th of four turns.  A group of 32 columns
-// takes all lanes; wider ones let a lane have two neighbours, so that eight lanes reading X meet no bank twice.
-template <int G>
-__device__ __forceinline__ int chunk_of(int i, int q) {
-    if constexpr (G == 32) return i * 4 + q;
-    return (i >> 1) * 8 + q * 2 + (i & 1);
-}
-
-// A half of a stage: 16 rows times 128 columns.  codes: the unit's rows, 128 bytes each, 16 bytes j of row r at j ^ r % 8; x: the
-// tokens' rows in boxes of 64 columns, 128 bytes each, the same way.  sz: scale (low half) and zero (high half) of rows g and
-// g + 8, in a lane of group (its q) of the half.  left: columns of the half that exist.
-template <typename T, int NT, int G>
-__device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *x, uint32_t szg, uint32_t szh, int half, int left,
-                                           int lane, float (&acc)[NT][4]) {
-    constexpr int GROUPS = HALF / G, TURNS = 4 / GROUPS;
-    const int g = lane >> 2, q = lane & 3;
-    uint32_t wg[4], wh[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = chunk_of<G>(i, q);
-        const uint8_t *at = codes + g * 128 + (((half * 4 + (c >> 2)) ^ g) << 4) + (c & 3) * 4;
-        wg[i] = *reinterpret_cast<const uint32_t *>(at);
-        wh[i] = *reinterpret_cast<const uint32_t *>(at + 8 * 128);
+// Which 8 columns of 128 (of 16 such) the lanes with q = lane % 4 take in the i-th of four turns.  A group of 32 columns takes
+// all lanes: chunk 4 i + q.  Wider ones let a lane have two neighbours, 8 (i / 2) + 2 q + i % 2, so that the eight lanes that
+// read X together meet no bank twice.  Where they lie, 16 bytes j of row r at j ^ r % 8, an XOR of a lane's own offset tells:
+struct Place {
+    uint32_t codes, x;  // offsets of turn 0 in the half's codes and X
+    template <int G>
+    static __device__ __forceinline__ Place of(int lane) {
+        const uint32_t g = lane >> 2, q = lane & 3;
+        if (G == 32) return {g * 128 + (g << 4) + q * 4, g * 128 + ((q ^ g) << 4)};
+        return {g * 128 + (((q >> 1) ^ g) << 4) + (q & 1) * 8, g * 128 + (((q * 2) ^ g) << 4)};
     }
+    // 128 columns further: four 16-byte pieces of codes; two boxes of X (added by the caller)
+    template <int G>
+    __device__ __forceinline__ uint32_t code(int i, int part) const {
+        if (G == 32) return codes ^ (uint32_t)((part * 4 + i) << 4);
+        return (codes ^ (uint32_t)((part * 4 + (i >> 1) * 2) << 4)) + (i & 1) * 4;
+    }
+    template <int G>
+    __device__ __forceinline__ uint32_t column(int i) const {
+        return x ^ (uint32_t)(G == 32 ? (i & 1) << 6 : (i & 1) << 4);
+    }
+};
+
+// Scales (low half) and zeros (high half) of rows g and g + 8 for a half of a stage: lane q holds group q (and, of 32 columns,
+// group q + 4) of it.
+template <int G>
+struct Scales {
+    static constexpr int N = G == 32 ? 2 : 1;
+    uint32_t g[N], h[N];
+};
+
+// A half of a stage: 16 rows times 256 columns.  codes: the tile's rows of a box; x: the half's four boxes; left: columns of the
+// half that exist.
+template <typename T, int NT, int G>
+__device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *x, const Place &at, const Scales<G> &sz, int left,
+                                           int lane, float (&acc)[NT][4]) {
+    constexpr int GROUPS = 128 / G, TURNS = 4 / GROUPS;
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-        uint32_t sg = szg, sh = szh;
-        if constexpr (GROUPS > 1) {
-            sg = __shfl_sync(~0u, szg, (lane & ~3) | j);
-            sh = __shfl_sync(~0u, szh, (lane & ~3) | j);
+    for (int part = 0; part < 2; ++part) {
+        if (part * 128 >= left) break;
+        uint32_t wg[4], wh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t *from = codes + at.code<G>(i, part);
+            wg[i] = *reinterpret_cast<const uint32_t *>(from);
+            wh[i] = *reinterpret_cast<const uint32_t *>(from + 8 * 128);
         }
-        const Zero4<T> zg = Zero4<T>::of(sg >> 16), zh = Zero4<T>::of(sh >> 16);
-        float d[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+        for (int j = 0; j < GROUPS; ++j) {
+            constexpr int LANES = HALF / G < 4 ? HALF / G : 4;
+            const int group = part * GROUPS + j, from = (lane & ~3) | (group & (LANES - 1));
+            const uint32_t sg = __shfl_sync(~0u, sz.g[group / 4], from), sh = __shfl_sync(~0u, sz.h[group / 4], from);
+            const Zero4<T> zg = Zero4<T>::of(sg >> 16), zh = Zero4<T>::of(sh >> 16);
+            float d[NT][4];
 #pragma unroll
-        for (int i = j * TURNS; i < (j + 1) * TURNS; ++i) {
-            uint32_t pg[4], ph[4];
-            zg.decode(wg[i], pg);
-            zh.decode(wh[i], ph);
-            const uint32_t a0[4] = {pg[0], ph[0], pg[1], ph[1]}, a1[4] = {pg[2], ph[2], pg[3], ph[3]};
-            const int c = chunk_of<G>(i, q), box = half * 2 + (c >> 3);
+            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+#pragma unroll
+            for (int i = j * TURNS; i < (j + 1) * TURNS; ++i) {
+                uint32_t pg[4], ph[4];
+                zg.decode(wg[i], pg);
+                zh.decode(wh[i], ph);
+                const uint32_t a0[4] = {pg[0], ph[0], pg[1], ph[1]}, a1[4] = {pg[2], ph[2], pg[3], ph[3]};
+                const int box = part * 2 + (i >> 1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint4 v = *reinterpret_cast<const uint4 *>(x + box * (NT * 1024) + n * 1024 + at.column<G>(i));
+                    if (box * 64 >= left) v = make_uint4(0, 0, 0, 0);  // a box that was not loaded
+                    mma<T>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
+                    mma<T>(d[n], a1, prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+                }
+            }
+            const float fg = Code4<T>::f32((uint16_t)sg), fh = Code4<T>::f32((uint16_t)sh);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint4 v = *reinterpret_cast<const uint4 *>(x + box * (NT * 1024) + n * 1024 + g * 128 + (((c & 7) ^ g) << 4));
-                if (left < HALF && (c >> 3) * 64 >= left) v = make_uint4(0, 0, 0, 0);  // a box that was not loaded
-                mma<T>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
-                mma<T>(d[n], a1, prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+                acc[n][0] = fmaf(fg, d[n][0], acc[n][0]);
+                acc[n][1] = fmaf(fg, d[n][1], acc[n][1]);
+                acc[n][2] = fmaf(fh, d[n][2], acc[n][2]);
+                acc[n][3] = fmaf(fh, d[n][3], acc[n][3]);
             }
-        }
-        const float fg = Code4<T>::f32((uint16_t)sg), fh = Code4<T>::f32((uint16_t)sh);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            acc[n][0] = fmaf(fg, d[n][0], acc[n][0]);
-            acc[n][1] = fmaf(fg, d[n][1], acc[n][1]);
-            acc[n][2] = fmaf(fh, d[n][2], acc[n][2]);
-            acc[n][3] = fmaf(fh, d[n][3], acc[n][3]);
         }
     }
 }
@@ -242,11 +264,13 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             const int64_t r = lane < TOKENS && c.t0 + lane < c.count ? x_row(a, c.first + c.t0 + lane, &err) : 0;
             row = r < 0 ? 0 : (int)r;
         };
-        const auto boxes_of = [&](int s) { return min(4, (a.cols - s * BK + 63) / 64); };
+        const auto boxes_of = [&](int s) { return min(8, (a.cols - s * BK + 63) / 64); };
         const auto codes = [&](const Cursor &k, int b) {
             const int rows = a.order ? min(TOKENS, (k.count - k.t0 + 3) & ~3) : xbox;
-            mbar_arrive_expect_tx(&full[b], CODES + (uint32_t)(boxes_of(k.s) * rows) * 128u);
-            tma_load_3d(smem + b * P::STAGE, &tmW, &full[b], k.s * (BK / 2), k.r0, k.e);
+            const int wide = a.cols - k.s * BK > HALF ? 2 : 1;
+            mbar_arrive_expect_tx(&full[b], (uint32_t)wide * (CODES / 2) + (uint32_t)(boxes_of(k.s) * rows) * 128u);
+            for (int i = 0; i < wide; ++i)
+                tma_load_3d(smem + b * P::STAGE + i * (CODES / 2), &tmW, &full[b], k.s * (BK / 2) + i * 128, k.r0, k.e);
         };
         const auto xs = [&](const Cursor &k, int b) {
             uint8_t *dst = smem + b * P::STAGE + CODES;
@@ -316,11 +340,15 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         }
     } else {
         const int g = lane >> 2, q = lane & 3, tile = warp & 3, half = warp >> 2;
+        const Place place = Place::of<G>(lane);
         // scales and zeros AHEAD stages ahead, with a cursor of their own
+        constexpr int LANES = HALF / G < 4 ? HALF / G : 4, N = Scales<G>::N;
         Cursor sc;
         const uint16_t *sg = nullptr, *sh = nullptr;
         const uint8_t *zg = nullptr, *zh = nullptr;
         sc.unit = cid;
+        const int j0 = (s0 * BK + half * HALF) / G + (q & (LANES - 1));  // this lane's first group
+        int j = j0;
         const auto point = [&] {
             if (sc.unit >= units) return;
             const int rg = min(sc.r0 + tile * TILE + g, a.rows - 1), rh = min(sc.r0 + tile * TILE + g + 8, a.rows - 1);
@@ -331,18 +359,21 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                 zg = z + rg * a.scales_row, zh = z + rh * a.scales_row;
             }
         };
-        uint32_t szg[AHEAD], szh[AHEAD];
-        const auto fetch = [&](uint32_t &x, uint32_t &y) {
-            x = y = 8u << 16;
-            if (sc.unit >= units || s0 >= s1) return;
-            const int j = (sc.s * BK + half * HALF) / G + (q & (HALF / G - 1));
-            if (j < a.groups) {
-                x = __ldg(sg + j) | (zg ? (uint32_t)(__ldg(zg + j) & 15) : 8u) << 16;
-                y = __ldg(sh + j) | (zh ? (uint32_t)(__ldg(zh + j) & 15) : 8u) << 16;
+        Scales<G> sz[AHEAD];
+        const auto fetch = [&](Scales<G> &x) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                x.g[n] = x.h[n] = 8u << 16;
+                if (sc.unit < units && j + 4 * n < a.groups) {
+                    x.g[n] = __ldg(sg + j + 4 * n) | (zg ? (uint32_t)(__ldg(zg + j + 4 * n) & 15) : 8u) << 16;
+                    x.h[n] = __ldg(sh + j + 4 * n) | (zh ? (uint32_t)(__ldg(zh + j + 4 * n) & 15) : 8u) << 16;
+                }
             }
+            j += BK / G;
             if (++sc.s == s1) {
                 const int unit = sc.unit;
                 next_chunk(sc);
+                j = j0;
                 if (sc.unit != unit) point();
             }
         };
@@ -350,7 +381,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         point();
         if (early) {
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) fetch(szg[i], szh[i]);
+            for (int i = 0; i < AHEAD; ++i) fetch(sz[i]);
         }
         if (!a.offsets) {
             pdl_wait();
@@ -358,11 +389,12 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         }
         if (!early) {
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) fetch(szg[i], szh[i]);
+            for (int i = 0; i < AHEAD; ++i) fetch(sz[i]);
         }
         float *const red = reinterpret_cast<float *>(smem + P::RED), *const part = reinterpret_cast<float *>(smem + P::PART);
         int b = 0, turn = 0, ahead = 0;
         uint32_t use = 0;
+        bool stop = false;
         Cursor c;
         c.unit = cid;
         enter(c);
@@ -374,16 +406,17 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     if (i < ahead || s >= s1) continue;
-                    const uint32_t x = szg[i], y = szh[i];
-                    fetch(szg[i], szh[i]);
-                    if (!*abort_flag && !mbar_wait(&full[b], use & 1)) {
+                    const Scales<G> now = sz[i];
+                    fetch(sz[i]);
+                    if (!stop && !mbar_wait(&full[b], use & 1)) {
                         if (lane == 0) atomicExch(&g_packed4_rows_err, kDevErrWaitFull);
                         *abort_flag = 1;
+                        stop = true;  // nothing waits any more, the warps' barriers are still met
                     }
                     __syncwarp();
-                    const int left = a.cols - s * BK - half * HALF;
                     const uint8_t *st = smem + b * P::STAGE;
-                    if (left > 0 && !*abort_flag) half_stage<T, NT, G>(st + tile * (TILE * 128), st + CODES, x, y, half, left, lane, acc);
+                    half_stage<T, NT, G>(st + half * (CODES / 2) + tile * (TILE * 128), st + CODES + half * (4 * NT * 1024), place, now,
+                                         a.cols - s * BK - half * HALF, lane, acc);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[b]);
                     if (++b == DEPTH) b = 0, ++use;
@@ -450,7 +483,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     const int xbox = a.slots < P::TOKENS ? (int)a.slots : P::TOKENS;
     CUtensorMap tx, tw;
     e = packed4_tmap_x(&tx, a, a.order ? 1 : xbox);
-    if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, HALF / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     // K is cut over as many CTAs of a cluster as the GPU holds beside each other
     const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
@@ -482,8 +515,8 @@ cudaError_t launch_g(const Packed4MmArgs &a, int sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_t(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    // 16 at a time where a matrix has more than 8 rows of X on average
-    return a.slots > (a.offsets ? 8 * (int64_t)a.experts : 8) ? launch_g<T, 2>(a, sms, s) : launch_g<T, 1>(a, sms, s);
+    // 16 at a time where a matrix has more than 8 rows of X; of experts some have twice the average
+    return a.slots > (a.offsets ? 3 * (int64_t)a.experts : 8) ? launch_g<T, 2>(a, sms, s) : launch_g<T, 1>(a, sms, s);
 }
 
 }  // namespace
