@@ -182,6 +182,32 @@ __device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *
     }
 }
 
+// Columns r .. r + 3 of Y (rows of W) for a slot; vec: four of them are 16 (8) aligned bytes
+template <typename T>
+__device__ __forceinline__ void store4(const Packed4MmArgs &a, int64_t slot, int r, const float4 &v, bool vec) {
+    const int64_t row = slot * a.y_stride;
+    if (a.swiglu) {
+        const float p = silu(v.x) * v.y, q = silu(v.z) * v.w;
+        if (vec && r + 3 < a.rows) {
+            if (a.y_dtype == 2) *reinterpret_cast<float2 *>(static_cast<float *>(a.Y) + row + (r >> 1)) = make_float2(p, q);
+            else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.Y) + row + (r >> 1)) = Code4<T>::round(p) | (uint32_t)Code4<T>::round(q) << 16;
+        } else {
+            if (r < a.rows) store_y(a, slot, r >> 1, p);
+            if (r + 2 < a.rows) store_y(a, slot, (r >> 1) + 1, q);
+        }
+    } else if (vec && r + 3 < a.rows) {
+        if (a.y_dtype == 2) *reinterpret_cast<float4 *>(static_cast<float *>(a.Y) + row + r) = v;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.Y) + row + r) =
+                make_uint2(Code4<T>::round(v.x) | (uint32_t)Code4<T>::round(v.y) << 16, Code4<T>::round(v.z) | (uint32_t)Code4<T>::round(v.w) << 16);
+    } else {
+        if (r < a.rows) store_y(a, slot, r, v.x);
+        if (r + 1 < a.rows) store_y(a, slot, r + 1, v.y);
+        if (r + 2 < a.rows) store_y(a, slot, r + 2, v.z);
+        if (r + 3 < a.rows) store_y(a, slot, r + 3, v.w);
+    }
+}
+
 // Where a warp is in the CTA's work: units in turn, of each its slots TOKENS at a time, of those its stages.
 struct Cursor {
     int unit;
@@ -344,20 +370,18 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         // scales and zeros AHEAD stages ahead, with a cursor of their own
         constexpr int LANES = HALF / G < 4 ? HALF / G : 4, N = Scales<G>::N;
         Cursor sc;
-        const uint16_t *sg = nullptr, *sh = nullptr;
-        const uint8_t *zg = nullptr, *zh = nullptr;
+        uint32_t rg = 0, rh = 0;  // the rows' first scale in their matrix
+        const uint16_t *scales = nullptr;
+        const uint8_t *zeros = nullptr;
         sc.unit = cid;
         const int j0 = (s0 * BK + half * HALF) / G + (q & (LANES - 1));  // this lane's first group
         int j = j0;
         const auto point = [&] {
             if (sc.unit >= units) return;
-            const int rg = min(sc.r0 + tile * TILE + g, a.rows - 1), rh = min(sc.r0 + tile * TILE + g + 8, a.rows - 1);
-            const uint16_t *s = static_cast<const uint16_t *>(a.scales) + sc.e * a.scales_expert;
-            sg = s + rg * a.scales_row, sh = s + rh * a.scales_row;
-            if (a.zeros) {
-                const uint8_t *z = a.zeros + sc.e * a.scales_expert;
-                zg = z + rg * a.scales_row, zh = z + rh * a.scales_row;
-            }
+            scales = static_cast<const uint16_t *>(a.scales) + sc.e * a.scales_expert;
+            if (a.zeros) zeros = a.zeros + sc.e * a.scales_expert;
+            rg = (uint32_t)min(sc.r0 + tile * TILE + g, a.rows - 1) * (uint32_t)a.scales_row;
+            rh = (uint32_t)min(sc.r0 + tile * TILE + g + 8, a.rows - 1) * (uint32_t)a.scales_row;
         };
         Scales<G> sz[AHEAD];
         const auto fetch = [&](Scales<G> &x) {
@@ -365,8 +389,9 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             for (int n = 0; n < N; ++n) {
                 x.g[n] = x.h[n] = 8u << 16;
                 if (sc.unit < units && j + 4 * n < a.groups) {
-                    x.g[n] = __ldg(sg + j + 4 * n) | (zg ? (uint32_t)(__ldg(zg + j + 4 * n) & 15) : 8u) << 16;
-                    x.h[n] = __ldg(sh + j + 4 * n) | (zh ? (uint32_t)(__ldg(zh + j + 4 * n) & 15) : 8u) << 16;
+                    const uint32_t k = (uint32_t)(j + 4 * n);
+                    x.g[n] = __ldg(scales + (rg + k)) | (zeros ? (uint32_t)(__ldg(zeros + (rg + k)) & 15) : 8u) << 16;
+                    x.h[n] = __ldg(scales + (rh + k)) | (zeros ? (uint32_t)(__ldg(zeros + (rh + k)) & 15) : 8u) << 16;
                 }
             }
             j += BK / G;
@@ -398,6 +423,8 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         Cursor c;
         c.unit = cid;
         enter(c);
+        const int size = a.y_dtype == 2 ? 4 : 2;
+        const bool vec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.y_stride * size % 16 == 0;
         while (c.unit < units) {
             float acc[NT][4];
 #pragma unroll
@@ -432,38 +459,38 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                 for (int i = 0; i < 4; ++i) mine[(8 * n + 2 * q + (i & 1)) * P::STRIDE + g + 8 * (i >> 1)] = acc[n][i];
             bar_sync(1, CONSUMERS);
             const float *sum = red + turn * 2 * (TOKENS * P::STRIDE);
-            const auto total = [&](int t, int r) { return sum[t * P::STRIDE + r] + sum[(TOKENS + t) * P::STRIDE + r]; };
+            // four rows to a thread
+            constexpr int QUADS = ROWS / 4;
+            const int n = min(TOKENS, c.count - c.t0) * QUADS;
+            const auto total = [&](int i) {
+                const float *p = sum + i / QUADS * P::STRIDE + i % QUADS * 4;
+                const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + TOKENS * P::STRIDE);
+                return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            };
             if (cluster > 1) {
-                for (int i = threadIdx.x; i < TOKENS * ROWS; i += CONSUMERS) part[i] = total(i / ROWS, i % ROWS);
+                for (int i = threadIdx.x; i < n; i += CONSUMERS) reinterpret_cast<float4 *>(part)[i] = total(i);
                 cluster_sync();
             }
             if (rank == 0) {
-                const int n = min(TOKENS, c.count - c.t0) * ROWS;
                 for (int i = threadIdx.x; i < n; i += CONSUMERS) {
-                    const int t = c.t0 + i / ROWS, r = c.r0 + i % ROWS;
-                    float v = 0.f;
+                    const int t = c.t0 + i / QUADS, r = c.r0 + i % QUADS * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (cluster > 1) {
-                        const uint32_t from = smem_u32(&part[i]);
-                        float p[MAX_CLUSTER];
+                        const uint32_t from = smem_u32(part + i * 4);
+                        float4 p[MAX_CLUSTER];
 #pragma unroll
                         for (int k = 0; k < MAX_CLUSTER; ++k)
-                            if (k < cluster)
-                                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[k]) : "r"(cluster_map(from, k)) : "memory");
+                            if (k < cluster) p[k] = ld_cluster_v4(cluster_map(from, k));
 #pragma unroll
                         for (int k = 0; k < MAX_CLUSTER; ++k)
-                            if (k < cluster) v += p[k];
+                            if (k < cluster) v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
                     } else {
-                        v = total(i / ROWS, i % ROWS);
+                        v = total(i);
                     }
                     // a slot whose row of X does not exist (reported where X was loaded) counts as 0s
                     unsigned int seen = 0;
-                    if (a.order && x_row(a, c.first + t, &seen) < 0) v = 0.f;
-                    // a row's neighbour is the lane beside it: n and the CTA's threads are multiples of 32, whole warps are here
-                    const float up = __shfl_down_sync(~0u, v, 1);
-                    if (r < a.rows) {
-                        if (!a.swiglu) store_y(a, c.first + t, r, v);
-                        else if ((r & 1) == 0) store_y(a, c.first + t, r >> 1, silu(v) * up);
-                    }
+                    if (a.order && x_row(a, c.first + t, &seen) < 0) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < a.rows) store4<T>(a, c.first + t, r, v, vec);
                 }
             }
             if (cluster > 1) cluster_sync();  // nobody leaves, or writes part again, before it has been read

@@ -1297,6 +1297,8 @@ mm_status check_packed4_weights(const mm_packed4 *W, mm::Packed4MmArgs *a) {
     if ((double)(W->rows - 1) * (double)W->codes_row + (double)(W->experts - 1) * (double)W->codes_expert + (double)bytes > (double)far ||
         (double)(W->rows - 1) * (double)W->scales_row + (double)(W->experts - 1) * (double)W->scales_expert + (double)groups > (double)(far / 2))
         return fail(MM_ERR_INVALID_ARG, "codes or scales span more than 2^47 bytes");
+    if ((double)W->rows * (double)W->scales_row > 4294967295.0)
+        return fail(MM_ERR_INVALID_ARG, "the scales of a matrix span 2^32 elements or more");
     if (W->experts > 1 && (W->codes_expert < (W->rows - 1) * W->codes_row + bytes || W->scales_expert < (W->rows - 1) * W->scales_row + groups))
         return fail(MM_ERR_INVALID_ARG, "codes_expert or scales_expert does not hold a matrix");
     if (W->weights_static != 0 && W->weights_static != 1) return fail(MM_ERR_INVALID_ARG, "weights_static must be 0 or 1");
