@@ -46,24 +46,21 @@ struct Plan {
     static constexpr int PART = RED + 4 * TOKENS * STRIDE * 4;     // [TOKENS][ROWS], of a cluster's CTA
     static constexpr int BAR = PART + TOKENS * ROWS * 4;
     static constexpr int TOTAL = BAR + 2 * DEPTH * 8 + 16 + 1024;  // + alignment of the dynamic allocation
-    static_assert(CTAS * (TOTAL + MAX_EXPERTS * 2 + 1024 + 64) <= 227 * 1024, "shared memory");
+    static_assert(CTAS * (TOTAL + MAX_EXPERTS * 10 + 1024 + 64) <= 227 * 1024, "shared memory");
 };
 
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d += a b, or with FIRST d = a b
+template <typename T, bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    const float c0 = FIRST ? 0.f : d[0], c1 = FIRST ? 0.f : d[1], c2 = FIRST ? 0.f : d[2], c3 = FIRST ? 0.f : d[3];
+    if constexpr (sizeof(T) && __is_same(T, __half))
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The 8 codes of w less z as pairs (0, 4), (1, 5), (2, 6), (3, 7); zero: Zero4<T>::of(z).  In fp16 the second field of a
@@ -131,14 +128,14 @@ struct Scales {
 };
 
 // A half of a stage: 16 rows times 256 columns.  codes: the tile's rows of a box; x: the half's four boxes; left: columns of the
-// half that exist.
-template <typename T, int NT, int G>
+// half that exist (TAIL: not all).
+template <typename T, int NT, int G, bool TAIL>
 __device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *x, const Place &at, const Scales<G> &sz, int left,
                                            int lane, float (&acc)[NT][4]) {
     constexpr int GROUPS = 128 / G, TURNS = 4 / GROUPS;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-        if (part * 128 >= left) break;
+        if (TAIL && part * 128 >= left) break;
         uint32_t wg[4], wh[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -154,8 +151,6 @@ __device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *
             const Zero4<T> zg = Zero4<T>::of(sg >> 16), zh = Zero4<T>::of(sh >> 16);
             float d[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-#pragma unroll
             for (int i = j * TURNS; i < (j + 1) * TURNS; ++i) {
                 uint32_t pg[4], ph[4];
                 zg.decode(wg[i], pg);
@@ -165,9 +160,10 @@ __device__ __forceinline__ void half_stage(const uint8_t *codes, const uint8_t *
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     uint4 v = *reinterpret_cast<const uint4 *>(x + box * (NT * 1024) + n * 1024 + at.column<G>(i));
-                    if (box * 64 >= left) v = make_uint4(0, 0, 0, 0);  // a box that was not loaded
-                    mma<T>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
-                    mma<T>(d[n], a1, prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+                    if (TAIL && box * 64 >= left) v = make_uint4(0, 0, 0, 0);  // a box that was not loaded
+                    if (i == j * TURNS) mma<T, true>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
+                    else mma<T, false>(d[n], a0, prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632));
+                    mma<T, false>(d[n], a1, prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
                 }
             }
             const float fg = Code4<T>::f32((uint16_t)sg), fh = Code4<T>::f32((uint16_t)sh);
@@ -227,7 +223,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR), *empty = full + DEPTH;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + DEPTH);
     __shared__ int16_t listed[MAX_EXPERTS];  // the experts that have slots
-    __shared__ int listed_n;
+    __shared__ int listed_n, first[MAX_EXPERTS], count[MAX_EXPERTS];  // and their slots
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
     const int cid = blockIdx.x / cluster, clusters = gridDim.x / cluster;
@@ -254,9 +250,14 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         if (warp == 0) {
             int n = 0;
             for (int e0 = 0; e0 < a.experts; e0 += 32) {
-                const bool some = e0 + lane < a.experts && slots_of(a, e0 + lane, &err).count > 0;
+                const Slots s = e0 + lane < a.experts ? slots_of(a, e0 + lane, &err) : Slots{0, 0};
+                const bool some = s.count > 0;
                 const uint32_t m = __ballot_sync(~0u, some);
-                if (some) listed[n + __popc(m & ((1u << lane) - 1u))] = (int16_t)(e0 + lane);
+                if (some) {
+                    const int at = n + __popc(m & ((1u << lane) - 1u));
+                    listed[at] = (int16_t)(e0 + lane);
+                    first[at] = s.first, count[at] = s.count;
+                }
                 n += __popc(m);
             }
             if (lane == 0) listed_n = n;
@@ -269,10 +270,8 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         c.t0 = 0, c.s = s0;
         if (c.unit >= units) return;
         const int at = a.offsets ? c.unit / tiles : 0;
-        c.e = a.offsets ? listed[at] : 0;
         c.r0 = (c.unit - at * tiles) * ROWS;
-        const Slots s = slots_of(a, c.e, &err);
-        c.first = s.first, c.count = s.count;
+        c.e = a.offsets ? listed[at] : 0, c.first = a.offsets ? first[at] : 0, c.count = a.offsets ? count[at] : (int)a.slots;
     };
     const auto next_chunk = [&](Cursor &c) {
         c.s = s0, c.t0 += TOKENS;
@@ -442,8 +441,10 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                     }
                     __syncwarp();
                     const uint8_t *st = smem + b * P::STAGE;
-                    half_stage<T, NT, G>(st + half * (CODES / 2) + tile * (TILE * 128), st + CODES + half * (4 * NT * 1024), place, now,
-                                         a.cols - s * BK - half * HALF, lane, acc);
+                    const uint8_t *w = st + half * (CODES / 2) + tile * (TILE * 128), *x = st + CODES + half * (4 * NT * 1024);
+                    const int left = a.cols - s * BK - half * HALF;
+                    if (left >= HALF) half_stage<T, NT, G, false>(w, x, place, now, left, lane, acc);
+                    else half_stage<T, NT, G, true>(w, x, place, now, left, lane, acc);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[b]);
                     if (++b == DEPTH) b = 0, ++use;
