@@ -21,6 +21,7 @@
 // Persistent: the units of work -- a chunk of an expert's slots times a tile of rows of W -- are dealt to the CTAs in
 // turn, tiles of rows first, so that X is read once and the codes, 4 bits a weight, come from L2.  The slots of an expert
 // are cut into chunks of one size; the longest chunk is the largest of 256, 128 and 64 that leaves no SM without work.
+// Where one matrix gives few units, K is cut over the CTAs of a cluster, whose sums are added in order through shared memory.
 #include "packed4.cuh"
 #include "smem_limit.h"
 #include "tcgen05.cuh"
@@ -209,13 +210,13 @@ __device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float 
 template <typename T, int CG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                         const __grid_constant__ Packed4MmArgs a) {
+                         const __grid_constant__ Packed4MmArgs a, const int ksplit, const int longest) {
     using P = Plan<CG>;
     constexpr int STAGES = P::STAGES, CRING = P::CRING;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_aligned<1024>(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR);  // X has arrived (this CTA's)
-    uint64_t *ready = full + STAGES;   // numbers and X are there (the leader's)
+    uint64_t *ready = full + STAGES;   // the numbers are there, and the other CTA's X (the leader's)
     uint64_t *empty = ready + STAGES;  // the stage's MMAs are done (every CTA's)
     uint64_t *cfull = empty + STAGES;  // codes have arrived (this CTA's)
     uint64_t *cempty = cfull + CRING;  // they have been read (this CTA's)
@@ -227,8 +228,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int *pre = reinterpret_cast<int *>(smem + P::PRE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
-    const int cid = blockIdx.x / CG, ncl = gridDim.x / CG;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u, part = CG == 1 && ksplit > 1 ? cluster_ctarank() : 0u;
+    const int cid = blockIdx.x / (CG * ksplit), ncl = gridDim.x / (CG * ksplit);
+    // this CTA's part of K, in whole boxes of codes: stages st0 .. st0 + stages - 1
+    const int boxes = (a.cols + 2 * BK - 1) / (2 * BK), st0 = 2 * (boxes * (int)part / ksplit);
+    const int stages = min((a.cols + BK - 1) / BK, 2 * (boxes * ((int)part + 1) / ksplit)) - st0;
 
     if (warp == WARP_MMA) {
         if constexpr (CG == 2) {
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], a.order ? 2 : 1);
-            mbar_init(&ready[s], DEC_WARPS / 2 * CG);
+            mbar_init(&ready[s], DEC_WARPS / 2 * CG + CG - 1);  // of a pair the other CTA tells that its X is there
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < CRING; ++s) {
@@ -282,8 +286,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) sums[k][warp] = all;
         }
         __syncthreads();
-        int k = 0;
-        for (; k < 2; ++k) {
+        int k = ksplit == 1 || longest == 256 ? 0 : longest == 128 ? 1 : 2;
+        for (; ksplit == 1 && k < 2; ++k) {
             int64_t all = 0;
             for (int w = 0; w < NTHREADS / 32; ++w) all += sums[k][w];
             if (all * wk.tiles >= ncl) break;
@@ -311,7 +315,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sh->tmem;
-    const int stages = (a.cols + BK - 1) / BK;
 
     const auto late_wait = [&] {
         if (early) {
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (elected()) {
                         mbar_arrive_expect_tx(&full[b], (uint32_t)boxes * BOX * 128u);
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &full[b], s * BK, t.first + from + i * BOX);
+                            tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &full[b], (st0 + s) * BK, t.first + from + i * BOX);
                     }
                     __syncwarp();
                     if (++b == STAGES) b = 0, ++use;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 4
                         for (int i = 0; i < n; i += 4) {
                             const int4 r = *reinterpret_cast<const int4 *>(rows + i);
-                            tma_gather4(dst + i * 128, &tmX, &full[b], s * BK, r.x, r.y, r.z, r.w);
+                            tma_gather4(dst + i * 128, &tmX, &full[b], (st0 + s) * BK, r.x, r.y, r.z, r.w);
                         }
                     }
                     __syncwarp();
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             break;
                         }
                         mbar_arrive_expect_tx(&cfull[b], CBOX);
-                        tma_load_3d(smem + P::CODES + b * CBOX, &tmW, &cfull[b], s * (BK / 2), t.r0 + (int)rank * BM, t.e);
+                        tma_load_3d(smem + P::CODES + b * CBOX, &tmW, &cfull[b], (st0 + s) * (BK / 2), t.r0 + (int)rank * BM, t.e);
                         if (++b == CRING) b = 0, ++use;
                     }
                 }
@@ -455,6 +458,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         // stage's, of 32 two in a stage
                         const bool first = a.group <= BK || (s & 1) == 0;
                         if (first) begin();
+                        wait(&full[b], use & 1, kDevErrWaitFull);
                         wait(&ready[b], use & 1, kDevErrWaitFull);
                         if (stop) break;
                         const uint32_t at = smem_u32(smem + b * P::STAGE);
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         uint32_t d = tmem + (uint32_t)((gi & 1) * BN);
                         mma<CG>(d, da, db, idesc, !first);
                         mma<CG>(d, da + 2, db + 2, idesc, 1);
-                        const bool halves = a.group == 32 && s * BK + 32 < a.cols;
+                        const bool halves = a.group == 32 && (st0 + s) * BK + 32 < a.cols;
                         if (halves) {
                             end();
                             begin();
@@ -480,6 +484,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 // every MMA issued must be complete before the tensor memory is freed
                 commit<CG>(last);
                 if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
+            }
+            __syncwarp();
+        } else if (warp == WARP_MMA) {
+            // the pair's other CTA: the leader's MMAs read its X too
+            late_wait();
+            if (elected()) {
+                int b = 0;
+                uint32_t use = 0;
+                bool stop = false;
+                for (int u = cid; u < wk.units && !stop; u += ncl)
+                    for (int s = 0; s < stages; ++s) {
+                        if (*abort_flag || !mbar_wait_sleep(&full[b], use & 1)) {
+                            if (!*abort_flag) fail<CG>(abort_flag, kDevErrWaitFull);
+                            stop = true;
+                            break;
+                        }
+                        arrive_leader<CG>(&ready[b]);
+                        if (++b == STAGES) b = 0, ++use;
+                    }
             }
             __syncwarp();
         } else {
@@ -508,7 +531,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             const auto zeros_at = [&](int s) {  // low half: of the stage's first 32 columns, high half: of the others
                 if (!zeros || s >= stages) return 0x00080008u;
-                const int j = (s * BK) >> shift;
+                const int j = ((st0 + s) * BK) >> shift;
                 const uint32_t z = __ldg(zeros + j) & 15u;
                 return z | (a.group == 32 ? __ldg(zeros + min(j + 1, a.groups - 1)) & 15u : z) << 16;
             };
@@ -524,8 +547,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     stop = true;
                     break;
                 }
+                const uint4 v = *reinterpret_cast<const uint4 *>(box + cb * CBOX + lo), w = *reinterpret_cast<const uint4 *>(box + cb * CBOX + hi);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cempty[cb]);
                 if (!box_only) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(box + cb * CBOX + lo), w = *reinterpret_cast<const uint4 *>(box + cb * CBOX + hi);
                     if (use > 0 && !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
                         fail<CG>(abort_flag, kDevErrWaitEmpty);
                         stop = true;
@@ -534,17 +559,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     store_codes<T>(row + b * P::STAGE, r, 0, v, z & 0xFFFFu);
                     store_codes<T>(row + b * P::STAGE, r, 4, w, z >> 16);
                     fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&cempty[cb]);
-                    if (!box_only) {
-                        // the stage is ready when X is there too: one warp of each CTA waits for it
-                        if (warp == WARP_DEC0 + 4 * odd) {
-                            if (!mbar_wait(&full[b], use & 1)) fail<CG>(abort_flag, kDevErrWaitFull);
-                        }
-                        arrive_leader<CG>(&ready[b]);
-                    }
+                    __syncwarp();
+                    if (lane == 0) arrive_leader<CG>(&ready[b]);
                 }
                 if (!box_only) next_stage(), next_stage();
                 if (++cb == CRING) cb = 0, ++cuse;
@@ -571,13 +587,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Unit t = {0, 0, 0, 0, 0};
         const uint16_t *sc = nullptr;
         uint16_t next[SC];
+        const int gfirst = st0 * BK / a.group, glast = (min(a.cols, (st0 + stages) * BK) + a.group - 1) / a.group;
         const auto enter = [&](int u) {  // the unit's first scales
             if (u >= wk.units) return;
             t = unit_at<CG>(a, wk, u, &err);
             sc = static_cast<const uint16_t *>(a.scales) + t.e * a.scales_expert +
                  min(t.r0 + (int)rank * BM + 32 * quarter + lane, a.rows - 1) * a.scales_row;
 #pragma unroll
-            for (int i = 0; i < SC; ++i) next[i] = i < a.groups ? __ldg(sc + i) : 0;
+            for (int i = 0; i < SC; ++i) next[i] = gfirst + i < glast ? __ldg(sc + gfirst + i) : 0;
         };
         enter(cid);
         for (int u = cid; u < wk.units; u += ncl) {
@@ -585,16 +602,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            for (int g0 = 0; g0 < a.groups && !stop; g0 += SC) {
+            for (int g0 = gfirst; g0 < glast && !stop; g0 += SC) {
                 float now[SC];
 #pragma unroll
                 for (int i = 0; i < SC; ++i) {
                     now[i] = Code4<T>::f32(next[i]);
-                    next[i] = g0 + SC + i < a.groups ? __ldg(sc + g0 + SC + i) : 0;
+                    next[i] = g0 + SC + i < glast ? __ldg(sc + g0 + SC + i) : 0;
                 }
 #pragma unroll 1
                 for (int i = 0; i < SC; ++i, ++gi) {
-                    if (g0 + i >= a.groups) break;
+                    if (g0 + i >= glast) break;
                     const float f = i == 0 ? now[0] : i == 1 ? now[1] : i == 2 ? now[2] : now[3];
                     if (*abort_flag) { stop = true; break; }
                     if (!mbar_wait_sleep(&accf[gi & 1], (uint32_t)(gi / 2) & 1)) {
@@ -622,6 +639,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (lane == 0) arrive_leader<CG>(&acce[gi & 1]);
                 }
             }
+            if (CG == 1 && ksplit > 1) {
+                // The cluster's CTAs have a part of K each, of this one unit.  Every MMA and copy of the CTA has ended: its ring
+                // takes the partial sums, [slot][128 rows], and the CTAs add up a share of the slots each, in order.
+                float *sums = reinterpret_cast<float *>(smem);
+                const int row = 32 * quarter + lane;
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j < cols) sums[(c0 + j) * BM + row] = acc[j];
+                cluster_sync();
+                const int share = (t.n + ksplit - 1) / ksplit, n0 = (int)part * share, n1 = min(t.n, n0 + share);
+                const int quad = lane * 4;
+                for (int n = n0 + warp - WARP_EPI0; n < n1; n += EPI_WARPS) {
+                    const uint32_t from = smem_u32(sums + n * BM + quad);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), p[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < ksplit) p[k] = ld_cluster_v4(cluster_map(from, k));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < ksplit) v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
+                    if (t.r0 + quad < a.rows) store4<T>(a, t.first + n, t.r0 + quad, v, vec);
+                }
+                cluster_sync();  // nobody leaves before its sums have been read
+                break;
+            }
             if (stop) break;
             const Unit done = t;
             enter(u + ncl);  // its scales come while this one is stored
@@ -647,6 +689,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         }
     }
+    if (CG == 1 && ksplit > 1 && warp < WARP_EPI0) {  // the epilogue's two barriers count every thread
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+    }
     if (err) atomicExch(&g_packed4_tiles_err, err);
     __syncwarp();
     tc_fence_before_sync();
@@ -669,12 +716,19 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     e = packed4_tmap_x(&tx, a, a.order ? 1 : BOX);
     if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK, BM, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
-    // no more CTAs than units of the shortest chunks
     const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG);
-    const int64_t most = ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
+    // One matrix that gives few units: K is cut over a cluster first (codes are then made numbers once), to at least one and a
+    // half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
+    const auto units_of = [&](int64_t longest) { return (a.slots + longest - 1) / longest * tiles; };
+    const int boxes = (a.cols + 2 * BK - 1) / (2 * BK);
+    int ksplit = 1, longest = BN;
+    while (CG == 1 && !a.offsets && ksplit < 8 && units_of(BN) * ksplit * 2 <= sms && ksplit * 3 <= boxes) ksplit *= 2;
+    while (ksplit > 1 && longest > 64 && units_of(longest / 2) * ksplit <= sms) longest /= 2;
+    // no more CTAs than units of the shortest chunks
+    const int64_t most = ksplit > 1 ? units_of(longest) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
     const int64_t clusters = most < sms / CG ? most : sms / CG;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(clusters * CG));
+    lc.gridDim = dim3((unsigned)(clusters * CG * ksplit));
     lc.blockDim = dim3(NTHREADS);
     lc.dynamicSmemBytes = P::TOTAL;
     lc.stream = s;
@@ -682,10 +736,10 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = (unsigned)(CG * ksplit), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
-    lc.numAttrs = CG == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tx, tw, a);
+    lc.numAttrs = CG * ksplit > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tx, tw, a, ksplit, longest);
 }
 
 }  // namespace

@@ -94,6 +94,32 @@ __device__ __forceinline__ void store_y(const Packed4MmArgs &a, int64_t slot, in
     else static_cast<uint16_t *>(a.Y)[i] = Code4<__half>::round(v);
 }
 
+// Columns r .. r + 3 of Y (rows of W) for a slot; vec: four of them are 16 (8) aligned bytes
+template <typename T>
+__device__ __forceinline__ void store4(const Packed4MmArgs &a, int64_t slot, int r, const float4 &v, bool vec) {
+    const int64_t row = slot * a.y_stride;
+    if (a.swiglu) {
+        const float p = silu(v.x) * v.y, q = silu(v.z) * v.w;
+        if (vec && r + 3 < a.rows) {
+            if (a.y_dtype == 2) *reinterpret_cast<float2 *>(static_cast<float *>(a.Y) + row + (r >> 1)) = make_float2(p, q);
+            else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.Y) + row + (r >> 1)) = Code4<T>::round(p) | (uint32_t)Code4<T>::round(q) << 16;
+        } else {
+            if (r < a.rows) store_y(a, slot, r >> 1, p);
+            if (r + 2 < a.rows) store_y(a, slot, (r >> 1) + 1, q);
+        }
+    } else if (vec && r + 3 < a.rows) {
+        if (a.y_dtype == 2) *reinterpret_cast<float4 *>(static_cast<float *>(a.Y) + row + r) = v;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.Y) + row + r) =
+                make_uint2(Code4<T>::round(v.x) | (uint32_t)Code4<T>::round(v.y) << 16, Code4<T>::round(v.z) | (uint32_t)Code4<T>::round(v.w) << 16);
+    } else {
+        if (r < a.rows) store_y(a, slot, r, v.x);
+        if (r + 1 < a.rows) store_y(a, slot, r + 1, v.y);
+        if (r + 2 < a.rows) store_y(a, slot, r + 2, v.z);
+        if (r + 3 < a.rows) store_y(a, slot, r + 3, v.w);
+    }
+}
+
 // True in one thread of the warp.  The compiler knows that of elect.sync, and puts the operands of TMA copies and MMAs behind
 // it straight into uniform registers: four MMAs and a commit are issued in 160 clocks, behind a test of the lane in 700; a
 // gather of four rows in a third of the 70 clocks that a lane for each takes.
