@@ -37,17 +37,27 @@ struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
 
+// Rows of Y are read once
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load(const T *p) {
+    if constexpr (sizeof(T) * N == 16) {
+        const uint4 v = ld_stream_v4(p);
+        return *reinterpret_cast<const Pack<T, N> *>(&v);
+    } else {
+        return *reinterpret_cast<const Pack<T, N> *>(p);
+    }
+}
+
 constexpr int THREADS = 256, AHEAD = 8;
 
-// N columns to a thread (1 where strides or pointers do not allow vectors)
+// A block per token and THREADS N columns of it (1 where strides or pointers do not allow vectors)
 template <typename TY, typename TO, int N>
 __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t vecs = a.cols / N, n = a.tokens * vecs;
     unsigned int err = 0;
-    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
-        const int64_t t = i / vecs, c = (i - t * vecs) * N;
+    const int64_t t = blockIdx.x;
+    for (int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * N; c < a.cols; c += (int64_t)gridDim.y * blockDim.x * N) {
         float sum[N];
         if (a.residual) {
             const Pack<TO, N> r = *reinterpret_cast<const Pack<TO, N> *>(static_cast<const TO *>(a.residual) + t * a.r_stride + c);
@@ -70,7 +80,7 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant_
                 else have[j] = slot >= 0;
                 if (!have[j]) continue;
                 w[j] = __ldg(a.weights + t * a.top_k + j0 + j);
-                y[j] = *reinterpret_cast<const Pack<TY, N> *>(static_cast<const TY *>(a.Y) + slot * a.y_stride + c);
+                y[j] = load<TY, N>(static_cast<const TY *>(a.Y) + slot * a.y_stride + c);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j)
@@ -95,10 +105,11 @@ cudaError_t launch(const CombineArgs &a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(TY);
     const bool vec = a.cols % N == 0 && fits(a.Y, a.y_stride, sizeof(TY), N) && fits(a.out, a.out_stride, sizeof(TO), N) &&
                      (!a.residual || fits(a.residual, a.r_stride, sizeof(TO), N));
-    const int64_t work = a.tokens * (a.cols / (vec ? N : 1)), blocks = (work + THREADS - 1) / THREADS;
-    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
-    if (vec) return launch_pdl(combine_kernel<TY, TO, N>, grid, THREADS, 0, s, a);
-    return launch_pdl(combine_kernel<TY, TO, 1>, grid, THREADS, 0, s, a);
+    const int64_t vecs = a.cols / (vec ? N : 1), blocks = (vecs + THREADS - 1) / THREADS;
+    const int threads = vecs < THREADS ? (int)(vecs + 31) / 32 * 32 : THREADS;
+    const dim3 grid((unsigned)a.tokens, (unsigned)(blocks < 65535 ? blocks : 65535));
+    if (vec) return launch_pdl(combine_kernel<TY, TO, N>, grid, threads, 0, s, a);
+    return launch_pdl(combine_kernel<TY, TO, 1>, grid, threads, 0, s, a);
 }
 
 template <typename TY>

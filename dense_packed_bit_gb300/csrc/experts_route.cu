@@ -27,9 +27,9 @@ constexpr int BLOCKS = 128;       // blocks of tokens otherwise, at most (more o
 constexpr int MAX_PER = 1 << 15;  // tokens of a block
 constexpr int COUNTS = 8192;      // shared counts: [warps][experts]
 
-__device__ __forceinline__ float logit(const float *p) { return __ldg(p); }
-__device__ __forceinline__ float logit(const __half *p) { return __half2float(__ldg(p)); }
-__device__ __forceinline__ float logit(const __nv_bfloat16 *p) { return __bfloat162float(__ldg(p)); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // Orders like x (both zeros alike); 0 for NaN and -infinity, which are never picked.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -45,13 +45,24 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A token's logits, those of experts lane, lane + 32, ... to a lane
+template <typename T, int PER>
+struct Logits {
+    T v[PER];
+    __device__ __forceinline__ void load(const RouteArgs &a, int64_t t, int lane) {
+        const T *x = static_cast<const T *>(a.logits) + t * a.stride + lane;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 32 * i < a.experts) v[i] = __ldg(x + 32 * i);
+    }
+};
+
 // The picks of token t: lane j < top_k returns expert j (or -1) and its weight is written.
 template <typename T, int PER>
-__device__ __forceinline__ int pick(const RouteArgs &a, int64_t t, int lane) {
-    const T *x = static_cast<const T *>(a.logits) + t * a.stride;
+__device__ __forceinline__ int pick(const RouteArgs &a, int64_t t, const Logits<T, PER> &x, int lane) {
     uint32_t key[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < a.experts ? key_of(logit(x + lane + 32 * i)) : 0;
+    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < a.experts ? key_of(widen(x.v[i])) : 0;
     float sum = 0.f;  // of the softmax over all experts
     uint32_t first = 0;
     int id = -1;
@@ -183,8 +194,12 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_pick_kernel(const 
     for (int i = threadIdx.x; i < warps * a.experts; i += blockDim.x) counts[i] = 0;
     __syncthreads();
     if (warp < warps) {
+        Logits<T, PER> x, next;
+        if (s.begin < s.end) x.load(a, s.begin, lane);
         for (int64_t t = s.begin; t < s.end; ++t) {
-            const int id = pick<T, PER>(a, t, lane);
+            if (t + 1 < s.end) next.load(a, t + 1, lane);
+            const int id = pick<T, PER>(a, t, x, lane);
+            x = next;
             if (id >= 0) ++counts[warp * a.experts + id];
             __syncwarp();
         }
@@ -216,18 +231,21 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_place_kernel(const
     for (int i = threadIdx.x; i < warps * a.experts; i += blockDim.x) counts[i] = 0;
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) total[e] = base[e] = 0;
     __syncthreads();
-    // the blocks' counts, a warp to a block at a time
-    for (int b = warp; b < (int)gridDim.x; b += blockDim.x >> 5) {
-        int n[PER];
+    // The blocks' counts: a thread to an expert and a stretch of the blocks, eight loads on their way; whole numbers, whose
+    // sums any order of the additions gives.
+    const int wide = (a.experts + 31) & ~31, teams = max(1, (int)blockDim.x / wide), team = threadIdx.x / wide;
+    for (int e = threadIdx.x - team * wide; team < teams && e < a.experts; e += blockDim.x) {
+        const int each = ((int)gridDim.x + teams - 1) / teams, b0 = team * each, b1 = min(b0 + each, (int)gridDim.x);
+        int all = 0, before = 0;
+        for (int b = b0; b < b1; b += 8) {
+            int n[8];
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            n[i] = lane + 32 * i < a.experts ? __ldg(a.counts + (int64_t)b * a.experts + lane + 32 * i) : 0;
+            for (int i = 0; i < 8; ++i) n[i] = b + i < b1 ? __ldg(a.counts + (int64_t)(b + i) * a.experts + e) : 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (n[i] == 0) continue;
-            atomicAdd(&total[lane + 32 * i], n[i]);  // whole numbers: any order gives the same
-            if (b < (int)blockIdx.x) atomicAdd(&base[lane + 32 * i], n[i]);
+            for (int i = 0; i < 8; ++i) all += n[i], before += b + i < (int)blockIdx.x ? n[i] : 0;
         }
+        atomicAdd(&total[e], all);
+        atomicAdd(&base[e], before);
     }
     if (warp < warps) {
         for (int64_t t = s.begin; t < s.end; ++t) {

@@ -43,9 +43,9 @@ constexpr int DEC_WARPS = 8, EPI_WARPS = 8;
 constexpr int MAX_EXPERTS = 1024;
 constexpr int BOX = 64;        // rows of X per TMA box
 
-// Registers of a thread once the roles part, of the 96 at launch: 384 x 48 + 256 x 168 = 640 x 96.
-#define MM_PACKED4_REGS_FEW "48"
-#define MM_PACKED4_REGS_EPI "168"
+// Registers of a thread once the roles part, of the 96 at launch: 384 x 40 + 256 x 176 <= 640 x 96.
+#define MM_PACKED4_REGS_FEW "40"
+#define MM_PACKED4_REGS_EPI "176"
 
 template <int CG>
 struct Plan {
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         late_wait();
         const int quarter = warp & 3, half = (warp - WARP_EPI0) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        constexpr int SC = 4;  // scales on their way
+        constexpr int SC = 2;  // scales on their way
         int gi = 0;
         bool stop = false;
         const int size = a.y_dtype == 2 ? 4 : 2;
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
                 for (int i = 0; i < SC; ++i, ++gi) {
                     if (g0 + i >= glast) break;
-                    const float f = i == 0 ? now[0] : i == 1 ? now[1] : i == 2 ? now[2] : now[3];
+                    const float f = i == 0 ? now[0] : now[1];
                     if (*abort_flag) { stop = true; break; }
                     if (!mbar_wait_sleep(&accf[gi & 1], (uint32_t)(gi / 2) & 1)) {
                         fail<CG>(abort_flag, kDevErrWaitMma);
