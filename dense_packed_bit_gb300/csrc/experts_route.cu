@@ -25,7 +25,7 @@ namespace {
 constexpr int ONE = 128;          // tokens that one CTA takes
 constexpr int BLOCKS = 128;       // blocks of tokens otherwise, at most (more only above 2^22 tokens)
 constexpr int MAX_PER = 1 << 15;  // tokens of a block
-constexpr int COUNTS = 8192;      // shared counts: [warps][experts]
+constexpr int COUNTS = 8448;      // shared counts: [warps][experts], rows an odd number of words apart
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
@@ -120,6 +120,8 @@ __device__ __forceinline__ Share share_of(int64_t tokens, int64_t per, int b, in
     return {t0 + begin, t0 + end};
 }
 
+__device__ __forceinline__ int row_of(int experts) { return experts | 1; }
+
 // From each expert's count over all blocks, and over the blocks before this one, to the first place of its picks in this
 // block: base[e].  Whole block; scratch [33].
 __device__ __forceinline__ void scan_experts(int *total, int *base, int experts, int32_t *offsets, int *scratch) {
@@ -136,7 +138,8 @@ __device__ __forceinline__ void scan_experts(int *total, int *base, int experts,
         if (lane == 31) scratch[warp] = run;
         __syncthreads();
         int before = carry, all = 0;
-        for (int w = 0; w < warps; ++w) {
+        const int used = min(warps, (experts - e0 + 31) / 32);
+        for (int w = 0; w < used; ++w) {
             const int v = scratch[w];
             if (w < warp) before += v;
             all += v;
@@ -151,20 +154,23 @@ __device__ __forceinline__ void scan_experts(int *total, int *base, int experts,
     if (offsets && threadIdx.x == 0) offsets[experts] = carry;
 }
 
-// Places: counts[warp][e] become the warps' first places from base[e], then every warp walks its tokens.
+// Places: counts[warp][e] become the warps' first places from base[e] (a warp to an expert, a lane to a warp's count), then
+// every warp walks its tokens.
 __device__ __forceinline__ void place(const RouteArgs &a, const Share &s, int *counts, const int *base, int warps) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = a.top_k;
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-        int at = base[e];
-        for (int w = 0; w < warps; ++w) {
-            const int n = counts[w * a.experts + e];
-            counts[w * a.experts + e] = at;
-            at += n;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = a.top_k, row = row_of(a.experts);
+    for (int e = warp; e < a.experts; e += blockDim.x >> 5) {
+        const int n = lane < warps ? counts[lane * row + e] : 0;
+        int run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(~0u, run, o);
+            if (lane >= o) run += up;
         }
+        if (lane < warps) counts[lane * row + e] = base[e] + run - n;
     }
     __syncthreads();
     if (warp >= warps) return;
-    int *next = counts + warp * a.experts;
+    int *next = counts + warp * row;
     int id = s.begin < s.end && lane < k ? a.ids[s.begin * k + lane] : -1;
     for (int64_t t = s.begin; t < s.end; ++t) {
         const int after = t + 1 < s.end && lane < k ? a.ids[(t + 1) * k + lane] : -1;
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_pick_kernel(const 
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Share s = share_of(a.tokens, per, blockIdx.x, warp, warps);
-    for (int i = threadIdx.x; i < warps * a.experts; i += blockDim.x) counts[i] = 0;
+    for (int i = threadIdx.x; i < warps * row_of(a.experts); i += blockDim.x) counts[i] = 0;
     __syncthreads();
     if (warp < warps) {
         Logits<T, PER> x, next;
@@ -200,16 +206,17 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_pick_kernel(const 
             if (t + 1 < s.end) next.load(a, t + 1, lane);
             const int id = pick<T, PER>(a, t, x, lane);
             x = next;
-            if (id >= 0) ++counts[warp * a.experts + id];
+            if (id >= 0) ++counts[warp * row_of(a.experts) + id];
             __syncwarp();
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-        int n = 0;
-        for (int w = 0; w < warps; ++w) n += counts[w * a.experts + e];
-        if (gridDim.x > 1) a.counts[(int64_t)blockIdx.x * a.experts + e] = n;
-        total[e] = n;
+    for (int e = warp; e < a.experts; e += blockDim.x >> 5) {
+        const int n = __reduce_add_sync(~0u, lane < warps ? counts[lane * row_of(a.experts) + e] : 0);
+        if (lane == 0) {
+            if (gridDim.x > 1) a.counts[(int64_t)blockIdx.x * a.experts + e] = n;
+            total[e] = n;
+        }
     }
     if (gridDim.x > 1) return;
     __shared__ int base[32 * PER];
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_place_kernel(const
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Share s = share_of(a.tokens, per, blockIdx.x, warp, warps);
-    for (int i = threadIdx.x; i < warps * a.experts; i += blockDim.x) counts[i] = 0;
+    for (int i = threadIdx.x; i < warps * row_of(a.experts); i += blockDim.x) counts[i] = 0;
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) total[e] = base[e] = 0;
     __syncthreads();
     // The blocks' counts: a thread to an expert and a stretch of the blocks, eight loads on their way; whole numbers, whose
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(PER > 8 ? 512 : 1024) route_place_kernel(const
     if (warp < warps) {
         for (int64_t t = s.begin; t < s.end; ++t) {
             const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-            if (id >= 0) ++counts[warp * a.experts + id];
+            if (id >= 0) ++counts[warp * row_of(a.experts) + id];
             __syncwarp();
         }
     }
@@ -275,7 +282,7 @@ Split split_of(int64_t tokens) {
 template <typename T, int PER>
 cudaError_t launch(const RouteArgs &a, cudaStream_t s) {
     const Split p = split_of(a.tokens);
-    int64_t warps = COUNTS / a.experts, most = PER > 8 ? 16 : 32;
+    int64_t warps = COUNTS / (a.experts | 1), most = PER > 8 ? 16 : 32;
     if (warps > most) warps = most;
     if (warps > p.per) warps = p.per;
     // the scan takes an expert to a thread, so a CTA is not less than four warps

@@ -2,10 +2,11 @@
 packed products for the projections, a paged cache of keys and values, attention over it, drafted tokens verified as a
 tree, and the sampler.
 
-    python -m dense_packed_bit_gb300.generate [--answers N] [--tokens N] [--depth N] [--temperature T] [--window W]
+    python -m dense_packed_bit_gb300.generate [--answers N] [--tokens N] [--depth N] [--temperature T] [--window W] [--experts N]
 
 The model is GPT-2's block (pre-norm, learned positions, GELU) with grouped key and value heads and random weights: there
-is no checkpoint here, so the text means nothing, but every step runs as it would with one.  A batch of prompts is
+is no checkpoint here, so the text means nothing, but every step runs as it would with one.  With --experts the feed-forward
+layer is a mixture of that many experts with 4-bit weights, two of them to a token.  A batch of prompts is
 processed in one call per layer, each is forked into several answers that share its full pages, and each round then
 verifies a tree of drafted tokens per answer: by default what follows earlier occurrences of the last token in the
 answer's own history.  The sampler gets the same uniform number at a position whatever was drafted, so drafts change how
@@ -35,6 +36,9 @@ class Shape:
     dim: int = 64
     hidden: int = 1024
     positions: int = 2048
+    experts: int = 0       # 0: a ternary feed-forward layer
+    expert_hidden: int = 256
+    top_k: int = 2
 
     @property
     def width(self):
@@ -57,6 +61,42 @@ class Packed:
         return y
 
 
+class Experts:
+    """A mixture of experts: a router in fp32, and per expert a gate, an up- and a down-projection in 4 bits with a scale per
+    64 weights of a row.  Called with x [tokens][width] fp32 and its norm h (fp16): x plus the layer."""
+
+    def __init__(self, seed, shape, device):
+        e, d, n = shape.experts, shape.width, shape.expert_hidden
+        self.shape = shape
+        self.router = torch.from_numpy(synth.normal_f32(seed, (e, d), 1.0 / math.sqrt(d))).to(device)
+        self.up = self.matrices(seed + 1, e, 2 * n, d, device)  # rows 2 i and 2 i + 1: gate and up-projection of hidden unit i
+        self.down = self.matrices(seed + 3, e, d, n, device)
+
+    @staticmethod
+    def matrices(seed, experts, rows, cols, device, group=64):
+        codes = synth.random_bytes(seed, experts * rows * cols // 2).reshape(experts, rows, cols // 2)
+        size = 1.0 / (4.6 * math.sqrt(cols))  # codes less 8 are of about 4.6
+        scales = synth.uniform_f16_bits(seed + 1, (experts, rows, -(-cols // group)), 0.9 * size, 1.1 * size)
+        return mm.mm_packed4(torch.from_numpy(codes).to(device), torch.from_numpy(scales).to(device).view(torch.float16), None, cols, group)
+
+    def __call__(self, x, h):
+        s, t, dev = self.shape, x.shape[0], x.device
+        e, k, d, n = s.experts, s.top_k, s.width, t * s.top_k
+        new = lambda *shape, dtype=torch.int32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
+        logits, weights = new(t, e, dtype=torch.float32), new(t, k, dtype=torch.float32)
+        ids, offsets, order, slots = new(t, k), new(e + 1), new(n), new(t, k)
+        workspace = new(mm.mm_experts_route_workspace(t, e, k), dtype=torch.uint8)
+        mm.mm_gemm_f32(0, 1, t, e, d, h.float(), d, self.router, d, logits, e)
+        mm.mm_experts_route(logits, t, e, e, k, mm.MM_ROUTE_SOFTMAX, True, 1.0, ids, weights, offsets, order, slots, workspace,
+                            workspace.numel())
+        hidden, y = new(n, s.expert_hidden, dtype=torch.float16), new(n, d, dtype=torch.float32)
+        mm.mm_experts_gemm_packed4(self.up, h, d, t, order, k, offsets, n, mm.MM_ACT_SWIGLU, hidden, s.expert_hidden)
+        mm.mm_experts_gemm_packed4(self.down, hidden, s.expert_hidden, n, None, 1, offsets, n, mm.MM_ACT_NONE, y, d)
+        out = torch.empty_like(x)
+        mm.mm_experts_combine(y, d, n, slots, weights, t, k, d, x, d, out, d)
+        return out
+
+
 class Model:
     def __init__(self, shape, seed=7, device="cuda"):
         self.shape, self.device = shape, device
@@ -67,18 +107,26 @@ class Model:
         self.blocks = []
         for i in range(shape.layers):
             s = seed + 10 * (i + 1)
-            self.blocks.append([Packed(s, d + 2 * kv, d, device), Packed(s + 2, d, d, device),
-                                Packed(s + 4, shape.hidden, d, device), Packed(s + 6, d, shape.hidden, device)])
+            attention = [Packed(s, d + 2 * kv, d, device), Packed(s + 2, d, d, device)]
+            if shape.experts:
+                self.blocks.append(attention + [Experts(s + 4, shape, device)])
+            else:
+                self.blocks.append(attention + [Packed(s + 4, shape.hidden, d, device), Packed(s + 6, d, shape.hidden, device)])
 
     def forward(self, tokens, places, attend):
         """Logits [tokens][vocab] fp32.  attend(layer, q, k, v): appends k, v and returns the attention of q."""
         s = self.shape
         d, kv = s.width, s.kv_heads * s.dim
         x = self.tokens[tokens] + self.places[places]
-        for layer, (qkv, out, up, down) in enumerate(self.blocks):
+        for layer, (qkv, out, *feed) in enumerate(self.blocks):
             h = qkv(F.layer_norm(x, (d,)).half()).half()
             x = x + out(attend(layer, h[:, :d], h[:, d:d + kv], h[:, d + kv:]))
-            x = x + down(F.gelu(up(F.layer_norm(x, (d,)).half()), approximate="tanh").half())
+            h = F.layer_norm(x, (d,)).half()
+            if s.experts:
+                x = feed[0](x, h)
+            else:
+                up, down = feed
+                x = x + down(F.gelu(up(h), approximate="tanh").half())
         x = F.layer_norm(x, (d,))
         logits = torch.empty(x.shape[0], s.vocab, dtype=torch.float32, device=x.device)
         mm.mm_gemm_f32(0, 1, x.shape[0], s.vocab, d, x, d, self.head, d, logits, s.vocab)
@@ -267,8 +315,9 @@ def main():
     p.add_argument("--temperature", type=float, default=0.3)
     p.add_argument("--window", type=int, default=0)
     p.add_argument("--accept", type=float, default=0.8)
+    p.add_argument("--experts", type=int, default=0)
     a = p.parse_args()
-    model = Model(Shape())
+    model = Model(Shape(experts=a.experts))
     rng = np.random.default_rng(3)
     prompts = [rng.integers(0, model.shape.vocab, n).tolist() for n in (37, 5, 120)]
     out = None
