@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                 __syncwarp();
                 if (++f.s == s1) next_chunk(f);
             }
+        }
+        if (!a.offsets) {
             pdl_wait();
             pdl_launch_dependents();
         }

@@ -14,7 +14,8 @@
     python -m dense_packed_bit_gb300.profile_case gemv_t --reps 3 --matrices 8   (1,536 x 12,288, automatic)
     python -m dense_packed_bit_gb300.profile_case gemv_t --reps 3 --matrices 4 --dequant 6 --rows 3   (fp4 decode)
     python -m dense_packed_bit_gb300.profile_case attn --reps 2   (causal attention 32 x 512 x 64, forward + backward)
-    python -m dense_packed_bit_gb300.profile_case case --name "decode 48 ragged" --reps 2   (one of perf/operators.py)
+    python -m dense_packed_bit_gb300.profile_case case --name "decode 48 ragged" --reps 2
+        (one of perf/operators.py or perf/more_operators.py)
 
 One warm-up launch precedes the `reps` launches.  No timing is done here:
 numbers come from the profiler or from bench.py.
@@ -29,7 +30,7 @@ import sys
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("op", choices=["gemm", "c1", "gemv", "gemv4", "ternary", "gemv_batched", "gemv_t", "attn", "case"])
-    ap.add_argument("--name", default="decode 48 ragged", help="case: its name in perf/operators.py")
+    ap.add_argument("--name", default="decode 48 ragged", help="case: its name in perf/operators.py or perf/more_operators.py")
     ap.add_argument("--layout", default="nn", choices=["nn", "nt", "tn"])
     ap.add_argument("--size", type=int, default=2048)
     ap.add_argument("--path", type=int, default=0)
@@ -95,9 +96,11 @@ def main(argv=None):
             mm.mm_attention_bwd(Q, K, V, O, dO, L, dQ, dK, dV, c.heads, c.T, c.D, c.causal, 0.125)
     elif a.op == "case":
         sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-        import perf.operators as operators
+        import perf.more_operators
+        import perf.operators
+        operators, case = next((m, c) for m in (perf.operators, perf.more_operators) for c in m.listed() if c["name"] == a.name)
         operators.own = True
-        state = operators.prepare({c["name"]: c for c in operators.listed()}[a.name], 1)
+        state = operators.prepare(case, 1)
         for _ in range(1 + a.reps):
             operators.run(state)
     elif a.op == "gemv":

@@ -160,3 +160,29 @@ def test_weights_beyond_4_gib():
         mm.mm_gemm_packed4(w, x, cols, m, mm.MM_ACT_NONE, y, rows)
         ref, tol = reference(x.double().cpu(), code * float(scales[0, 0]), False)
         check(y[:, -100:], ref, tol, "f32")
+
+
+@pytest.mark.parametrize("static", [False, True])
+@pytest.mark.parametrize("m", [1, 16, 40, 300])
+def test_a_product_waits_for_the_one_whose_result_it_takes(m, static):
+    """X of a call is Y of the call in front, which runs much longer: results of the time before show (each turn has other
+    data, and the bits must be those of calls with the GPU waited for in between)."""
+    first, _ = make_weights(1, 1, 4096, 8192, 128, "f16", static=static, spare=0)
+    second, _ = make_weights(2, 1, 200, 4096, 64, "f16", static=static, spare=0)
+    torch.cuda.synchronize()
+    g = torch.Generator().manual_seed(m)
+    xs = [torch.randn(m, 8192, generator=g).half().cuda() for _ in range(6)]
+    y, z = torch.zeros(m, 4096, dtype=torch.float16, device="cuda"), torch.zeros(m, 200, device="cuda")
+
+    def both(x, between):
+        mm.mm_gemm_packed4(first, x, 8192, m, mm.MM_ACT_NONE, y, 4096)
+        between()
+        mm.mm_gemm_packed4(second, y, 4096, m, mm.MM_ACT_NONE, z, 200)
+        between()
+        return z.clone()
+
+    want = [both(x, torch.cuda.synchronize) for x in xs]
+    for _ in range(3):
+        got = [both(x, lambda: None) for x in xs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
