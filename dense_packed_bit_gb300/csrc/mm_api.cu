@@ -1299,6 +1299,9 @@ mm_status check_packed4_weights(const mm_packed4 *W, mm::Packed4MmArgs *a) {
         return fail(MM_ERR_INVALID_ARG, "codes or scales span more than 2^47 bytes");
     if ((double)W->rows * (double)W->scales_row > 4294967295.0)
         return fail(MM_ERR_INVALID_ARG, "the scales of a matrix span 2^32 elements or more");
+    const int64_t stride_end = (int64_t)1 << 40;  // of a tensor map
+    if (W->codes_row >= stride_end || W->codes_expert >= stride_end) return fail(MM_ERR_INVALID_ARG, "codes_row and codes_expert must be below 2^40");
+    if ((W->rows + 63) / 64 * W->experts > ((int64_t)1 << 30)) return fail(MM_ERR_INVALID_ARG, "rows * experts is above 2^36");
     if (W->experts > 1 && (W->codes_expert < (W->rows - 1) * W->codes_row + bytes || W->scales_expert < (W->rows - 1) * W->scales_row + groups))
         return fail(MM_ERR_INVALID_ARG, "codes_expert or scales_expert does not hold a matrix");
     if (W->weights_static != 0 && W->weights_static != 1) return fail(MM_ERR_INVALID_ARG, "weights_static must be 0 or 1");
@@ -1321,6 +1324,8 @@ mm_status packed4_product(const mm_packed4 *W, const void *X, int64_t x_stride, 
     if (s != MM_OK) return s;
     const int64_t most = (int64_t)1 << 30, wide = (int64_t)1 << 30;
     if (slots < 1 || slots > most || x_rows < 1 || x_rows > most) return fail(MM_ERR_INVALID_ARG, "rows of X and Y must be 1 .. 2^30");
+    if (((slots + 63) / 64 + W->experts) * ((W->rows + 127) / 128) > most)
+        return fail(MM_ERR_INVALID_ARG, "Y has too many elements (32 bits number the units of work)");
     if (!order && (x_rows < slots || per_row != 1)) return fail(MM_ERR_INVALID_ARG, "without order X has a row for each of Y, and per_row is 1");
     if (per_row < 1 || per_row > most) return fail(MM_ERR_INVALID_ARG, "per_row must be 1 .. 2^30");
     if (!X || !is_aligned(X, 16)) return fail(MM_ERR_INVALID_ARG, "X is NULL or not 16-byte aligned");

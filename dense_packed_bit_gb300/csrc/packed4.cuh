@@ -139,7 +139,7 @@ inline cudaError_t packed4_tmap_x(CUtensorMap *map, const Packed4MmArgs &a, int 
 inline cudaError_t packed4_tmap_w(CUtensorMap *map, const Packed4MmArgs &a, int bytes, int rows, CUtensorMapSwizzle swizzle) {
     const uint64_t held = ((uint64_t)a.cols + 31) / 32 * 16, row = a.rows > 1 ? (uint64_t)a.codes_row : held;
     return make_tmap_3d(CU_TENSOR_MAP_DATA_TYPE_UINT8, map, a.codes, held, (uint64_t)a.rows, (uint64_t)a.experts, row,
-                        a.experts > 1 ? (uint64_t)a.codes_expert : row * a.rows, (uint32_t)bytes, (uint32_t)rows, swizzle);
+                        a.experts > 1 ? (uint64_t)a.codes_expert : row, (uint32_t)bytes, (uint32_t)rows, swizzle);
 }
 
 }  // namespace mm

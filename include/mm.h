@@ -737,8 +737,9 @@ mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, 
  * group: 32, 64 or 128.  dtype: MM_F16 or MM_BF16, that of scales and X.
  * weights_static: 1 promises that codes, scales and zeros are not written by work that is still queued or running when
  *   a call is made (weights laid out once), so their loads may start before the kernel in front of it has ended.
- * rows, cols at most 2^28, experts at most 1024, rows * scales_row below 2^32, 2^47 bytes from the first code to the last; strides of X, Y, logits,
- * residual and out below at most 2^30.
+ * rows, cols at most 2^28, experts at most 1024, rows * experts at most 2^36, rows * scales_row below 2^32, 2^47 bytes
+ * from the first code to the last and less than 2^40 from a row or a matrix to the next; strides of X, Y, logits, residual and out
+ * below at most 2^30.  Y of a call has at most about 2^43 elements.
  * The struct is host memory, read during each call.
  */
 typedef struct {

@@ -35,7 +35,8 @@ BAD = [dict(codes=None), dict(scales=None), dict(codes=P[0] + 8), dict(scales=P[
        dict(rows=(1 << 28) + 1), dict(cols=0), dict(cols=(1 << 28) + 1), dict(group=0), dict(group=16), dict(group=96), dict(group=256),
        dict(codes_row=96), dict(codes_row=120), dict(codes_row=-112), dict(scales_row=3), dict(dtype=mm.MM_F32), dict(dtype=-1),
        dict(weights_static=2), dict(codes_row=1 << 46), dict(scales_row=1 << 46), dict(codes_row=1 << 60), dict(codes_expert=-16),
-       dict(scales_expert=-1), dict(codes_expert=1 << 60), dict(codes_expert=40 * 112 + 8)]
+       dict(scales_expert=-1), dict(codes_expert=1 << 60), dict(codes_expert=40 * 112 + 8), dict(codes_row=1 << 40), dict(codes_expert=1 << 40),
+       dict(rows=1 << 28, scales_row=16)]
 
 
 @pytest.mark.parametrize("bad", BAD, ids=str)
@@ -68,6 +69,12 @@ def test_bad_products(lib, bad):
     refused(lib, lib.mm_gemm_packed4(weights(), a["X"], a["x_stride"], a["M"], a["act"], a["Y"], a["y_dtype"], a["y_stride"], None))
     refused(lib, lib.mm_experts_gemm_packed4(weights(3), a["X"], a["x_stride"], max(a["M"], 1), P[6], 1, P[5], a["M"], a["act"], a["Y"],
                                              a["y_dtype"], a["y_stride"], None))
+
+
+def test_more_units_of_work_than_32_bits(lib):
+    big = dict(rows=1 << 28, codes_expert=(1 << 28) * 112, scales_expert=(1 << 28) * 4)
+    refused(lib, lib.mm_experts_gemm_packed4(weights(1024, **big), P[3], 200, 5, None, 1, P[5], 5, 0, P[4], mm.MM_F32, 1 << 28, None))
+    refused(lib, lib.mm_gemm_packed4(weights(rows=1 << 28), P[3], 200, 1 << 30, 0, P[4], mm.MM_F32, 1 << 28, None))
 
 
 def test_swiglu_takes_pairs(lib):
