@@ -27,17 +27,36 @@ constexpr int BLOCKS = 128;       // blocks of tokens otherwise, at most (more o
 constexpr int MAX_PER = 1 << 15;  // tokens of a block
 constexpr int COUNTS = 8448;      // shared counts: [warps][experts], rows an odd number of words apart
 
-__device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
 __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Orders like x (both zeros alike); 0 for NaN and -infinity, which are never picked.
-__device__ __forceinline__ uint32_t key_of(float x) {
-    if (!(x > -INFINITY)) return 0;
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    return b >> 31 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+// Whole numbers that order like the logits (both zeros alike); 0 for NaN and -infinity, which are never picked.  A logit of
+// 16 bits leaves the lower half to the expert, lower ones larger, so that the largest number is the pick: one reduction finds
+// the value and the lowest index that has it (with fp32 it takes a second one).
+template <typename T>
+struct Key {
+    static constexpr bool kHasIndex = true;
+    static __device__ __forceinline__ uint32_t of(T x, int expert) {
+        if (!(widen(x) > -INFINITY)) return 0;
+        uint32_t b = *reinterpret_cast<const uint16_t *>(&x);
+        if (b == 0x8000u) b = 0;
+        return ((b >> 15 ? ~b : b | 0x8000u) << 16) | (0xFFFFu - (uint32_t)expert);
+    }
+    static __device__ __forceinline__ float value(uint32_t k) {
+        const uint16_t b = (uint16_t)(k >> 31 ? (k >> 16) & 0x7FFFu : ~(k >> 16));
+        return widen(*reinterpret_cast<const T *>(&b));
+    }
+};
+template <>
+struct Key<float> {
+    static constexpr bool kHasIndex = false;
+    static __device__ __forceinline__ uint32_t of(float x, int) {
+        if (!(x > -INFINITY)) return 0;
+        const uint32_t b = __float_as_uint(x + 0.0f);
+        return b >> 31 ? ~b : b | 0x80000000u;
+    }
+    static __device__ __forceinline__ float value(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -62,7 +81,9 @@ template <typename T, int PER>
 __device__ __forceinline__ int pick(const RouteArgs &a, int64_t t, const Logits<T, PER> &x, int lane) {
     uint32_t key[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < a.experts ? key_of(widen(x.v[i])) : 0;
+    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < a.experts ? Key<T>::of(x.v[i], lane + 32 * i) : 0;
+    const auto value = [](uint32_t k) { return Key<T>::value(k); };
+    constexpr bool SHORT = Key<T>::kHasIndex;
     float sum = 0.f;  // of the softmax over all experts
     uint32_t first = 0;
     int id = -1;
@@ -73,28 +94,33 @@ __device__ __forceinline__ int pick(const RouteArgs &a, int64_t t, const Logits<
         for (int i = 0; i < PER; ++i) best = max(best, key[i]);
         const uint32_t top = __reduce_max_sync(~0u, best);
         if (top == 0) break;
-        int at = 1 << 30;
+        int at;
+        if constexpr (SHORT) {
+            at = (int)(0xFFFFu - (top & 0xFFFFu));
+        } else {
+            at = 1 << 30;
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == top) at = lane + 32 * i;
-        at = (int)__reduce_min_sync(~0u, (unsigned)at);
+            for (int i = PER - 1; i >= 0; --i)
+                if (key[i] == top) at = lane + 32 * i;
+            at = (int)__reduce_min_sync(~0u, (unsigned)at);
+        }
         if (j == 0) {
             first = top;
             if (!a.sigmoid && !a.renorm) {
-                const float m = of_key(top);
+                const float m = value(top);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(of_key(key[i]) - m) : 0.f;
+                for (int i = 0; i < PER; ++i) sum += key[i] ? expf(value(key[i]) - m) : 0.f;
                 sum = warp_sum(sum);
             }
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (at == lane + 32 * i) key[i] = 0;
-        if (lane == j) id = at, mine = of_key(top);
+            if (SHORT ? key[i] == top : at == lane + 32 * i) key[i] = 0;
+        if (lane == j) id = at, mine = value(top);
     }
     // Softmax: exp(x - largest) over its sum; sigmoid: 1 / (1 + exp(-x)).  Normalised sigmoids are divided by the largest
     // one's exp(x) first where that is below 1, so that they do not all vanish.
-    const float m = of_key(first);
+    const float m = value(first);
     float w = 0.f;
     if (id >= 0) {
         if (!a.sigmoid) w = expf(mine - m);
