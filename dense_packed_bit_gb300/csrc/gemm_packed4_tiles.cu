@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr int STAGES = P::STAGES, CRING = P::CRING;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_aligned<1024>(smem_raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR);  // X has arrived (this CTA's)
-    uint64_t *ready = full + STAGES;   // the numbers are there, and the other CTA's X (the leader's)
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::BAR);  // X has arrived (a pair's other CTA's)
+    uint64_t *ready = full + STAGES;   // the numbers and X are there (the leader's)
     uint64_t *empty = ready + STAGES;  // the stage's MMAs are done (every CTA's)
     uint64_t *cfull = empty + STAGES;  // codes have arrived (this CTA's)
     uint64_t *cempty = cfull + CRING;  // they have been read (this CTA's)
@@ -243,10 +243,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_relinquish();
         }
     }
+    const int xwarps = a.order ? 2 : 1;
+    uint64_t *const xbar = CG == 2 && rank == 1 ? full : ready;  // where this CTA's X arrives
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], a.order ? 2 : 1);
-            mbar_init(&ready[s], DEC_WARPS / 2 * CG + CG - 1);  // of a pair the other CTA tells that its X is there
+            mbar_init(&full[s], xwarps);
+            // the decode warps, the leader's X, and of a pair the other CTA, which tells that its X is there
+            mbar_init(&ready[s], DEC_WARPS / 2 * CG + xwarps + CG - 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < CRING; ++s) {
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const auto drain = [&](int it) {
             for (int i = 0; i < STAGES && i < it; ++i) {
                 const int lastit = i + ((it - 1 - i) / STAGES) * STAGES;
-                if (!mbar_wait(&full[i], (uint32_t)(lastit / STAGES) & 1)) {
+                if (!mbar_wait(&xbar[i], (uint32_t)(lastit / STAGES) & 1)) {
                     atomicExch(&g_packed4_tiles_err, kDevErrDrain);
                     break;
                 }
@@ -352,9 +355,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         break;
                     }
                     if (elected()) {
-                        mbar_arrive_expect_tx(&full[b], (uint32_t)boxes * BOX * 128u);
+                        mbar_arrive_expect_tx(&xbar[b], (uint32_t)boxes * BOX * 128u);
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &full[b], (st0 + s) * BK, t.first + from + i * BOX);
+                            tma_load_2d(smem + b * P::STAGE + P::A_BYTES + i * BOX * 128, &tmX, &xbar[b], (st0 + s) * BK, t.first + from + i * BOX);
                     }
                     __syncwarp();
                     if (++b == STAGES) b = 0, ++use;
@@ -388,11 +391,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                     if (elected()) {
                         uint8_t *dst = smem + b * P::STAGE + P::A_BYTES + half * n * 128;
-                        mbar_arrive_expect_tx(&full[b], (uint32_t)n * 128u);
+                        mbar_arrive_expect_tx(&xbar[b], (uint32_t)n * 128u);
 #pragma unroll 4
                         for (int i = 0; i < n; i += 4) {
                             const int4 r = *reinterpret_cast<const int4 *>(rows + i);
-                            tma_gather4(dst + i * 128, &tmX, &full[b], (st0 + s) * BK, r.x, r.y, r.z, r.w);
+                            tma_gather4(dst + i * 128, &tmX, &xbar[b], (st0 + s) * BK, r.x, r.y, r.z, r.w);
                         }
                     }
                     __syncwarp();
@@ -458,7 +461,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         // stage's, of 32 two in a stage
                         const bool first = a.group <= BK || (s & 1) == 0;
                         if (first) begin();
-                        wait(&full[b], use & 1, kDevErrWaitFull);
                         wait(&ready[b], use & 1, kDevErrWaitFull);
                         if (stop) break;
                         const uint32_t at = smem_u32(smem + b * P::STAGE);
