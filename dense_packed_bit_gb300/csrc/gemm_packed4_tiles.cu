@@ -116,9 +116,32 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32
     else umma_f16(d, da, db, idesc, accumulate);
 }
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    if constexpr (CG == 2) umma_commit_pair(bar, 3);
-    else umma_commit(bar);
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// mbar_try_wait and mbar_wait of a barrier by its address
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (true) {
+        for (int i = 0; i < 64; ++i)
+            if (try_wait(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+    }
 }
 
 template <int CG>
@@ -436,55 +459,57 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             late_wait();
             constexpr uint32_t fmt = __is_same(T, __half) ? kFmtF16 : kFmtBF16;
             if (elected()) {
-                int b = 0, gi = 0;  // stage of the ring, groups so far
-                uint32_t use = 0;
+                // One thread issues all MMAs, and a stage of few rows of X takes no longer than its instructions: addresses
+                // are 32-bit numbers, a stage's parity turns with the ring, and a descriptor is its lower word.
+                const uint32_t ready0 = smem_u32(ready), empty0 = smem_u32(empty), accf0 = smem_u32(accf), acce0 = smem_u32(acce);
+                const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(smem)), db0 = sdesc_kmajor_sw128(smem_u32(smem) + P::A_BYTES);
+                const int steps = a.group / 32;  // half stages of a group: 1, 2 or 4
+                uint32_t b = 0, parity = 0;      // stage of the ring, its barriers' parity
+                uint32_t acc = 0, taken = 1;     // accumulator in turn, the parity of its being taken (at first it is free)
                 bool stop = false;
-                const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned int code) {
-                    if (!mbar_wait(bar, parity)) {
+                const auto wait = [&](uint32_t bar, uint32_t at, unsigned int code) {
+                    if (!try_wait(bar, at) && !slow_wait(bar, at)) {
                         fail<CG>(abort_flag, code);
                         stop = true;
                     }
-                    tc_fence_after_sync();
-                };
-                const auto begin = [&] {  // a group's accumulator is free
-                    if (gi >= 2) wait(&acce[gi & 1], (uint32_t)(gi / 2 - 1) & 1, kDevErrWaitEmpty);
-                };
-                const auto end = [&] {
-                    commit<CG>(&accf[gi & 1]);
-                    ++gi;
                 };
                 for (int u = cid; u < wk.units && !stop; u += ncl) {
                     const Unit t = unit_at<CG>(a, wk, u, &err);
                     const uint32_t idesc = make_idesc(fmt, fmt, (uint32_t)t.N, BM * CG);
-                    for (int s = 0; s < stages; ++s) {
-                        // the first MMA of a group clears the accumulator: of 128 columns every other stage's, of 64 every
-                        // stage's, of 32 two in a stage
-                        const bool first = a.group <= BK || (s & 1) == 0;
-                        if (first) begin();
-                        wait(&ready[b], use & 1, kDevErrWaitFull);
+                    int left = (min(a.cols, (st0 + stages) * BK) - st0 * BK + 31) / 32, in_group = 0;  // half stages
+                    for (; left > 0; left -= 2) {
+                        if (in_group == 0) wait(acce0 + 8 * acc, taken, kDevErrWaitEmpty);  // a group's accumulator is free
+                        wait(ready0 + 8 * b, parity, kDevErrWaitFull);
                         if (stop) break;
-                        const uint32_t at = smem_u32(smem + b * P::STAGE);
-                        const uint64_t da = sdesc_kmajor_sw128(at), db = sdesc_kmajor_sw128(at + P::A_BYTES);
-                        uint32_t d = tmem + (uint32_t)((gi & 1) * BN);
-                        mma<CG>(d, da, db, idesc, !first);
-                        mma<CG>(d, da + 2, db + 2, idesc, 1);
-                        const bool halves = a.group == 32 && (st0 + s) * BK + 32 < a.cols;
-                        if (halves) {
-                            end();
-                            begin();
+                        tc_fence_after_sync();
+                        const uint64_t da = da0 + b * (P::STAGE >> 4), db = db0 + b * (P::STAGE >> 4);
+                        // the first MMA of a group clears the accumulator
+                        mma<CG>(tmem + acc * BN, da, db, idesc, in_group);
+                        mma<CG>(tmem + acc * BN, da + 2, db + 2, idesc, 1);
+                        if (steps == 1 && left > 1) {  // groups of 32: the second half is another
+                            commit<CG>(accf0 + 8 * acc);
+                            acc ^= 1, taken ^= acc ^ 1;
+                            wait(acce0 + 8 * acc, taken, kDevErrWaitEmpty);
                             if (stop) break;
-                            d = tmem + (uint32_t)((gi & 1) * BN);
+                            tc_fence_after_sync();
+                            mma<CG>(tmem + acc * BN, da + 4, db + 4, idesc, 0);
+                            mma<CG>(tmem + acc * BN, da + 6, db + 6, idesc, 1);
+                        } else if (steps > 1) {
+                            mma<CG>(tmem + acc * BN, da + 4, db + 4, idesc, 1);
+                            mma<CG>(tmem + acc * BN, da + 6, db + 6, idesc, 1);
                         }
-                        mma<CG>(d, da + 4, db + 4, idesc, !halves);
-                        mma<CG>(d, da + 6, db + 6, idesc, 1);
-                        commit<CG>(&empty[b]);
-                        if (a.group <= BK || (s & 1) || s == stages - 1) end();
-                        if (++b == STAGES) b = 0, ++use;
+                        commit<CG>(empty0 + 8 * b);
+                        in_group += 2;
+                        if (in_group >= steps || left <= 2) {
+                            commit<CG>(accf0 + 8 * acc);
+                            acc ^= 1, taken ^= acc ^ 1, in_group = 0;
+                        }
+                        if (++b == STAGES) b = 0, parity ^= 1;
                     }
                     if (*abort_flag) stop = true;
                 }
                 // every MMA issued must be complete before the tensor memory is freed
-                commit<CG>(last);
+                commit<CG>(smem_u32(last));
                 if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
             }
             __syncwarp();
