@@ -54,8 +54,8 @@ struct Plan {
     static constexpr int CRING = CG == 2 ? 6 : 5;              // boxes of codes on their way to shared memory
     static constexpr int CODES = STAGES * STAGE;
     static constexpr int OUT = CODES + CRING * CBOX;           // 32 x 32 results of each epilogue warp
-    static constexpr int ROWS = OUT + EPI_WARPS * 4096;        // rows of X of two units, where they are gathered
-    static constexpr int BAR = ROWS + 2 * BN * 4;
+    static constexpr int ROWS = OUT + EPI_WARPS * 4096;        // rows of X, where they are gathered: 128 to a warp
+    static constexpr int BAR = ROWS + 2 * 128 * 4;
     static constexpr int PRE = BAR + 320;                      // chunks before each expert
     static constexpr int TOTAL = PRE + (MAX_EXPERTS + 1) * 4 + 12 + 1024;  // + alignment of the dynamic allocation
     static_assert((3 * STAGES + 2 * CRING + 5) * 8 + 8 <= 320, "barriers");
@@ -391,13 +391,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // Gathered rows, four to an instruction, half of them to each of two warps.  (Issued by a lane for each four, 70
             // clocks an instruction; copied by the warps 16 bytes at a time, 60 clocks for four rows.)
             const int half = warp == WARP_X2;
+            int *const rows = reinterpret_cast<int *>(smem + P::ROWS) + half * 128;  // this warp's own
             int b = 0, it = 0;
             uint32_t use = 0;
             bool stop = false;
-            for (int u = cid, turn = 0; u < wk.units && !stop; u += ncl, turn ^= 1) {
+            for (int u = cid; u < wk.units && !stop; u += ncl) {
                 const Unit t = unit_at<CG>(a, wk, u, &err);
                 const int mine = t.N / CG, from = (int)rank * mine, n = mine / 2;  // a multiple of 8
-                int *rows = reinterpret_cast<int *>(smem + P::ROWS) + turn * BN + half * n;
                 for (int i = lane; i < n; i += 32) {  // rows that are none, or behind the chunk: any row, not stored
                     const int at = from + half * n + i;
                     const int64_t row = at < t.n ? x_row(a, t.first + at, &err) : 0;

@@ -157,6 +157,14 @@ def test_experts(name, gather):
     experts(3, counts, 32, 200, 32, "f16", "f16", gather, swiglu=gather, per_row=1 if gather else 2)
 
 
+@pytest.mark.parametrize("cols,group", [(64, 32), (128, 64), (120, 128), (192, 64), (24, 32)])
+def test_short_rows_of_experts_of_many_lengths(cols, group):
+    """Units of one to three stages: a warp that gathers X may be two units ahead of the other, whose rows must stay."""
+    counts = [(17, 250, 33, 256, 90, 1, 128, 300)[i * 5 % 8] for i in range(40)]
+    experts(4, counts, 2600, cols, group, "bf16", "f32", True)
+    experts(5, counts, 700, cols, group, "f16", "f16", True, swiglu=True)
+
+
 def test_experts_without_slots():
     w, _ = make_weights(1, 5, 30, 64, 32, "f16")
     y, buf = make_y(6, 30, "f32")
