@@ -165,6 +165,15 @@ def test_short_rows_of_experts_of_many_lengths(cols, group):
     experts(5, counts, 700, cols, group, "f16", "f16", True, swiglu=True)
 
 
+@pytest.mark.parametrize("rows,cols,group,dtype,out,swiglu", [
+    (10722, 328, 64, "bf16", "f32", False), (10752, 64, 64, "f16", "f16", True), (10500, 192, 128, "bf16", "bf16", True),
+    (21504, 136, 128, "f16", "f32", False)])
+def test_many_rows_of_x_to_an_expert(rows, cols, group, dtype, out, swiglu):
+    """Two pairs of CTAs that gather X for each other."""
+    experts(6, [900, 3, 1201, 0], rows, cols, group, dtype, out, True, swiglu=swiglu)
+    experts(7, [1100, 300, 200], rows, cols, group, dtype, out, True, swiglu=swiglu, zeros=False, per_row=1)
+
+
 def test_experts_without_slots():
     w, _ = make_weights(1, 5, 30, 64, 32, "f16")
     y, buf = make_y(6, 30, "f32")
