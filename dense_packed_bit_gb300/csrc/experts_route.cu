@@ -22,7 +22,7 @@ namespace mm {
 
 namespace {
 
-constexpr int ONE = 128;          // tokens that one CTA takes
+constexpr int ONE = 64;           // tokens that one CTA takes
 constexpr int BLOCKS = 128;       // blocks of tokens otherwise, at most (more only above 2^22 tokens)
 constexpr int MAX_PER = 1 << 15;  // tokens of a block
 constexpr int COUNTS = 8448;      // shared counts: [warps][experts], rows an odd number of words apart

@@ -21,7 +21,7 @@
 //                   (at a fixed row of X a warp writes 32 neighbouring columns of Y).
 // Persistent: the units of work -- a chunk of an expert's slots times a tile of rows of W -- are dealt to the CTAs in
 // turn, tiles of rows first, so that X is read once and the codes, 4 bits a weight, come from L2.  The slots of an expert
-// are cut into chunks of one size; the longest chunk is the largest of 256, 128 and 64 that leaves no SM without work.
+// are cut into chunks of one size, of up to 256, 128 or 64, whichever takes the least time in whole rounds of units.
 // Where one matrix gives few units, K is cut over the CTAs of a cluster, whose sums are added in order through shared memory.
 #include <atomic>
 
@@ -49,6 +49,12 @@ constexpr int BOX = 64;        // rows of X per TMA box
 // Registers of a thread once the roles part, of the 96 at launch: 384 x 40 + 256 x 176 <= 640 x 96.
 #define MM_PACKED4_REGS_FEW "40"
 #define MM_PACKED4_REGS_EPI "176"
+
+// What a stage of 256, 128 and 64 rows of X costs, about.  A stage of few rows costs nearly as much as one of many, so shorter
+// chunks pay where they fill SMs that would be idle, and not in a second round.  Measured (us, chunks of up to 256, 128 and 64):
+// 600 x 4096 to 4096 34, 54, 72; 512 x 2048 to 8192 21, 32, 54; of experts of 2048 columns, 2000 slots of 4 of 512 rows
+// 29, 23, 20 (gathered 49, 34, 25); 4000 slots of 8 of 300 rows 32, 26, 37 (58, 38, 48); of 8 of 1024 rows 45, 44, 68 (75, 63, 85).
+__device__ __forceinline__ int cost_of(bool gathered, int i) { return i == 0 ? (gathered ? 25 : 17) : i == 1 ? (gathered ? 15 : 13) : 10; }
 
 template <int CG>
 struct Plan {
@@ -240,7 +246,7 @@ __device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float 
 template <typename T, int CG, int PAIRS>
 __global__ void __launch_bounds__(NTHREADS, 1)
     packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                         const __grid_constant__ Packed4MmArgs a, const int ksplit, const int longest) {
+                         const __grid_constant__ Packed4MmArgs a, const int ksplit) {
     using P = Plan<CG>;
     constexpr int STAGES = P::STAGES, CRING = P::CRING;
     extern __shared__ uint8_t smem_raw[];
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         pdl_launch_dependents();
     }
 
-    // chunks before each expert, for the longest chunk that leaves no SM idle
+    // chunks before each expert
     unsigned int err = 0;
     Work wk;
     wk.pre = pre, wk.experts = a.experts, wk.step = BM * CG * PAIRS, wk.at = (int)pair * BM * CG;
@@ -322,13 +328,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) sums[k][warp] = all;
         }
         __syncthreads();
-        int k = ksplit == 1 || longest == 256 ? 0 : longest == 128 ? 1 : 2;
-        for (; ksplit == 1 && k < 2; ++k) {
-            int64_t all = 0;
-            for (int w = 0; w < NTHREADS / 32; ++w) all += sums[k][w];
-            if (all * wk.tiles >= ncl) break;
+        // the longest chunk: the one whose rounds of units take the least time, of equal ones the largest
+        int of_warp = 0, all = 0;
+        int64_t least = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int v = lane < NTHREADS / 32 ? sums[k][lane] : 0, chunks = __reduce_add_sync(~0u, v);
+            const int64_t cost = (int64_t)((uint32_t)(chunks * wk.tiles + ncl - 1) / (uint32_t)ncl) * cost_of(a.order != nullptr, k);
+            if (k == 0 || (ksplit == 1 && cost < least)) least = cost, wk.longest = 256 >> k, of_warp = v, all = chunks;
         }
-        wk.longest = 256 >> k;
         const int c0 = chunks_of(n[0], wk.longest), c1 = chunks_of(n[1], wk.longest);
         int run = c0 + c1;
 #pragma unroll
@@ -336,11 +344,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const int up = __shfl_up_sync(~0u, run, o);
             if (lane >= o) run += up;
         }
-        int before = run - c0 - c1, all = 0;
-        for (int w = 0; w < NTHREADS / 32; ++w) {
-            if (w < warp) before += sums[k][w];
-            all += sums[k][w];
-        }
+        const int before = __reduce_add_sync(~0u, lane < warp ? of_warp : 0) + run - c0 - c1;
         if (e0 < a.experts) pre[e0] = before;
         if (e0 + 1 < a.experts) pre[e0 + 1] = before + c0;
         if (threadIdx.x == 0) pre[a.experts] = all;
@@ -787,11 +791,10 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     // half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
     const auto units_of = [&](int64_t longest) { return (a.slots + longest - 1) / longest * tiles; };
     const int boxes = (a.cols + 2 * BK - 1) / (2 * BK);
-    int ksplit = 1, longest = BN;
+    int ksplit = 1;
     while (CG == 1 && !a.offsets && ksplit < 8 && units_of(BN) * ksplit * 2 <= sms && ksplit * 3 <= boxes) ksplit *= 2;
-    while (ksplit > 1 && longest > 64 && units_of(longest / 2) * ksplit <= sms) longest /= 2;
     // no more CTAs than units of the shortest chunks
-    const int64_t most = ksplit > 1 ? units_of(longest) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
+    const int64_t most = ksplit > 1 ? units_of(BN) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
     int fit = sms / CG;
     if (PAIRS > 1) {
         e = clusters_at_once<T, CG, PAIRS>(&fit);
@@ -810,7 +813,7 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.x = (unsigned)(CG * PAIRS * ksplit), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = CG * ksplit > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG, PAIRS>, tx, tw, a, ksplit, longest);
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG, PAIRS>, tx, tw, a, ksplit);
 }
 
 }  // namespace
