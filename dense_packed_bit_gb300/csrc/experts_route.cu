@@ -8,8 +8,8 @@
 // first kernel leaves each block's counts in the workspace and a second adds them up and places.  Nothing is counted
 // with atomics whose order could show, so the order by expert is by token within.
 //
-// What bounds it: the launches and the chains of dependent reductions for few tokens; a call reads the logits once and
-// writes 16 bytes a pick.
+// What bounds it: the launches and the chains of dependent reductions for few tokens (1 x 8: 3.0 us); a call reads the logits
+// once and writes 16 bytes a pick (8191 x 128, 8 picks: 14.1 us, half of it picks, half places).
 #include "cache_view.cuh"
 #include "mm_common.cuh"
 #include "mm_internal.h"
@@ -22,7 +22,8 @@ namespace mm {
 
 namespace {
 
-constexpr int ONE = 64;           // tokens that one CTA takes
+// Tokens that one CTA takes (us, one CTA and two kernels: 64 x 64 6.2 and 7.0, 80 x 64 7.9 and 7.4, 128 x 64 9.0 and 7.3)
+constexpr int ONE = 64;
 constexpr int BLOCKS = 128;       // blocks of tokens otherwise, at most (more only above 2^22 tokens)
 constexpr int MAX_PER = 1 << 15;  // tokens of a block
 constexpr int COUNTS = 8448;      // shared counts: [warps][experts], rows an odd number of words apart

@@ -15,6 +15,9 @@
 //
 // K is cut over a cluster of CTAs where the rows alone would leave SMs idle; all parts are added in a fixed order through
 // shared memory, so results repeat bit for bit.  More rows of X than 8 (16) go around again with the codes read from L2.
+//
+// Measured on a GB300: 1 x 1536 to 12288 5.2 us, of which most is latency; 13 x 4096 to 10240 15.1 us = 1.48 TB/s, bound by
+// dependent instructions of 8 warps an SM; 64 tokens of 8 of 64 experts of 2048 x 1408 54 us = 1.96 TB/s, issue 53% of cycles.
 #include "packed4.cuh"
 #include "smem_limit.h"
 #include "tcgen05.cuh"
@@ -489,7 +492,8 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     e = packed4_tmap_x(&tx, a, a.order ? 1 : xbox);
     if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, HALF / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    // K is cut over as many CTAs of a cluster as the GPU holds beside each other
+    // K is cut over as many CTAs of a cluster as the GPU holds beside each other (1 x 12288 to 1536 7.2 us, uncut 22.2; 8 x 4096
+    // to 4096 6.2 and 8.7)
     const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
     const int64_t units = tiles * (a.offsets ? (a.slots < a.experts ? a.slots : a.experts) : 1);
     int cluster = 1;
@@ -519,7 +523,8 @@ cudaError_t launch_g(const Packed4MmArgs &a, int sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_t(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    // 16 at a time where a matrix has more than 8 rows of X; of experts some have twice the average
+    // 16 at a time where a matrix has more than 8 rows of X; of experts some have twice the average (us, 8 and 16 at a time: 8 x
+    // 4096 to 4096 6.2 and 7.0, 13 rows 11.0 and 7.3; 64 experts of 2048 x 2048 with 3 slots each 48 and 50, with 4 58 and 57)
     return a.slots > (a.offsets ? 3 * (int64_t)a.experts : 8) ? launch_g<T, 2>(a, sms, s) : launch_g<T, 1>(a, sms, s);
 }
 
