@@ -10,8 +10,7 @@
 // of the MMAs, beside which it runs (two accumulators of 256 columns), with groups of 32 all of it.
 //
 // Roles of a CTA's 20 warps, over a ring of stages of 64 columns:
-//   warp 0          X by TMA, 64 rows to a box; where `order` names the rows, warps 0 and 3 gather them four at a time, in a
-//                   cluster of two pairs each pair half of the rows for both (multicast);
+//   warp 0          X by TMA, 64 rows to a box; where `order` names the rows, warps 0 and 3 gather them four at a time;
 //   warp 1          issues the MMAs (in a pair: the even CTA's, for both);
 //   warp 2          codes by TMA, 128 rows x 128 codes to a box, into a ring of their own that is CRING boxes deep;
 //   warps 4 - 11    make 16-bit numbers of them and store them as the MMA's A (128-byte swizzle), a thread to 32 codes of a
@@ -27,9 +26,7 @@
 //
 // Measured on a GB300 (groups of 128): 4096 x 4096 to 8192 in bf16 222 us = 1,240 TFLOP/s, 64% of a library product, where the
 // MMAs alone take 145: the ends of units, sums and numbers do not all hide behind them.  4096 tokens of 2 of 8 experts of 8192 x
-// 2048 with SwiGLU 354 us, bound by the gathers of X.  222 x 776 to 2304 9.2 us: latency, 0.4 us a stage.
-#include <atomic>
-
+// 2048 with SwiGLU 421 us, bound by the gathers of X.  222 x 776 to 2304 9.2 us: latency, 0.4 us a stage.
 #include "packed4.cuh"
 #include "smem_limit.h"
 #include "tcgen05.cuh"
@@ -90,7 +87,6 @@ struct Unit {
 struct Work {
     const int *pre;    // chunks before expert e; pre[experts]: all
     int experts, tiles;
-    int step, at;      // rows of W of a tile, and this pair's first of them
     int longest;       // slots of a chunk, at most
     int units;
 };
@@ -113,7 +109,7 @@ __device__ __forceinline__ Unit unit_at(const Packed4MmArgs &a, const Work &w, i
     // (many - 1) each <= (many - 1) longest < count: the last chunk has slots too
     r.e = lo, r.first = s.first + part * each, r.n = min(each, s.count - part * each);
     r.N = (r.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
-    r.r0 = tile * w.step + w.at;
+    r.r0 = tile * BM * CG;
     return r;
 }
 
@@ -121,11 +117,8 @@ template <int CG>
 __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code) {
     atomicExch(&g_packed4_tiles_err, code);
     *abort_flag = 1;
-    if constexpr (CG == 2) {
-        uint32_t ctas;
-        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-        for (uint32_t r = 0; r < ctas; ++r) st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), r), 1u);
-    }
+    if constexpr (CG == 2)
+        st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
 }
 
 template <int CG>
@@ -134,11 +127,11 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32
     else umma_f16(d, da, db, idesc, accumulate);
 }
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar, uint16_t ctas) {
+__device__ __forceinline__ void commit(uint32_t bar) {
     if constexpr (CG == 2)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(ctas)
+            "h"((uint16_t)3)
             : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -163,8 +156,8 @@ __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) {
 }
 
 template <int CG>
-__device__ __forceinline__ void arrive_leader(uint64_t *bar, uint32_t leader) {
-    if constexpr (CG == 2) mbar_arrive_cluster(cluster_map(smem_u32(bar), leader));
+__device__ __forceinline__ void arrive_leader(uint64_t *bar) {
+    if constexpr (CG == 2) mbar_arrive_cluster(cluster_map(smem_u32(bar), 0));
     else mbar_arrive(bar);
 }
 
@@ -248,7 +241,7 @@ __device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float 
     }
 }
 
-template <typename T, int CG, int PAIRS>
+template <typename T, int CG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ Packed4MmArgs a, const int ksplit) {
@@ -269,10 +262,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int *pre = reinterpret_cast<int *>(smem + P::PRE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u, rank = crank & 1, pair = crank >> 1, leader = PAIRS == 2 ? crank & 2 : 0;
-    const uint16_t of_pair = (uint16_t)(3u << leader), of_all = (uint16_t)((1u << (2 * PAIRS)) - 1);
-    const uint32_t part = CG == 1 && ksplit > 1 ? cluster_ctarank() : 0u;
-    const int cid = blockIdx.x / (CG * PAIRS * ksplit), ncl = gridDim.x / (CG * PAIRS * ksplit);
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u, part = CG == 1 && ksplit > 1 ? cluster_ctarank() : 0u;
+    const int cid = blockIdx.x / (CG * ksplit), ncl = gridDim.x / (CG * ksplit);
     // this CTA's part of K, in whole boxes of codes: stages st0 .. st0 + stages - 1
     const int boxes = (a.cols + 2 * BK - 1) / (2 * BK), st0 = 2 * (boxes * (int)part / ksplit);
     const int stages = min((a.cols + BK - 1) / BK, 2 * (boxes * ((int)part + 1) / ksplit)) - st0;
@@ -293,7 +284,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(&full[s], xwarps);
             // the decode warps, the leader's X, and of a pair the other CTA, which tells that its X is there
             mbar_init(&ready[s], DEC_WARPS / 2 * CG + xwarps + CG - 1);
-            mbar_init(&empty[s], PAIRS);
+            mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < CRING; ++s) {
             mbar_init(&cfull[s], 1);
@@ -319,8 +310,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // chunks before each expert
     unsigned int err = 0;
     Work wk;
-    wk.pre = pre, wk.experts = a.experts, wk.step = BM * CG * PAIRS, wk.at = (int)pair * BM * CG;
-    wk.tiles = (a.rows + wk.step - 1) / wk.step;
+    wk.pre = pre, wk.experts = a.experts, wk.tiles = (a.rows + BM * CG - 1) / (BM * CG);
     {
         __shared__ int sums[3][NTHREADS / 32];
         const int e0 = 2 * threadIdx.x;
@@ -410,7 +400,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // Gathered rows, four to an instruction, half of them to each of two warps: 27 clocks an instruction for both, which
             // is what the TMA unit takes.  (One lane for each four rows: 70 clocks; three warps, the third of which asks for
             // codes too: the whole call 6 to 16% slower; copies of 16 bytes: 60 for four rows, and beside gathers no sooner.)
-            // Of two pairs each brings half of the rows for both.
             const int half = warp == WARP_X2;
             int *const rows = reinterpret_cast<int *>(smem + P::ROWS) + half * 128;  // this warp's own
             int b = 0, it = 0;
@@ -418,8 +407,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             bool stop = false;
             for (int u = cid; u < wk.units && !stop; u += ncl) {
                 const Unit t = unit_at<CG>(a, wk, u, &err);
-                const int mine = t.N / CG, n = mine / (2 * PAIRS);  // a multiple of 8, of two pairs 4
-                const int g0 = ((int)pair * 2 + half) * n, from = (int)rank * mine + g0;
+                const int mine = t.N / CG, n = mine / 2;  // a multiple of 8
+                const int g0 = half * n, from = (int)rank * mine + g0;
                 for (int i = lane; i < n; i += 32) {  // rows that are none, or behind the chunk: any row, not stored
                     const int64_t row = from + i < t.n ? x_row(a, t.first + from + i, &err) : 0;
                     rows[i] = row < 0 ? 0 : (int)row;
@@ -435,12 +424,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                     if (elected()) {
                         uint8_t *dst = smem + b * P::STAGE + P::A_BYTES + g0 * 128;
-                        mbar_arrive_expect_tx(&xbar[b], (uint32_t)(n * PAIRS) * 128u);  // the other pair's too
+                        mbar_arrive_expect_tx(&xbar[b], (uint32_t)n * 128u);
 #pragma unroll 4
                         for (int i = 0; i < n; i += 4) {
                             const int4 r = *reinterpret_cast<const int4 *>(rows + i);
-                            if constexpr (PAIRS == 1) tma_gather4(dst + i * 128, &tmX, &xbar[b], (st0 + s) * BK, r.x, r.y, r.z, r.w);
-                            else tma_gather4_multicast(dst + i * 128, &tmX, &xbar[b], (st0 + s) * BK, r.x, r.y, r.z, r.w, (uint16_t)(5u << rank));
+                            tma_gather4(dst + i * 128, &tmX, &xbar[b], (st0 + s) * BK, r.x, r.y, r.z, r.w);
                         }
                     }
                     __syncwarp();
@@ -448,7 +436,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             }
             if (half == 0) drain(it);
-            if (PAIRS == 2 && stop) __nanosleep(500000);  // the other pair's copies on their way here
         } else if (warp == WARP_CODES) {
             if (lane == 0) {
                 int b = 0, it = 0;
@@ -510,7 +497,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         mma<CG>(tmem + acc * BN, da, db, idesc, in_group);
                         mma<CG>(tmem + acc * BN, da + 2, db + 2, idesc, 1);
                         if (steps == 1 && left > 1) {  // groups of 32: the second half is another
-                            commit<CG>(accf0 + 8 * acc, of_pair);
+                            commit<CG>(accf0 + 8 * acc);
                             acc ^= 1, taken ^= acc ^ 1;
                             wait(acce0 + 8 * acc, taken, kDevErrWaitEmpty);
                             if (stop) break;
@@ -521,10 +508,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             mma<CG>(tmem + acc * BN, da + 4, db + 4, idesc, 1);
                             mma<CG>(tmem + acc * BN, da + 6, db + 6, idesc, 1);
                         }
-                        commit<CG>(empty0 + 8 * b, of_all);
+                        commit<CG>(empty0 + 8 * b);
                         in_group += 2;
                         if (in_group >= steps || left <= 2) {
-                            commit<CG>(accf0 + 8 * acc, of_pair);
+                            commit<CG>(accf0 + 8 * acc);
                             acc ^= 1, taken ^= acc ^ 1, in_group = 0;
                         }
                         if (++b == STAGES) b = 0, parity ^= 1;
@@ -532,7 +519,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     if (*abort_flag) stop = true;
                 }
                 // every MMA issued must be complete before the tensor memory is freed
-                commit<CG>(smem_u32(last), of_pair);
+                commit<CG>(smem_u32(last));
                 if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
             }
             __syncwarp();
@@ -550,7 +537,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             stop = true;
                             break;
                         }
-                        arrive_leader<CG>(&ready[b], leader);
+                        arrive_leader<CG>(&ready[b]);
                         if (++b == STAGES) b = 0, ++use;
                     }
             }
@@ -610,7 +597,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     store_codes<T>(row + b * P::STAGE, r, 4, w, z >> 16);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&ready[b], leader);
+                    if (lane == 0) arrive_leader<CG>(&ready[b]);
                 }
                 if (!box_only) next_stage(), next_stage();
                 if (++cb == CRING) cb = 0, ++cuse;
@@ -686,7 +673,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
                     tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&acce[gi & 1], leader);
+                    if (lane == 0) arrive_leader<CG>(&acce[gi & 1]);
                 }
             }
             if (CG == 1 && ksplit > 1) {
@@ -756,42 +743,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
 }
 
-// Clusters of CG x PAIRS CTAs that the current device runs at once, as it answers the first time.  (GPCs whose SMs are no
-// multiple of it leave some idle: of 152 SMs clusters of four take 144.)
-template <typename T, int CG, int PAIRS>
-cudaError_t clusters_at_once(int *fit) {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    *fit = known[dev & 63].load(std::memory_order_relaxed);
-    if (*fit > 0) return cudaSuccess;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(CG * PAIRS);
-    lc.blockDim = dim3(NTHREADS);
-    lc.dynamicSmemBytes = Plan<CG>::TOTAL;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG * PAIRS, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(fit, (const void *)packed4_tiles_kernel<T, CG, PAIRS>, &lc);
-    if (e == cudaSuccess && *fit < 1) e = cudaErrorInvalidConfiguration;
-    if (e == cudaSuccess) known[dev & 63].store(*fit, std::memory_order_relaxed);
-    return e;
-}
-
-template <typename T, int CG, int PAIRS = 1>
+template <typename T, int CG>
 cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     using P = Plan<CG>;
     static SmemLimit limit;
-    cudaError_t e = limit.allow((const void *)packed4_tiles_kernel<T, CG, PAIRS>, P::TOTAL);
+    cudaError_t e = limit.allow((const void *)packed4_tiles_kernel<T, CG>, P::TOTAL);
     if (e != cudaSuccess) return e;
     CUtensorMap tx, tw;
     e = packed4_tmap_x(&tx, a, a.order ? 1 : BOX);
     if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK, BM, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (a.rows + BM * CG * PAIRS - 1) / (BM * CG * PAIRS);
+    const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG);
     // One matrix that gives few units: K is cut over a cluster first (codes are then made numbers once), to at least one and a
     // half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
     const auto units_of = [&](int64_t longest) { return (a.slots + longest - 1) / longest * tiles; };
@@ -800,14 +762,9 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     while (CG == 1 && !a.offsets && ksplit < 8 && units_of(BN) * ksplit * 2 <= sms && ksplit * 3 <= boxes) ksplit *= 2;
     // no more CTAs than units of the shortest chunks
     const int64_t most = ksplit > 1 ? units_of(BN) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
-    int fit = sms / CG;
-    if (PAIRS > 1) {
-        e = clusters_at_once<T, CG, PAIRS>(&fit);
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t clusters = most < fit ? most : fit;
+    const int64_t clusters = most < sms / CG ? most : sms / CG;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(clusters * CG * PAIRS * ksplit));
+    lc.gridDim = dim3((unsigned)(clusters * CG * ksplit));
     lc.blockDim = dim3(NTHREADS);
     lc.dynamicSmemBytes = P::TOTAL;
     lc.stream = s;
@@ -815,25 +772,16 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)(CG * PAIRS * ksplit), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.x = (unsigned)(CG * ksplit), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = CG * ksplit > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG, PAIRS>, tx, tw, a, ksplit);
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tx, tw, a, ksplit);
 }
 
 }  // namespace
 
 cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    const int64_t tiles = (a.rows + 2 * BM - 1) / (2 * BM), pairs = ((a.slots + BN - 1) / BN) * tiles;
-    // Gathered rows that two pairs of CTAs bring for each other, where gathering bounds the work: many rows to an expert,
-    // groups that are not taken out faster than that, and rounds enough that the SMs which clusters of four leave idle
-    // (8 of 152) and the coarser units do not show.  Measured (us, pairs and two pairs; slots an expert, experts, columns
-    // to rows, group): 1024, 8, 2048 to 8192, 128: 411 and 356; 8192, 4, 4096 to 4096, 128: 1492 and 1268; 2048, 8, 2048 to
-    // 2048, 64: 247 and 210; 512, 32, 2048 to 2048, 64: 293 and 278; against it 1024, 8, 2048 to 2048 (4 rounds): 139
-    // and 149; 128, 64, 2048 to 1408: 171 and 181; 2048, 16, 2048 to 768 (three tiles): 209 and 254; groups of 32: 399 and 401.
-    const bool fours = a.order && tiles % 2 == 0 && a.group >= 64 && a.slots >= 512 * (int64_t)a.experts &&
-                       ((a.slots + BN - 1) / BN + a.experts / 2) * (tiles / 2) >= 6 * (sms / 4);
-    if (fours) return a.dtype == 0 ? launch<__half, 2, 2>(a, sms, s) : launch<__nv_bfloat16, 2, 2>(a, sms, s);
+    const int64_t pairs = ((a.slots + BN - 1) / BN) * ((a.rows + 2 * BM - 1) / (2 * BM));
     // Pairs of CTAs share X where they fill the SMs (us, single CTAs and pairs: 2048 x 4096 to 4096 67 and 64, 512 x 4096 to 12288
     // 66 and 63; 1024 x 4096 to 4096 56 and 55), else single ones have twice the units (512 x 4096 to 4096 24 and 51).
     if (pairs >= sms / 2) return a.dtype == 0 ? launch<__half, 2>(a, sms, s) : launch<__nv_bfloat16, 2>(a, sms, s);

@@ -192,16 +192,6 @@ __device__ __forceinline__ void tma_gather4(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
-// To the same place in the CTAs of the cluster that `ctas` names, each of which counts the bytes on its own barrier.
-__device__ __forceinline__ void tma_gather4_multicast(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int r0, int r1, int r2, int r3,
-                                                      uint16_t ctas) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(smem_dst)),
-        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "h"(ctas)
-        : "memory");
-}
-
 // 3-D form of tma_load_2d (c2: the outermost coordinate, e.g. the matrix of a batch).
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
     asm volatile(
