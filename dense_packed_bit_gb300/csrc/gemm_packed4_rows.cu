@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         while (more() && !stop) {
             if (use > 0) {
                 if (*abort_flag || !mbar_wait_sleep(&empty[b], (use - 1) & 1)) {
-                    if (lane == 0 && !*abort_flag) atomicExch(&g_packed4_rows_err, kDevErrWaitEmpty);
+                    if (lane == 0 && !*abort_flag) atomicOr(&g_packed4_rows_err, kDevErrWaitEmpty);
                     *abort_flag = 1;
                     stop = true;
                     break;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
         for (int i = 0; i < DEPTH && i < n; ++i) {
             const int lastn = i + ((n - 1 - i) / DEPTH) * DEPTH;
             if (!mbar_wait(&full[i], (uint32_t)(lastn / DEPTH) & 1)) {
-                if (lane == 0) atomicExch(&g_packed4_rows_err, kDevErrDrain);
+                if (lane == 0) atomicOr(&g_packed4_rows_err, kDevErrDrain);
                 break;
             }
         }
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                     const Scales<G> now = sz[i];
                     fetch(sz[i]);
                     if (!stop && !mbar_wait(&full[b], use & 1)) {
-                        if (lane == 0) atomicExch(&g_packed4_rows_err, kDevErrWaitFull);
+                        if (lane == 0) atomicOr(&g_packed4_rows_err, kDevErrWaitFull);
                         *abort_flag = 1;
                         stop = true;  // nothing waits any more, the warps' barriers are still met
                     }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             next_chunk(c);
         }
     }
-    if (err) atomicExch(&g_packed4_rows_err, err);
+    if (err) atomicOr(&g_packed4_rows_err, err);
 }
 
 template <typename T, int NT, int G>

@@ -115,7 +115,7 @@ __device__ __forceinline__ Unit unit_at(const Packed4MmArgs &a, const Work &w, i
 
 template <int CG>
 __device__ __forceinline__ void fail(volatile int *abort_flag, unsigned int code) {
-    atomicExch(&g_packed4_tiles_err, code);
+    atomicOr(&g_packed4_tiles_err, code);
     *abort_flag = 1;
     if constexpr (CG == 2)
         st_cluster_u32(cluster_map(smem_u32(const_cast<int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int i = 0; i < STAGES && i < it; ++i) {
                 const int lastit = i + ((it - 1 - i) / STAGES) * STAGES;
                 if (!mbar_wait(&xbar[i], (uint32_t)(lastit / STAGES) & 1)) {
-                    atomicExch(&g_packed4_tiles_err, kDevErrDrain);
+                    atomicOr(&g_packed4_tiles_err, kDevErrDrain);
                     break;
                 }
             }
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 for (int i = 0; i < CRING && i < it; ++i) {
                     const int lastit = i + ((it - 1 - i) / CRING) * CRING;
                     if (!mbar_wait(&cfull[i], (uint32_t)(lastit / CRING) & 1)) {
-                        atomicExch(&g_packed4_tiles_err, kDevErrDrain);
+                        atomicOr(&g_packed4_tiles_err, kDevErrDrain);
                         break;
                     }
                 }
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 // every MMA issued must be complete before the tensor memory is freed
                 commit<CG>(smem_u32(last));
-                if (!mbar_wait(last, 0)) atomicExch(&g_packed4_tiles_err, kDevErrWaitMma);
+                if (!mbar_wait(last, 0)) atomicOr(&g_packed4_tiles_err, kDevErrWaitMma);
             }
             __syncwarp();
         } else if (warp == WARP_MMA) {
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         cluster_sync();
         cluster_sync();
     }
-    if (err) atomicExch(&g_packed4_tiles_err, err);
+    if (err) atomicOr(&g_packed4_tiles_err, err);
     __syncwarp();
     tc_fence_before_sync();
     if constexpr (CG == 2) cluster_sync();

@@ -3,6 +3,7 @@
 // Argument checks, variant selection and launches on the caller's stream.
 // Every check happens before the first CUDA call, so argument errors are
 // reported the same way on machines without a GPU.
+#include "device_error.h"
 #include "mm.h"
 #include "mm_internal.h"
 
@@ -836,6 +837,15 @@ mm_status mm_gemv_packed4(const uint8_t *codes, const uint16_t *scales, const ui
     return mm_gemv_packed4_ex(codes, scales, x, y, rows, cols, codebook, stream, nullptr);
 }
 
+// The 4-bit products' words, as a status with its message.
+static mm_status packed4_status(unsigned int word) {
+    static_assert(mm::kCacheErrRange == mm::kRangeBit, "the code that the kernels add for a range");
+    const mm_status s = mm::device_error_status(word);
+    if (s == MM_ERR_TIMEOUT) return fail(s, "a bounded device wait ran out in the 4-bit products (code %u)", word);
+    if (s != MM_OK) return fail(s, "4-bit products: an expert's slots or a row of X in device memory is out of range");
+    return s;
+}
+
 mm_status mm_check_device_error(mm_stream_t stream) {
     cudaError_t e;
     const unsigned int v = mm::gemm_ffma_take_device_error(reinterpret_cast<cudaStream_t>(stream), &e);
@@ -891,12 +901,10 @@ mm_status mm_check_device_error(mm_stream_t stream) {
     if (ca != 0) return fail(MM_ERR_TIMEOUT, "a bounded device wait ran out in the cache attention (code %u)", ca);
     const unsigned int pw = mm::packed4_rows_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
-    if (pw != 0) return fail(MM_ERR_INVALID_ARG, "4-bit products: an expert's slots or a row of X in device memory is out of range");
+    if (const mm_status st = packed4_status(pw); st != MM_OK) return st;
     const unsigned int pt = mm::packed4_tiles_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
-    if (pt == mm::kCacheErrRange)
-        return fail(MM_ERR_INVALID_ARG, "4-bit products: an expert's slots or a row of X in device memory is out of range");
-    if (pt != 0) return fail(MM_ERR_TIMEOUT, "a bounded device wait ran out in the 4-bit products (code %u)", pt);
+    if (const mm_status st = packed4_status(pt); st != MM_OK) return st;
     const unsigned int co = mm::experts_combine_take_device_error(&e);
     if (e != cudaSuccess) return cuda_fail(e, "mm_check_device_error");
     if (co != 0) return fail(MM_ERR_INVALID_ARG, "experts combine: a slot in device memory is out of range");

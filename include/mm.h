@@ -131,8 +131,9 @@ mm_status mm_gemm_packed2(const uint8_t *codes, const uint16_t *scales, const ui
 
 /*
  * Waits for `stream`, then reads and clears the device error word set by a
- * kernel whose bounded wait ran out.  Returns MM_OK, MM_ERR_TIMEOUT or
- * MM_ERR_CUDA.
+ * kernel whose bounded wait ran out (MM_ERR_TIMEOUT) or that found indices in
+ * device memory out of range (MM_ERR_INVALID_ARG).  Returns MM_OK, one of these
+ * or MM_ERR_CUDA.
  */
 mm_status mm_check_device_error(mm_stream_t stream);
 
