@@ -445,6 +445,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const Unit t = unit_at<CG>(a, wk, u, &err);
                     for (int s = 0; s < stages; s += 2, ++it) {
                         if (*abort_flag) { stop = true; break; }
+                        // The warps that empty the ring wait for the kernel in front, however long that runs: so does this
+                        // one once the ring is full, before the first wait that has a limit.
+                        if (it == CRING) late_wait();
                         if (use > 0 && !mbar_wait_sleep(&cempty[b], (use - 1) & 1)) {
                             fail<CG>(abort_flag, kDevErrWaitEmpty);
                             stop = true;
