@@ -481,6 +481,21 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
     if (err) atomicOr(&g_packed4_rows_err, err);
 }
 
+// K is cut over as many CTAs of a cluster as the GPU holds beside each other (1 x 12288 to 1536 7.2 us,
+// uncut 22.2; 8 x 4096 to 4096 6.2 and 8.7)
+struct Cut {
+    int64_t units;
+    int cluster, ctas;  // ctas: that the GPU holds
+};
+Cut cut_of(const Packed4MmArgs &a, int sms) {
+    const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
+    const int64_t units = tiles * (a.offsets ? (a.slots < a.experts ? a.slots : a.experts) : 1);
+    const int ctas = sms * 2;
+    int cluster = 1;
+    while (cluster < MAX_CLUSTER && cluster * 2 <= stages && units * cluster * 2 <= ctas) cluster *= 2;
+    return {units, cluster, ctas};
+}
+
 template <typename T, int NT, int G>
 cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     using P = Plan<NT>;
@@ -492,13 +507,9 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     e = packed4_tmap_x(&tx, a, a.order ? 1 : xbox);
     if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, HALF / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    // K is cut over as many CTAs of a cluster as the GPU holds beside each other (1 x 12288 to 1536 7.2 us, uncut 22.2; 8 x 4096
-    // to 4096 6.2 and 8.7)
-    const int tiles = (a.rows + ROWS - 1) / ROWS, stages = (a.cols + BK - 1) / BK;
-    const int64_t units = tiles * (a.offsets ? (a.slots < a.experts ? a.slots : a.experts) : 1);
-    int cluster = 1;
-    while (cluster < MAX_CLUSTER && cluster * 2 <= stages && units * cluster * 2 <= sms * P::CTAS) cluster *= 2;
-    const int64_t fit = (int64_t)sms * P::CTAS / cluster, clusters = units < fit ? units : fit;
+    const auto [units, cluster, ctas] = cut_of(a, sms);
+    static_assert(P::CTAS == 2, "as cut_of counts");
+    const int64_t fit = ctas / cluster, clusters = units < fit ? units : fit;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(clusters * cluster));
     lc.blockDim = dim3(NTHREADS);
@@ -529,6 +540,14 @@ cudaError_t launch_t(const Packed4MmArgs &a, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+// A warp adds the sums of half of a CTA's groups one after another in fp32, each addition off by 2^-24 of the sum so far at most:
+// 1,024 of them (65,536 columns in groups of 32, more where K is cut) are what the bound of the error allows.
+bool packed4_rows_holds(const Packed4MmArgs &a, int sms) {
+    const Cut c = cut_of(a, sms);
+    const int64_t stages = ((a.cols + BK - 1) / BK + c.cluster - 1) / c.cluster;
+    return stages * (HALF / a.group) <= 1024;
+}
 
 cudaError_t launch_packed4_rows(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     return a.dtype == 0 ? launch_t<__half>(a, sms, s) : launch_t<__nv_bfloat16>(a, sms, s);

@@ -48,6 +48,12 @@ constexpr int DEC_WARPS = 8, EPI_WARPS = 8;
 constexpr int MAX_EXPERTS = 1024;
 constexpr int BOX = 64;        // rows of X per TMA box
 
+// A row's group sums are added one after another in fp32, each addition off by 2^-24 of the sum so far at most.  Where a CTA adds
+// more than LONG_GROUPS (32,768 columns in groups of 32), units are of LONG_BN rows of X, which leaves a thread registers for a
+// compensated total (Kahan's) to which its sums of FOLD groups go: the error stays that of FOLD groups at any length.  (64 x
+// 2^20 in groups of 32, the first group large and the others just below half a place: 1.2e-4 of the terms without.)
+constexpr int LONG_GROUPS = 1024, LONG_BN = 64, FOLD = 512;
+
 // Registers of a thread once the roles part, of the 96 at launch: 384 x 40 + 256 x 176 <= 640 x 96.
 #define MM_PACKED4_REGS_FEW "40"
 #define MM_PACKED4_REGS_EPI "176"
@@ -241,7 +247,7 @@ __device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float 
     }
 }
 
-template <typename T, int CG>
+template <typename T, int CG, bool LONG>
 __global__ void __launch_bounds__(NTHREADS, 1)
     packed4_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                          const __grid_constant__ Packed4MmArgs a, const int ksplit) {
@@ -323,14 +329,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) sums[k][warp] = all;
         }
         __syncthreads();
-        // the longest chunk: the one whose rounds of units take the least time, of equal ones the largest
+        // the longest chunk: the one whose rounds of units take the least time, of equal ones the largest (256 where K is cut)
         int of_warp = 0, all = 0;
         int64_t least = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const int v = lane < NTHREADS / 32 ? sums[k][lane] : 0, chunks = __reduce_add_sync(~0u, v);
             const int64_t cost = (int64_t)((uint32_t)(chunks * wk.tiles + ncl - 1) / (uint32_t)ncl) * cost_of(a.order != nullptr, k);
-            if (k == 0 || (ksplit == 1 && cost < least)) least = cost, wk.longest = 256 >> k, of_warp = v, all = chunks;
+            if (LONG ? k == 2 : k == 0 || (ksplit == 1 && cost < least)) least = cost, wk.longest = 256 >> k, of_warp = v, all = chunks;
         }
         const int c0 = chunks_of(n[0], wk.longest), c1 = chunks_of(n[1], wk.longest);
         int run = c0 + c1;
@@ -639,9 +645,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         enter(cid);
         for (int u = cid; u < wk.units; u += ncl) {
             const int cols = (t.N + 63) / 64 * 32, c0 = half * cols;  // this half's columns of D
-            float acc[128];
+            constexpr int ACC = LONG ? LONG_BN / 2 : BN / 2;
+            float acc[ACC], all[LONG ? ACC : 1], lost[LONG ? ACC : 1];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            for (int i = 0; i < ACC; ++i) {
+                acc[i] = 0.f;
+                if constexpr (LONG) all[i] = lost[i] = 0.f;
+            }
+            const auto fold = [&] {  // all += acc; lost: what that addition, and those before it, added too much
+                if constexpr (LONG) {
+#pragma unroll
+                    for (int i = 0; i < ACC; ++i) {
+                        const float y = acc[i] - lost[i], t = all[i] + y, c = (t - all[i]) - y;
+                        all[i] = t, lost[i] = fabsf(c) < INFINITY ? c : 0.f, acc[i] = 0.f;  // of an infinity it is NaN
+                    }
+                }
+            };
             for (int g0 = gfirst; g0 < glast && !stop; g0 += SC) {
                 float now[SC];
 #pragma unroll
@@ -666,10 +685,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     uint32_t v[2][8];
                     tmem_ld8(d, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < ACC / 8; ++c) {
                         if (c % 4 == 0 && c * 8 >= cols) break;
                         tmem_wait8(v[c & 1]);
-                        if (c < 15 && (c + 1) * 8 < cols) tmem_ld8(d + (c + 1) * 8, v[(c + 1) & 1]);
+                        if (c < ACC / 8 - 1 && (c + 1) * 8 < cols) tmem_ld8(d + (c + 1) * 8, v[(c + 1) & 1]);
 #pragma unroll
                         for (int j = 0; j < 8; j += 2)
                             fma2_bcast(acc[c * 8 + j], acc[c * 8 + j + 1], f, __uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
@@ -678,6 +697,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     __syncwarp();
                     if (lane == 0) arrive_leader<CG>(&acce[gi & 1]);
                 }
+                if (LONG && (g0 - gfirst) % FOLD == FOLD - SC) fold();
+            }
+            if constexpr (LONG) {
+                fold();
+#pragma unroll
+                for (int i = 0; i < ACC; ++i) acc[i] = all[i];
             }
             if (CG == 1 && ksplit > 1) {
                 // The cluster's CTAs have a part of K each, of this one unit.  Every MMA and copy of the CTA has ended: its ring
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 float *sums = reinterpret_cast<float *>(smem);
                 const int row = 32 * quarter + lane;
 #pragma unroll
-                for (int j = 0; j < 128; ++j)
+                for (int j = 0; j < ACC; ++j)
                     if (j < cols) sums[(c0 + j) * BM + row] = acc[j];
                 cluster_sync();
                 const int share = (t.n + ksplit - 1) / ksplit, n0 = (int)part * share, n1 = min(t.n, n0 + share);
@@ -710,7 +735,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             float *const out = reinterpret_cast<float *>(smem + P::OUT) + (warp - WARP_EPI0) * 1024;
             const int r0 = done.r0 + (int)rank * BM + 32 * quarter;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < ACC / 32; ++c) {
                 const int base = c0 + c * 32;
                 if (c * 32 >= cols || base >= done.n || r0 >= a.rows) break;
                 if (a.order) {  // a slot whose row of X does not exist (reported where X was loaded) counts as 0s
@@ -746,25 +771,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
 }
 
-template <typename T, int CG>
+int64_t units_of(const Packed4MmArgs &a, int64_t rows, int64_t longest) {
+    return (a.slots + longest - 1) / longest * ((a.rows + rows - 1) / rows);
+}
+
+// One matrix that gives few units: K is cut over a cluster first (codes are then made numbers once), to at least one and a
+// half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
+int ksplit_of(const Packed4MmArgs &a, int sms, int64_t longest) {
+    const int boxes = (a.cols + 2 * BK - 1) / (2 * BK);
+    int ksplit = 1;
+    while (!a.offsets && ksplit < 8 && units_of(a, BM, longest) * ksplit * 2 <= sms && ksplit * 3 <= boxes) ksplit *= 2;
+    return ksplit;
+}
+
+template <typename T, int CG, bool LONG>
 cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     using P = Plan<CG>;
     static SmemLimit limit;
-    cudaError_t e = limit.allow((const void *)packed4_tiles_kernel<T, CG>, P::TOTAL);
+    cudaError_t e = limit.allow((const void *)packed4_tiles_kernel<T, CG, LONG>, P::TOTAL);
     if (e != cudaSuccess) return e;
     CUtensorMap tx, tw;
     e = packed4_tmap_x(&tx, a, a.order ? 1 : BOX);
     if (e == cudaSuccess) e = packed4_tmap_w(&tw, a, BK, BM, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG);
-    // One matrix that gives few units: K is cut over a cluster first (codes are then made numbers once), to at least one and a
-    // half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
-    const auto units_of = [&](int64_t longest) { return (a.slots + longest - 1) / longest * tiles; };
-    const int boxes = (a.cols + 2 * BK - 1) / (2 * BK);
-    int ksplit = 1;
-    while (CG == 1 && !a.offsets && ksplit < 8 && units_of(BN) * ksplit * 2 <= sms && ksplit * 3 <= boxes) ksplit *= 2;
+    const int64_t tiles = (a.rows + BM * CG - 1) / (BM * CG), longest = LONG ? LONG_BN : BN;
+    const int ksplit = CG == 1 ? ksplit_of(a, sms, longest) : 1;
     // no more CTAs than units of the shortest chunks
-    const int64_t most = ksplit > 1 ? units_of(BN) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
+    const int64_t most = ksplit > 1 ? units_of(a, BM, longest) : ((a.slots + 63) / 64 + (a.offsets ? a.experts : 0)) * tiles;
     const int64_t clusters = most < sms / CG ? most : sms / CG;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(clusters * CG * ksplit));
@@ -778,17 +811,21 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.x = (unsigned)(CG * ksplit), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = CG * ksplit > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG>, tx, tw, a, ksplit);
+    return cudaLaunchKernelEx(&lc, packed4_tiles_kernel<T, CG, LONG>, tx, tw, a, ksplit);
 }
 
 }  // namespace
 
 cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    const int64_t pairs = ((a.slots + BN - 1) / BN) * ((a.rows + 2 * BM - 1) / (2 * BM));
     // Pairs of CTAs share X where they fill the SMs (us, single CTAs and pairs: 2048 x 4096 to 4096 67 and 64, 512 x 4096 to 12288
     // 66 and 63; 1024 x 4096 to 4096 56 and 55), else single ones have twice the units (512 x 4096 to 4096 24 and 51).
-    if (pairs >= sms / 2) return a.dtype == 0 ? launch<__half, 2>(a, sms, s) : launch<__nv_bfloat16, 2>(a, sms, s);
-    return a.dtype == 0 ? launch<__half, 1>(a, sms, s) : launch<__nv_bfloat16, 1>(a, sms, s);
+    const bool pairs = units_of(a, 2 * BM, BN) >= sms / 2;
+    // groups that a CTA adds at most, of equal shares in whole boxes
+    const int ksplit = pairs ? 1 : ksplit_of(a, sms, BN);
+    const int64_t each = ((a.cols + 2 * BK - 1) / (2 * BK) + ksplit - 1) / ksplit * (2 * BK) / a.group;
+    if (each > LONG_GROUPS) return a.dtype == 0 ? launch<__half, 1, true>(a, sms, s) : launch<__nv_bfloat16, 1, true>(a, sms, s);
+    if (pairs) return a.dtype == 0 ? launch<__half, 2, false>(a, sms, s) : launch<__nv_bfloat16, 2, false>(a, sms, s);
+    return a.dtype == 0 ? launch<__half, 1, false>(a, sms, s) : launch<__nv_bfloat16, 1, false>(a, sms, s);
 }
 
 unsigned int packed4_tiles_take_device_error(cudaError_t *err) {

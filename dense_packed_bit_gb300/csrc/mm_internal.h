@@ -334,6 +334,7 @@ struct Packed4MmArgs {
     int y_dtype;             // 0 f16, 1 bf16, 2 f32
     int64_t y_stride;
 };
+bool packed4_rows_holds(const Packed4MmArgs &a, int sms);  // a row is short enough for the error's bound
 cudaError_t launch_packed4_rows(const Packed4MmArgs &a, int sms, cudaStream_t s);
 unsigned int packed4_rows_take_device_error(cudaError_t *err);
 cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s);

@@ -762,7 +762,8 @@ typedef struct {
  *   (1 + exp(-z)): a gate's and an up-projection's rows taken in turn; Y then has rows / 2 columns.
  * Y: y_dtype MM_F32 or W's dtype, rows y_stride elements apart, aligned to its elements; every element is written.
  * Codes less their zeros are exact, products and sums are fp32, the scale is applied to a group's fp32 sum, Y is rounded
- * once: |z - z_exact| <= 1e-5 * sum_k |W[r][k] X[m][k]| before that.  Results repeat bit for bit.
+ * once: |z - z_exact| <= e * sum_k |W[r][k] X[m][k]| before that, where e is 1e-5 for rows of up to 128 groups and 2^-24 more
+ * for each further one of 1024 (6.4e-5), at any length.  Results repeat bit for bit.
  * 1 <= M <= 2^30.
  * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, strides, types or options out of range, Y
  * overlapping an input.
