@@ -195,10 +195,6 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// silu in few instructions, for results of 16 bits: an exponential and a quotient of a few ulp each (at a gate of -20 about
-// 2^-19, of which a half-ulp of fp16 is 2^7)
-__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
-
 // Slots first .. first + n - 1 and rows r0 .. r0 + 31 of Y from `out`, [32 slots][32 rows] of a warp: 16 bytes to a lane where
 // Y allows it (vec), else element by element.
 template <typename T>
@@ -213,17 +209,17 @@ __device__ __forceinline__ void store_block(const Packed4MmArgs &a, const float 
                 const int64_t at = (int64_t)(first + j) * a.y_stride + (r0 >> 1) + c;
                 if (a.y_dtype == 2) {
                     *reinterpret_cast<float4 *>(static_cast<float *>(a.Y) + at) =
-                        make_float4(silu(p.x) * p.y, silu(p.z) * p.w, silu(q.x) * q.y, silu(q.z) * q.w);
+                        make_float4(swiglu(p.x, p.y, true), swiglu(p.z, p.w, true), swiglu(q.x, q.y, true), swiglu(q.z, q.w, true));
                 } else {
-                    const uint32_t lo = Code4<T>::round(silu_fast(p.x) * p.y) | (uint32_t)Code4<T>::round(silu_fast(p.z) * p.w) << 16;
-                    const uint32_t hi = Code4<T>::round(silu_fast(q.x) * q.y) | (uint32_t)Code4<T>::round(silu_fast(q.z) * q.w) << 16;
+                    const uint32_t lo = Code4<T>::round(swiglu(p.x, p.y, false)) | (uint32_t)Code4<T>::round(swiglu(p.z, p.w, false)) << 16;
+                    const uint32_t hi = Code4<T>::round(swiglu(q.x, q.y, false)) | (uint32_t)Code4<T>::round(swiglu(q.z, q.w, false)) << 16;
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.Y) + at) = make_uint2(lo, hi);
                 }
             }
         } else {
             for (int i = lane; i < n * per; i += 32) {
                 const int j = i / per, c = i % per;
-                if (2 * c < left) store_y(a, first + j, (r0 >> 1) + c, silu(out[j * 32 + 2 * c]) * out[j * 32 + 2 * c + 1]);
+                if (2 * c < left) store_y(a, first + j, (r0 >> 1) + c, swiglu(out[j * 32 + 2 * c], out[j * 32 + 2 * c + 1], a.y_dtype == 2));
             }
         }
     } else if (vec && left == 32) {

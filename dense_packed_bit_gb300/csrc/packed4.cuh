@@ -58,7 +58,13 @@ struct Code4<__nv_bfloat16> {
     static __device__ __forceinline__ uint16_t round(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 };
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// silu(g) u, the same wherever Y lies.  For fp32 an exponential and a quotient of an ulp or two.  For results of 16 bits, of which
+// half a step is 2^-11 of the value or more, few instructions: an exponential of 2 + 1.18 |g| ulp (1.3e-5 at a gate of -88)
+// and a quotient of 2 ulp, whose divisor has to stay below 2^126: a quarter of 1 + exp(-g) does wherever that is finite.
+__device__ __forceinline__ float swiglu(float g, float u, bool wide) {
+    if (wide) return g / (1.0f + expf(-g)) * u;
+    return __fdividef(0.25f * g, fmaf(0.25f, __expf(-g), 0.25f)) * u;
+}
 
 // Slots [first, first + count) of expert e.
 struct Slots {
@@ -99,7 +105,8 @@ template <typename T>
 __device__ __forceinline__ void store4(const Packed4MmArgs &a, int64_t slot, int r, const float4 &v, bool vec) {
     const int64_t row = slot * a.y_stride;
     if (a.swiglu) {
-        const float p = silu(v.x) * v.y, q = silu(v.z) * v.w;
+        const bool wide = a.y_dtype == 2;
+        const float p = swiglu(v.x, v.y, wide), q = swiglu(v.z, v.w, wide);
         if (vec && r + 3 < a.rows) {
             if (a.y_dtype == 2) *reinterpret_cast<float2 *>(static_cast<float *>(a.Y) + row + (r >> 1)) = make_float2(p, q);
             else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.Y) + row + (r >> 1)) = Code4<T>::round(p) | (uint32_t)Code4<T>::round(q) << 16;

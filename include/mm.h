@@ -759,11 +759,12 @@ typedef struct {
  * Y = X W^T for W->experts = 1: Y[m][r] = sum_k W[r][k] X[m][k], m < M.
  * X: [M][cols] of W's dtype, rows x_stride elements apart (a multiple of 8; X 16-byte aligned).
  * act: MM_ACT_NONE; MM_ACT_SWIGLU (rows even): column i of Y is silu(z[2 i]) * z[2 i + 1], z the product, silu(z) = z /
- *   (1 + exp(-z)): a gate's and an up-projection's rows taken in turn; Y then has rows / 2 columns.
+ *   (1 + exp(-z)): a gate's and an up-projection's rows taken in turn; Y then has rows / 2 columns.  silu is computed in fp32,
+ *   within 2e-5 of itself where Y is of 16 bits (0 for gates below -88.7, where exp(-z) is infinite).
  * Y: y_dtype MM_F32 or W's dtype, rows y_stride elements apart, aligned to its elements; every element is written.
  * Codes less their zeros are exact, products and sums are fp32, the scale is applied to a group's fp32 sum, Y is rounded
  * once: |z - z_exact| <= e * sum_k |W[r][k] X[m][k]| before that, where e is 1e-5 for rows of up to 128 groups and 2^-24 more
- * for each further one of 1024 (6.4e-5), at any length.  Results repeat bit for bit.
+ * for each further one of 1024 (6.4e-5), at any length.  A call's results repeat bit for bit, wherever Y lies.
  * 1 <= M <= 2^30.
  * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, strides, types or options out of range, Y
  * overlapping an input.
