@@ -33,8 +33,9 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// N elements, 16 bytes of them at a time
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
     T v[N];
 };
 
@@ -97,8 +98,10 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant_
     if (err) atomicExch(&g_combine_err, err);
 }
 
+// Rows of packs of n elements start where a pack may
 bool fits(const void *p, int64_t stride, int64_t size, int n) {
-    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(size * n) == 0 && stride % n == 0;
+    const int64_t bytes = size * n < 16 ? size * n : 16;
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0 && stride * size % bytes == 0;
 }
 
 template <typename TY, typename TO>
