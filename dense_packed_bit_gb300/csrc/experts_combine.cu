@@ -39,16 +39,26 @@ struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack {
     T v[N];
 };
 
-// Rows of Y are read once
+// Rows of Y are read once, and stay as they lie in memory until they are added: elements of bf16 taken apart at the load made the
+// eight loads wait for one another (8191 x 2048 from 8 rows each in bf16 to fp32 163 us, as words 61)
 template <typename T, int N>
-__device__ __forceinline__ Pack<T, N> load(const T *p) {
-    if constexpr (sizeof(T) * N == 16) {
-        const uint4 v = ld_stream_v4(p);
-        return *reinterpret_cast<const Pack<T, N> *>(&v);
-    } else {
-        return *reinterpret_cast<const Pack<T, N> *>(p);
+struct Row {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ float at(int) const { return widen<T>(v); }
+};
+template <typename T>
+struct Row<T, 16 / sizeof(T)> {
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = ld_stream_v4(p); }
+    __device__ __forceinline__ float at(int i) const {
+        const int word = i * (int)sizeof(T) / 4;
+        const uint32_t w = word == 0 ? v.x : word == 1 ? v.y : word == 2 ? v.z : v.w;
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+        else if constexpr (__is_same(T, __half)) return __half2float(__ushort_as_half((unsigned short)(w >> (16 * (i & 1)))));
+        else return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
     }
-}
+};
 
 constexpr int THREADS = 256, AHEAD = 8;
 
@@ -70,7 +80,7 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant_
             for (int x = 0; x < N; ++x) sum[x] = 0.f;
         }
         for (int j0 = 0; j0 < a.top_k; j0 += AHEAD) {
-            Pack<TY, N> y[AHEAD];
+            Row<TY, N> y[AHEAD];
             float w[AHEAD];
             bool have[AHEAD];
 #pragma unroll
@@ -82,13 +92,13 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant_
                 else have[j] = slot >= 0;
                 if (!have[j]) continue;
                 w[j] = __ldg(a.weights + t * a.top_k + j0 + j);
-                y[j] = load<TY, N>(static_cast<const TY *>(a.Y) + slot * a.y_stride + c);
+                y[j].load(static_cast<const TY *>(a.Y) + slot * a.y_stride + c);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j)
                 if (have[j])
 #pragma unroll
-                    for (int x = 0; x < N; ++x) sum[x] = fmaf(w[j], widen<TY>(y[j].v[x]), sum[x]);
+                    for (int x = 0; x < N; ++x) sum[x] = fmaf(w[j], y[j].at(x), sum[x]);
         }
         Pack<TO, N> o;
 #pragma unroll

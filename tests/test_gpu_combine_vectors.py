@@ -1,5 +1,5 @@
 """The combination takes 16 bytes at a time wherever rows of Y, residual and out start at 16 bytes and are a multiple of 16
-bytes, for every pair of types here: right there, and faster than element by element (a thread to an element takes 1.7 to 3.7 times as
+bytes, for every pair of types: right there, and faster than element by element (a thread to an element takes 1.6 to 3.7 times as
 long; 0.85 is asked for, of the best of several turns)."""
 import pytest
 import torch
@@ -22,7 +22,7 @@ def at(buf, first, rows, stride, cols):
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("y_dtype", ["f32", "f16"])
+@pytest.mark.parametrize("y_dtype", ["f32", "f16", "bf16"])
 def test_rows_that_start_at_16_bytes(y_dtype, out):
     tokens, top_k, cols = 4096, 8, 2048
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -43,7 +43,8 @@ def test_rows_that_start_at_16_bytes(y_dtype, out):
     def time(first):
         start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         start.record()
-        call(first)
+        for _ in range(5):
+            call(first)
         end.record()
         torch.cuda.synchronize()
         return start.elapsed_time(end)
