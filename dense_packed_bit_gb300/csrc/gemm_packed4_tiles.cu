@@ -327,13 +327,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncthreads();
         // the longest chunk: the one whose rounds of units take the least time, of equal ones the largest (256 where K is cut)
         int of_warp = 0, all = 0;
+        bool too_many = false;
         int64_t least = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const int v = lane < NTHREADS / 32 ? sums[k][lane] : 0, chunks = __reduce_add_sync(~0u, v);
+            // (a warp's sum is 2^30 at most, the limit below less than 2^26)
+            const int v = lane < NTHREADS / 32 ? min(sums[k][lane], 1 << 26) : 0, chunks = __reduce_add_sync(~0u, v);
+            too_many = chunks > (a.slots + 63) / 64 + a.experts;  // of k = 2 in the end: the shortest
             const int64_t cost = (int64_t)((uint32_t)(chunks * wk.tiles + ncl - 1) / (uint32_t)ncl) * cost_of(a.order != nullptr, k);
             if (LONG ? k == 2 : k == 0 || (ksplit == 1 && cost < least)) least = cost, wk.longest = 256 >> k, of_warp = v, all = chunks;
         }
+        // Ranges that overlap may hold more slots than there are: the numbers of units would pass 32 bits
+        if (too_many) err = kDevErrRange, all = 0;
         const int c0 = chunks_of(n[0], wk.longest), c1 = chunks_of(n[1], wk.longest);
         int run = c0 + c1;
 #pragma unroll

@@ -803,7 +803,8 @@ mm_status mm_experts_route(const void *logits, int dtype, int64_t tokens, int64_
  * takes the slots in place (order NULL, x_rows = slots).  slots: the rows of Y and entries of order, an upper bound of
  * offsets[experts]; rows of Y in no expert's range are left as they were.  offsets and order are checked on the device: a
  * range that is not ascending within 0 .. slots is skipped, a row out of range counts as 0s, and mm_check_device_error
- * then returns MM_ERR_INVALID_ARG.  Types, act, layout and error bound as mm_gemm_packed4.  1 <= slots <= 2^30.
+ * then returns MM_ERR_INVALID_ARG; rows of Y in several ranges hold one of their products or, where the ranges' lengths add up
+ * to far more than slots (by over 64 an expert), all may be left as they were.  Types, act, layout and error bound as mm_gemm_packed4.  1 <= slots <= 2^30.
  * Errors: as mm_gemm_packed4, plus x_rows < 1, or < slots where order is NULL.
  */
 mm_status mm_experts_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, int64_t x_rows,
