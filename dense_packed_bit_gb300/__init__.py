@@ -449,8 +449,8 @@ def _tokens(t, what, cache, tokens, row, heads):
 
 
 def _reach(t, what, n):
-    """t holds n elements from its first to its last, on the GPU."""
-    if t.numel() < n and 1 + sum((a - 1) * b for a, b in zip(t.shape, t.stride())) < n:
+    """t holds n elements from its first to its last, on the GPU.  (Of an expanded tensor many share one place.)"""
+    if (1 + sum((a - 1) * b for a, b in zip(t.shape, t.stride())) if t.numel() else 0) < n:
         _refuse(f"{what} ends before the {n} elements that the call's sizes span")
     if not t.is_cuda:
         _refuse(f"{what} is not on the GPU")
