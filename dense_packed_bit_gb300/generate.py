@@ -99,6 +99,8 @@ class Experts:
 
 class Model:
     def __init__(self, shape, seed=7, device="cuda"):
+        if shape.experts and not 1 <= shape.top_k <= shape.experts <= 1024:
+            raise ValueError(f"{shape.experts} experts of which a token takes {shape.top_k}: at least that many, at most 1024")
         self.shape, self.device = shape, device
         d, kv = shape.width, shape.kv_heads * shape.dim
         self.tokens = torch.from_numpy(synth.normal_f32(seed, (shape.vocab, d), 1.0)).to(device)
