@@ -1360,8 +1360,9 @@ mm_status packed4_product(const mm_packed4 *W, const void *X, int64_t x_stride, 
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // us, rows and tiles: 16 x 4096 to 4096 7.5 and 11.4, 20 rows 12.9 and 11.6; 16 x 4096 to 10240 15 and 26, 24 rows 28 and 26;
     // 64 experts of 2048 x 2048 with 8 slots each 77 and 112, with 16 117 and 120, with 20 147 and 123
-    const bool many = slots > 16 * W->experts || !mm::packed4_rows_holds(a, sm_count());
-    const cudaError_t e = many ? mm::launch_packed4_tiles(a, sm_count(), st) : mm::launch_packed4_rows(a, sm_count(), st);
+    const int sms = sm_count();
+    const bool many = slots > 16 * W->experts || !mm::packed4_rows_holds(a, sms);
+    const cudaError_t e = many ? mm::launch_packed4_tiles(a, sms, st) : mm::launch_packed4_rows(a, sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
     return ok();
 }
