@@ -739,8 +739,8 @@ mm_status mm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab, 
  * weights_static: 1 promises that codes, scales and zeros are not written by work that is still queued or running when
  *   a call is made (weights laid out once), so their loads may start before the kernel in front of it has ended.
  * rows, cols at most 2^28, experts at most 1024, rows * experts at most 2^36, rows * scales_row below 2^32, 2^47 bytes
- * from the first code to the last and less than 2^40 from a row or a matrix to the next; strides of X, Y, logits, residual and out
- * below at most 2^30.  Y of a call has at most about 2^43 elements.
+ * from the first code to the last and less than 2^40 from a row or a matrix to the next; strides of X, Y and the logits at
+ * most 2^30.  Y of a call has at most about 2^43 elements.
  * The struct is host memory, read during each call.
  */
 typedef struct {
@@ -778,8 +778,8 @@ mm_status mm_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_stride, 
  * Token t's picks are the top_k largest of its logits, larger first, equal ones by index; NaN and -infinity are never
  * picked.  ids: [tokens][top_k], -1 where there are fewer.  weights: [tokens][top_k] fp32, `scale` times the scores of the
  * picks: score MM_ROUTE_SOFTMAX exp(x) / sum over all experts, MM_ROUTE_SIGMOID 1 / (1 + exp(-x)); renorm = 1: divided by
- * their sum over the token's picks.  A pick of -1 has weight 0.  A logit of +infinity makes the weights that depend on it
- * NaN (MM_ROUTE_SIGMOID without renorm: 1).
+ * their sum over the token's picks.  A pick of -1 has weight 0.  A logit of +infinity makes its token's softmax weights NaN;
+ * its sigmoid is 1.
  * The picks in order of expert, within an expert of token: order[i] = token * top_k + j is the pick in slot i, the slots
  * of expert e are offsets[e] .. offsets[e + 1] - 1 (offsets: [experts + 1]), and slots[token * top_k + j] is a pick's slot,
  * -1 for none.  order: [tokens * top_k], of which the first offsets[experts] are written.
@@ -818,6 +818,7 @@ mm_status mm_experts_gemm_packed4(const mm_packed4 *W, const void *X, int64_t x_
  * Y: [y_rows][cols] of y_dtype; residual (NULL: 0) and out: [tokens][cols] of out_dtype; any of MM_F16, MM_BF16, MM_F32,
  * rows their strides apart, aligned to their elements (16-byte aligned rows of a multiple of 16 bytes are faster).  out may
  * be the residual itself with the same stride, and overlaps nothing else.
+ * 1 <= top_k <= 1024, tokens * top_k and y_rows at most 2^30, cols at most 2^28, strides at most 2^30.
  * Errors: MM_ERR_INVALID_ARG for NULL or misaligned pointers, sizes, strides or types out of range, overlaps.
  */
 mm_status mm_experts_combine(const void *Y, int y_dtype, int64_t y_stride, int64_t y_rows, const int32_t *slots,
