@@ -4,7 +4,7 @@
 //
 // in fp32, j ascending, rounded once.  Bound by memory: a call reads tokens x top_k rows of Y, one of the residual and
 // writes one.  A thread takes 16 bytes of Y's columns with up to 8 rows' loads on their way at once: 8191 x 2048 from 8 rows each
-// 93.4 us = 6.43 TB/s, 96% of a copy.
+// 93.2 us = 6.44 TB/s, 96% of a copy (Y in fp32, out in bf16); from rows of 16 bits to fp32 61 us.
 #include "cache_view.cuh"
 #include "mm_common.cuh"
 #include "mm_internal.h"

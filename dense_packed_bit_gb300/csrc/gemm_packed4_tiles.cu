@@ -6,8 +6,9 @@
 // codes less their zeros are whole numbers of -15 .. 15, exact in X's type, so the tensor cores sum exact products in
 // fp32; a group's sum is taken out of tensor memory, multiplied by the group's scale in fp32 and added up in registers.
 // Scaled weights are never rounded, and no sum in the tensor core is longer than a group.  Taking D_g out costs a read of
-// tensor memory and an FMA for each of its elements against G MMA steps of each: with groups of 128 a quarter of the time
-// of the MMAs, beside which it runs (two accumulators of 256 columns), with groups of 32 all of it.
+// tensor memory and an FMA for each of its elements against G MMA steps of each.  With groups of 128 it mostly hides behind
+// the MMAs (two accumulators of 256 columns); with groups of 64 and 32 it is what bounds the kernel: 2048 x 4096 to 4096 takes
+// 66, 100 and 171 us, of which the MMAs 36.
 //
 // Roles of a CTA's 20 warps, over a ring of stages of 64 columns:
 //   warp 0          X by TMA, 64 rows to a box; where `order` names the rows, warps 0 and 3 gather them four at a time;
@@ -26,7 +27,7 @@
 //
 // Measured on a GB300 (groups of 128): 4096 x 4096 to 8192 in bf16 222 us = 1,240 TFLOP/s, 64% of a library product, where the
 // MMAs alone take 145: the ends of units, sums and numbers do not all hide behind them.  4096 tokens of 2 of 8 experts of 8192 x
-// 2048 with SwiGLU 421 us, bound by the gathers of X.  222 x 776 to 2304 9.2 us: latency, 0.4 us a stage.
+// 2048 with SwiGLU 416 us, bound by the gathers of X.  222 x 776 to 2304 9.2 us: latency, 0.4 us a stage.
 #include "packed4.cuh"
 #include "smem_limit.h"
 #include "tcgen05.cuh"
@@ -818,8 +819,9 @@ cudaError_t launch(const Packed4MmArgs &a, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_packed4_tiles(const Packed4MmArgs &a, int sms, cudaStream_t s) {
-    // Pairs of CTAs share X where they fill the SMs (us, single CTAs and pairs: 2048 x 4096 to 4096 67 and 64, 512 x 4096 to 12288
-    // 66 and 63; 1024 x 4096 to 4096 56 and 55), else single ones have twice the units (512 x 4096 to 4096 24 and 51).
+    // Pairs of CTAs share X where they fill the SMs (us, single CTAs and pairs, bf16 in groups of 128: 2048 x 4096 to 4096 70 and 67,
+    // 512 x 4096 to 12288 70 and 66), else single ones have twice the units (512 x 4096 to 4096 26 and 32; 1024 x 4096 to 4096,
+    // with 64 pairs, 37 and 36).
     const bool pairs = units_of(a, 2 * BM, BN) >= sms / 2;
     // groups that a CTA adds at most, of equal shares in whole boxes
     const int ksplit = pairs ? 1 : ksplit_of(a, sms, BN);

@@ -1358,8 +1358,10 @@ mm_status packed4_product(const mm_packed4 *W, const void *X, int64_t x_stride, 
     a.X = X, a.x_stride = x_stride, a.x_rows = x_rows, a.order = order, a.per_row = (int)per_row, a.offsets = offsets;
     a.slots = slots, a.swiglu = act == MM_ACT_SWIGLU, a.Y = Y, a.y_dtype = y_dtype, a.y_stride = y_stride;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // us, rows and tiles: 16 x 4096 to 4096 7.5 and 11.4, 20 rows 12.9 and 11.6; 16 x 4096 to 10240 15 and 26, 24 rows 28 and 26;
-    // 64 experts of 2048 x 2048 with 8 slots each 77 and 112, with 16 117 and 120, with 20 147 and 123
+    // us, the kernels for few rows and for many (groups of 128): 16 x 4096 to 4096 8.1 and 12.2, 20 rows 13.8 and 12.3; 16 x 4096 to
+    // 10240 15.5 and 28.2, 24 rows 28.7 and 28.4; 64 experts of 2048 x 2048 with 8 slots each 58 and 96, with 16 60 and 97, with 20
+    // 107 and 97.  How the slots are spread is known on the device only: with one expert far above the average the rule is
+    // wrong (1024 slots of 64 experts: 128 of one 98 and 97, 512 of one 238 and 109, all of one 448 and 21).
     const int sms = sm_count();
     const bool many = slots > 16 * W->experts || !mm::packed4_rows_holds(a, sms);
     const cudaError_t e = many ? mm::launch_packed4_tiles(a, sms, st) : mm::launch_packed4_rows(a, sms, st);
