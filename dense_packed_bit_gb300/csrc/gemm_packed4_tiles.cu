@@ -778,7 +778,7 @@ int64_t units_of(const Packed4MmArgs &a, int64_t rows, int64_t longest) {
 }
 
 // One matrix that gives few units: K is cut over a cluster first (codes are then made numbers once), to at least one and a
-// half boxes of codes (192 columns) a CTA, then the slots into shorter chunks, as far as all CTAs run at once.
+// half boxes of codes (192 columns) a CTA, as far as all CTAs run at once; chunks stay whole then.
 int ksplit_of(const Packed4MmArgs &a, int sms, int64_t longest) {
     const int boxes = (a.cols + 2 * BK - 1) / (2 * BK);
     int ksplit = 1;
