@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             if (++b == DEPTH) b = 0, ++use;
             if (++c.s == s1) {
                 if (cluster > 1) {  // the consumers' barriers count every thread; a cluster seldom has a second chunk
+                    __syncwarp();
                     cluster_sync();
                     cluster_sync();
                 }
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mine[(8 * n + 2 * q + (i & 1)) * P::STRIDE + g + 8 * (i >> 1)] = acc[n][i];
+            __syncwarp();
             bar_sync(1, CONSUMERS);
             const float *sum = red + turn * 2 * (TOKENS * P::STRIDE);
             // four rows to a thread
@@ -449,6 +451,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
             };
             if (cluster > 1) {
                 for (int i = threadIdx.x; i < n; i += CONSUMERS) reinterpret_cast<float4 *>(part)[i] = total(i);
+                __syncwarp();
                 cluster_sync();
             }
             if (rank == 0) {
@@ -473,6 +476,7 @@ __global__ void __launch_bounds__(NTHREADS, Plan<NT>::CTAS)
                     if (r < a.rows) store4<T>(a, c.first + t, r, v, vec);
                 }
             }
+            __syncwarp();
             if (cluster > 1) cluster_sync();  // nobody leaves, or writes part again, before it has been read
             turn ^= 1;  // of two buffers the other is free: the barrier above was behind its last reader
             next_chunk(c);

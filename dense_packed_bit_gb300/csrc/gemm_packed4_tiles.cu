@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (threadIdx.x == 0) pre[a.experts] = all;
         wk.units = all * wk.tiles;
     }
+    __syncwarp();
     tc_fence_before_sync();
     if constexpr (CG == 2) cluster_sync();
     else __syncthreads();
@@ -714,6 +715,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int j = 0; j < ACC; ++j)
                     if (j < cols) sums[(c0 + j) * BM + row] = acc[j];
+                __syncwarp();
                 cluster_sync();
                 const int share = (t.n + ksplit - 1) / ksplit, n0 = (int)part * share, n1 = min(t.n, n0 + share);
                 const int quad = lane * 4;
@@ -728,6 +730,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         if (k < ksplit) v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
                     if (t.r0 + quad < a.rows) store4<T>(a, t.first + n, t.r0 + quad, v, vec);
                 }
+                __syncwarp();
                 cluster_sync();  // nobody leaves before its sums have been read
                 break;
             }
